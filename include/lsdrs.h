@@ -289,7 +289,8 @@ rs_status rs_copy_probe(void* dst, const void* src, size_t bytes, void* stream);
  * rs_profile_read synchronises on the last event and writes up to `max`
  * records (kernel id, milliseconds, keys processed), oldest first, then
  * clears the log; it returns the number written.  Kernel ids: 0 upfront
- * histogram, 1 scan, 2 onesweep pass, 3 copy probe. */
+ * histogram, 1 scan, 2 onesweep pass, 3 copy probe, 8 a row loss, 9 the
+ * balance loss. */
 typedef struct rs_kernel_time {
   int kernel;
   float ms;
@@ -342,6 +343,175 @@ rs_status radix_sort_pairs_u32_noalloc_status(void* stream);
  * Synchronises `stream`; writes the probe's own reading of the word to
  * *result.  Allocates nothing. */
 rs_status rs_noalloc_timeout_probe(uint64_t timeout_ns, void* stream, rs_status* result);
+
+/* ------------------------------------------------------------------------
+ * Losses over rows of scores.
+ *
+ * What the sorts above order, these train on: rows of logits with the
+ * teacher's top values and columns that a descending row sort returns
+ * (rs_distill_loss), rows of logits with the one column that was sampled
+ * (rs_policy_loss), and rows of a router's scores with the expert ids chosen
+ * in them (rs_balance_loss, whose counts are the segment lengths of the
+ * (expert, token) pairs that radix_sort_pairs_u32 groups).
+ *
+ * Shared by the three:
+ *  - Every pointer of an argument struct is device memory of the current
+ *    device (the structs themselves are host memory, read before the call
+ *    returns).  Nothing is allocated and nothing synchronises; the results
+ *    are the same bits in every run on one GPU.
+ *  - Rows have unit stride inside and *_stride elements from one to the next
+ *    (at least the row's length); no alignment beyond the element's own is
+ *    needed.  A gradient may be written over the logits (same pointer and
+ *    stride); any other overlap of a gradient with the logits is rejected.
+ *  - Statistics, sums and losses are 32-bit floats whatever the scores'
+ *    type; a gradient has the scores' type and is rounded to it once.
+ *  - -inf scores take no part (their probability is 0).  A row without any
+ *    score above -inf has loss 0 and gradient 0, its lse is -inf.  NaN, or
+ *    +inf, makes its row's results NaN and no other row's (a balance loss is
+ *    one number over all rows, so that is NaN too).
+ *  - Argument errors return RS_ERR_INVALID (RS_ERR_TEMP_TOO_SMALL) before
+ *    anything is enqueued.  No rows (tokens): RS_OK (see each call). */
+typedef enum rs_score_type { RS_SCORE_F16 = 0, RS_SCORE_BF16 = 1, RS_SCORE_F32 = 2 } rs_score_type;
+
+/* Longest list of a teacher's top logits, and most experts of a router. */
+#define RS_MAX_TOP 1024
+#define RS_MAX_EXPERTS 1024
+
+/* Distillation from a teacher's top logits.  With z = x / temperature,
+ * lse = log sum_j exp(z_j) and q_j = exp(z_j - lse) of a row x of logits,
+ * and p = the softmax of its teacher's live entries (top_values /
+ * temperature; an entry is live when 0 <= index < cols):
+ *
+ *   losses[r] = w * temperature^2 * sum_k p_k (log p_k - log q_{i_k})
+ *   d losses[r] / d x_j = w * temperature * (q_j - sum_{k: i_k = j} p_k)
+ *
+ * A row with no live entry (or only -inf teacher values) has loss 0 and
+ * gradient 0.  A column named twice gets both entries' p.
+ *   logits      rows x cols scores; 0 <= rows < 2^31, 1 <= cols <= RS_MAX_ROW_KEYS
+ *   top_values  rows x top scores (of their own type); 1 <= top <= RS_MAX_TOP
+ *   top_indices rows x top columns, int32 or int64 (index_bytes 4 or 8)
+ *   weights     rows floats or NULL (1); a row of weight 0 is not read: its
+ *               losses and lse are 0, its gradient 0
+ *   temperature > 0, finite
+ *   losses, lse rows floats
+ *   grad        rows x cols of the logits' type; rs_distill_loss: may be
+ *               NULL (losses only), else the gradient of the sum of losses */
+typedef struct rs_distill_args {
+  const void* logits;
+  int64_t logits_stride, rows, cols;
+  const void* top_values;
+  int64_t top_values_stride;
+  const void* top_indices;
+  int64_t top_indices_stride;
+  const float* weights;
+  float* losses;
+  float* lse;
+  void* grad;
+  int64_t grad_stride;
+  int logits_type, top_values_type, index_bytes, top;
+  float temperature;
+} rs_distill_args;
+
+/* The losses and, where args->grad is given, the gradient of their sum. */
+rs_status rs_distill_loss(const rs_distill_args* args, void* stream);
+
+/* The gradient of sum_r grad_losses[r] * losses[r] (grad_losses: rows floats,
+ * NULL: ones), with args->lse as rs_distill_loss wrote it for the same
+ * arguments; args->losses is not used. */
+rs_status rs_distill_loss_backward(const rs_distill_args* args, const float* grad_losses,
+                                   void* stream);
+
+/* Clipped policy loss with a KL term, of one taken action (column) a per
+ * row.  With z and lse as above, logp = z_a - lse, r = exp(logp - old) and
+ * d = ref - logp:
+ *
+ *   losses[r] = w * (-min(r A, clip(r, 1 - clip_low, 1 + clip_high) A)
+ *                    + kl_coef * (exp(d) - d - 1))
+ *   d losses[r] / d x_j = w * g * ([j = a] - q_j) / temperature,
+ *   g = -A r unless the clip holds (A > 0 and r > 1 + clip_high, or A < 0
+ *       and r < 1 - clip_low: 0), plus kl_coef * (1 - exp(d))
+ *
+ *   actions     rows columns, int32 or int64; a row whose action is outside
+ *               [0, cols) counts as a row of weight 0
+ *   old_logprobs, advantages  rows floats
+ *   ref_logprobs  rows floats, or NULL with kl_coef 0
+ *   clip_low, clip_high >= 0, finite; kl_coef finite
+ *   losses, logprobs (logp), lse  rows floats, 0 in rows of weight 0
+ * The other arguments as rs_distill_args. */
+typedef struct rs_policy_args {
+  const void* logits;
+  int64_t logits_stride, rows, cols;
+  const void* actions;
+  const float* old_logprobs;
+  const float* advantages;
+  const float* ref_logprobs;
+  const float* weights;
+  float* losses;
+  float* logprobs;
+  float* lse;
+  void* grad;
+  int64_t grad_stride;
+  int logits_type, index_bytes;
+  float clip_low, clip_high, kl_coef, temperature;
+} rs_policy_args;
+
+/* The losses and, where args->grad is given, the gradient of their sum. */
+rs_status rs_policy_loss(const rs_policy_args* args, void* stream);
+
+/* The gradient of sum_r grad_losses[r] * losses[r] (NULL: ones), with
+ * args->lse as rs_policy_loss wrote it; losses and logprobs are not used. */
+rs_status rs_policy_loss_backward(const rs_policy_args* args, const float* grad_losses,
+                                  void* stream);
+
+/* A router's load-balancing loss and its per-expert counts.  With p = the
+ * softmax of a token's scores, over the N tokens that the mask keeps, c_e the
+ * number of their expert ids equal to e and P_e = 1/N sum_t p_te:
+ *
+ *   loss = experts / (top * N) * sum_e c_e P_e
+ *   d loss / d x_tj = experts / (top * N^2) * p_tj (c_j - sum_e c_e p_te)
+ *
+ * (the counts are constants of the gradient).  N = 0: loss 0, gradient 0.
+ *   scores      tokens x experts; 0 <= tokens, tokens * top < 2^31,
+ *               1 <= experts <= RS_MAX_EXPERTS
+ *   expert_ids  tokens x top ids, int32 or int64; an id outside
+ *               [0, experts) is a dropped slot: not counted (top stays)
+ *   token_mask  tokens bytes (0: a padded token, not read) or NULL
+ *   loss        1 float; mean_probs experts floats (P); counts experts
+ *               int32 (c); n_tokens 1 int32 (N)
+ *   grad        tokens x experts of the scores' type; rs_balance_loss: may
+ *               be NULL, else the gradient of scale * loss
+ *   temp, temp_bytes  scratch of rs_balance_temp_bytes(), 256-byte aligned
+ * With tokens = 0 the outputs are still written (zeros). */
+typedef struct rs_balance_args {
+  const void* scores;
+  int64_t scores_stride, tokens;
+  const void* expert_ids;
+  int64_t expert_ids_stride;
+  const unsigned char* token_mask;
+  float* loss;
+  float* mean_probs;
+  int* counts;
+  int* n_tokens;
+  void* grad;
+  int64_t grad_stride;
+  void* temp;
+  size_t temp_bytes;
+  int scores_type, experts, index_bytes, top;
+  float scale;
+} rs_balance_args;
+
+/* Scratch size of rs_balance_loss (host only). */
+rs_status rs_balance_temp_bytes(int64_t tokens, int experts, size_t* bytes);
+
+/* Loss, mean_probs, counts, n_tokens and, where args->grad is given, the
+ * gradient of args->scale * loss. */
+rs_status rs_balance_loss(const rs_balance_args* args, void* stream);
+
+/* The gradient of grad_loss[0] * loss (one float on the device, NULL: 1)
+ * with args->counts and args->n_tokens as rs_balance_loss wrote them;
+ * expert_ids, loss, mean_probs, temp and scale are not used. */
+rs_status rs_balance_loss_backward(const rs_balance_args* args, const float* grad_loss,
+                                   void* stream);
 
 #ifdef __cplusplus
 }

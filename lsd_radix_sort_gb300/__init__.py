@@ -15,6 +15,9 @@ one-kernel path for short rows, the look-back wait limit) are keyword
 arguments of each call: the library holds no
 mode state, so calls on different threads or streams never affect each
 other.
+
+The losses over rows of scores (distillation from a teacher's top logits, the
+clipped policy loss, a router's balance loss) are in ``losses.py``.
 """
 from __future__ import annotations
 
@@ -30,7 +33,9 @@ __all__ = [
     "device_status", "passes_run", "SMALL_SORT_MAX_KEYS", "copy_probe",
     "lookback_timeout_probe", "profile_enable", "profile_read", "launch_count_reset",
     "noalloc_status", "noalloc_timeout_probe", "EXPORTED_SYMBOLS", "RS_MAX_KEYS", "RS_MAX_ROW_KEYS", "checked_build",
-    "BoundsViolation",
+    "BoundsViolation", "distill_loss", "distill_loss_grad", "distill_loss_backward",
+    "policy_loss", "policy_loss_grad", "policy_loss_backward", "balance_loss",
+    "balance_loss_grad", "balance_loss_backward", "balance_temp_bytes",
 ]
 
 RS_OK, RS_ERR_INVALID, RS_ERR_TEMP_TOO_SMALL, RS_ERR_CUDA, RS_ERR_LOOKBACK_TIMEOUT = range(5)
@@ -46,7 +51,7 @@ RS_OPT_PASS_SKIPPING, RS_OPT_TILE_OFFSETS, RS_OPT_NO_SMALL_SORT = 0x1, 0x2, 0x4
 SMALL_SORT_MAX_KEYS = 8192
 KERNEL_NAMES = {0: "upfront_hist", 1: "digit_scan", 2: "onesweep", 3: "copy_probe",
                 4: "timeout_probe", 5: "finish", 6: "tile_counts",
-                7: "small_sort"}
+                7: "small_sort", 8: "row_loss", 9: "balance_loss"}
 
 EXPORTED_SYMBOLS = (
     "radix_sort_keys_temp_bytes", "radix_sort_keys_u32", "radix_sort_keys_u64",
@@ -57,6 +62,8 @@ EXPORTED_SYMBOLS = (
     "radix_sort_pairs_u32_noalloc", "radix_sort_pairs_u32_noalloc_status",
     "rs_noalloc_timeout_probe", "radix_sort_keys_typed", "radix_sort_pairs_typed", "radix_sort_passes_run",
     "rs_checked_build", "radix_sort_checked_violations",
+    "rs_distill_loss", "rs_distill_loss_backward", "rs_policy_loss", "rs_policy_loss_backward",
+    "rs_balance_loss", "rs_balance_loss_backward", "rs_balance_temp_bytes",
 )
 
 
@@ -134,6 +141,13 @@ def load_library() -> ctypes.CDLL:
             "radix_sort_passes_run": [P, P, P],
             "radix_sort_pairs_typed": [i, i, P, P, P, P, sz, i, i, i, P, sz, P, P],
             "radix_sort_checked_violations": [P, P, P, P],
+            "rs_distill_loss": [P, P],
+            "rs_distill_loss_backward": [P, P, P],
+            "rs_policy_loss": [P, P],
+            "rs_policy_loss_backward": [P, P, P],
+            "rs_balance_loss": [P, P],
+            "rs_balance_loss_backward": [P, P, P],
+            "rs_balance_temp_bytes": [i64, i, P],
         }
         for name, args in sig.items():
             f = getattr(lib, name)
@@ -149,6 +163,17 @@ def load_library() -> ctypes.CDLL:
         lib.rs_checked_build.restype = i
         _lib = lib
         return lib
+
+
+def _lib_of():
+    """The library once it is loaded, without the lock of the first load."""
+    return _lib if _lib is not None else load_library()
+
+
+def _stream_of(t, stream=None):
+    """The given stream, or the current one of the tensor's device."""
+    import torch
+    return (stream if stream is not None else torch.cuda.current_stream(t.device)).cuda_stream
 
 
 def _status_name(status: int) -> str:
@@ -497,3 +522,9 @@ def noalloc_timeout_probe(timeout_ns: int, stream=None) -> int:
                                                    ctypes.byref(res)),
            "rs_noalloc_timeout_probe")
     return res.value
+
+
+from .losses import (  # noqa: E402  (the losses use the helpers above)
+    balance_loss, balance_loss_backward, balance_loss_grad, balance_temp_bytes, distill_loss,
+    distill_loss_backward, distill_loss_grad, policy_loss, policy_loss_backward,
+    policy_loss_grad)

@@ -495,6 +495,13 @@ bool typed_key(rs_key_type type, int descending, KeyKind* kind, KeyXform* xf) {
 
 }  // namespace
 
+namespace lsdrs {
+cudaError_t counted_launch(int kernel, uint64_t units, cudaStream_t s,
+                           cudaError_t (*launch)(void* ctx, int* launched), void* ctx) {
+  return timed_launch(kernel, units, s, [&](int* launched) { return launch(ctx, launched); });
+}
+}  // namespace lsdrs
+
 extern "C" {
 
 rs_status radix_sort_keys_temp_bytes(size_t n, int key_bytes, int value_bytes, int begin_bit,

@@ -332,6 +332,10 @@ struct FinishArgs {
 cudaError_t launch_finish(const FinishArgs& f, cudaStream_t s);
 // Streaming multiprocessors of the current device (queried once per device).
 int device_sm_count();
+// One launch bracketed by profiling events when they are enabled, and counted
+// (rs_profile_enable, rs_launch_count_reset); `launch` may raise the count.
+cudaError_t counted_launch(int kernel, uint64_t units, cudaStream_t s,
+                           cudaError_t (*launch)(void* ctx, int* launched), void* ctx);
 cudaError_t launch_timeout_probe(uint32_t* word, uint32_t* error, uint64_t timeout_ns,
                                  cudaStream_t s);
 

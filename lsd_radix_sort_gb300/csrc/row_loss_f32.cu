@@ -1,0 +1,8 @@
+// The row losses over f32 logits (row_loss.cuh).
+#include "row_loss_launch.cuh"
+
+namespace lsdrs {
+cudaError_t launch_row_loss_f32(RowLossOp op, LossMode mode, const RowLossArgs& a, cudaStream_t s) {
+  return launch_row_loss_of<RS_SCORE_F32>(op, mode, a, s);
+}
+}  // namespace lsdrs
