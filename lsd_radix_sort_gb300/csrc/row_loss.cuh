@@ -23,30 +23,64 @@ struct Targets {
   float* x;    // its score
 };
 
-// What the targets contribute to the loss and the coefficient.
+// What the target warp hands to the threads that hold the row.
 struct Head {
-  float a;     // distill: sum p (log p - (x - ref) / t)
-  float ref;   // the score that `a` is taken from: the largest target's, which
-               // is near the row's maximum, so that the loss is a sum of
-               // small terms instead of a difference of large ones
-  int live;    // 0: the row has no target
+  int off;       // weight 0 (or no action): the row is not read
+  int live;      // 0: the row has no target
+  float w, up;   // weight; weight times the upstream gradient
+  float a;       // distill: sum p (log p - (x - ref) / t)
+  float ref;     // the score that `a` is taken from: the largest target's,
+                 // which is near the row's maximum, so that the loss is a sum
+                 // of small terms instead of a difference of large ones
+  float x0, adv, old, ref_logp;  // policy
 };
 
-template <int TYPE, int OP>
+// Slots of the table in which the columns of k entries are looked up: a power
+// of two, at least 2 k.
+__host__ __device__ constexpr inline int target_slots(int k) {
+  int n = 64;
+  while (n < 2 * k) n *= 2;
+  return n;
+}
+
+// Whether the row takes part at all; read by every warp that decides on it.
+template <int OP>
+__device__ __forceinline__ bool row_off(const RowLossArgs& a, int64_t row) {
+  bool off = a.weights != nullptr && a.weights[row] == 0.0f;
+  if (OP == kOpPolicy) {
+    const int64_t i = load_index(a.actions, a.index_bytes, row);
+    off = off || i < 0 || i >= a.cols;
+  }
+  return off;
+}
+
+// One warp reads a row's targets: their columns, scores and probabilities,
+// and what they contribute to the loss.  slots: target_slots(k) words.
+template <int TYPE, int OP, int MODE>
 __device__ __forceinline__ void load_targets(const RowLossArgs& a, int64_t row, const Targets& t,
-                                             Head* h) {
+                                             int* slots, Head* h) {
   using S = Score<TYPE>;
   using Raw = typename S::Raw;
   const Raw* x = static_cast<const Raw*>(a.logits) + row * a.stride;
   const int lane = static_cast<int>(lane_id());
+  const float w = a.weights != nullptr ? a.weights[row] : 1.0f;
+  const float up = MODE == kLossBwd && a.grad_losses != nullptr ? w * a.grad_losses[row] : w;
   if (OP == kOpPolicy) {
     if (lane == 0) {
       const int64_t i = load_index(a.actions, a.index_bytes, row);
       const bool live = i >= 0 && i < a.cols;
       t.col[0] = live ? static_cast<int>(i) : -1;
       t.p[0] = 1.0f;
-      t.x[0] = live ? S::load(x[i]) : 0.0f;
-      h->live = live;
+      const float x0 = live ? S::load(x[i]) : 0.0f;
+      t.x[0] = x0;
+      h->off = !live || w == 0.0f;
+      h->live = 1;
+      h->w = w;
+      h->up = up;
+      h->x0 = x0;
+      h->adv = a.advantages[row];
+      h->old = a.old_logprobs[row];
+      h->ref_logp = a.ref_logprobs != nullptr ? a.ref_logprobs[row] : 0.0f;
     }
     return;
   }
@@ -71,41 +105,65 @@ __device__ __forceinline__ void load_targets(const RowLossArgs& a, int64_t row, 
   const float log_sum = logf(sum);
   float acc = 0.0f;
   for (int k = lane; k < a.k; k += kWarp) {
-    const float lp = (t.p[k] - vm) * a.inv_tau - log_sum;
-    const float p = sum == 0.0f ? 0.0f : exp2_approx((t.p[k] - vm) * scale2) / sum;
-    acc += p == 0.0f ? 0.0f : p * (lp - (t.x[k] - xm) * a.inv_tau);
+    const float v = t.p[k] - vm;
+    const float p = sum == 0.0f ? 0.0f : exp2_approx(v * scale2) / sum;
+    if (MODE != kLossBwd && p != 0.0f)
+      acc += p * (v * a.inv_tau - log_sum - (t.x[k] - xm) * a.inv_tau);
     t.p[k] = p;
   }
-  acc = warp_sum(acc);
-  __syncwarp();
-  // A column named twice: its first entry gets the sum, the others are
-  // dropped.  Every lane reads before any lane writes.
-  for (int k0 = 0; k0 < a.k; k0 += kWarp) {
-    const int k = k0 + lane;
-    const int col = k < a.k ? t.col[k] : -1;
-    bool first = true;
-    float p = 0.0f;
-    for (int j = 0; j < a.k; ++j) {
-      if (t.col[j] == col) {
-        if (j < k) first = false;
-        p += t.p[j];
+  if (MODE != kLossBwd) acc = warp_sum(acc);
+  // A column named twice: its first entry gets the sum, in the entries'
+  // order, and the others are dropped.  Lists of a sort name none twice, so
+  // the columns are first looked up in a table; only a list that does repeat
+  // one is compared entry by entry.
+  if (MODE != kLossFwd && a.k > 1) {
+    const int n = target_slots(a.k);
+    for (int i = lane; i < n; i += kWarp) slots[i] = -1;
+    __syncwarp();
+    bool twice = false;
+    for (int k = lane; k < a.k; k += kWarp) {
+      const int col = t.col[k];
+      if (col < 0) continue;
+      int at = static_cast<int>((static_cast<uint32_t>(col) * 2654435769u) >> 7) & (n - 1);
+      for (int probe = 0; probe < n; ++probe) {  // the table is at most half full
+        const int was = atomicCAS(&slots[at], -1, col);
+        if (was == -1) break;
+        if (was == col) {
+          twice = true;
+          break;
+        }
+        at = (at + 1) & (n - 1);
       }
     }
-    __syncwarp();
-    // entries before k0 + 32 are settled by their own group: only p changes
-    if (k < a.k && first && col >= 0) t.x[k] = p;
-    if (k < a.k && !first) t.x[k] = -1.0f;
-    __syncwarp();
-  }
-  for (int k = lane; k < a.k; k += kWarp) {
-    const float p = t.x[k];
-    if (p < 0.0f) t.col[k] = -1;
-    t.p[k] = p;
+    if (__any_sync(kFull, twice)) {
+      __syncwarp();
+      for (int k = lane; k < a.k; k += kWarp) {
+        const int col = t.col[k];
+        float p = 0.0f;
+        bool first = true;
+        for (int j = 0; j < a.k; ++j) {
+          if (t.col[j] == col) {
+            if (j < k) first = false;
+            p += t.p[j];
+          }
+        }
+        slots[k] = __float_as_int(first ? p : -1.0f);
+      }
+      __syncwarp();
+      for (int k = lane; k < a.k; k += kWarp) {
+        const float p = __int_as_float(slots[k]);
+        if (p < 0.0f) t.col[k] = -1;
+        t.p[k] = p;
+      }
+    }
   }
   if (lane == 0) {
+    h->off = w == 0.0f;
+    h->live = !(sum == 0.0f);
+    h->w = w;
+    h->up = up;
     h->a = acc;
     h->ref = xm;
-    h->live = !(sum == 0.0f);
   }
 }
 
@@ -114,25 +172,23 @@ struct RowResult {
   float loss, logp, lse, c;
 };
 
+// kLossBwd: m is t * lse, sum is 1.
 template <int OP, int MODE>
-__device__ __forceinline__ RowResult row_result(const RowLossArgs& a, int64_t row, float w,
-                                                const Head& h, float x0, float m, float sum) {
+__device__ __forceinline__ RowResult row_result(const RowLossArgs& a, const Head& h, float m,
+                                                float sum) {
   RowResult r;
   const bool empty = MODE == kLossBwd ? m == -INFINITY : sum == 0.0f;
   const float log_sum = MODE == kLossBwd ? 0.0f : logf(sum);
   r.lse = empty ? -INFINITY : m * a.inv_tau + log_sum;
-  float up = w;
-  if (MODE == kLossBwd && a.grad_losses != nullptr) up *= a.grad_losses[row];
   if (OP == kOpDistill) {
     const bool none = empty || !h.live;
     r.logp = 0.0f;
-    r.loss = none ? 0.0f : a.tau * a.tau * w * (h.a + ((m - h.ref) * a.inv_tau + log_sum));
-    r.c = none ? 0.0f : up * a.tau;
+    r.loss = none ? 0.0f : a.tau * a.tau * h.w * (h.a + ((m - h.ref) * a.inv_tau + log_sum));
+    r.c = none ? 0.0f : h.up * a.tau;
   } else {
-    // m is the maximum, or t * lse with log_sum = 0
-    const float logp = empty ? -INFINITY : (x0 - m) * a.inv_tau - log_sum;
-    const float adv = a.advantages[row];
-    const float ratio = expf(logp - a.old_logprobs[row]);
+    const float logp = empty ? -INFINITY : (h.x0 - m) * a.inv_tau - log_sum;
+    const float adv = h.adv;
+    const float ratio = expf(logp - h.old);
     const bool held = (adv > 0.0f && ratio > a.clip_high) || (adv < 0.0f && ratio < a.clip_low);
     // an advantage of 0 takes no part, however large the ratio
     const float clipped = fminf(fmaxf(ratio, a.clip_low), a.clip_high);
@@ -140,107 +196,547 @@ __device__ __forceinline__ RowResult row_result(const RowLossArgs& a, int64_t ro
     float g = held || adv == 0.0f ? 0.0f : -adv * ratio;
     if (isnan(ratio)) loss = g = ratio;
     if (a.ref_logprobs != nullptr) {
-      const float d = a.ref_logprobs[row] - logp;
+      const float d = h.ref_logp - logp;
       const float e = expm1f(d);
       loss += a.kl_coef * (e - d);
       g -= a.kl_coef * e;
     }
     r.logp = logp;
-    r.loss = empty ? 0.0f : w * loss;
-    r.c = empty ? 0.0f : -up * g * a.inv_tau;
+    r.loss = empty ? 0.0f : h.w * loss;
+    r.c = empty ? 0.0f : -h.up * g * a.inv_tau;
   }
   return r;
 }
 
-constexpr int kRowThreads = 512;
+template <int OP>
+__device__ __forceinline__ void store_result(const RowLossArgs& a, int64_t row,
+                                             const RowResult& r) {
+  a.losses[row] = r.loss;
+  a.lse[row] = r.lse;
+  if (OP == kOpPolicy) a.logprobs[row] = r.logp;
+}
 
-template <int TYPE, int OP, int MODE>
-__global__ void __launch_bounds__(kRowThreads) row_loss_kernel(const RowLossArgs a) {
+// ---------------------------------------------------------------- short rows
+// One CTA per row, the row in registers: rows of at most kThreads * VECS
+// 16-byte vectors.  Many CTAs per SM hide each other's loads and reductions.
+template <int TYPE, int OP, int MODE, int kThreads, int VECS>
+__global__ void __launch_bounds__(kThreads) row_loss_short_kernel(const RowLossArgs a) {
   grid_dependency_sync();
   using S = Score<TYPE>;
   using Raw = typename S::Raw;
-  extern __shared__ unsigned char smem[];
-  __shared__ Softmax part[kRowThreads / kWarp];
+  using V = ScoreVec<TYPE>;
+  constexpr int kWarps = kThreads / kWarp;
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ Softmax part[kWarps];
   __shared__ Head head;
   Targets t;
   t.col = reinterpret_cast<int*>(smem);
   t.p = reinterpret_cast<float*>(t.col + a.k);
   t.x = t.p + a.k;
+  int* slots = reinterpret_cast<int*>(t.x + a.k);
   const int tid = static_cast<int>(threadIdx.x), warp = tid / kWarp;
+  const int64_t row = blockIdx.x;
+  const Raw* x = static_cast<const Raw*>(a.logits) + row * a.stride;
+  Raw* g = static_cast<Raw*>(a.grad) + row * a.grad_stride;
+  const RowVecs<TYPE> vecs(x, static_cast<int>(a.cols));
+  const uint4* xv = reinterpret_cast<const uint4*>(x - vecs.lead);
+  uint4* gv = reinterpret_cast<uint4*>(g - vecs.lead);
+  const bool same = reinterpret_cast<uintptr_t>(gv) % 16 == 0;
   const float scale2 = a.inv_tau * kLog2e;
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    __syncthreads();  // the last row's lists are no longer read
-    const Raw* x = static_cast<const Raw*>(a.logits) + row * a.stride;
-    Raw* g = static_cast<Raw*>(a.grad) + row * a.grad_stride;
-    const float w = a.weights != nullptr ? a.weights[row] : 1.0f;
-    bool off = w == 0.0f;
-    if (OP == kOpPolicy) {
-      const int64_t i = load_index(a.actions, a.index_bytes, row);
-      off = off || i < 0 || i >= a.cols;
-    }
-    if (off) {
-      if (MODE != kLossBwd && tid == 0) {
-        a.losses[row] = 0.0f;
-        a.lse[row] = 0.0f;
-        if (OP == kOpPolicy) a.logprobs[row] = 0.0f;
-      }
-      if (MODE != kLossFwd)
-        for (int64_t j = tid; j < a.cols; j += kRowThreads) g[j] = 0;
-      continue;
-    }
-    if (warp == 0) load_targets<TYPE, OP>(a, row, t, &head);
-    Softmax s{-INFINITY, 0.0f};
-    if (MODE == kLossBwd) {
-      s = {a.lse[row] * a.tau, 1.0f};
-      __syncthreads();
-    } else {
-      for (int64_t j = tid; j < a.cols; j += kRowThreads) {
-        const float v = S::load(x[j]);
-        if (v > s.m) {
-          s.sum *= exp2_approx((s.m - v) * scale2);
-          s.m = v;
-        }
-        s.sum += exp2_approx((v - origin(s.m)) * scale2);
-      }
-      s = warp_join(s, scale2);
-      if (lane_id() == 0) part[warp] = s;
-      __syncthreads();
-      s = part[0];
-      for (int i = 1; i < kRowThreads / kWarp; ++i) s = join(s, part[i], scale2);
-    }
-    const RowResult r = row_result<OP, MODE>(a, row, w, head, t.x[0], s.m, s.sum);
-    if (MODE != kLossBwd && tid == 0) {
-      a.losses[row] = r.loss;
-      a.lse[row] = r.lse;
-      if (OP == kOpPolicy) a.logprobs[row] = r.logp;
-    }
-    if (MODE == kLossFwd) continue;
-    const float o = origin(s.m), f = r.c / s.sum;
-    auto q_of = [&](float v) { return r.c == 0.0f ? 0.0f : exp2_approx((v - o) * scale2) * f; };
-    // the targets' values before any of the row is overwritten
-    float fix[RS_MAX_TOP / kRowThreads];
+  auto put = [&](int v, const uint4& y) {
+    if (same && vecs.whole(v))
+      gv[v] = y;
+    else
+      vecs.store_scores(g, v, y);
+  };
+  if (row_off<OP>(a, row)) {
+    if (MODE != kLossBwd && tid == 0) store_result<OP>(a, row, RowResult{0, 0, 0, 0});
+    if (MODE != kLossFwd)
+      for (int v = tid; v < vecs.count; v += kThreads) put(v, make_uint4(0, 0, 0, 0));
+    return;
+  }
+  uint4 r[VECS];
 #pragma unroll
-    for (int u = 0; u < RS_MAX_TOP / kRowThreads; ++u) {
-      const int k = tid + u * kRowThreads;
-      if (k < a.k && t.col[k] >= 0) fix[u] = q_of(S::load(x[t.col[k]])) - r.c * t.p[k];
-    }
+  for (int u = 0; u < VECS; ++u) {
+    const int v = tid + u * kThreads;
+    if (vecs.whole(v))
+      r[u] = xv[v];
+    else
+      r[u] = v < vecs.count ? vecs.load_edge(x, v)
+                            : make_uint4(V::kMinusInf, V::kMinusInf, V::kMinusInf, V::kMinusInf);
+  }
+  if (warp == kWarps - 1) load_targets<TYPE, OP, MODE>(a, row, t, slots, &head);
+  Softmax s;
+  if (MODE == kLossBwd) {
+    s = {a.lse[row] * a.tau, 1.0f};
     __syncthreads();
-    for (int64_t j = tid; j < a.cols; j += kRowThreads) g[j] = S::store(q_of(S::load(x[j])));
-    __syncthreads();
+  } else {
+    s.m = vec_max<TYPE>(r);
+    const float o = origin(s.m);
+    uint64_t acc = 0;
 #pragma unroll
-    for (int u = 0; u < RS_MAX_TOP / kRowThreads; ++u) {
-      const int k = tid + u * kRowThreads;
-      if (k < a.k && t.col[k] >= 0 && r.c != 0.0f) g[t.col[k]] = S::store(fix[u]);
+    for (int u = 0; u < VECS; ++u)
+      acc = vec_exp_sum<TYPE>(r[u], pack2(-o, -o), pack2(scale2, scale2), acc);
+    float lo, hi;
+    unpack2(acc, lo, hi);
+    s.sum = lo + hi;
+    s = warp_join(s, scale2);
+    if (lane_id() == 0) part[warp] = s;
+    __syncthreads();
+    s = lane_id() < kWarps ? part[lane_id()] : Softmax{-INFINITY, 0.0f};
+    s = warp_join(s, scale2);
+  }
+  const RowResult res = row_result<OP, MODE>(a, head, s.m, s.sum);
+  if (MODE != kLossBwd && tid == 0) store_result<OP>(a, row, res);
+  if (MODE == kLossFwd) return;
+  const float o = origin(s.m), f = res.c / s.sum;
+#pragma unroll
+  for (int u = 0; u < VECS; ++u) {
+    const int v = tid + u * kThreads;
+    if (v < vecs.count)
+      put(v, res.c == 0.0f ? make_uint4(0, 0, 0, 0)
+                           : vec_grad<TYPE>(r[u], pack2(-o, -o), pack2(scale2, scale2), pack2(f, f)));
+  }
+  if (res.c == 0.0f) return;
+  __syncthreads();
+  for (int k = tid; k < a.k; k += kThreads)
+    if (t.col[k] >= 0)
+      g[t.col[k]] = S::store(exp2_approx((t.x[k] - o) * scale2) * f - res.c * t.p[k]);
+}
+
+// ----------------------------------------------------------------- long rows
+// A row is shared by the S CTAs of a cluster (S = 1: one CTA), each of which
+// takes a contiguous segment of it in chunks of 16 KB.  One warp (the
+// producer) copies the chunks of row after row by TMA bulk copies into a ring
+// of shared-memory slots, as far ahead as slots are free; one warp reads the
+// next row's targets; 16 warps go over the row's chunks twice: once for the
+// maximum and the sum, and, after the CTAs have exchanged theirs through
+// distributed shared memory, once more, out of the same slots, to write the
+// gradient, freeing the slots for the next rows.  So a row is read from
+// memory once, as long as its segments fit into the ring; what does not fit
+// is copied a second time (from L2, mostly).
+constexpr int kRowConsumers = 512;
+constexpr int kRowWarps = kRowConsumers / kWarp;
+constexpr int kRowThreads = kRowConsumers + 2 * kWarp;
+constexpr int kChunkUnits = 2;                                // vectors per thread and chunk
+constexpr int kChunkVecs = kRowConsumers * kChunkUnits;
+constexpr int kChunkBytes = kChunkVecs * 16;
+constexpr int kRowSlots = 12;                                 // ring slots
+constexpr int kRowKeep = kRowSlots - 2;                       // chunks of a row kept in them
+constexpr int kMaxCluster = 16;
+constexpr uint64_t kRowWaitNs = 2000000000ull;
+
+// Barriers and small arrays in front of the ring.
+struct RowShared {
+  uint64_t full[kRowSlots], empty[kRowSlots];
+  uint64_t head_full[2], head_empty[2];
+  uint64_t together;                                          // all consumer warps
+  uint64_t peers;                                             // exchange of the CTAs' softmaxes
+  Softmax part[2][kRowWarps];
+  Softmax peer[2][kMaxCluster];
+  Head head[2];
+  int failed;                                                 // a wait ran out of time
+};
+
+__host__ __device__ constexpr inline size_t row_targets_bytes(int k) {
+  return align_up(static_cast<size_t>(k) * 12, 16);
+}
+__host__ constexpr inline size_t row_ring_smem(int k) {
+  return static_cast<size_t>(kRowSlots) * kChunkBytes + align_up(sizeof(RowShared), 16) +
+         2 * row_targets_bytes(k) + static_cast<size_t>(target_slots(k)) * 4;
+}
+
+// Waits for a phase of a barrier; after kRowWaitNs, or once another wait of
+// the CTA has run out, it gives up: the caller goes on without touching what
+// it waited for, so that every thread still reaches every barrier, and the
+// rows it had left get NaN.
+__device__ __forceinline__ bool row_wait(uint64_t* bar, uint32_t parity, volatile int* failed) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*failed) return false;
+    if (global_timer_ns() - t0 > kRowWaitNs) {
+      *failed = 1;
+      return false;
     }
   }
+  return true;
+}
+
+// The same for a barrier on which other CTAs arrive: what they wrote before is
+// seen after it.
+__device__ __forceinline__ bool row_wait_cluster(uint64_t* bar, uint32_t parity,
+                                                 volatile int* failed) {
+  auto done = [&] {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n"
+        " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+  };
+  if (done()) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (!done()) {
+    if (*failed) return false;
+    if (global_timer_ns() - t0 > kRowWaitNs) {
+      *failed = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+// A warp's wait: all of its lanes agree on the outcome.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* failed) {
+  return __all_sync(kFull, row_wait(bar, parity, failed));
+}
+
+__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+
+template <int TYPE, int OP, int MODE>
+__global__ void __launch_bounds__(kRowThreads, 1) row_loss_ring_kernel(const RowLossArgs a,
+                                                                    const int split) {
+  using S = Score<TYPE>;
+  using Raw = typename S::Raw;
+  using V = ScoreVec<TYPE>;
+  extern __shared__ __align__(16) unsigned char smem[];
+  unsigned char* ring = smem;
+  RowShared* sh = reinterpret_cast<RowShared*>(smem + kRowSlots * kChunkBytes);
+  unsigned char* lists = reinterpret_cast<unsigned char*>(sh) + align_up(sizeof(RowShared), 16);
+  int* slots = reinterpret_cast<int*>(lists + 2 * row_targets_bytes(a.k));
+  auto targets = [&](int i) {
+    Targets t;
+    t.col = reinterpret_cast<int*>(lists + i * row_targets_bytes(a.k));
+    t.p = reinterpret_cast<float*>(t.col + a.k);
+    t.x = t.p + a.k;
+    return t;
+  };
+  const int tid = static_cast<int>(threadIdx.x), warp = tid / kWarp;
+  const int lane = static_cast<int>(lane_id());
+  // kLossBwd has nothing to exchange and is launched without clusters
+  const int rank = static_cast<int>(blockIdx.x) % split;
+  const int64_t row0 = blockIdx.x / split, row_step = gridDim.x / split;
+  // vectors per CTA, whatever the row's first address
+  const int per = (static_cast<int>(a.cols + 2 * (V::kCount - 1)) / V::kCount + split - 1) / split;
+  if (tid == 0) {
+    for (int i = 0; i < kRowSlots; ++i) {
+      mbar_init(&sh->full[i], 1);
+      mbar_init(&sh->empty[i], kRowWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh->head_full[i], 1);
+      mbar_init(&sh->head_empty[i], kRowWarps);
+    }
+    mbar_init(&sh->together, kRowWarps);
+    mbar_init(&sh->peers, split);
+    sh->failed = 0;
+  }
+  if (MODE != kLossBwd && split > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  grid_dependency_sync();
+
+  struct Segment {
+    const Raw* x;
+    RowVecs<TYPE> vecs;
+    int begin, end, chunks, keep;
+  };
+  auto segment = [&](int64_t row) {
+    const Raw* x = static_cast<const Raw*>(a.logits) + row * a.stride;
+    Segment s{x, RowVecs<TYPE>(x, static_cast<int>(a.cols)), 0, 0, 0, 0};
+    s.begin = min(rank * per, s.vecs.count);
+    s.end = min(s.begin + per, s.vecs.count);
+    s.chunks = (s.end - s.begin + kChunkVecs - 1) / kChunkVecs;
+    s.keep = MODE == kLossGrad ? min(s.chunks, kRowKeep) : 0;
+    return s;
+  };
+
+  if (warp == kRowWarps) {  // ---- producer
+    if (lane == 0) {
+      int slot = 0;
+      uint32_t use = 0;  // times round the ring
+      bool next_off = row0 < a.rows && row_off<OP>(a, row0);
+      for (int64_t row = row0; row < a.rows; row += row_step) {
+        const bool off = next_off;
+        if (row + row_step < a.rows) next_off = row_off<OP>(a, row + row_step);
+        if (off) continue;
+        const Segment s = segment(row);
+        const int loads = MODE == kLossGrad ? 2 * s.chunks - s.keep : s.chunks;
+        const uint4* xv = reinterpret_cast<const uint4*>(s.x - s.vecs.lead);
+        for (int i = 0; i < loads; ++i) {
+          if (use > 0 && !row_wait(&sh->empty[slot], (use - 1) & 1, &sh->failed)) break;
+          const int first = s.begin + (i < s.chunks ? i : i - s.chunks) * kChunkVecs;
+          const int b = max(first, s.vecs.whole_begin());
+          const int e = min(min(first + kChunkVecs, s.end), s.vecs.whole_end());
+          const uint32_t bytes = e > b ? static_cast<uint32_t>(e - b) * 16u : 0u;
+          mbar_arrive_expect_tx(&sh->full[slot], bytes);
+          if (bytes != 0)
+            bulk_copy_g2s(ring + slot * kChunkBytes + (b - first) * 16, xv + b, bytes,
+                          &sh->full[slot]);
+          if (++slot == kRowSlots) {
+            slot = 0;
+            ++use;
+          }
+        }
+        if (sh->failed) break;
+      }
+      if (sh->failed) {  // copies in flight end before the CTA does
+        for (int i = 0; i < kRowSlots; ++i)
+          mbar_wait_bounded(&sh->full[i], i < slot ? use & 1 : (use - 1) & 1, kCopyDrainNs);
+      }
+    }
+  } else if (warp == kRowWarps + 1) {  // ---- targets
+    int i = 0;
+    uint32_t use = 0;
+    for (int64_t row = row0; row < a.rows; row += row_step) {
+      if (use > 0) {
+        bool ok = true;
+        if (lane == 0) ok = row_wait(&sh->head_empty[i], (use - 1) & 1, &sh->failed);
+        if (!__shfl_sync(kFull, ok, 0)) break;
+      }
+      load_targets<TYPE, OP, MODE>(a, row, targets(i), slots, &sh->head[i]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->head_full[i]);
+      if (++i == 2) {
+        i = 0;
+        ++use;
+      }
+    }
+  } else {  // ---- consumers
+    const float scale2 = a.inv_tau * kLog2e;
+    const uint64_t scale22 = pack2(scale2, scale2);
+    int slot = 0, hi = 0;
+    uint32_t phase = 0, head_phase = 0, peer_phase = 0, together_phase = 0;
+    // the chunk's vector u of this thread, from its slot (or, at an edge of
+    // the row, score by score from memory)
+    auto fetch = [&](const Segment& s, int at, bool ok, int chunk, int u) {
+      const int i = tid + u * kRowConsumers, v = s.begin + chunk * kChunkVecs + i;
+      if (v >= s.end) return make_uint4(V::kMinusInf, V::kMinusInf, V::kMinusInf, V::kMinusInf);
+      if (!s.vecs.whole(v)) return s.vecs.load_edge(s.x, v);
+      if (!ok) return make_uint4(V::kNan, V::kNan, V::kNan, V::kNan);
+      return *reinterpret_cast<const uint4*>(ring + at * kChunkBytes + i * 16);
+    };
+    // every consumer warp has come here (a bounded wait, unlike bar.sync)
+    auto together = [&] {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->together);
+      warp_wait(&sh->together, together_phase, &sh->failed);
+      together_phase ^= 1;
+    };
+    auto release = [&](int at) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->empty[at]);
+    };
+    for (int64_t row = row0; row < a.rows; row += row_step) {
+      const bool got_head = warp_wait(&sh->head_full[hi], head_phase, &sh->failed);
+      const Head h = sh->head[hi];
+      const Targets t = targets(hi);
+      const int head_slot = hi;
+      if (++hi == 2) {
+        hi = 0;
+        head_phase ^= 1;
+      }
+      const Segment s = segment(row);
+      Raw* g = static_cast<Raw*>(a.grad) + row * a.grad_stride;
+      uint4* gv = reinterpret_cast<uint4*>(g - s.vecs.lead);
+      const bool same = reinterpret_cast<uintptr_t>(gv) % 16 == 0;
+      auto put = [&](int v, const uint4& y) {
+        if (same && s.vecs.whole(v))
+          gv[v] = y;
+        else
+          s.vecs.store_scores(g, v, y);
+      };
+      if (got_head && h.off) {
+        if (MODE != kLossBwd && rank == 0 && tid == 0)
+          store_result<OP>(a, row, RowResult{0, 0, 0, 0});
+        if (MODE != kLossFwd)
+          for (int v = s.begin + tid; v < s.end; v += kRowConsumers)
+            put(v, make_uint4(0, 0, 0, 0));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->head_empty[head_slot]);
+        continue;
+      }
+      Softmax st{-INFINITY, 0.0f};
+      const int slot0 = slot;
+      const uint32_t phase0 = phase;
+      if (MODE == kLossBwd) {
+        st = {a.lse[row] * a.tau, 1.0f};
+      } else {
+        for (int c = 0; c < s.chunks; ++c) {
+          const bool ok = warp_wait(&sh->full[slot], phase, &sh->failed);
+          uint4 r[kChunkUnits];
+#pragma unroll
+          for (int u = 0; u < kChunkUnits; ++u) r[u] = fetch(s, slot, ok, c, u);
+          if (c < s.chunks - s.keep) release(slot);
+          if (++slot == kRowSlots) {
+            slot = 0;
+            phase ^= 1;
+          }
+          const float m = fmaxf(st.m, vec_max<TYPE>(r));
+          const float o = origin(m);
+          uint64_t acc = pack2(st.sum * exp2_approx((st.m - o) * scale2), 0.0f);
+#pragma unroll
+          for (int u = 0; u < kChunkUnits; ++u)
+            acc = vec_exp_sum<TYPE>(r[u], pack2(-o, -o), scale22, acc);
+          float lo, up;
+          unpack2(acc, lo, up);
+          st = {m, lo + up};
+        }
+        st = warp_join(st, scale2);
+        Softmax* part = sh->part[peer_phase];
+        if (lane == 0) part[warp] = st;
+        together();
+        st = warp_join(lane < kRowWarps ? part[lane] : Softmax{-INFINITY, 0.0f}, scale2);
+        if (split > 1) {
+          if (tid < split) {  // thread i hands this CTA's part to CTA i
+            const uint32_t to = peer_addr(smem_addr(&sh->peer[peer_phase][rank]), tid);
+            const uint32_t bar = peer_addr(smem_addr(&sh->peers), tid);
+            asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(st.m),
+                         "f"(st.sum)
+                         : "memory");
+            asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+                         : "memory");
+          }
+          __all_sync(kFull, row_wait_cluster(&sh->peers, peer_phase, &sh->failed));
+          st = warp_join(lane < split ? sh->peer[peer_phase][lane] : Softmax{-INFINITY, 0.0f},
+                         scale2);
+        }
+        peer_phase ^= 1;
+      }
+      RowResult res = row_result<OP, MODE>(a, h, st.m, st.sum);
+      if (sh->failed) res = RowResult{NAN, NAN, NAN, NAN};
+      if (MODE != kLossBwd && rank == 0 && tid == 0) store_result<OP>(a, row, res);
+      if (MODE != kLossFwd) {
+        const float o = origin(st.m), f = res.c / st.sum;
+        const uint64_t neg_o = pack2(-o, -o), ff = pack2(f, f);
+        // the resident chunks, then those copied again
+        const int first = s.chunks - s.keep;
+        int at = slot0 + (MODE == kLossGrad ? first : 0);
+        uint32_t ph = phase0;
+        while (at >= kRowSlots) {
+          at -= kRowSlots;
+          ph ^= 1;
+        }
+        for (int i = 0; i < s.chunks; ++i) {
+          const int c = MODE == kLossGrad ? (i < s.keep ? first + i : i - s.keep) : i;
+          const bool ok = warp_wait(&sh->full[at], ph, &sh->failed);
+          uint4 r[kChunkUnits];
+#pragma unroll
+          for (int u = 0; u < kChunkUnits; ++u) r[u] = fetch(s, at, ok, c, u);
+          release(at);
+          if (++at == kRowSlots) {
+            at = 0;
+            ph ^= 1;
+          }
+#pragma unroll
+          for (int u = 0; u < kChunkUnits; ++u) {
+            const int v = s.begin + c * kChunkVecs + tid + u * kRowConsumers;
+            if (v < s.end)
+              put(v, res.c == 0.0f ? make_uint4(0, 0, 0, 0)
+                                   : vec_grad<TYPE>(r[u], neg_o, scale22, ff));
+          }
+        }
+        slot = at;
+        phase = ph;
+        together();  // the targets' columns are written last
+        if (res.c != 0.0f && got_head) {
+          const int64_t b = static_cast<int64_t>(s.begin) * V::kCount - s.vecs.lead;
+          const int64_t e = static_cast<int64_t>(s.end) * V::kCount - s.vecs.lead;
+          for (int k = tid; k < a.k; k += kRowConsumers) {
+            const int col = t.col[k];
+            if (col >= 0 && col >= b && col < e)
+              g[col] = S::store(exp2_approx((t.x[k] - o) * scale2) * f - res.c * t.p[k]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->head_empty[head_slot]);
+    }
+  }
+  // no CTA ends while another may still write into its shared memory
+  if (MODE != kLossBwd && split > 1) {
+    __syncwarp();
+    cluster_sync();
+  }
+}
+
+// -------------------------------------------------------------------- launch
+template <class K>
+cudaError_t prepare_ring(K kern, size_t smem, int split) {
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
+  if (e == cudaSuccess && split > 8)
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  return e;
 }
 
 template <int TYPE, int OP, int MODE>
 cudaError_t launch_row_loss_as(const RowLossArgs& a, cudaStream_t s) {
-  const int64_t most = static_cast<int64_t>(device_sm_count()) * 4;
-  const int grid = static_cast<int>(a.rows < most ? a.rows : most);
-  return launch_kernel(row_loss_kernel<TYPE, OP, MODE>, dim3(grid), dim3(kRowThreads),
-                       static_cast<size_t>(a.k) * 12, s, a);
+  constexpr int kEs = sizeof(typename Score<TYPE>::Raw);
+  const int64_t bytes = a.cols * kEs;
+  const size_t lists = static_cast<size_t>(a.k) * 12 + static_cast<size_t>(target_slots(a.k)) * 4;
+  // a row's vectors: one more than its bytes hold where it begins unaligned
+  const int64_t vecs = (a.cols + 2 * (ScoreVec<TYPE>::kCount - 1)) / ScoreVec<TYPE>::kCount;
+  if (vecs <= 128 * 4)
+    return launch_kernel(row_loss_short_kernel<TYPE, OP, MODE, 128, 4>,
+                         dim3(static_cast<unsigned>(a.rows)), dim3(128), lists, s, a);
+  if (vecs <= 256 * 8)
+    return launch_kernel(row_loss_short_kernel<TYPE, OP, MODE, 256, 8>,
+                         dim3(static_cast<unsigned>(a.rows)), dim3(256), lists, s, a);
+  const int sms = device_sm_count();
+  int split = 1;
+  if (MODE == kLossGrad)
+    while (split < 8 && bytes > int64_t(split) * kRowKeep * kChunkBytes) split *= 2;
+  while (split < kMaxCluster && a.rows * split * 2 <= sms && bytes >= int64_t(split) * 2 * 8192)
+    split *= 2;
+  // over its own logits the backward call of the policy loss must not write a
+  // segment before every segment has read the action's score
+  if (MODE == kLossBwd && OP == kOpPolicy && a.grad == a.logits) split = 1;
+  auto kern = row_loss_ring_kernel<TYPE, OP, MODE>;
+  const size_t smem = row_ring_smem(a.k);
+  cudaError_t e = prepare_ring(kern, smem, split);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kRowThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+#if LSDRS_PDL
+  attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[n++].val.programmaticStreamSerializationAllowed = 1;
+#endif
+  int64_t groups = sms / split;
+  if (MODE != kLossBwd && split > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = split;
+    attr[n].val.clusterDim.y = 1;
+    attr[n++].val.clusterDim.z = 1;
+  }
+  groups = groups < 1 ? 1 : groups;
+  if (groups > a.rows) groups = a.rows;
+  cfg.gridDim = dim3(static_cast<unsigned>(groups * split));
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
+  return cudaLaunchKernelEx(&cfg, kern, a, split);
 }
 
 }  // namespace lsdrs

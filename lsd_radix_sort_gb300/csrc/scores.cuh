@@ -91,4 +91,221 @@ __device__ __forceinline__ Softmax warp_join(Softmax v, float scale2) {
   return {m, warp_sum(v.sum * exp2_approx((v.m - origin(m)) * scale2))};
 }
 
+// ---- 16-byte vectors of scores --------------------------------------------
+// Pairs of floats in one 64-bit register: one instruction for both.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t exp2_2(uint64_t v) {
+  float a, b;
+  unpack2(v, a, b);
+  return pack2(exp2_approx(a), exp2_approx(b));
+}
+
+// One 32-bit word of two 16-bit scores, or two words of one 32-bit score
+// each, as a pair of floats; and the largest of four words (NaN ignored).
+template <int TYPE>
+struct ScoreVec;
+
+template <>
+struct ScoreVec<RS_SCORE_F16> {
+  static constexpr int kCount = 8;
+  static constexpr uint32_t kMinusInf = 0xFC00FC00u, kNan = 0x7E007E00u;
+  static __device__ __forceinline__ uint64_t pair(uint32_t w) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    return pack2(f.x, f.y);
+  }
+  static __device__ __forceinline__ uint32_t word(uint64_t v) {
+    float a, b;
+    unpack2(v, a, b);
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+    const __half2 h =
+        __hmax2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+};
+
+template <>
+struct ScoreVec<RS_SCORE_BF16> {
+  static constexpr int kCount = 8;
+  static constexpr uint32_t kMinusInf = 0xFF80FF80u, kNan = 0x7FC07FC0u;
+  static __device__ __forceinline__ uint64_t pair(uint32_t w) {
+    return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  }
+  static __device__ __forceinline__ uint32_t word(uint64_t v) {
+    float a, b;
+    unpack2(v, a, b);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 h = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                     *reinterpret_cast<const __nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+};
+
+template <>
+struct ScoreVec<RS_SCORE_F32> {
+  static constexpr int kCount = 4;
+  static constexpr uint32_t kMinusInf = 0xFF800000u, kNan = 0x7FC00000u;
+};
+
+// The largest score of VECS vectors; NaN is ignored.
+template <int TYPE, int VECS>
+__device__ __forceinline__ float vec_max(const uint4 (&v)[VECS]) {
+  if constexpr (TYPE == RS_SCORE_F32) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < VECS; ++u)
+      m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(v[u].x), __uint_as_float(v[u].y)),
+                         fmaxf(__uint_as_float(v[u].z), __uint_as_float(v[u].w))));
+    return m;
+  } else {
+    using V = ScoreVec<TYPE>;
+    uint32_t m = V::kMinusInf;
+#pragma unroll
+    for (int u = 0; u < VECS; ++u)
+      m = V::larger(m, V::larger(V::larger(v[u].x, v[u].y), V::larger(v[u].z, v[u].w)));
+    float a, b;
+    unpack2(V::pair(m), a, b);
+    return fmaxf(a, b);
+  }
+}
+
+// A vector as kCount / 2 pairs of floats.
+template <int TYPE>
+__device__ __forceinline__ void vec_pairs(const uint4& v, uint64_t (&p)[ScoreVec<TYPE>::kCount / 2]) {
+  if constexpr (TYPE == RS_SCORE_F32) {
+    p[0] = pack2(__uint_as_float(v.x), __uint_as_float(v.y));
+    p[1] = pack2(__uint_as_float(v.z), __uint_as_float(v.w));
+  } else {
+    using V = ScoreVec<TYPE>;
+    p[0] = V::pair(v.x);
+    p[1] = V::pair(v.y);
+    p[2] = V::pair(v.z);
+    p[3] = V::pair(v.w);
+  }
+}
+
+template <int TYPE>
+__device__ __forceinline__ uint4 vec_of(const uint64_t (&p)[ScoreVec<TYPE>::kCount / 2]) {
+  uint4 v;
+  if constexpr (TYPE == RS_SCORE_F32) {
+    float a, b;
+    unpack2(p[0], a, b);
+    v.x = __float_as_uint(a);
+    v.y = __float_as_uint(b);
+    unpack2(p[1], a, b);
+    v.z = __float_as_uint(a);
+    v.w = __float_as_uint(b);
+  } else {
+    using V = ScoreVec<TYPE>;
+    v = make_uint4(V::word(p[0]), V::word(p[1]), V::word(p[2]), V::word(p[3]));
+  }
+  return v;
+}
+
+// Adds sum exp2((x - o) scale2) of a vector to the pair of partial sums.
+// The difference is taken before the product, so that scores near the type's
+// lowest value stay finite.
+template <int TYPE>
+__device__ __forceinline__ uint64_t vec_exp_sum(const uint4& v, uint64_t neg_o, uint64_t scale2,
+                                                uint64_t acc) {
+  uint64_t p[ScoreVec<TYPE>::kCount / 2];
+  vec_pairs<TYPE>(v, p);
+#pragma unroll
+  for (int i = 0; i < ScoreVec<TYPE>::kCount / 2; ++i)
+    acc = add2(acc, exp2_2(mul2(add2(p[i], neg_o), scale2)));
+  return acc;
+}
+
+// f exp2((x - o) scale2) of a vector, rounded to the scores' type.
+template <int TYPE>
+__device__ __forceinline__ uint4 vec_grad(const uint4& v, uint64_t neg_o, uint64_t scale2,
+                                          uint64_t f) {
+  uint64_t p[ScoreVec<TYPE>::kCount / 2];
+  vec_pairs<TYPE>(v, p);
+#pragma unroll
+  for (int i = 0; i < ScoreVec<TYPE>::kCount / 2; ++i)
+    p[i] = mul2(exp2_2(mul2(add2(p[i], neg_o), scale2)), f);
+  return vec_of<TYPE>(p);
+}
+
+// A row of scores as 16-byte vectors of memory: vector 0 begins at the row's
+// address rounded down to 16 bytes, so its first `lead` scores, and the last
+// vector's scores past the row, belong to others and are never touched.
+template <int TYPE>
+struct RowVecs {
+  using Raw = typename Score<TYPE>::Raw;
+  static constexpr int kN = ScoreVec<TYPE>::kCount;
+  int lead, cols, count;
+
+  __device__ __forceinline__ RowVecs(const void* row, int cols_)
+      : lead(static_cast<int>(reinterpret_cast<uintptr_t>(row) % 16 / sizeof(Raw))),
+        cols(cols_),
+        count((lead + cols_ + kN - 1) / kN) {}
+
+  // Vectors [whole_begin, whole_end) lie inside the row entirely.
+  __device__ __forceinline__ int whole_begin() const { return lead != 0; }
+  __device__ __forceinline__ int whole_end() const { return (lead + cols) / kN; }
+  __device__ __forceinline__ bool whole(int v) const {
+    return v >= whole_begin() && v < whole_end();
+  }
+
+  // A vector that is not whole, the foreign places filled with -inf.
+  __device__ __forceinline__ uint4 load_edge(const Raw* row, int v) const {
+    uint32_t w[4] = {ScoreVec<TYPE>::kMinusInf, ScoreVec<TYPE>::kMinusInf,
+                     ScoreVec<TYPE>::kMinusInf, ScoreVec<TYPE>::kMinusInf};
+    const int64_t first = static_cast<int64_t>(v) * kN - lead;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int64_t j = first + i;
+      if (j >= 0 && j < cols) {
+        if constexpr (sizeof(Raw) == 4) {
+          w[i] = row[j];
+        } else {
+          const int sh = 16 * (i & 1);
+          w[i >> 1] = (w[i >> 1] & ~(0xFFFFu << sh)) | (static_cast<uint32_t>(row[j]) << sh);
+        }
+      }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+
+  // Any vector, score by score.
+  __device__ __forceinline__ void store_scores(Raw* row, int v, const uint4& x) const {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    const int64_t first = static_cast<int64_t>(v) * kN - lead;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int64_t j = first + i;
+      if (j >= 0 && j < cols) {
+        if constexpr (sizeof(Raw) == 4)
+          row[j] = w[i];
+        else
+          row[j] = static_cast<Raw>(w[i >> 1] >> (16 * (i & 1)));
+      }
+    }
+  }
+};
+
 }  // namespace lsdrs
