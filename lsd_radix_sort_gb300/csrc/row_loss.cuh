@@ -315,13 +315,18 @@ __global__ void __launch_bounds__(kThreads) row_loss_short_kernel(const RowLossA
 // gradient, freeing the slots for the next rows.  So a row is read from
 // memory once, as long as its segments fit into the ring; what does not fit
 // is copied a second time (from L2, mostly).
-constexpr int kRowConsumers = 512;
+#ifndef LSDRS_ROW_CONSUMERS
+#define LSDRS_ROW_CONSUMERS 512
+#define LSDRS_ROW_UNITS 2
+#define LSDRS_ROW_SLOTS 12
+#endif
+constexpr int kRowConsumers = LSDRS_ROW_CONSUMERS;
 constexpr int kRowWarps = kRowConsumers / kWarp;
 constexpr int kRowThreads = kRowConsumers + 2 * kWarp;
-constexpr int kChunkUnits = 2;                                // vectors per thread and chunk
+constexpr int kChunkUnits = LSDRS_ROW_UNITS;                                // vectors per thread and chunk
 constexpr int kChunkVecs = kRowConsumers * kChunkUnits;
 constexpr int kChunkBytes = kChunkVecs * 16;
-constexpr int kRowSlots = 12;                                 // ring slots
+constexpr int kRowSlots = LSDRS_ROW_SLOTS;                                 // ring slots
 constexpr int kRowKeep = kRowSlots - 2;                       // chunks of a row kept in them
 constexpr int kMaxCluster = 16;
 constexpr uint64_t kRowWaitNs = 2000000000ull;
@@ -527,12 +532,27 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_ring_kernel(const Row
     uint32_t phase = 0, head_phase = 0, peer_phase = 0, together_phase = 0;
     // the chunk's vector u of this thread, from its slot (or, at an edge of
     // the row, score by score from memory)
-    auto fetch = [&](const Segment& s, int at, bool ok, int chunk, int u) {
-      const int i = tid + u * kRowConsumers, v = s.begin + chunk * kChunkVecs + i;
-      if (v >= s.end) return make_uint4(V::kMinusInf, V::kMinusInf, V::kMinusInf, V::kMinusInf);
-      if (!s.vecs.whole(v)) return s.vecs.load_edge(s.x, v);
-      if (!ok) return make_uint4(V::kNan, V::kNan, V::kNan, V::kNan);
-      return *reinterpret_cast<const uint4*>(ring + at * kChunkBytes + i * 16);
+    auto fetch = [&](const Segment& s, int at, int first, bool inner, uint4 (&r)[kChunkUnits]) {
+      const uint4* from = reinterpret_cast<const uint4*>(ring + at * kChunkBytes) + tid;
+      if (inner) {
+#pragma unroll
+        for (int u = 0; u < kChunkUnits; ++u) r[u] = from[u * kRowConsumers];
+        return;
+      }
+#pragma unroll
+      for (int u = 0; u < kChunkUnits; ++u) {
+        const int v = first + tid + u * kRowConsumers;
+        if (v >= s.end)
+          r[u] = make_uint4(V::kMinusInf, V::kMinusInf, V::kMinusInf, V::kMinusInf);
+        else if (s.vecs.whole(v))
+          r[u] = from[u * kRowConsumers];
+        else
+          r[u] = s.vecs.load_edge(s.x, v);
+      }
+    };
+    // every vector of the chunk lies in the segment and inside the row
+    auto inner_chunk = [&](const Segment& s, int first) {
+      return first >= s.vecs.whole_begin() && first + kChunkVecs <= min(s.end, s.vecs.whole_end());
     };
     // every consumer warp has come here (a bounded wait, unlike bar.sync)
     auto together = [&] {
@@ -581,10 +601,10 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_ring_kernel(const Row
         st = {a.lse[row] * a.tau, 1.0f};
       } else {
         for (int c = 0; c < s.chunks; ++c) {
-          const bool ok = warp_wait(&sh->full[slot], phase, &sh->failed);
+          warp_wait(&sh->full[slot], phase, &sh->failed);
+          const int first = s.begin + c * kChunkVecs;
           uint4 r[kChunkUnits];
-#pragma unroll
-          for (int u = 0; u < kChunkUnits; ++u) r[u] = fetch(s, slot, ok, c, u);
+          fetch(s, slot, first, inner_chunk(s, first), r);
           if (c < s.chunks - s.keep) release(slot);
           if (++slot == kRowSlots) {
             slot = 0;
@@ -637,21 +657,33 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_ring_kernel(const Row
         }
         for (int i = 0; i < s.chunks; ++i) {
           const int c = MODE == kLossGrad ? (i < s.keep ? first + i : i - s.keep) : i;
-          const bool ok = warp_wait(&sh->full[at], ph, &sh->failed);
+          const int begin = s.begin + c * kChunkVecs;
+          const bool inner = inner_chunk(s, begin);
+          const uint64_t fc =
+              warp_wait(&sh->full[at], ph, &sh->failed) ? ff : pack2(NAN, NAN);
           uint4 r[kChunkUnits];
-#pragma unroll
-          for (int u = 0; u < kChunkUnits; ++u) r[u] = fetch(s, at, ok, c, u);
+          fetch(s, at, begin, inner, r);
           release(at);
           if (++at == kRowSlots) {
             at = 0;
             ph ^= 1;
           }
+          if (res.c == 0.0f) {  // also where the row holds NaN
 #pragma unroll
-          for (int u = 0; u < kChunkUnits; ++u) {
-            const int v = s.begin + c * kChunkVecs + tid + u * kRowConsumers;
-            if (v < s.end)
-              put(v, res.c == 0.0f ? make_uint4(0, 0, 0, 0)
-                                   : vec_grad<TYPE>(r[u], neg_o, scale22, ff));
+            for (int u = 0; u < kChunkUnits; ++u) r[u] = make_uint4(0, 0, 0, 0);
+          } else {
+#pragma unroll
+            for (int u = 0; u < kChunkUnits; ++u) r[u] = vec_grad<TYPE>(r[u], neg_o, scale22, fc);
+          }
+          if (inner && same) {
+#pragma unroll
+            for (int u = 0; u < kChunkUnits; ++u) gv[begin + tid + u * kRowConsumers] = r[u];
+          } else {
+#pragma unroll
+            for (int u = 0; u < kChunkUnits; ++u) {
+              const int v = begin + tid + u * kRowConsumers;
+              if (v < s.end) put(v, r[u]);
+            }
           }
         }
         slot = at;

@@ -125,7 +125,7 @@ struct ScoreVec;
 template <>
 struct ScoreVec<RS_SCORE_F16> {
   static constexpr int kCount = 8;
-  static constexpr uint32_t kMinusInf = 0xFC00FC00u, kNan = 0x7E007E00u;
+  static constexpr uint32_t kMinusInf = 0xFC00FC00u;
   static __device__ __forceinline__ uint64_t pair(uint32_t w) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
     return pack2(f.x, f.y);
@@ -146,7 +146,7 @@ struct ScoreVec<RS_SCORE_F16> {
 template <>
 struct ScoreVec<RS_SCORE_BF16> {
   static constexpr int kCount = 8;
-  static constexpr uint32_t kMinusInf = 0xFF80FF80u, kNan = 0x7FC07FC0u;
+  static constexpr uint32_t kMinusInf = 0xFF80FF80u;
   static __device__ __forceinline__ uint64_t pair(uint32_t w) {
     return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
   }
@@ -166,7 +166,7 @@ struct ScoreVec<RS_SCORE_BF16> {
 template <>
 struct ScoreVec<RS_SCORE_F32> {
   static constexpr int kCount = 4;
-  static constexpr uint32_t kMinusInf = 0xFF800000u, kNan = 0x7FC00000u;
+  static constexpr uint32_t kMinusInf = 0xFF800000u;
 };
 
 // The largest score of VECS vectors; NaN is ignored.
