@@ -84,18 +84,58 @@ __device__ __forceinline__ void load_targets(const RowLossArgs& a, int64_t row, 
     }
     return;
   }
+  if (w == 0.0f) {  // neither the list nor the row is read
+    if (lane == 0) h->off = 1;
+    return;
+  }
   const float scale2 = a.inv_tau * kLog2e;
   float vm = -INFINITY, xm = -INFINITY;
-  for (int k = lane; k < a.k; k += kWarp) {
-    const int64_t i = load_index(a.top_indices, a.index_bytes, row * a.index_stride + k);
-    const bool live = i >= 0 && i < a.cols;
-    const float v = live ? load_score(a.top_values, a.top_type, row * a.top_stride + k) : -INFINITY;
-    const float xi = live ? S::load(x[i]) : -INFINITY;
-    t.col[k] = live ? static_cast<int>(i) : -1;
-    t.p[k] = v;
-    t.x[k] = xi;
-    vm = fmaxf(vm, v);
-    xm = fmaxf(xm, xi);
+  // Columns and values of up to 256 entries are in flight together, then
+  // their scores: two trips to memory, whatever the length up to there.
+  constexpr int kBatch = 8;
+  for (int k0 = lane; k0 < a.k; k0 += kBatch * kWarp) {
+    int col[kBatch];
+    float v[kBatch], xi[kBatch];
+    auto columns = [&](auto* list) {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int k = k0 + u * kWarp;
+        const int64_t i = k < a.k ? static_cast<int64_t>(list[k]) : -1;
+        col[u] = i >= 0 && i < a.cols ? static_cast<int>(i) : -1;
+      }
+    };
+    auto values = [&](auto type, auto* list) {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int k = k0 + u * kWarp;
+        v[u] = k < a.k ? Score<decltype(type)::value>::load(list[k]) : -INFINITY;
+      }
+    };
+    const int64_t at_i = row * a.index_stride, at_v = row * a.top_stride;
+    if (a.top_type == RS_SCORE_BF16)
+      values(ScoreTag<RS_SCORE_BF16>{}, static_cast<const uint16_t*>(a.top_values) + at_v);
+    else if (a.top_type == RS_SCORE_F16)
+      values(ScoreTag<RS_SCORE_F16>{}, static_cast<const uint16_t*>(a.top_values) + at_v);
+    else
+      values(ScoreTag<RS_SCORE_F32>{}, static_cast<const uint32_t*>(a.top_values) + at_v);
+    if (a.index_bytes == 8)
+      columns(static_cast<const int64_t*>(a.top_indices) + at_i);
+    else
+      columns(static_cast<const int32_t*>(a.top_indices) + at_i);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) xi[u] = col[u] >= 0 ? S::load(x[col[u]]) : -INFINITY;
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int k = k0 + u * kWarp;
+      if (k < a.k) {
+        const float vu = col[u] >= 0 ? v[u] : -INFINITY;
+        t.col[k] = col[u];
+        t.p[k] = vu;
+        t.x[k] = xi[u];
+        vm = fmaxf(vm, vu);
+        xm = fmaxf(xm, xi[u]);
+      }
+    }
   }
   vm = origin(warp_max(vm));
   xm = origin(warp_max(xm));
@@ -158,7 +198,7 @@ __device__ __forceinline__ void load_targets(const RowLossArgs& a, int64_t row, 
     }
   }
   if (lane == 0) {
-    h->off = w == 0.0f;
+    h->off = 0;
     h->live = !(sum == 0.0f);
     h->w = w;
     h->up = up;
@@ -305,50 +345,78 @@ __global__ void __launch_bounds__(kThreads) row_loss_short_kernel(const RowLossA
 }
 
 // ----------------------------------------------------------------- long rows
-// A row is shared by the S CTAs of a cluster (S = 1: one CTA), each of which
-// takes a contiguous segment of it in chunks of 16 KB.  One warp (the
+// A row is shared by the `split` CTAs of a cluster (1: a CTA of its own), each
+// of which takes a contiguous segment of it in chunks of 16 KB.  One warp (the
 // producer) copies the chunks of row after row by TMA bulk copies into a ring
-// of shared-memory slots, as far ahead as slots are free; one warp reads the
-// next row's targets; 16 warps go over the row's chunks twice: once for the
+// of shared-memory slots, as far ahead as slots are free; two warps read the
+// next rows' targets; 16 warps go over the row's chunks twice: once for the
 // maximum and the sum, and, after the CTAs have exchanged theirs through
 // distributed shared memory, once more, out of the same slots, to write the
 // gradient, freeing the slots for the next rows.  So a row is read from
 // memory once, as long as its segments fit into the ring; what does not fit
 // is copied a second time (from L2, mostly).
+//
+// Rows cost unequally (a masked row is not read), so they are not dealt out
+// beforehand: the grid has a CTA (cluster) per row, and a running one takes
+// over the rows of CTAs that have not been launched yet, one row after
+// another, by cancelling their launch (cluster launch control).  One thread
+// per CTA (the scheduler) does so a few rows ahead and hands the answers to
+// the other warps.
 #ifndef LSDRS_ROW_CONSUMERS
 #define LSDRS_ROW_CONSUMERS 512
 #define LSDRS_ROW_UNITS 2
-#define LSDRS_ROW_SLOTS 12
 #endif
 constexpr int kRowConsumers = LSDRS_ROW_CONSUMERS;
 constexpr int kRowWarps = kRowConsumers / kWarp;
-constexpr int kRowThreads = kRowConsumers + 2 * kWarp;
-constexpr int kChunkUnits = LSDRS_ROW_UNITS;                                // vectors per thread and chunk
+constexpr int kTargetWarps = 2;
+constexpr int kProducerWarp = kRowWarps, kSchedulerWarp = kRowWarps + 1,
+              kFirstTargetWarp = kRowWarps + 2;
+constexpr int kRowThreads = kRowConsumers + (2 + kTargetWarps) * kWarp;
+constexpr int kChunkUnits = LSDRS_ROW_UNITS;                  // vectors per thread and chunk
 constexpr int kChunkVecs = kRowConsumers * kChunkUnits;
 constexpr int kChunkBytes = kChunkVecs * 16;
-constexpr int kRowSlots = LSDRS_ROW_SLOTS;                                 // ring slots
-constexpr int kRowKeep = kRowSlots - 2;                       // chunks of a row kept in them
+constexpr int kMaxSlots = 13;                                 // most ring slots
+constexpr int kAheadRows = 4;                                 // rows that the scheduler is ahead
+constexpr int kRowReaders = kRowWarps + 1 + kTargetWarps;     // warps that read its list
+#ifndef LSDRS_ROW_PAIR
+#define LSDRS_ROW_PAIR 1
+#endif
+constexpr bool kPair = LSDRS_ROW_PAIR;
+#ifndef LSDRS_ROW_STEAL
+#define LSDRS_ROW_STEAL 1
+#endif
 constexpr int kMaxCluster = 16;
 constexpr uint64_t kRowWaitNs = 2000000000ull;
 
-// Barriers and small arrays in front of the ring.
+// Barriers and small arrays behind the ring.
 struct RowShared {
-  uint64_t full[kRowSlots], empty[kRowSlots];
-  uint64_t head_full[2], head_empty[2];
+  uint4 answer[2];                                            // of cluster launch control
+  uint64_t answer_full[2], answer_empty[2];
+  uint64_t unit_full[kAheadRows], unit_empty[kAheadRows];
+  int unit[kAheadRows];                                       // the rows taken over
+  uint64_t full[kMaxSlots], empty[kMaxSlots];
+  uint64_t head_full[kTargetWarps], head_empty[kTargetWarps];
   uint64_t together;                                          // all consumer warps
   uint64_t peers;                                             // exchange of the CTAs' softmaxes
   Softmax part[2][kRowWarps];
   Softmax peer[2][kMaxCluster];
-  Head head[2];
+  Head head[kTargetWarps];
   int failed;                                                 // a wait ran out of time
 };
 
 __host__ __device__ constexpr inline size_t row_targets_bytes(int k) {
-  return align_up(static_cast<size_t>(k) * 12, 16);
+  return align_up(static_cast<size_t>(k) * 12 + static_cast<size_t>(target_slots(k)) * 4, 16);
 }
-__host__ constexpr inline size_t row_ring_smem(int k) {
-  return static_cast<size_t>(kRowSlots) * kChunkBytes + align_up(sizeof(RowShared), 16) +
-         2 * row_targets_bytes(k) + static_cast<size_t>(target_slots(k)) * 4;
+__host__ constexpr inline size_t row_ring_smem(int k, int slots) {
+  return static_cast<size_t>(slots) * kChunkBytes + align_up(sizeof(RowShared), 16) +
+         kTargetWarps * row_targets_bytes(k);
+}
+// As many slots as fit beside the lists of k entries.
+constexpr size_t kMaxSmem = 232448;
+__host__ constexpr inline int row_ring_slots(int k) {
+  int n = kMaxSlots;
+  while (row_ring_smem(k, n) > kMaxSmem) --n;
+  return n;
 }
 
 // Waits for a phase of a barrier; after kRowWaitNs, or once another wait of
@@ -410,22 +478,65 @@ __device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
   return r;
 }
 
+// Arrives on a barrier of any CTA of the cluster.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr)
+               : "memory");
+}
+
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
 }
 
+// Asks for the launch of a CTA (cluster) that has not begun yet to be
+// cancelled; the answer (16 bytes) arrives in shared memory, with `everyone`
+// in that of every CTA of the cluster.
+__device__ __forceinline__ void ask_next(uint4* answer, uint64_t* bar, bool everyone) {
+  if (everyone)
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes"
+        ".multicast::cluster::all.b128 [%0], [%1];" ::"r"(smem_addr(answer)),
+        "r"(smem_addr(bar))
+        : "memory");
+  else
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128"
+        " [%0], [%1];" ::"r"(smem_addr(answer)),
+        "r"(smem_addr(bar))
+        : "memory");
+}
+
+// The first CTA of the cancelled launch, or -1: nothing was left.
+__device__ __forceinline__ int next_cta(const uint4* answer) {
+  uint32_t ok, x;
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b128 r;\n .reg .b32 y, z, w;\n"
+      " ld.shared.b128 r, [%2];\n"
+      " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n"
+      " selp.u32 %0, 1, 0, p;\n"
+      " mov.u32 %1, 0;\n"
+      " @p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, r;\n}"
+      : "=r"(ok), "=r"(x)
+      : "r"(smem_addr(answer))
+      : "memory");
+  // the answer has been read before the next one may be written there
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  return ok != 0 ? static_cast<int>(x) : -1;
+}
+
 template <int TYPE, int OP, int MODE>
 __global__ void __launch_bounds__(kRowThreads, 1) row_loss_ring_kernel(const RowLossArgs a,
-                                                                    const int split) {
+                                                                    const int split,
+                                                                    const int ring_slots,
+                                                                    const bool steal) {
   using S = Score<TYPE>;
   using Raw = typename S::Raw;
   using V = ScoreVec<TYPE>;
   extern __shared__ __align__(16) unsigned char smem[];
   unsigned char* ring = smem;
-  RowShared* sh = reinterpret_cast<RowShared*>(smem + kRowSlots * kChunkBytes);
+  RowShared* sh = reinterpret_cast<RowShared*>(smem + ring_slots * kChunkBytes);
   unsigned char* lists = reinterpret_cast<unsigned char*>(sh) + align_up(sizeof(RowShared), 16);
-  int* slots = reinterpret_cast<int*>(lists + 2 * row_targets_bytes(a.k));
   auto targets = [&](int i) {
     Targets t;
     t.col = reinterpret_cast<int*>(lists + i * row_targets_bytes(a.k));
@@ -435,55 +546,89 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_ring_kernel(const Row
   };
   const int tid = static_cast<int>(threadIdx.x), warp = tid / kWarp;
   const int lane = static_cast<int>(lane_id());
-  // kLossBwd has nothing to exchange and is launched without clusters
-  const int rank = static_cast<int>(blockIdx.x) % split;
-  const int64_t row0 = blockIdx.x / split, row_step = gridDim.x / split;
+  // kLossBwd has nothing to exchange: its CTAs are launched without clusters,
+  // one per segment of a row
+  const bool clustered = MODE != kLossBwd && split > 1;
   // vectors per CTA, whatever the row's first address
   const int per = (static_cast<int>(a.cols + 2 * (V::kCount - 1)) / V::kCount + split - 1) / split;
+  const int keep_slots = ring_slots - 2;  // chunks of a row that stay for the second pass
   if (tid == 0) {
-    for (int i = 0; i < kRowSlots; ++i) {
+    for (int i = 0; i < ring_slots; ++i) {
       mbar_init(&sh->full[i], 1);
       mbar_init(&sh->empty[i], kRowWarps);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kTargetWarps; ++i) {
       mbar_init(&sh->head_full[i], 1);
       mbar_init(&sh->head_empty[i], kRowWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh->answer_full[i], 1);
+      mbar_init(&sh->answer_empty[i], clustered ? split : 1);
+    }
+    for (int i = 0; i < kAheadRows; ++i) {
+      mbar_init(&sh->unit_full[i], 1);
+      mbar_init(&sh->unit_empty[i], kRowReaders);
     }
     mbar_init(&sh->together, kRowWarps);
     mbar_init(&sh->peers, split);
     sh->failed = 0;
   }
-  if (MODE != kLossBwd && split > 1)
+  if (clustered)
     cluster_sync();
   else
     __syncthreads();
   grid_dependency_sync();
+
+  // One warp's way through the units (a row's segment each): its own first,
+  // then those that the scheduler took over.
+  struct Way {
+    int slot;
+    uint32_t phase;
+  };
+  auto next_unit = [&](Way& way) {
+    if (!steal) return -1;
+    const bool ok = warp_wait(&sh->unit_full[way.slot], way.phase, &sh->failed);
+    const int unit = ok ? sh->unit[way.slot] : -1;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh->unit_empty[way.slot]);
+    if (++way.slot == kAheadRows) {
+      way.slot = 0;
+      way.phase ^= 1;
+    }
+    return unit;
+  };
+  const int first_unit = static_cast<int>(blockIdx.x);
+  const int cluster_rank = first_unit % split;
+  auto rank_of = [&](int unit) { return clustered ? cluster_rank : unit % split; };
 
   struct Segment {
     const Raw* x;
     RowVecs<TYPE> vecs;
     int begin, end, chunks, keep;
   };
-  auto segment = [&](int64_t row) {
+  auto segment = [&](int unit) {
+    const int64_t row = unit / split;
+    const int rank = rank_of(unit);
     const Raw* x = static_cast<const Raw*>(a.logits) + row * a.stride;
     Segment s{x, RowVecs<TYPE>(x, static_cast<int>(a.cols)), 0, 0, 0, 0};
     s.begin = min(rank * per, s.vecs.count);
     s.end = min(s.begin + per, s.vecs.count);
     s.chunks = (s.end - s.begin + kChunkVecs - 1) / kChunkVecs;
-    s.keep = MODE == kLossGrad ? min(s.chunks, kRowKeep) : 0;
+    s.keep = MODE == kLossGrad ? min(s.chunks, keep_slots) : 0;
     return s;
   };
 
-  if (warp == kRowWarps) {  // ---- producer
-    if (lane == 0) {
-      int slot = 0;
-      uint32_t use = 0;  // times round the ring
-      bool next_off = row0 < a.rows && row_off<OP>(a, row0);
-      for (int64_t row = row0; row < a.rows; row += row_step) {
-        const bool off = next_off;
-        if (row + row_step < a.rows) next_off = row_off<OP>(a, row + row_step);
-        if (off) continue;
-        const Segment s = segment(row);
+  if (warp == kProducerWarp) {
+    int slot = 0;
+    uint32_t use = 0;  // times round the ring
+    Way way{0, 0};
+    int unit = first_unit;
+    bool off = row_off<OP>(a, unit / split);
+    while (unit >= 0) {
+      const int next = next_unit(way);
+      const bool next_off = next >= 0 && row_off<OP>(a, next / split);
+      if (!off && lane == 0) {
+        const Segment s = segment(unit);
         const int loads = MODE == kLossGrad ? 2 * s.chunks - s.keep : s.chunks;
         const uint4* xv = reinterpret_cast<const uint4*>(s.x - s.vecs.lead);
         for (int i = 0; i < loads; ++i) {
@@ -496,34 +641,65 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_ring_kernel(const Row
           if (bytes != 0)
             bulk_copy_g2s(ring + slot * kChunkBytes + (b - first) * 16, xv + b, bytes,
                           &sh->full[slot]);
-          if (++slot == kRowSlots) {
+          if (++slot == ring_slots) {
             slot = 0;
             ++use;
           }
         }
-        if (sh->failed) break;
       }
-      if (sh->failed) {  // copies in flight end before the CTA does
-        for (int i = 0; i < kRowSlots; ++i)
-          mbar_wait_bounded(&sh->full[i], i < slot ? use & 1 : (use - 1) & 1, kCopyDrainNs);
+      __syncwarp();
+      if (sh->failed) break;
+      unit = next;
+      off = next_off;
+    }
+    if (sh->failed && lane == 0)  // copies in flight end before the CTA does
+      for (int i = 0; i < ring_slots; ++i)
+        if (i < slot || use > 0)
+          mbar_wait_bounded(&sh->full[i], (i < slot ? use : use - 1) & 1, kCopyDrainNs);
+  } else if (warp == kSchedulerWarp) {
+    if (lane == 0 && steal) {
+      // The cluster's first CTA asks, and not before the last answer was a
+      // success; every CTA arms its own barrier for the shared answer and
+      // tells the first CTA when it has read it.
+      const bool asks = !clustered || cluster_rank == 0;
+      int unit = 0;
+      for (uint32_t n = 0; unit >= 0; ++n) {
+        const int s = n & 1;
+        if (asks && n >= 2 &&
+            !row_wait_cluster(&sh->answer_empty[s], ((n >> 1) - 1) & 1, &sh->failed))
+          break;
+        mbar_arrive_expect_tx(&sh->answer_full[s], 16);
+        if (asks) ask_next(&sh->answer[s], &sh->answer_full[s], clustered);
+        if (!row_wait(&sh->answer_full[s], (n >> 1) & 1, &sh->failed)) break;
+        unit = next_cta(&sh->answer[s]);
+        if (clustered)
+          mbar_arrive_cluster(peer_addr(smem_addr(&sh->answer_empty[s]), 0));
+        else
+          mbar_arrive(&sh->answer_empty[s]);
+        const int at = n % kAheadRows;
+        if (n >= kAheadRows &&
+            !row_wait(&sh->unit_empty[at], (n / kAheadRows - 1) & 1, &sh->failed))
+          break;
+        sh->unit[at] = unit;
+        mbar_arrive(&sh->unit_full[at]);
       }
     }
-  } else if (warp == kRowWarps + 1) {  // ---- targets
-    int i = 0;
+  } else if (warp >= kFirstTargetWarp) {  // every kTargetWarps-th row each
+    const int mine = warp - kFirstTargetWarp;
     uint32_t use = 0;
-    for (int64_t row = row0; row < a.rows; row += row_step) {
-      if (use > 0) {
-        bool ok = true;
-        if (lane == 0) ok = row_wait(&sh->head_empty[i], (use - 1) & 1, &sh->failed);
-        if (!__shfl_sync(kFull, ok, 0)) break;
-      }
-      load_targets<TYPE, OP, MODE>(a, row, targets(i), slots, &sh->head[i]);
+    Way way{0, 0};
+    int turn = 0;
+    for (int unit = first_unit; unit >= 0; unit = next_unit(way)) {
+      const bool skip = turn != mine;
+      turn = turn + 1 == kTargetWarps ? 0 : turn + 1;
+      if (skip) continue;
+      if (use > 0 && !warp_wait(&sh->head_empty[mine], (use - 1) & 1, &sh->failed)) break;
+      const Targets t = targets(mine);
+      load_targets<TYPE, OP, MODE>(a, unit / split, t, reinterpret_cast<int*>(t.x + a.k),
+                                   &sh->head[mine]);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->head_full[i]);
-      if (++i == 2) {
-        i = 0;
-        ++use;
-      }
+      if (lane == 0) mbar_arrive(&sh->head_full[mine]);
+      ++use;
     }
   } else {  // ---- consumers
     const float scale2 = a.inv_tau * kLog2e;
@@ -565,16 +741,19 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_ring_kernel(const Row
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->empty[at]);
     };
-    for (int64_t row = row0; row < a.rows; row += row_step) {
+    Way way{0, 0};
+    for (int unit = first_unit; unit >= 0; unit = next_unit(way)) {
+      const int64_t row = unit / split;
+      const int rank = rank_of(unit);
       const bool got_head = warp_wait(&sh->head_full[hi], head_phase, &sh->failed);
       const Head h = sh->head[hi];
       const Targets t = targets(hi);
       const int head_slot = hi;
-      if (++hi == 2) {
+      if (++hi == kTargetWarps) {
         hi = 0;
         head_phase ^= 1;
       }
-      const Segment s = segment(row);
+      const Segment s = segment(unit);
       Raw* g = static_cast<Raw*>(a.grad) + row * a.grad_stride;
       uint4* gv = reinterpret_cast<uint4*>(g - s.vecs.lead);
       const bool same = reinterpret_cast<uintptr_t>(gv) % 16 == 0;
@@ -600,22 +779,42 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_ring_kernel(const Row
       if (MODE == kLossBwd) {
         st = {a.lse[row] * a.tau, 1.0f};
       } else {
-        for (int c = 0; c < s.chunks; ++c) {
-          warp_wait(&sh->full[slot], phase, &sh->failed);
+        // two chunks at a time, where there are two: half the updates of the
+        // maximum, twice the loads in flight
+        for (int c = 0; c < s.chunks; c += kPair ? 2 : 1) {
           const int first = s.begin + c * kChunkVecs;
-          uint4 r[kChunkUnits];
-          fetch(s, slot, first, inner_chunk(s, first), r);
+          const bool two = kPair && c + 1 < s.chunks;
+          uint4 r[2][kChunkUnits];
+          warp_wait(&sh->full[slot], phase, &sh->failed);
+          fetch(s, slot, first, inner_chunk(s, first), r[0]);
           if (c < s.chunks - s.keep) release(slot);
-          if (++slot == kRowSlots) {
+          if (++slot == ring_slots) {
             slot = 0;
             phase ^= 1;
           }
-          const float m = fmaxf(st.m, vec_max<TYPE>(r));
+          float m = fmaxf(st.m, vec_max<TYPE>(r[0]));
+          if (two) {
+            warp_wait(&sh->full[slot], phase, &sh->failed);
+            fetch(s, slot, first + kChunkVecs, inner_chunk(s, first + kChunkVecs), r[1]);
+            if (c + 1 < s.chunks - s.keep) release(slot);
+            if (++slot == ring_slots) {
+              slot = 0;
+              phase ^= 1;
+            }
+            m = fmaxf(m, vec_max<TYPE>(r[1]));
+          }
           const float o = origin(m);
+          const uint64_t neg_o = pack2(-o, -o);
           uint64_t acc = pack2(st.sum * exp2_approx((st.m - o) * scale2), 0.0f);
 #pragma unroll
-          for (int u = 0; u < kChunkUnits; ++u)
-            acc = vec_exp_sum<TYPE>(r[u], pack2(-o, -o), scale22, acc);
+          for (int u = 0; u < kChunkUnits; ++u) acc = vec_exp_sum<TYPE>(r[0][u], neg_o, scale22, acc);
+          if (two) {
+            uint64_t acc1 = 0;
+#pragma unroll
+            for (int u = 0; u < kChunkUnits; ++u)
+              acc1 = vec_exp_sum<TYPE>(r[1][u], neg_o, scale22, acc1);
+            acc = add2(acc, acc1);
+          }
           float lo, up;
           unpack2(acc, lo, up);
           st = {m, lo + up};
@@ -632,8 +831,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_ring_kernel(const Row
             asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(st.m),
                          "f"(st.sum)
                          : "memory");
-            asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
-                         : "memory");
+            mbar_arrive_cluster(bar);
           }
           __all_sync(kFull, row_wait_cluster(&sh->peers, peer_phase, &sh->failed));
           st = warp_join(lane < split ? sh->peer[peer_phase][lane] : Softmax{-INFINITY, 0.0f},
@@ -651,20 +849,22 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_ring_kernel(const Row
         const int first = s.chunks - s.keep;
         int at = slot0 + (MODE == kLossGrad ? first : 0);
         uint32_t ph = phase0;
-        while (at >= kRowSlots) {
-          at -= kRowSlots;
+        while (at >= ring_slots) {
+          at -= ring_slots;
           ph ^= 1;
         }
         for (int i = 0; i < s.chunks; ++i) {
           const int c = MODE == kLossGrad ? (i < s.keep ? first + i : i - s.keep) : i;
           const int begin = s.begin + c * kChunkVecs;
           const bool inner = inner_chunk(s, begin);
-          const uint64_t fc =
-              warp_wait(&sh->full[at], ph, &sh->failed) ? ff : pack2(NAN, NAN);
+          // a resident chunk was waited for in the first pass
+          const bool ok = (MODE == kLossGrad && i < s.keep) ||
+                          warp_wait(&sh->full[at], ph, &sh->failed);
+          const uint64_t fc = ok ? ff : pack2(NAN, NAN);
           uint4 r[kChunkUnits];
           fetch(s, at, begin, inner, r);
           release(at);
-          if (++at == kRowSlots) {
+          if (++at == ring_slots) {
             at = 0;
             ph ^= 1;
           }
@@ -704,7 +904,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_ring_kernel(const Row
     }
   }
   // no CTA ends while another may still write into its shared memory
-  if (MODE != kLossBwd && split > 1) {
+  if (clustered) {
     __syncwarp();
     cluster_sync();
   }
@@ -734,19 +934,22 @@ cudaError_t launch_row_loss_as(const RowLossArgs& a, cudaStream_t s) {
     return launch_kernel(row_loss_short_kernel<TYPE, OP, MODE, 256, 8>,
                          dim3(static_cast<unsigned>(a.rows)), dim3(256), lists, s, a);
   const int sms = device_sm_count();
+  const int slots = row_ring_slots(a.k);
   int split = 1;
   if (MODE == kLossGrad)
-    while (split < 8 && bytes > int64_t(split) * kRowKeep * kChunkBytes) split *= 2;
+    while (split < 8 && bytes > int64_t(split) * (slots - 2) * kChunkBytes) split *= 2;
   while (split < kMaxCluster && a.rows * split * 2 <= sms && bytes >= int64_t(split) * 2 * 8192)
     split *= 2;
   // over its own logits the backward call of the policy loss must not write a
   // segment before every segment has read the action's score
   if (MODE == kLossBwd && OP == kOpPolicy && a.grad == a.logits) split = 1;
+  while (a.rows * split >= (int64_t(1) << 31)) split /= 2;  // CTA numbers are 31 bits
   auto kern = row_loss_ring_kernel<TYPE, OP, MODE>;
-  const size_t smem = row_ring_smem(a.k);
+  const size_t smem = row_ring_smem(a.k, slots);
   cudaError_t e = prepare_ring(kern, smem, split);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.rows * split));
   cfg.blockDim = dim3(kRowThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -756,19 +959,15 @@ cudaError_t launch_row_loss_as(const RowLossArgs& a, cudaStream_t s) {
   attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[n++].val.programmaticStreamSerializationAllowed = 1;
 #endif
-  int64_t groups = sms / split;
   if (MODE != kLossBwd && split > 1) {
     attr[n].id = cudaLaunchAttributeClusterDimension;
     attr[n].val.clusterDim.x = split;
     attr[n].val.clusterDim.y = 1;
     attr[n++].val.clusterDim.z = 1;
   }
-  groups = groups < 1 ? 1 : groups;
-  if (groups > a.rows) groups = a.rows;
-  cfg.gridDim = dim3(static_cast<unsigned>(groups * split));
   cfg.attrs = attr;
   cfg.numAttrs = n;
-  return cudaLaunchKernelEx(&cfg, kern, a, split);
+  return cudaLaunchKernelEx(&cfg, kern, a, split, slots, a.rows * split > sms);
 }
 
 }  // namespace lsdrs

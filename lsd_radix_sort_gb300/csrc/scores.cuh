@@ -39,12 +39,10 @@ struct Score<RS_SCORE_F32> {
   static __device__ __forceinline__ Raw store(float v) { return __float_as_uint(v); }
 };
 
-// A score of a type known at run time (short lists only).
-__device__ __forceinline__ float load_score(const void* p, int type, int64_t i) {
-  if (type == RS_SCORE_F32) return static_cast<const float*>(p)[i];
-  const uint16_t r = static_cast<const uint16_t*>(p)[i];
-  return type == RS_SCORE_F16 ? Score<RS_SCORE_F16>::load(r) : Score<RS_SCORE_BF16>::load(r);
-}
+template <int TYPE>
+struct ScoreTag {
+  static constexpr int value = TYPE;
+};
 
 __device__ __forceinline__ int64_t load_index(const void* p, int bytes, int64_t i) {
   return bytes == 8 ? static_cast<const int64_t*>(p)[i] : static_cast<const int32_t*>(p)[i];
