@@ -376,6 +376,8 @@ typedef enum rs_score_type { RS_SCORE_F16 = 0, RS_SCORE_BF16 = 1, RS_SCORE_F32 =
 /* Longest list of a teacher's top logits, and most experts of a router. */
 #define RS_MAX_TOP 1024
 #define RS_MAX_EXPERTS 1024
+/* Least temperature (2^-64): below it no difference of two scores is small. */
+#define RS_MIN_TEMPERATURE 5.42101086e-20f
 
 /* Distillation from a teacher's top logits.  With z = x / temperature,
  * lse = log sum_j exp(z_j) and q_j = exp(z_j - lse) of a row x of logits,
@@ -392,7 +394,7 @@ typedef enum rs_score_type { RS_SCORE_F16 = 0, RS_SCORE_BF16 = 1, RS_SCORE_F32 =
  *   top_indices rows x top columns, int32 or int64 (index_bytes 4 or 8)
  *   weights     rows floats or NULL (1); a row of weight 0 is not read: its
  *               losses and lse are 0, its gradient 0
- *   temperature > 0, finite
+ *   temperature >= RS_MIN_TEMPERATURE, finite
  *   losses, lse rows floats
  *   grad        rows x cols of the logits' type; rs_distill_loss: may be
  *               NULL (losses only), else the gradient of the sum of losses */
@@ -481,6 +483,7 @@ rs_status rs_policy_loss_backward(const rs_policy_args* args, const float* grad_
  *   grad        tokens x experts of the scores' type; rs_balance_loss: may
  *               be NULL, else the gradient of scale * loss
  *   temp, temp_bytes  scratch of rs_balance_temp_bytes(), 256-byte aligned
+ *               (none, and temp may be NULL, where that is 0)
  * With tokens = 0 the outputs are still written (zeros). */
 typedef struct rs_balance_args {
   const void* scores;
@@ -500,7 +503,7 @@ typedef struct rs_balance_args {
   float scale;
 } rs_balance_args;
 
-/* Scratch size of rs_balance_loss (host only). */
+/* Scratch size of rs_balance_loss (host only); 0 for small calls. */
 rs_status rs_balance_temp_bytes(int64_t tokens, int experts, size_t* bytes);
 
 /* Loss, mean_probs, counts, n_tokens and, where args->grad is given, the

@@ -170,12 +170,6 @@ def _lib_of():
     return _lib if _lib is not None else load_library()
 
 
-def _stream_of(t, stream=None):
-    """The given stream, or the current one of the tensor's device."""
-    import torch
-    return (stream if stream is not None else torch.cuda.current_stream(t.device)).cuda_stream
-
-
 def _status_name(status: int) -> str:
     try:
         return load_library().rs_status_string(status).decode()

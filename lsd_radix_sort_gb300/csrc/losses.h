@@ -65,6 +65,7 @@ cudaError_t launch_row_loss(RowLossOp op, int type, LossMode mode, const RowLoss
                             int* launched, cudaStream_t s);
 cudaError_t launch_balance(int type, LossMode mode, const BalanceArgs& a, int* launched,
                            cudaStream_t s);
-size_t balance_temp(int experts);
+// Scratch of a call; 0 where one cluster does all of it.
+size_t balance_temp(int64_t tokens, int experts);
 
 }  // namespace lsdrs

@@ -68,8 +68,7 @@ rs_status rows_check(const void* logits, int64_t stride, int64_t rows, int64_t c
   const int es = score_bytes(type);
   if (rows < 0 || rows > kMaxRows || cols < 1 || cols > RS_MAX_ROW_KEYS) return RS_ERR_INVALID;
   if (!matrix_ok(rows, cols, stride, es)) return RS_ERR_INVALID;
-  if (!(temperature > 0.0f) || !std::isfinite(temperature) || !std::isfinite(1.0f / temperature))
-    return RS_ERR_INVALID;
+  if (!(temperature >= RS_MIN_TEMPERATURE) || !std::isfinite(temperature)) return RS_ERR_INVALID;
   if (rows == 0) return RS_OK;
   if (!given(logits, es) || !given(lse, 4) || !aligned(weights, 4)) return RS_ERR_INVALID;
   if (mode != kLossBwd && !given(losses, 4)) return RS_ERR_INVALID;
@@ -180,8 +179,9 @@ rs_status balance(const rs_balance_args* p, const float* grad_loss, LossMode mod
       return RS_ERR_INVALID;
     if (!given(p->loss, 4) || !given(p->mean_probs, 4)) return RS_ERR_INVALID;
     if (p->tokens > 0 && !given(p->expert_ids, p->index_bytes)) return RS_ERR_INVALID;
-    if (!given(p->temp, 256)) return RS_ERR_INVALID;
-    if (p->temp_bytes < balance_temp(p->experts)) return RS_ERR_TEMP_TOO_SMALL;
+    const size_t need = balance_temp(p->tokens, p->experts);
+    if (need != 0 && !given(p->temp, 256)) return RS_ERR_INVALID;
+    if (p->temp_bytes < need) return RS_ERR_TEMP_TOO_SMALL;
     if (!std::isfinite(p->scale)) return RS_ERR_INVALID;
   }
   if (!aligned(grad_loss, 4)) return RS_ERR_INVALID;
@@ -240,8 +240,9 @@ rs_status rs_policy_loss_backward(const rs_policy_args* args, const float* grad_
 }
 
 rs_status rs_balance_temp_bytes(int64_t tokens, int experts, size_t* bytes) {
-  if (!bytes || tokens < 0 || experts < 1 || experts > RS_MAX_EXPERTS) return RS_ERR_INVALID;
-  *bytes = balance_temp(experts);
+  if (!bytes || tokens < 0 || tokens > kMaxRows || experts < 1 || experts > RS_MAX_EXPERTS)
+    return RS_ERR_INVALID;
+  *bytes = balance_temp(tokens, experts);
   return RS_OK;
 }
 

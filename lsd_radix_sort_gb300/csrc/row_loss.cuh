@@ -11,6 +11,8 @@
 // (one pass, rescaling the sum whenever the maximum grows), the coefficient,
 // a pass that writes c q_j, and a last step that rewrites the target columns.
 #pragma once
+#include <atomic>
+
 #include "losses.h"
 #include "scores.cuh"
 
@@ -257,10 +259,14 @@ __device__ __forceinline__ void store_result(const RowLossArgs& a, int64_t row,
 }
 
 // ---------------------------------------------------------------- short rows
+#ifndef LSDRS_SHORT_WARPS
+#define LSDRS_SHORT_WARPS 32
+#endif
 // One CTA per row, the row in registers: rows of at most kThreads * VECS
 // 16-byte vectors.  Many CTAs per SM hide each other's loads and reductions.
 template <int TYPE, int OP, int MODE, int kThreads, int VECS>
-__global__ void __launch_bounds__(kThreads) row_loss_short_kernel(const RowLossArgs a) {
+__global__ void __launch_bounds__(kThreads, LSDRS_SHORT_WARPS / (kThreads / kWarp))
+    row_loss_short_kernel(const RowLossArgs a) {
   grid_dependency_sync();
   using S = Score<TYPE>;
   using Raw = typename S::Raw;
@@ -311,16 +317,9 @@ __global__ void __launch_bounds__(kThreads) row_loss_short_kernel(const RowLossA
     s = {a.lse[row] * a.tau, 1.0f};
     __syncthreads();
   } else {
-    s.m = vec_max<TYPE>(r);
-    const float o = origin(s.m);
-    uint64_t acc = 0;
-#pragma unroll
-    for (int u = 0; u < VECS; ++u)
-      acc = vec_exp_sum<TYPE>(r[u], pack2(-o, -o), pack2(scale2, scale2), acc);
-    float lo, hi;
-    unpack2(acc, lo, hi);
-    s.sum = lo + hi;
-    s = warp_join(s, scale2);
+    RunningSoftmax<TYPE> run(scale2);
+    run.add(r);
+    s = warp_join(run.result(), scale2);
     if (lane_id() == 0) part[warp] = s;
     __syncthreads();
     s = lane_id() < kWarps ? part[lane_id()] : Softmax{-INFINITY, 0.0f};
@@ -330,18 +329,214 @@ __global__ void __launch_bounds__(kThreads) row_loss_short_kernel(const RowLossA
   if (MODE != kLossBwd && tid == 0) store_result<OP>(a, row, res);
   if (MODE == kLossFwd) return;
   const float o = origin(s.m), f = res.c / s.sum;
+  const Exponent e(o, scale2);
+  const uint64_t ff = pack2(f * e.mend, f * e.mend);
 #pragma unroll
   for (int u = 0; u < VECS; ++u) {
     const int v = tid + u * kThreads;
     if (v < vecs.count)
       put(v, res.c == 0.0f ? make_uint4(0, 0, 0, 0)
-                           : vec_grad<TYPE>(r[u], pack2(-o, -o), pack2(scale2, scale2), pack2(f, f)));
+                           : vec_grad<TYPE>(r[u], e, ff));
   }
   if (res.c == 0.0f) return;
   __syncthreads();
   for (int k = tid; k < a.k; k += kThreads)
     if (t.col[k] >= 0)
       g[t.col[k]] = S::store(exp2_approx((t.x[k] - o) * scale2) * f - res.c * t.p[k]);
+}
+
+// -------------------------------------------- long rows, one pass over a row
+// The losses alone, and the backward call, read a row once and keep nothing
+// of it: plain wide loads, a batch of them always ahead of the arithmetic,
+// with three CTAs per SM.  A row is cut into `split` segments when there are
+// too few rows.  One more warp reads the row's targets meanwhile.
+constexpr int kStreamThreads = 256;
+constexpr int kStreamWarps = kStreamThreads / kWarp;
+#ifndef LSDRS_STREAM_BATCH
+#define LSDRS_STREAM_BATCH 4
+#define LSDRS_STREAM_CTAS 3
+#endif
+#ifndef LSDRS_STREAM_WAVES
+#define LSDRS_STREAM_WAVES 2
+#define LSDRS_STREAM_LEAST 16384
+#endif
+constexpr int kStreamBatch = LSDRS_STREAM_BATCH;
+constexpr int kMaxCluster = 16;
+
+__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+
+__device__ __forceinline__ void store_peer(Softmax* at, uint32_t rank, const Softmax& v) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(peer_addr(smem_addr(at), rank)),
+               "f"(v.m), "f"(v.sum)
+               : "memory");
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+
+// A thread's vectors of a segment [begin, end): begin + tid, + kStreamThreads,
+// ...  Calls body(v, vectors) for batches of kStreamBatch of them, the next
+// batch's loads under way; vectors past the end are -inf.
+template <int TYPE, class F>
+__device__ __forceinline__ void stream_segment(const typename Score<TYPE>::Raw* x,
+                                               const RowVecs<TYPE>& vecs, int begin, int end,
+                                               int tid, F&& body) {
+  using V = ScoreVec<TYPE>;
+  const uint4* xv = reinterpret_cast<const uint4*>(x - vecs.lead);
+  constexpr int kStep = kStreamThreads * kStreamBatch;
+  const int inner_end = min(end, vecs.whole_end());
+  auto load = [&](int v0, uint4 (&r)[kStreamBatch]) {
+    const int v1 = v0 + (kStreamBatch - 1) * kStreamThreads;
+    if (v0 >= vecs.whole_begin() && v1 < inner_end) {
+#pragma unroll
+      for (int u = 0; u < kStreamBatch; ++u) r[u] = __ldcs(xv + v0 + u * kStreamThreads);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kStreamBatch; ++u) {
+        const int v = v0 + u * kStreamThreads;
+        if (v >= end)
+          r[u] = make_uint4(V::kMinusInf, V::kMinusInf, V::kMinusInf, V::kMinusInf);
+        else if (vecs.whole(v))
+          r[u] = __ldcs(xv + v);
+        else
+          r[u] = vecs.load_edge(x, v);
+      }
+    }
+  };
+  uint4 r[kStreamBatch], ahead[kStreamBatch];
+  int v = begin + tid;
+  if (v >= end) return;
+  load(v, r);
+  for (; v < end; v += kStep) {
+    if (v + kStep < end) load(v + kStep, ahead);
+    body(v, r);
+#pragma unroll
+    for (int u = 0; u < kStreamBatch; ++u) r[u] = ahead[u];
+  }
+}
+
+template <int TYPE, int OP>
+__global__ void __launch_bounds__(kStreamThreads + kWarp, LSDRS_STREAM_CTAS)
+    row_loss_forward_kernel(const RowLossArgs a, const int split) {
+  using Raw = typename Score<TYPE>::Raw;
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ Softmax part[kStreamWarps], peer[kMaxCluster];
+  __shared__ Head head;
+  grid_dependency_sync();
+  Targets t;
+  t.col = reinterpret_cast<int*>(smem);
+  t.p = reinterpret_cast<float*>(t.col + a.k);
+  t.x = t.p + a.k;
+  const int tid = static_cast<int>(threadIdx.x), warp = tid / kWarp;
+  const int lane = static_cast<int>(lane_id());
+  const int64_t row = blockIdx.x / split;
+  const int rank = static_cast<int>(blockIdx.x % split);
+  if (row_off<OP>(a, row)) {  // the whole cluster's answer
+    if (rank == 0 && tid == 0) store_result<OP>(a, row, RowResult{0, 0, 0, 0});
+    return;
+  }
+  const float scale2 = a.inv_tau * kLog2e;
+  if (warp == kStreamWarps) {
+    if (rank == 0) load_targets<TYPE, OP, kLossFwd>(a, row, t, nullptr, &head);
+  } else {
+    const Raw* x = static_cast<const Raw*>(a.logits) + row * a.stride;
+    const RowVecs<TYPE> vecs(x, static_cast<int>(a.cols));
+    const int per = (vecs.count + split - 1) / split;
+    const int begin = min(rank * per, vecs.count), end = min(begin + per, vecs.count);
+    RunningSoftmax<TYPE> run(scale2);
+    stream_segment<TYPE>(x, vecs, begin, end, tid,
+                         [&](int, const uint4(&r)[kStreamBatch]) { run.add(r); });
+    const Softmax s = warp_join(run.result(), scale2);
+    if (lane == 0) part[warp] = s;
+  }
+  __syncthreads();
+  Softmax s{-INFINITY, 0.0f};
+  if (warp == 0) s = warp_join(lane < kStreamWarps ? part[lane] : s, scale2);
+  if (split > 1) {
+    if (tid == 0) store_peer(&peer[rank], 0, s);
+    cluster_sync();
+    if (rank != 0) return;
+    if (warp == 0) s = warp_join(lane < split ? peer[lane] : Softmax{-INFINITY, 0.0f}, scale2);
+  }
+  if (tid == 0) store_result<OP>(a, row, row_result<OP, kLossFwd>(a, head, s.m, s.sum));
+}
+
+template <int TYPE, int OP>
+__global__ void __launch_bounds__(kStreamThreads + kWarp, LSDRS_STREAM_CTAS)
+    row_loss_backward_kernel(const RowLossArgs a, const int split) {
+  using S = Score<TYPE>;
+  using Raw = typename S::Raw;
+  using V = ScoreVec<TYPE>;
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ Head head;
+  grid_dependency_sync();
+  Targets t;
+  t.col = reinterpret_cast<int*>(smem);
+  t.p = reinterpret_cast<float*>(t.col + a.k);
+  t.x = t.p + a.k;
+  const int tid = static_cast<int>(threadIdx.x), warp = tid / kWarp;
+  const int64_t row = blockIdx.x / split;
+  const int rank = static_cast<int>(blockIdx.x % split);
+  const Raw* x = static_cast<const Raw*>(a.logits) + row * a.stride;
+  Raw* g = static_cast<Raw*>(a.grad) + row * a.grad_stride;
+  const RowVecs<TYPE> vecs(x, static_cast<int>(a.cols));
+  const int per = (vecs.count + split - 1) / split;
+  const int begin = min(rank * per, vecs.count), end = min(begin + per, vecs.count);
+  uint4* gv = reinterpret_cast<uint4*>(g - vecs.lead);
+  const bool same = reinterpret_cast<uintptr_t>(gv) % 16 == 0;
+  const int inner_end = min(end, vecs.whole_end());
+  auto put = [&](int v0, const uint4(&r)[kStreamBatch]) {
+    if (same && v0 >= vecs.whole_begin() && v0 + (kStreamBatch - 1) * kStreamThreads < inner_end) {
+#pragma unroll
+      for (int u = 0; u < kStreamBatch; ++u) __stcs(gv + v0 + u * kStreamThreads, r[u]);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kStreamBatch; ++u) {
+        const int v = v0 + u * kStreamThreads;
+        if (v >= end) break;
+        if (same && vecs.whole(v))
+          __stcs(gv + v, r[u]);
+        else
+          vecs.store_scores(g, v, r[u]);
+      }
+    }
+  };
+  const bool off = row_off<OP>(a, row);
+  if (warp == kStreamWarps && !off)
+    load_targets<TYPE, OP, kLossBwd>(a, row, t, reinterpret_cast<int*>(t.x + a.k), &head);
+  const float m = off ? 0.0f : a.lse[row] * a.tau;
+  __syncthreads();
+  const float c = off ? 0.0f : row_result<OP, kLossBwd>(a, head, m, 1.0f).c;
+  const float o = origin(m), scale2 = a.inv_tau * kLog2e;
+  if (warp < kStreamWarps) {
+    if (c == 0.0f) {  // nothing of the row is read
+      const uint4 zero[kStreamBatch] = {};
+      for (int v = begin + tid; v < end; v += kStreamThreads * kStreamBatch) put(v, zero);
+    } else {
+      const Exponent e(o, scale2);
+      const uint64_t f = pack2(c * e.mend, c * e.mend);
+      stream_segment<TYPE>(x, vecs, begin, end, tid, [&](int v, uint4(&r)[kStreamBatch]) {
+#pragma unroll
+        for (int u = 0; u < kStreamBatch; ++u) r[u] = vec_grad<TYPE>(r[u], e, f);
+        put(v, r);
+      });
+    }
+  }
+  if (c == 0.0f) return;
+  __syncthreads();  // the targets' columns are written last
+  const int64_t b = static_cast<int64_t>(begin) * V::kCount - vecs.lead;
+  const int64_t last = static_cast<int64_t>(end) * V::kCount - vecs.lead;
+  for (int k = tid; k < a.k; k += kStreamThreads + kWarp) {
+    const int col = t.col[k];
+    if (col >= 0 && col >= b && col < last)
+      g[col] = S::store(exp2_approx((t.x[k] - o) * scale2) * c - c * t.p[k]);
+  }
 }
 
 // ----------------------------------------------------------------- long rows
@@ -375,17 +570,9 @@ constexpr int kRowThreads = kRowConsumers + (2 + kTargetWarps) * kWarp;
 constexpr int kChunkUnits = LSDRS_ROW_UNITS;                  // vectors per thread and chunk
 constexpr int kChunkVecs = kRowConsumers * kChunkUnits;
 constexpr int kChunkBytes = kChunkVecs * 16;
-constexpr int kMaxSlots = 13;                                 // most ring slots
+constexpr int kMaxSlots = 13 * 16384 / kChunkBytes;           // most ring slots
 constexpr int kAheadRows = 4;                                 // rows that the scheduler is ahead
 constexpr int kRowReaders = kRowWarps + 1 + kTargetWarps;     // warps that read its list
-#ifndef LSDRS_ROW_PAIR
-#define LSDRS_ROW_PAIR 1
-#endif
-constexpr bool kPair = LSDRS_ROW_PAIR;
-#ifndef LSDRS_ROW_STEAL
-#define LSDRS_ROW_STEAL 1
-#endif
-constexpr int kMaxCluster = 16;
 constexpr uint64_t kRowWaitNs = 2000000000ull;
 
 // Barriers and small arrays behind the ring.
@@ -419,36 +606,35 @@ __host__ constexpr inline int row_ring_slots(int k) {
   return n;
 }
 
-// Waits for a phase of a barrier; after kRowWaitNs, or once another wait of
-// the CTA has run out, it gives up: the caller goes on without touching what
-// it waited for, so that every thread still reaches every barrier, and the
-// rows it had left get NaN.
-__device__ __forceinline__ bool row_wait(uint64_t* bar, uint32_t parity, volatile int* failed) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
-  while (!mbar_try_wait(bar, parity)) {
-    if (*failed) return false;
-    if (global_timer_ns() - t0 > kRowWaitNs) {
-      *failed = 1;
-      return false;
-    }
-  }
-  return true;
-}
-
-// The same for a barrier on which other CTAs arrive: what they wrote before is
-// seen after it.
-__device__ __forceinline__ bool row_wait_cluster(uint64_t* bar, uint32_t parity,
-                                                 volatile int* failed) {
+// Waits for a phase of a barrier, with CLUSTER for one on which other CTAs
+// arrive (what they wrote before is then seen after it).  After kRowWaitNs,
+// or once another wait of the CTA has run out, it gives up: the caller goes
+// on without using what it waited for, so that every thread still reaches
+// every barrier, and the rows it had left get NaN.  Each try names a time to
+// sleep: warps that poll in a tight loop take the issue slots and the
+// shared-memory ports of those that work (a 4096 x 131072 bf16 gradient took
+// 500 us so, 441 with a read of the clock between polls).
+template <bool CLUSTER>
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* failed) {
+  constexpr uint32_t kSleepNs = 1000000;
   auto done = [&] {
     uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n"
-        " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-        " selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok)
-        : "r"(smem_addr(bar)), "r"(parity)
-        : "memory");
+    if (CLUSTER)
+      asm volatile(
+          "{\n .reg .pred p;\n"
+          " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
+          " selp.u32 %0, 1, 0, p;\n}"
+          : "=r"(ok)
+          : "r"(smem_addr(bar)), "r"(parity), "r"(kSleepNs)
+          : "memory");
+    else
+      asm volatile(
+          "{\n .reg .pred p;\n"
+          " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+          " selp.u32 %0, 1, 0, p;\n}"
+          : "=r"(ok)
+          : "r"(smem_addr(bar)), "r"(parity), "r"(kSleepNs)
+          : "memory");
     return ok != 0;
   };
   if (done()) return true;
@@ -463,6 +649,14 @@ __device__ __forceinline__ bool row_wait_cluster(uint64_t* bar, uint32_t parity,
   return true;
 }
 
+__device__ __forceinline__ bool row_wait(uint64_t* bar, uint32_t parity, volatile int* failed) {
+  return wait_phase<false>(bar, parity, failed);
+}
+__device__ __forceinline__ bool row_wait_cluster(uint64_t* bar, uint32_t parity,
+                                                 volatile int* failed) {
+  return wait_phase<true>(bar, parity, failed);
+}
+
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
@@ -472,21 +666,10 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(kFull, row_wait(bar, parity, failed));
 }
 
-__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
-  uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
-}
-
 // Arrives on a barrier of any CTA of the cluster.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr)
                : "memory");
-}
-
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::
-                   : "memory");
 }
 
 // Asks for the launch of a CTA (cluster) that has not begun yet to be
@@ -703,7 +886,6 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_ring_kernel(const Row
     }
   } else {  // ---- consumers
     const float scale2 = a.inv_tau * kLog2e;
-    const uint64_t scale22 = pack2(scale2, scale2);
     int slot = 0, hi = 0;
     uint32_t phase = 0, head_phase = 0, peer_phase = 0, together_phase = 0;
     // the chunk's vector u of this thread, from its slot (or, at an edge of
@@ -725,10 +907,6 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_ring_kernel(const Row
         else
           r[u] = s.vecs.load_edge(s.x, v);
       }
-    };
-    // every vector of the chunk lies in the segment and inside the row
-    auto inner_chunk = [&](const Segment& s, int first) {
-      return first >= s.vecs.whole_begin() && first + kChunkVecs <= min(s.end, s.vecs.whole_end());
     };
     // every consumer warp has come here (a bounded wait, unlike bar.sync)
     auto together = [&] {
@@ -754,6 +932,10 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_ring_kernel(const Row
         head_phase ^= 1;
       }
       const Segment s = segment(unit);
+      // chunks [inner0, inner1) lie in the segment and inside the row entirely
+      const int inner0 = s.begin < s.vecs.whole_begin();
+      const int inner1 = max(inner0, (min(s.end, s.vecs.whole_end()) - s.begin) / kChunkVecs);
+      const int early = s.chunks - s.keep;  // chunks that do not stay
       Raw* g = static_cast<Raw*>(a.grad) + row * a.grad_stride;
       uint4* gv = reinterpret_cast<uint4*>(g - s.vecs.lead);
       const bool same = reinterpret_cast<uintptr_t>(gv) % 16 == 0;
@@ -779,46 +961,19 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_ring_kernel(const Row
       if (MODE == kLossBwd) {
         st = {a.lse[row] * a.tau, 1.0f};
       } else {
-        // two chunks at a time, where there are two: half the updates of the
-        // maximum, twice the loads in flight
-        for (int c = 0; c < s.chunks; c += kPair ? 2 : 1) {
-          const int first = s.begin + c * kChunkVecs;
-          const bool two = kPair && c + 1 < s.chunks;
-          uint4 r[2][kChunkUnits];
-          warp_wait(&sh->full[slot], phase, &sh->failed);
-          fetch(s, slot, first, inner_chunk(s, first), r[0]);
-          if (c < s.chunks - s.keep) release(slot);
+        RunningSoftmax<TYPE> run(scale2);
+        for (int c = 0; c < s.chunks; ++c) {
+          uint4 r[kChunkUnits];
+          row_wait(&sh->full[slot], phase, &sh->failed);
+          fetch(s, slot, s.begin + c * kChunkVecs, c >= inner0 && c < inner1, r);
+          if (MODE == kLossFwd || c < early) release(slot);
           if (++slot == ring_slots) {
             slot = 0;
             phase ^= 1;
           }
-          float m = fmaxf(st.m, vec_max<TYPE>(r[0]));
-          if (two) {
-            warp_wait(&sh->full[slot], phase, &sh->failed);
-            fetch(s, slot, first + kChunkVecs, inner_chunk(s, first + kChunkVecs), r[1]);
-            if (c + 1 < s.chunks - s.keep) release(slot);
-            if (++slot == ring_slots) {
-              slot = 0;
-              phase ^= 1;
-            }
-            m = fmaxf(m, vec_max<TYPE>(r[1]));
-          }
-          const float o = origin(m);
-          const uint64_t neg_o = pack2(-o, -o);
-          uint64_t acc = pack2(st.sum * exp2_approx((st.m - o) * scale2), 0.0f);
-#pragma unroll
-          for (int u = 0; u < kChunkUnits; ++u) acc = vec_exp_sum<TYPE>(r[0][u], neg_o, scale22, acc);
-          if (two) {
-            uint64_t acc1 = 0;
-#pragma unroll
-            for (int u = 0; u < kChunkUnits; ++u)
-              acc1 = vec_exp_sum<TYPE>(r[1][u], neg_o, scale22, acc1);
-            acc = add2(acc, acc1);
-          }
-          float lo, up;
-          unpack2(acc, lo, up);
-          st = {m, lo + up};
+          run.add(r);
         }
+        st = run.result();
         st = warp_join(st, scale2);
         Softmax* part = sh->part[peer_phase];
         if (lane == 0) part[warp] = st;
@@ -826,12 +981,8 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_ring_kernel(const Row
         st = warp_join(lane < kRowWarps ? part[lane] : Softmax{-INFINITY, 0.0f}, scale2);
         if (split > 1) {
           if (tid < split) {  // thread i hands this CTA's part to CTA i
-            const uint32_t to = peer_addr(smem_addr(&sh->peer[peer_phase][rank]), tid);
-            const uint32_t bar = peer_addr(smem_addr(&sh->peers), tid);
-            asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(st.m),
-                         "f"(st.sum)
-                         : "memory");
-            mbar_arrive_cluster(bar);
+            store_peer(&sh->peer[peer_phase][rank], tid, st);
+            mbar_arrive_cluster(peer_addr(smem_addr(&sh->peers), tid));
           }
           __all_sync(kFull, row_wait_cluster(&sh->peers, peer_phase, &sh->failed));
           st = warp_join(lane < split ? sh->peer[peer_phase][lane] : Softmax{-INFINITY, 0.0f},
@@ -844,22 +995,22 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_ring_kernel(const Row
       if (MODE != kLossBwd && rank == 0 && tid == 0) store_result<OP>(a, row, res);
       if (MODE != kLossFwd) {
         const float o = origin(st.m), f = res.c / st.sum;
-        const uint64_t neg_o = pack2(-o, -o), ff = pack2(f, f);
+        const Exponent e(o, scale2);
+        const uint64_t ff = pack2(f * e.mend, f * e.mend);
         // the resident chunks, then those copied again
-        const int first = s.chunks - s.keep;
-        int at = slot0 + (MODE == kLossGrad ? first : 0);
+        int at = slot0 + (MODE == kLossGrad ? early : 0);
         uint32_t ph = phase0;
         while (at >= ring_slots) {
           at -= ring_slots;
           ph ^= 1;
         }
         for (int i = 0; i < s.chunks; ++i) {
-          const int c = MODE == kLossGrad ? (i < s.keep ? first + i : i - s.keep) : i;
+          const int c = MODE == kLossGrad ? (i < s.keep ? early + i : i - s.keep) : i;
           const int begin = s.begin + c * kChunkVecs;
-          const bool inner = inner_chunk(s, begin);
+          const bool inner = c >= inner0 && c < inner1;
           // a resident chunk was waited for in the first pass
           const bool ok = (MODE == kLossGrad && i < s.keep) ||
-                          warp_wait(&sh->full[at], ph, &sh->failed);
+                          row_wait(&sh->full[at], ph, &sh->failed);
           const uint64_t fc = ok ? ff : pack2(NAN, NAN);
           uint4 r[kChunkUnits];
           fetch(s, at, begin, inner, r);
@@ -873,7 +1024,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_ring_kernel(const Row
             for (int u = 0; u < kChunkUnits; ++u) r[u] = make_uint4(0, 0, 0, 0);
           } else {
 #pragma unroll
-            for (int u = 0; u < kChunkUnits; ++u) r[u] = vec_grad<TYPE>(r[u], neg_o, scale22, fc);
+            for (int u = 0; u < kChunkUnits; ++u) r[u] = vec_grad<TYPE>(r[u], e, fc);
           }
           if (inner && same) {
 #pragma unroll
@@ -911,13 +1062,84 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_ring_kernel(const Row
 }
 
 // -------------------------------------------------------------------- launch
+// Opts a kernel into what its launches need (all of the shared memory, or
+// clusters of 16), once per device.
 template <class K>
-cudaError_t prepare_ring(K kern, size_t smem, int split) {
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
-  if (e == cudaSuccess && split > 8)
+cudaError_t allow(K kern, bool smem, bool big_cluster, std::atomic<uint64_t>* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (dev < 64 && (done->load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  if (smem)
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kMaxSmem));
+  if (e == cudaSuccess && big_cluster)
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_release);
   return e;
+}
+
+inline int add_attributes(cudaLaunchAttribute* attr, int cluster) {
+  int n = 0;
+#if LSDRS_PDL
+  attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[n++].val.programmaticStreamSerializationAllowed = 1;
+#endif
+  if (cluster > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = cluster;
+    attr[n].val.clusterDim.y = 1;
+    attr[n++].val.clusterDim.z = 1;
+  }
+  return n;
+}
+
+template <int TYPE, int OP, int MODE>
+cudaError_t launch_stream(const RowLossArgs& a, int split, size_t smem, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.rows * split));
+  cfg.blockDim = dim3(kStreamThreads + kWarp);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  cfg.attrs = attr;
+  cfg.numAttrs = add_attributes(attr, MODE == kLossFwd ? split : 1);
+  if constexpr (MODE == kLossFwd) {
+    auto kern = row_loss_forward_kernel<TYPE, OP>;
+    static std::atomic<uint64_t> done{0};
+    if (split > 8) {
+      const cudaError_t e = allow(kern, false, true, &done);
+      if (e != cudaSuccess) return e;
+    }
+    return cudaLaunchKernelEx(&cfg, kern, a, split);
+  } else {
+    return cudaLaunchKernelEx(&cfg, row_loss_backward_kernel<TYPE, OP>, a, split);
+  }
+}
+
+template <int TYPE, int OP>
+cudaError_t launch_ring(const RowLossArgs& a, int sms, int64_t bytes, cudaStream_t s) {
+  const int slots = row_ring_slots(a.k);
+  int split = 1;
+  while (split < 8 && bytes > int64_t(split) * (slots - 2) * kChunkBytes) split *= 2;
+  while (split < kMaxCluster && a.rows * split * 2 <= sms && bytes >= int64_t(split) * 2 * 8192)
+    split *= 2;
+  while (a.rows * split >= (int64_t(1) << 31)) split /= 2;  // CTA numbers are 31 bits
+  auto kern = row_loss_ring_kernel<TYPE, OP, kLossGrad>;
+  const size_t smem = row_ring_smem(a.k, slots);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow(kern, true, true, &done);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.rows * split));
+  cfg.blockDim = dim3(kRowThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  cfg.attrs = attr;
+  cfg.numAttrs = add_attributes(attr, split);
+  return cudaLaunchKernelEx(&cfg, kern, a, split, slots, a.rows * split > sms);
 }
 
 template <int TYPE, int OP, int MODE>
@@ -934,40 +1156,21 @@ cudaError_t launch_row_loss_as(const RowLossArgs& a, cudaStream_t s) {
     return launch_kernel(row_loss_short_kernel<TYPE, OP, MODE, 256, 8>,
                          dim3(static_cast<unsigned>(a.rows)), dim3(256), lists, s, a);
   const int sms = device_sm_count();
-  const int slots = row_ring_slots(a.k);
-  int split = 1;
-  if (MODE == kLossGrad)
-    while (split < 8 && bytes > int64_t(split) * (slots - 2) * kChunkBytes) split *= 2;
-  while (split < kMaxCluster && a.rows * split * 2 <= sms && bytes >= int64_t(split) * 2 * 8192)
-    split *= 2;
-  // over its own logits the backward call of the policy loss must not write a
-  // segment before every segment has read the action's score
-  if (MODE == kLossBwd && OP == kOpPolicy && a.grad == a.logits) split = 1;
-  while (a.rows * split >= (int64_t(1) << 31)) split /= 2;  // CTA numbers are 31 bits
-  auto kern = row_loss_ring_kernel<TYPE, OP, MODE>;
-  const size_t smem = row_ring_smem(a.k, slots);
-  cudaError_t e = prepare_ring(kern, smem, split);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.rows * split));
-  cfg.blockDim = dim3(kRowThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  int n = 0;
-#if LSDRS_PDL
-  attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[n++].val.programmaticStreamSerializationAllowed = 1;
-#endif
-  if (MODE != kLossBwd && split > 1) {
-    attr[n].id = cudaLaunchAttributeClusterDimension;
-    attr[n].val.clusterDim.x = split;
-    attr[n].val.clusterDim.y = 1;
-    attr[n++].val.clusterDim.z = 1;
+  if constexpr (MODE != kLossGrad) {
+    // segments of at least 16 KB, until there are two for every place
+    int split = 1;
+    while (split < kMaxCluster &&
+           a.rows * split < int64_t(sms) * LSDRS_STREAM_CTAS * LSDRS_STREAM_WAVES &&
+           bytes >= int64_t(split) * 2 * LSDRS_STREAM_LEAST)
+      split *= 2;
+    // over its own logits the backward call of the policy loss must not write
+    // a segment before every segment has read the action's score
+    if (MODE == kLossBwd && OP == kOpPolicy && a.grad == a.logits) split = 1;
+    while (a.rows * split >= (int64_t(1) << 31)) split /= 2;  // CTA numbers are 31 bits
+    return launch_stream<TYPE, OP, MODE>(a, split, lists, s);
+  } else {
+    return launch_ring<TYPE, OP>(a, sms, bytes, s);
   }
-  cfg.attrs = attr;
-  cfg.numAttrs = n;
-  return cudaLaunchKernelEx(&cfg, kern, a, split, slots, a.rows * split > sms);
 }
 
 }  // namespace lsdrs

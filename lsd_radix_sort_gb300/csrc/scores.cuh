@@ -100,13 +100,37 @@ __device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
 }
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+#ifdef LSDRS_SCALAR_MATH
+  float a0, a1, b0, b1;
+  unpack2(a, a0, a1);
+  unpack2(b, b0, b1);
+  return pack2(a0 + b0, a1 + b1);
+#endif
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+#ifdef LSDRS_SCALAR_MATH
+  float a0, a1, b0, b1;
+  unpack2(a, a0, a1);
+  unpack2(b, b0, b1);
+  return pack2(a0 * b0, a1 * b1);
+#endif
   uint64_t r;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+#ifdef LSDRS_SCALAR_MATH
+  float a0, a1, b0, b1, c0, c1;
+  unpack2(a, a0, a1);
+  unpack2(b, b0, b1);
+  unpack2(c, c0, c1);
+  return pack2(__fmaf_rn(a0, b0, c0), __fmaf_rn(a1, b1, c1));
+#endif
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
 __device__ __forceinline__ uint64_t exp2_2(uint64_t v) {
@@ -222,31 +246,87 @@ __device__ __forceinline__ uint4 vec_of(const uint64_t (&p)[ScoreVec<TYPE>::kCou
   return v;
 }
 
-// Adds sum exp2((x - o) scale2) of a vector to the pair of partial sums.
-// The difference is taken before the product, so that scores near the type's
-// lowest value stay finite.
+// exp2((x - o) scale) of pairs of scores.  One multiply-add per score takes
+// x * scale - os2 with os2 = o * scale rounded: the product is exact inside,
+// so the result is that of a slightly other origin, and `mend` = the factor
+// 2^(os2 - o scale) puts it right, once per sum.  Where o * scale overflows
+// (a row that holds nothing above the type's lowest value, say; scale > 1
+// then, and below 2^65 by the least temperature) scores are at least 2^40
+// apart or equal, so any scale gives the same 0 or 1: 1 does.
+struct Exponent {
+  uint64_t scale2, neg_os2;
+  float mend;
+
+  __device__ __forceinline__ Exponent(float o, float scale) {
+    float os2 = o * scale;
+    const bool far = isinf(os2) && !isinf(o);
+    os2 = far ? o : os2;
+    const float used = far ? 1.0f : scale;
+    scale2 = pack2(used, used);
+    neg_os2 = pack2(-os2, -os2);
+    mend = far ? 1.0f : exp2_approx(__fmaf_rn(-o, scale, os2));
+  }
+  __device__ __forceinline__ uint64_t of(uint64_t x) const {
+    return exp2_2(fma2(x, scale2, neg_os2));
+  }
+};
+
+// Adds the exponentials of a vector to two pairs of partial sums.
 template <int TYPE>
-__device__ __forceinline__ uint64_t vec_exp_sum(const uint4& v, uint64_t neg_o, uint64_t scale2,
-                                                uint64_t acc) {
+__device__ __forceinline__ void vec_exp_sum(const uint4& v, const Exponent& e, uint64_t (&acc)[2]) {
   uint64_t p[ScoreVec<TYPE>::kCount / 2];
   vec_pairs<TYPE>(v, p);
 #pragma unroll
   for (int i = 0; i < ScoreVec<TYPE>::kCount / 2; ++i)
-    acc = add2(acc, exp2_2(mul2(add2(p[i], neg_o), scale2)));
-  return acc;
+    acc[i & 1] = add2(acc[i & 1], e.of(p[i]));
 }
 
-// f exp2((x - o) scale2) of a vector, rounded to the scores' type.
+// f times the exponentials of a vector, rounded to the scores' type.
 template <int TYPE>
-__device__ __forceinline__ uint4 vec_grad(const uint4& v, uint64_t neg_o, uint64_t scale2,
-                                          uint64_t f) {
+__device__ __forceinline__ uint4 vec_grad(const uint4& v, const Exponent& e, uint64_t f) {
   uint64_t p[ScoreVec<TYPE>::kCount / 2];
   vec_pairs<TYPE>(v, p);
 #pragma unroll
-  for (int i = 0; i < ScoreVec<TYPE>::kCount / 2; ++i)
-    p[i] = mul2(exp2_2(mul2(add2(p[i], neg_o), scale2)), f);
+  for (int i = 0; i < ScoreVec<TYPE>::kCount / 2; ++i) p[i] = mul2(e.of(p[i]), f);
   return vec_of<TYPE>(p);
 }
+
+// A thread's softmax in progress over many vectors.  The origin is the
+// largest score of some vectors past; it moves only when a score exceeds it
+// by more than 2^60 would (so no sum overflows), which keeps the maximum off
+// the path of the exponentials.
+template <int TYPE>
+struct RunningSoftmax {
+  float scale, o, limit;
+  Exponent e;
+  uint64_t acc[2];
+
+  __device__ __forceinline__ explicit RunningSoftmax(float scale2)
+      : scale(scale2), o(-INFINITY), limit(-INFINITY), e(0.0f, scale2) {
+    acc[0] = acc[1] = 0;
+  }
+  __device__ __forceinline__ float total() const {
+    float a, b;
+    unpack2(add2(acc[0], acc[1]), a, b);
+    return (a + b) * e.mend;
+  }
+  __device__ __forceinline__ void move(float m) {
+    const float sum = total() * exp2_approx((o - m) * scale);
+    o = m;
+    limit = m + 60.0f / scale;
+    e = Exponent(m, scale);
+    acc[0] = pack2(sum / e.mend, 0.0f);
+    acc[1] = 0;
+  }
+  template <int VECS>
+  __device__ __forceinline__ void add(const uint4 (&v)[VECS]) {
+    const float m = vec_max<TYPE>(v);
+    if (m > limit) move(m);
+#pragma unroll
+    for (int u = 0; u < VECS; ++u) vec_exp_sum<TYPE>(v[u], e, acc);
+  }
+  __device__ __forceinline__ Softmax result() const { return {o, total()}; }
+};
 
 // A row of scores as 16-byte vectors of memory: vector 0 begins at the row's
 // address rounded down to 16 bytes, so its first `lead` scores, and the last

@@ -22,9 +22,10 @@ synchronises; results are allocated by torch on that stream unless given.
 from __future__ import annotations
 
 import ctypes
+import functools
 import types
 
-from . import _check, _lib_of, _stream_of
+from . import _check, _lib_of
 
 __all__ = [
     "distill_loss", "distill_loss_grad", "distill_loss_backward", "policy_loss",
@@ -66,91 +67,88 @@ class BalanceArgs(ctypes.Structure):
                 ("experts", _I), ("index_bytes", _I), ("top", _I), ("scale", _F)]
 
 
-_TYPES = None
+# torch, its score types and its raw current stream, once a call has needed them
+_torch = None
+_TYPES = {}
+_raw_stream = None
 
 
-def _score_types():
-    global _TYPES
-    if _TYPES is None:
-        import torch
-        _TYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
-    return _TYPES
+def _load():
+    global _torch, _raw_stream
+    import torch
+    _TYPES.update({torch.float16: 0, torch.bfloat16: 1, torch.float32: 2})
+    # the current stream's address without a Stream object around it, where
+    # this torch has that call
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _torch = torch
+    return torch
 
 
-def _scores(t, what):
-    """The rs_score_type of a 2-D tensor of scores with unit stride in its rows."""
-    kind = _score_types().get(t.dtype)
+def _kind(t, what):
+    """The rs_score_type of a tensor of scores."""
+    kind = _TYPES.get(t.dtype)
     if kind is None:
         raise TypeError(f"{what} must be float16, bfloat16 or float32, got {t.dtype}")
-    if t.dim() != 2:
-        raise ValueError(f"{what} must be a 2-D tensor")
-    _rows(t, what)
     return kind
 
 
-def _rows(t, what):
-    if t.shape[1] > 1 and t.stride(1) != 1:
+def _matrix(t, what):
+    """(rows, cols, elements from one row to the next) of a 2-D tensor with unit
+    stride in its rows (a lone row's stride means nothing)."""
+    if t.dim() != 2:
+        raise ValueError(f"{what} must be a 2-D tensor")
+    rows, cols = t.shape
+    stride, unit = t.stride()
+    if unit != 1 and cols > 1:
         raise ValueError(f"{what} must have unit stride in its last dimension")
-    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+    if rows <= 1:
+        return rows, cols, cols
+    if stride < cols:
         raise ValueError(f"{what} must have rows that do not overlap")
-
-
-def _stride(t):
-    """Elements from one row to the next (a lone row's stride means nothing)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return rows, cols, stride
 
 
 def _index_bytes(t, what):
-    import torch
-    if t.dtype == torch.int64:
+    if t.dtype is _torch.int64:
         return 8
-    if t.dtype == torch.int32:
+    if t.dtype is _torch.int32:
         return 4
     raise TypeError(f"{what} must be int32 or int64, got {t.dtype}")
 
 
 def _vector(t, n, what, dtype=None):
     """A contiguous vector of n elements (float32 unless dtype is given)."""
-    import torch
-    dtype = torch.float32 if dtype is None else dtype
-    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n:
-        raise ValueError(f"{what} must be {dtype} of shape ({n},), got {t.dtype} of "
-                         f"{tuple(t.shape)}")
+    if t.dtype is not (_torch.float32 if dtype is None else dtype) or t.shape != (n,):
+        raise ValueError(f"{what} must be {dtype or _torch.float32} of shape ({n},), got "
+                         f"{t.dtype} of {tuple(t.shape)}")
     if n > 1 and t.stride(0) != 1:
         raise ValueError(f"{what} must be contiguous")
 
 
-def _same_device(x, *ts):
-    if not x.is_cuda:
+def _device(x, *ts):
+    """The index of the one CUDA device that all tensors are on."""
+    index = x.get_device()
+    if index < 0:
         raise ValueError("tensors must be on a CUDA device")
     for t in ts:
-        if t is not None and t.device != x.device:
+        if t is not None and t.get_device() != index:
             raise ValueError("tensors must be on one CUDA device")
+    return index
 
 
-def _grad_like(x, grad_out):
-    if grad_out is None:
-        return None
-    if grad_out.dtype != x.dtype or grad_out.shape != x.shape:
+def _grad_stride(x, grad_out):
+    if grad_out.dtype is not x.dtype or grad_out.shape != x.shape:
         raise ValueError(f"grad_out must be {x.dtype} of shape {tuple(x.shape)}")
-    _rows(grad_out, "grad_out")
-    return grad_out
+    return _matrix(grad_out, "grad_out")[2]
 
 
-class _On:
-    """Allocations belong to the stream that the work runs on."""
-
-    def __init__(self, stream):
-        import torch
-        self.ctx = torch.cuda.stream(stream) if stream is not None else None
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+def _allocate(stream, make):
+    """make(), its allocations belonging to the stream that the work runs on."""
+    if stream is None:
+        return make()
+    with _torch.cuda.stream(stream):
+        return make()
 
 
 def _ptr(t):
@@ -160,37 +158,40 @@ def _ptr(t):
 # ------------------------------------------------------------ distillation
 def _distill(logits, top_values, top_indices, temperature, weights, losses, lse, grad, with_grad,
              backward, grad_losses, stream):
-    import torch
-    kind = _scores(logits, "logits")
-    top_kind = _scores(top_values, "top_values")
-    rows, cols = logits.shape
-    if top_values.shape[0] != rows or top_indices.shape != top_values.shape:
+    torch = _torch or _load()
+    kind, top_kind = _kind(logits, "logits"), _kind(top_values, "top_values")
+    rows, cols, stride = _matrix(logits, "logits")
+    top_rows, k, values_stride = _matrix(top_values, "top_values")
+    if top_rows != rows or top_indices.shape != (rows, k):
         raise ValueError("top_values and top_indices must both have shape (rows, k)")
-    _rows(top_indices, "top_indices")
-    k = top_values.shape[1]
+    indices_stride = _matrix(top_indices, "top_indices")[2]
     if not 1 <= k <= MAX_TOP:
         raise ValueError(f"1 to {MAX_TOP} top logits per row, got {k}")
     ib = _index_bytes(top_indices, "top_indices")
-    for t, what in ((weights, "weights"), (losses, "losses_out"), (grad_losses, "grad_losses"),
-                    (lse, "lse" if backward else "lse_out")):
-        if t is not None:
-            _vector(t, rows, what)
-    _grad_like(logits, grad)
-    _same_device(logits, top_values, top_indices, weights, losses, lse, grad, grad_losses)
-    with _On(stream):
-        if not backward:
-            if losses is None:
-                losses = torch.empty(rows, dtype=torch.float32, device=logits.device)
-            if lse is None:
-                lse = torch.empty(rows, dtype=torch.float32, device=logits.device)
-        if with_grad and grad is None:
-            grad = torch.empty((rows, cols), dtype=logits.dtype, device=logits.device)
-    args = DistillArgs(logits.data_ptr(), _stride(logits), rows, cols, top_values.data_ptr(),
-                       _stride(top_values), top_indices.data_ptr(), _stride(top_indices),
-                       _ptr(weights), _ptr(losses), _ptr(lse), _ptr(grad),
-                       _stride(grad) if with_grad else 0, kind, top_kind, ib, k, temperature)
+    if weights is not None:
+        _vector(weights, rows, "weights")
+    if losses is not None:
+        _vector(losses, rows, "losses_out")
+    if lse is not None:
+        _vector(lse, rows, "lse" if backward else "lse_out")
+    if grad_losses is not None:
+        _vector(grad_losses, rows, "grad_losses")
+    grad_stride = cols if grad is None else _grad_stride(logits, grad)
+    index = _device(logits, top_values, top_indices, weights, losses, lse, grad, grad_losses)
+
+    def make():
+        device = logits.device
+        stat = lse if lse is not None else torch.empty(rows, dtype=torch.float32, device=device)
+        return (losses if losses is not None or backward else torch.empty_like(stat), stat,
+                grad if grad is not None or not with_grad else
+                torch.empty((rows, cols), dtype=logits.dtype, device=device))
+
+    losses, lse, grad = make() if stream is None else _allocate(stream, make)
+    args = DistillArgs(logits.data_ptr(), stride, rows, cols, top_values.data_ptr(), values_stride,
+                       top_indices.data_ptr(), indices_stride, _ptr(weights), _ptr(losses),
+                       lse.data_ptr(), _ptr(grad), grad_stride, kind, top_kind, ib, k, temperature)
     lib = _lib_of()
-    s = _stream_of(logits, stream)
+    s = _raw_stream(index) if stream is None else stream.cuda_stream
     if backward:
         _check(lib.rs_distill_loss_backward(ctypes.byref(args), _ptr(grad_losses), s),
                "rs_distill_loss_backward")
@@ -235,40 +236,46 @@ def distill_loss_backward(grad_losses, logits, lse, top_values, top_indices,
 # ------------------------------------------------------------- policy loss
 def _policy(logits, actions, old, advantages, ref, clip_low, clip_high, kl_coef, temperature,
             weights, losses, logprobs, lse, grad, with_grad, backward, grad_losses, stream):
-    import torch
-    kind = _scores(logits, "logits")
-    rows, cols = logits.shape
+    torch = _torch or _load()
+    kind = _kind(logits, "logits")
+    rows, cols, stride = _matrix(logits, "logits")
     ib = _index_bytes(actions, "actions")
     _vector(actions, rows, "actions", actions.dtype)
     _vector(old, rows, "old_logprobs")
     _vector(advantages, rows, "advantages")
-    for t, what in ((ref, "ref_logprobs"), (weights, "weights"), (losses, "losses_out"),
-                    (logprobs, "logprobs_out"), (grad_losses, "grad_losses"),
-                    (lse, "lse" if backward else "lse_out")):
-        if t is not None:
-            _vector(t, rows, what)
-    if kl_coef != 0 and ref is None:
+    if ref is not None:
+        _vector(ref, rows, "ref_logprobs")
+    elif kl_coef != 0:
         raise ValueError("a KL term needs ref_logprobs")
-    _grad_like(logits, grad)
-    _same_device(logits, actions, old, advantages, ref, weights, losses, logprobs, lse, grad,
-                 grad_losses)
-    with _On(stream):
-        if not backward:
-            if losses is None:
-                losses = torch.empty(rows, dtype=torch.float32, device=logits.device)
-            if logprobs is None:
-                logprobs = torch.empty(rows, dtype=torch.float32, device=logits.device)
-            if lse is None:
-                lse = torch.empty(rows, dtype=torch.float32, device=logits.device)
-        if with_grad and grad is None:
-            grad = torch.empty((rows, cols), dtype=logits.dtype, device=logits.device)
-    args = PolicyArgs(logits.data_ptr(), _stride(logits), rows, cols, actions.data_ptr(),
-                      old.data_ptr(), advantages.data_ptr(), _ptr(ref), _ptr(weights),
-                      _ptr(losses), _ptr(logprobs), _ptr(lse), _ptr(grad),
-                      _stride(grad) if with_grad else 0, kind, ib, clip_low, clip_high, kl_coef,
-                      temperature)
+    if weights is not None:
+        _vector(weights, rows, "weights")
+    if losses is not None:
+        _vector(losses, rows, "losses_out")
+    if logprobs is not None:
+        _vector(logprobs, rows, "logprobs_out")
+    if lse is not None:
+        _vector(lse, rows, "lse" if backward else "lse_out")
+    if grad_losses is not None:
+        _vector(grad_losses, rows, "grad_losses")
+    grad_stride = cols if grad is None else _grad_stride(logits, grad)
+    index = _device(logits, actions, old, advantages, ref, weights, losses, logprobs, lse, grad,
+                    grad_losses)
+
+    def make():
+        device = logits.device
+        stat = lse if lse is not None else torch.empty(rows, dtype=torch.float32, device=device)
+        return (losses if losses is not None or backward else torch.empty_like(stat),
+                logprobs if logprobs is not None or backward else torch.empty_like(stat), stat,
+                grad if grad is not None or not with_grad else
+                torch.empty((rows, cols), dtype=logits.dtype, device=device))
+
+    losses, logprobs, lse, grad = make() if stream is None else _allocate(stream, make)
+    args = PolicyArgs(logits.data_ptr(), stride, rows, cols, actions.data_ptr(), old.data_ptr(),
+                      advantages.data_ptr(), _ptr(ref), _ptr(weights), _ptr(losses),
+                      _ptr(logprobs), lse.data_ptr(), _ptr(grad), grad_stride, kind, ib, clip_low,
+                      clip_high, kl_coef, temperature)
     lib = _lib_of()
-    s = _stream_of(logits, stream)
+    s = _raw_stream(index) if stream is None else stream.cuda_stream
     if backward:
         _check(lib.rs_policy_loss_backward(ctypes.byref(args), _ptr(grad_losses), s),
                "rs_policy_loss_backward")
@@ -320,6 +327,7 @@ def policy_loss_backward(grad_losses, logits, lse, actions, old_logprobs, advant
 
 
 # ------------------------------------------------------------ balance loss
+@functools.lru_cache(maxsize=256)
 def balance_temp_bytes(tokens: int, experts: int) -> int:
     """Scratch size of ``balance_loss`` and ``balance_loss_grad``."""
     out = ctypes.c_size_t(0)
@@ -329,46 +337,47 @@ def balance_temp_bytes(tokens: int, experts: int) -> int:
 
 
 def _mask(mask, tokens):
-    import torch
-    if mask is None:
-        return
-    if mask.dtype not in (torch.bool, torch.uint8) or tuple(mask.shape) != (tokens,):
+    if mask.dtype not in (_torch.bool, _torch.uint8) or mask.shape != (tokens,):
         raise ValueError(f"token_mask must be bool or uint8 of shape ({tokens},)")
     if tokens > 1 and mask.stride(0) != 1:
         raise ValueError("token_mask must be contiguous")
 
 
 def _balance(scores, ids, mask, scale, grad, with_grad, temp, stream):
-    import torch
-    kind = _scores(scores, "scores")
-    tokens, experts = scores.shape
+    torch = _torch or _load()
+    kind = _kind(scores, "scores")
+    tokens, experts, stride = _matrix(scores, "scores")
     if ids.dim() != 2 or ids.shape[0] != tokens or ids.shape[1] < 1:
         raise ValueError("expert_ids must have shape (tokens, k), k >= 1")
-    _rows(ids, "expert_ids")
+    _, k, ids_stride = _matrix(ids, "expert_ids")
     ib = _index_bytes(ids, "expert_ids")
     if not 1 <= experts <= MAX_EXPERTS:
         raise ValueError(f"1 to {MAX_EXPERTS} experts, got {experts}")
-    _mask(mask, tokens)
-    _grad_like(scores, grad)
-    _same_device(scores, ids, mask, grad, temp)
+    if mask is not None:
+        _mask(mask, tokens)
+    grad_stride = experts if grad is None else _grad_stride(scores, grad)
+    index = _device(scores, ids, mask, grad, temp)
     need = balance_temp_bytes(tokens, experts)
-    dev = scores.device
-    with _On(stream):
-        if temp is None:
-            temp = torch.empty(need, dtype=torch.uint8, device=dev)
-        loss = torch.empty((), dtype=torch.float32, device=dev)
-        mean = torch.empty(experts, dtype=torch.float32, device=dev)
-        counts = torch.empty(experts, dtype=torch.int32, device=dev)
-        n = torch.empty(1, dtype=torch.int32, device=dev)
-        if with_grad and grad is None:
-            grad = torch.empty((tokens, experts), dtype=scores.dtype, device=dev)
-    args = BalanceArgs(scores.data_ptr(), _stride(scores), tokens, ids.data_ptr(), _stride(ids),
-                       _ptr(mask), loss.data_ptr(), mean.data_ptr(), counts.data_ptr(),
-                       n.data_ptr(), _ptr(grad), _stride(grad) if with_grad else 0,
-                       temp.data_ptr(), temp.numel() * temp.element_size(), kind, experts, ib,
-                       ids.shape[1], scale)
-    _check(_lib_of().rs_balance_loss(ctypes.byref(args), _stream_of(scores, stream)),
-           "rs_balance_loss")
+
+    def make():
+        device = scores.device
+        return (temp if temp is not None or not need else
+                torch.empty(need, dtype=torch.uint8, device=device),
+                torch.empty((), dtype=torch.float32, device=device),
+                torch.empty(experts, dtype=torch.float32, device=device),
+                torch.empty(experts, dtype=torch.int32, device=device),
+                torch.empty(1, dtype=torch.int32, device=device),
+                grad if grad is not None or not with_grad else
+                torch.empty((tokens, experts), dtype=scores.dtype, device=device))
+
+    temp, loss, mean, counts, n, grad = make() if stream is None else _allocate(stream, make)
+    args = BalanceArgs(scores.data_ptr(), stride, tokens, ids.data_ptr(), ids_stride, _ptr(mask),
+                       loss.data_ptr(), mean.data_ptr(), counts.data_ptr(), n.data_ptr(),
+                       _ptr(grad), grad_stride, _ptr(temp),
+                       0 if temp is None else temp.numel() * temp.element_size(),
+                       kind, experts, ib, k, scale)
+    s = _raw_stream(index) if stream is None else stream.cuda_stream
+    _check(_lib_of().rs_balance_loss(ctypes.byref(args), s), "rs_balance_loss")
     return (loss, counts, mean, n, grad) if with_grad else (loss, counts, mean, n)
 
 
@@ -398,28 +407,28 @@ def balance_loss_backward(grad_loss, scores, counts, n_tokens, top_k: int, token
     """Gradient of grad_loss * loss in ``scores`` (``grad_loss``: one float32 on
     the device, None: 1), with the ``counts`` and ``n_tokens`` of the forward
     call, whose expert ids had ``top_k`` columns."""
-    import torch
-    kind = _scores(scores, "scores")
-    tokens, experts = scores.shape
+    torch = _torch or _load()
+    kind = _kind(scores, "scores")
+    tokens, experts, stride = _matrix(scores, "scores")
     if not 1 <= experts <= MAX_EXPERTS:
         raise ValueError(f"1 to {MAX_EXPERTS} experts, got {experts}")
     if top_k < 1:
         raise ValueError("top_k must be at least 1")
     _vector(counts, experts, "counts", torch.int32)
     _vector(n_tokens, 1, "n_tokens", torch.int32)
-    if grad_loss is not None and (grad_loss.dtype != torch.float32 or grad_loss.numel() != 1):
+    if grad_loss is not None and (grad_loss.dtype is not torch.float32 or grad_loss.numel() != 1):
         raise ValueError("grad_loss must be one float32")
-    _mask(token_mask, tokens)
-    _grad_like(scores, grad_out)
-    _same_device(scores, counts, n_tokens, grad_loss, token_mask, grad_out)
-    with _On(stream):
-        grad = grad_out if grad_out is not None else torch.empty(
-            (tokens, experts), dtype=scores.dtype, device=scores.device)
-    args = BalanceArgs(scores.data_ptr(), _stride(scores), tokens, None, 0, _ptr(token_mask),
-                       None, None, counts.data_ptr(), n_tokens.data_ptr(), grad.data_ptr(),
-                       _stride(grad), None, 0, kind, experts, 0, top_k, 1.0)
-    _check(_lib_of().rs_balance_loss_backward(ctypes.byref(args), _ptr(grad_loss),
-                                              _stream_of(scores, stream)),
+    if token_mask is not None:
+        _mask(token_mask, tokens)
+    grad_stride = experts if grad_out is None else _grad_stride(scores, grad_out)
+    index = _device(scores, counts, n_tokens, grad_loss, token_mask, grad_out)
+    grad = grad_out if grad_out is not None else _allocate(
+        stream, lambda: torch.empty((tokens, experts), dtype=scores.dtype, device=scores.device))
+    args = BalanceArgs(scores.data_ptr(), stride, tokens, None, 0, _ptr(token_mask), None, None,
+                       counts.data_ptr(), n_tokens.data_ptr(), grad.data_ptr(), grad_stride, None,
+                       0, kind, experts, 0, top_k, 1.0)
+    s = _raw_stream(index) if stream is None else stream.cuda_stream
+    _check(_lib_of().rs_balance_loss_backward(ctypes.byref(args), _ptr(grad_loss), s),
            "rs_balance_loss_backward")
     return grad
 
@@ -428,8 +437,7 @@ def balance_loss_backward(grad_loss, scores, counts, n_tokens, top_k: int, token
 def _wants_grad(x, stream, *outs):
     """Whether the call is recorded by autograd, which allocates the outputs and
     runs the backward call on the stream that was current in the forward one."""
-    import torch
-    if not (x.requires_grad and torch.is_grad_enabled()):
+    if not x.requires_grad or not (_torch or _load()).is_grad_enabled():
         return False
     if stream is not None or any(o is not None for o in outs):
         raise ValueError("outputs or a stream cannot be given for scores that require a "

@@ -129,8 +129,10 @@ def test_policy_refuses(lib, change):
     (dict(scores=None), 1), (dict(scores=BASE + 1), 1), (dict(expert_ids=None), 1),
     (dict(expert_ids=BASE + 0x100004), 1), (dict(loss=None), 1), (dict(mean_probs=None), 1),
     (dict(counts=None), 1), (dict(n_tokens=None), 1), (dict(grad_stride=63), 1),
-    (dict(grad=BASE + 2), 1), (dict(temp=None), 1), (dict(temp=BASE + 0x500010), 1),
-    (dict(temp_bytes=64), 2), (dict(scale=NAN), 1)])
+    (dict(grad=BASE + 2), 1), (dict(scale=NAN), 1),
+    (dict(tokens=1 << 20, grad=None, temp=None), 1),          # large calls need scratch
+    (dict(tokens=1 << 20, grad=None, temp=BASE + 0x500010), 1),
+    (dict(tokens=1 << 20, grad=None, temp_bytes=64), 2)])
 def test_balance_refuses(lib, change, status):
     assert lib.rs_balance_loss(ctypes.byref(balance_args(**change)), None) == status
 
@@ -161,4 +163,5 @@ def test_balance_scratch_size(lib):
     for bad in ((-1, 8), (10, 0), (10, 1025)):
         assert lib.rs_balance_temp_bytes(*bad, ctypes.byref(out)) == 1
     assert lib.rs_balance_temp_bytes(10, 8, None) == 1
-    assert rs.balance_temp_bytes(1 << 20, 1024) >= rs.balance_temp_bytes(10, 8) > 0
+    assert rs.balance_temp_bytes(10, 8) == 0
+    assert rs.balance_temp_bytes(1 << 20, 1024) > rs.balance_temp_bytes(1 << 20, 8) > 0
