@@ -381,45 +381,55 @@ __device__ __forceinline__ void cluster_sync() {
 }
 
 // A thread's vectors of a segment [begin, end): begin + tid, + kStreamThreads,
-// ...  Calls body(v, vectors) for batches of kStreamBatch of them, the next
-// batch's loads under way; vectors past the end are -inf.
-template <int TYPE, class F>
-__device__ __forceinline__ void stream_segment(const typename Score<TYPE>::Raw* x,
-                                               const RowVecs<TYPE>& vecs, int begin, int end,
-                                               int tid, F&& body) {
+// ..., in batches of kStreamBatch, the next batch's loads under way while one
+// is worked on; vectors past the end are -inf.
+template <int TYPE>
+struct Stream {
+  using Raw = typename Score<TYPE>::Raw;
   using V = ScoreVec<TYPE>;
-  const uint4* xv = reinterpret_cast<const uint4*>(x - vecs.lead);
-  constexpr int kStep = kStreamThreads * kStreamBatch;
-  const int inner_end = min(end, vecs.whole_end());
-  auto load = [&](int v0, uint4 (&r)[kStreamBatch]) {
+  static constexpr int kStep = kStreamThreads * kStreamBatch;
+  const Raw* x;
+  const RowVecs<TYPE>& vecs;
+  const int end;
+  int v;
+  uint4 r[kStreamBatch];
+
+  __device__ __forceinline__ Stream(const Raw* x_, const RowVecs<TYPE>& vecs_, int begin, int end_,
+                                    int tid)
+      : x(x_), vecs(vecs_), end(end_), v(begin + tid) {
+    if (v < end) load(v, r);
+  }
+  __device__ __forceinline__ void load(int v0, uint4 (&to)[kStreamBatch]) const {
+    const uint4* xv = reinterpret_cast<const uint4*>(x - vecs.lead);
     const int v1 = v0 + (kStreamBatch - 1) * kStreamThreads;
-    if (v0 >= vecs.whole_begin() && v1 < inner_end) {
+    if (v0 >= vecs.whole_begin() && v1 < min(end, vecs.whole_end())) {
 #pragma unroll
-      for (int u = 0; u < kStreamBatch; ++u) r[u] = __ldcs(xv + v0 + u * kStreamThreads);
+      for (int u = 0; u < kStreamBatch; ++u) to[u] = __ldcs(xv + v0 + u * kStreamThreads);
     } else {
 #pragma unroll
       for (int u = 0; u < kStreamBatch; ++u) {
-        const int v = v0 + u * kStreamThreads;
-        if (v >= end)
-          r[u] = make_uint4(V::kMinusInf, V::kMinusInf, V::kMinusInf, V::kMinusInf);
-        else if (vecs.whole(v))
-          r[u] = __ldcs(xv + v);
+        const int w = v0 + u * kStreamThreads;
+        if (w >= end)
+          to[u] = make_uint4(V::kMinusInf, V::kMinusInf, V::kMinusInf, V::kMinusInf);
+        else if (vecs.whole(w))
+          to[u] = __ldcs(xv + w);
         else
-          r[u] = vecs.load_edge(x, v);
+          to[u] = vecs.load_edge(x, w);
       }
     }
-  };
-  uint4 r[kStreamBatch], ahead[kStreamBatch];
-  int v = begin + tid;
-  if (v >= end) return;
-  load(v, r);
-  for (; v < end; v += kStep) {
-    if (v + kStep < end) load(v + kStep, ahead);
-    body(v, r);
-#pragma unroll
-    for (int u = 0; u < kStreamBatch; ++u) r[u] = ahead[u];
   }
-}
+  // body(v, vectors) for every batch
+  template <class F>
+  __device__ __forceinline__ void run(F&& body) {
+    uint4 ahead[kStreamBatch];
+    for (; v < end; v += kStep) {
+      if (v + kStep < end) load(v + kStep, ahead);
+      body(v, r);
+#pragma unroll
+      for (int u = 0; u < kStreamBatch; ++u) r[u] = ahead[u];
+    }
+  }
+};
 
 template <int TYPE, int OP>
 __global__ void __launch_bounds__(kStreamThreads + kWarp, LSDRS_STREAM_CTAS)
@@ -450,8 +460,8 @@ __global__ void __launch_bounds__(kStreamThreads + kWarp, LSDRS_STREAM_CTAS)
     const int per = (vecs.count + split - 1) / split;
     const int begin = min(rank * per, vecs.count), end = min(begin + per, vecs.count);
     RunningSoftmax<TYPE> run(scale2);
-    stream_segment<TYPE>(x, vecs, begin, end, tid,
-                         [&](int, const uint4(&r)[kStreamBatch]) { run.add(r); });
+    Stream<TYPE> stream(x, vecs, begin, end, tid);
+    stream.run([&](int, const uint4(&r)[kStreamBatch]) { run.add(r); });
     const Softmax s = warp_join(run.result(), scale2);
     if (lane == 0) part[warp] = s;
   }
@@ -510,6 +520,8 @@ __global__ void __launch_bounds__(kStreamThreads + kWarp, LSDRS_STREAM_CTAS)
   const bool off = row_off<OP>(a, row);
   if (warp == kStreamWarps && !off)
     load_targets<TYPE, OP, kLossBwd>(a, row, t, reinterpret_cast<int*>(t.x + a.k), &head);
+  // the first loads are under way before the targets are known
+  Stream<TYPE> stream(x, vecs, begin, off || warp == kStreamWarps ? begin : end, tid);
   const float m = off ? 0.0f : a.lse[row] * a.tau;
   __syncthreads();
   const float c = off ? 0.0f : row_result<OP, kLossBwd>(a, head, m, 1.0f).c;
@@ -521,7 +533,7 @@ __global__ void __launch_bounds__(kStreamThreads + kWarp, LSDRS_STREAM_CTAS)
     } else {
       const Exponent e(o, scale2);
       const uint64_t f = pack2(c * e.mend, c * e.mend);
-      stream_segment<TYPE>(x, vecs, begin, end, tid, [&](int v, uint4(&r)[kStreamBatch]) {
+      stream.run([&](int v, uint4(&r)[kStreamBatch]) {
 #pragma unroll
         for (int u = 0; u < kStreamBatch; ++u) r[u] = vec_grad<TYPE>(r[u], e, f);
         put(v, r);
@@ -557,13 +569,25 @@ __global__ void __launch_bounds__(kStreamThreads + kWarp, LSDRS_STREAM_CTAS)
 // another, by cancelling their launch (cluster launch control).  One thread
 // per CTA (the scheduler) does so a few rows ahead and hands the answers to
 // the other warps.
+#ifndef LSDRS_RING_OVER
+#define LSDRS_RING_OVER 2
+#endif
+#ifndef LSDRS_RING_AHEAD
+#define LSDRS_RING_AHEAD 1
+#endif
+#ifndef LSDRS_RING_MODES
+#define LSDRS_RING_MODES 2
+#endif
 #ifndef LSDRS_ROW_CONSUMERS
 #define LSDRS_ROW_CONSUMERS 512
-#define LSDRS_ROW_UNITS 2
+#define LSDRS_ROW_UNITS 4
 #endif
 constexpr int kRowConsumers = LSDRS_ROW_CONSUMERS;
 constexpr int kRowWarps = kRowConsumers / kWarp;
-constexpr int kTargetWarps = 2;
+#ifndef LSDRS_TARGET_WARPS
+#define LSDRS_TARGET_WARPS 2
+#endif
+constexpr int kTargetWarps = LSDRS_TARGET_WARPS;
 constexpr int kProducerWarp = kRowWarps, kSchedulerWarp = kRowWarps + 1,
               kFirstTargetWarp = kRowWarps + 2;
 constexpr int kRowThreads = kRowConsumers + (2 + kTargetWarps) * kWarp;
@@ -571,6 +595,7 @@ constexpr int kChunkUnits = LSDRS_ROW_UNITS;                  // vectors per thr
 constexpr int kChunkVecs = kRowConsumers * kChunkUnits;
 constexpr int kChunkBytes = kChunkVecs * 16;
 constexpr int kMaxSlots = 13 * 16384 / kChunkBytes;           // most ring slots
+constexpr int kMaxHeads = 4;                                  // rows whose targets are held
 constexpr int kAheadRows = 4;                                 // rows that the scheduler is ahead
 constexpr int kRowReaders = kRowWarps + 1 + kTargetWarps;     // warps that read its list
 constexpr uint64_t kRowWaitNs = 2000000000ull;
@@ -582,21 +607,24 @@ struct RowShared {
   uint64_t unit_full[kAheadRows], unit_empty[kAheadRows];
   int unit[kAheadRows];                                       // the rows taken over
   uint64_t full[kMaxSlots], empty[kMaxSlots];
-  uint64_t head_full[kTargetWarps], head_empty[kTargetWarps];
+  uint64_t head_full[kMaxHeads], head_empty[kMaxHeads];
   uint64_t together;                                          // all consumer warps
   uint64_t peers;                                             // exchange of the CTAs' softmaxes
   Softmax part[2][kRowWarps];
   Softmax peer[2][kMaxCluster];
-  Head head[kTargetWarps];
+  Head head[kMaxHeads];
   int failed;                                                 // a wait ran out of time
 };
 
-__host__ __device__ constexpr inline size_t row_targets_bytes(int k) {
-  return align_up(static_cast<size_t>(k) * 12 + static_cast<size_t>(target_slots(k)) * 4, 16);
+// Rows whose targets are held at a time, their lists, and a table per target
+// warp.
+__host__ __device__ constexpr inline int row_heads(int k) { return k <= 256 ? kMaxHeads : 2; }
+__host__ __device__ constexpr inline size_t row_list_bytes(int k) {
+  return align_up(static_cast<size_t>(k) * 12, 16);
 }
 __host__ constexpr inline size_t row_ring_smem(int k, int slots) {
   return static_cast<size_t>(slots) * kChunkBytes + align_up(sizeof(RowShared), 16) +
-         kTargetWarps * row_targets_bytes(k);
+         row_heads(k) * row_list_bytes(k) + static_cast<size_t>(kTargetWarps) * target_slots(k) * 4;
 }
 // As many slots as fit beside the lists of k entries.
 constexpr size_t kMaxSmem = 232448;
@@ -722,11 +750,12 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_ring_kernel(const Row
   unsigned char* lists = reinterpret_cast<unsigned char*>(sh) + align_up(sizeof(RowShared), 16);
   auto targets = [&](int i) {
     Targets t;
-    t.col = reinterpret_cast<int*>(lists + i * row_targets_bytes(a.k));
+    t.col = reinterpret_cast<int*>(lists + i * row_list_bytes(a.k));
     t.p = reinterpret_cast<float*>(t.col + a.k);
     t.x = t.p + a.k;
     return t;
   };
+  const int heads = row_heads(a.k);
   const int tid = static_cast<int>(threadIdx.x), warp = tid / kWarp;
   const int lane = static_cast<int>(lane_id());
   // kLossBwd has nothing to exchange: its CTAs are launched without clusters,
@@ -734,13 +763,13 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_ring_kernel(const Row
   const bool clustered = MODE != kLossBwd && split > 1;
   // vectors per CTA, whatever the row's first address
   const int per = (static_cast<int>(a.cols + 2 * (V::kCount - 1)) / V::kCount + split - 1) / split;
-  const int keep_slots = ring_slots - 2;  // chunks of a row that stay for the second pass
+  const int keep_slots = ring_slots - LSDRS_RING_AHEAD;  // chunks of a row that stay for the second pass
   if (tid == 0) {
     for (int i = 0; i < ring_slots; ++i) {
       mbar_init(&sh->full[i], 1);
       mbar_init(&sh->empty[i], kRowWarps);
     }
-    for (int i = 0; i < kTargetWarps; ++i) {
+    for (int i = 0; i < heads; ++i) {
       mbar_init(&sh->head_full[i], 1);
       mbar_init(&sh->head_empty[i], kRowWarps);
     }
@@ -868,21 +897,19 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_ring_kernel(const Row
       }
     }
   } else if (warp >= kFirstTargetWarp) {  // every kTargetWarps-th row each
-    const int mine = warp - kFirstTargetWarp;
-    uint32_t use = 0;
+    int* table = reinterpret_cast<int*>(lists + heads * row_list_bytes(a.k)) +
+                 (warp - kFirstTargetWarp) * target_slots(a.k);
     Way way{0, 0};
-    int turn = 0;
-    for (int unit = first_unit; unit >= 0; unit = next_unit(way)) {
-      const bool skip = turn != mine;
-      turn = turn + 1 == kTargetWarps ? 0 : turn + 1;
-      if (skip) continue;
-      if (use > 0 && !warp_wait(&sh->head_empty[mine], (use - 1) & 1, &sh->failed)) break;
-      const Targets t = targets(mine);
-      load_targets<TYPE, OP, MODE>(a, unit / split, t, reinterpret_cast<int*>(t.x + a.k),
-                                   &sh->head[mine]);
+    uint32_t n = 0;  // the row's number in this CTA
+    for (int unit = first_unit; unit >= 0; unit = next_unit(way), ++n) {
+      if (static_cast<int>(n % kTargetWarps) != warp - kFirstTargetWarp) continue;
+      const int i = n % heads;
+      if (n >= static_cast<uint32_t>(heads) &&
+          !warp_wait(&sh->head_empty[i], (n / heads - 1) & 1, &sh->failed))
+        break;
+      load_targets<TYPE, OP, MODE>(a, unit / split, targets(i), table, &sh->head[i]);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->head_full[mine]);
-      ++use;
+      if (lane == 0) mbar_arrive(&sh->head_full[i]);
     }
   } else {  // ---- consumers
     const float scale2 = a.inv_tau * kLog2e;
@@ -927,7 +954,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_ring_kernel(const Row
       const Head h = sh->head[hi];
       const Targets t = targets(hi);
       const int head_slot = hi;
-      if (++hi == kTargetWarps) {
+      if (++hi == heads) {
         hi = 0;
         head_phase ^= 1;
       }
@@ -1118,15 +1145,19 @@ cudaError_t launch_stream(const RowLossArgs& a, int split, size_t smem, cudaStre
   }
 }
 
-template <int TYPE, int OP>
+template <int TYPE, int OP, int MODE>
 cudaError_t launch_ring(const RowLossArgs& a, int sms, int64_t bytes, cudaStream_t s) {
   const int slots = row_ring_slots(a.k);
   int split = 1;
-  while (split < 8 && bytes > int64_t(split) * (slots - 2) * kChunkBytes) split *= 2;
+  if (MODE == kLossGrad)
+    while (split < 8 && bytes > int64_t(split) * slots * kChunkBytes * LSDRS_RING_OVER) split *= 2;
   while (split < kMaxCluster && a.rows * split * 2 <= sms && bytes >= int64_t(split) * 2 * 8192)
     split *= 2;
+  // over its own logits the backward call of the policy loss must not write a
+  // segment before every segment has read the action's score
+  if (MODE == kLossBwd && OP == kOpPolicy && a.grad == a.logits) split = 1;
   while (a.rows * split >= (int64_t(1) << 31)) split /= 2;  // CTA numbers are 31 bits
-  auto kern = row_loss_ring_kernel<TYPE, OP, kLossGrad>;
+  auto kern = row_loss_ring_kernel<TYPE, OP, MODE>;
   const size_t smem = row_ring_smem(a.k, slots);
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow(kern, true, true, &done);
@@ -1138,7 +1169,7 @@ cudaError_t launch_ring(const RowLossArgs& a, int sms, int64_t bytes, cudaStream
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   cfg.attrs = attr;
-  cfg.numAttrs = add_attributes(attr, split);
+  cfg.numAttrs = add_attributes(attr, MODE == kLossBwd ? 1 : split);
   return cudaLaunchKernelEx(&cfg, kern, a, split, slots, a.rows * split > sms);
 }
 
@@ -1156,7 +1187,7 @@ cudaError_t launch_row_loss_as(const RowLossArgs& a, cudaStream_t s) {
     return launch_kernel(row_loss_short_kernel<TYPE, OP, MODE, 256, 8>,
                          dim3(static_cast<unsigned>(a.rows)), dim3(256), lists, s, a);
   const int sms = device_sm_count();
-  if constexpr (MODE != kLossGrad) {
+  if constexpr (MODE != kLossGrad && !((LSDRS_RING_MODES >> MODE) & 1)) {
     // segments of at least 16 KB, until there are two for every place
     int split = 1;
     while (split < kMaxCluster &&
@@ -1169,7 +1200,7 @@ cudaError_t launch_row_loss_as(const RowLossArgs& a, cudaStream_t s) {
     while (a.rows * split >= (int64_t(1) << 31)) split /= 2;  // CTA numbers are 31 bits
     return launch_stream<TYPE, OP, MODE>(a, split, lists, s);
   } else {
-    return launch_ring<TYPE, OP>(a, sms, bytes, s);
+    return launch_ring<TYPE, OP, MODE>(a, sms, bytes, s);
   }
 }
 
