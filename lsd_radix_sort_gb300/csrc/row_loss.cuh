@@ -551,52 +551,43 @@ __global__ void __launch_bounds__(kStreamThreads + kWarp, LSDRS_STREAM_CTAS)
   }
 }
 
-// ----------------------------------------------------------------- long rows
-// A row is shared by the `split` CTAs of a cluster (1: a CTA of its own), each
-// of which takes a contiguous segment of it in chunks of 16 KB.  One warp (the
-// producer) copies the chunks of row after row by TMA bulk copies into a ring
-// of shared-memory slots, as far ahead as slots are free; two warps read the
-// next rows' targets; 16 warps go over the row's chunks twice: once for the
-// maximum and the sum, and, after the CTAs have exchanged theirs through
-// distributed shared memory, once more, out of the same slots, to write the
-// gradient, freeing the slots for the next rows.  So a row is read from
-// memory once, as long as its segments fit into the ring; what does not fit
-// is copied a second time (from L2, mostly).
+// ------------------------------------- long rows, losses and gradient at once
+// One CTA holds a row: a producer warp copies it by TMA bulk copies, in chunks
+// of 32 KB, into a ring of shared-memory slots, row after row, as far ahead as
+// slots are free; two warps read the next rows' targets; 16 warps go over the
+// row's chunks twice: once for the maximum and the sum, and once more to write
+// the gradient, freeing the slots for the next row.  All but one of the ring's
+// slots may hold chunks of the row between the two passes (160 KB; the other
+// is what the copies go on through); what does not fit is copied again, from
+// L2.  So memory is read once, and the copies never stop for the arithmetic.
+//
+// Rows of more than twice the ring, and rows too few for the SMs, are shared
+// by the `split` CTAs of a cluster, which exchange maxima and sums through
+// distributed shared memory.  That exchange costs more than the second copy
+// from L2: bf16 rows of 131,072 took 443 us for 4,096 rows as clusters of two
+// that keep everything, 326 us as single CTAs that copy 96 of 256 KB again.
+// Chunks of 16 KB, every wait and release twice as often, took 361 us for
+// 8,192 rows of 65,536 instead of 339; per-warp rings of 2 KB copies 437,
+// per-thread cp.async rings 434.
 //
 // Rows cost unequally (a masked row is not read), so they are not dealt out
 // beforehand: the grid has a CTA (cluster) per row, and a running one takes
 // over the rows of CTAs that have not been launched yet, one row after
 // another, by cancelling their launch (cluster launch control).  One thread
-// per CTA (the scheduler) does so a few rows ahead and hands the answers to
-// the other warps.
-#ifndef LSDRS_RING_OVER
-#define LSDRS_RING_OVER 2
-#endif
-#ifndef LSDRS_RING_AHEAD
-#define LSDRS_RING_AHEAD 1
-#endif
-#ifndef LSDRS_RING_MODES
-#define LSDRS_RING_MODES 2
-#endif
-#ifndef LSDRS_ROW_CONSUMERS
-#define LSDRS_ROW_CONSUMERS 512
-#define LSDRS_ROW_UNITS 4
-#endif
-constexpr int kRowConsumers = LSDRS_ROW_CONSUMERS;
+// per CTA (the scheduler) does so a few rows ahead and lists them for the
+// other warps.
+constexpr int kRowConsumers = 512;
 constexpr int kRowWarps = kRowConsumers / kWarp;
-#ifndef LSDRS_TARGET_WARPS
-#define LSDRS_TARGET_WARPS 2
-#endif
-constexpr int kTargetWarps = LSDRS_TARGET_WARPS;
+constexpr int kTargetWarps = 2;
 constexpr int kProducerWarp = kRowWarps, kSchedulerWarp = kRowWarps + 1,
               kFirstTargetWarp = kRowWarps + 2;
 constexpr int kRowThreads = kRowConsumers + (2 + kTargetWarps) * kWarp;
-constexpr int kChunkUnits = LSDRS_ROW_UNITS;                  // vectors per thread and chunk
+constexpr int kChunkUnits = 4;                                // vectors per thread and chunk
 constexpr int kChunkVecs = kRowConsumers * kChunkUnits;
 constexpr int kChunkBytes = kChunkVecs * 16;
-constexpr int kMaxSlots = 13 * 16384 / kChunkBytes;           // most ring slots
+constexpr int kMaxSlots = 6;                                  // most ring slots
 constexpr int kMaxHeads = 4;                                  // rows whose targets are held
-constexpr int kAheadRows = 4;                                 // rows that the scheduler is ahead
+constexpr int kAheadRows = 8;                                 // rows that the scheduler is ahead
 constexpr int kRowReaders = kRowWarps + 1 + kTargetWarps;     // warps that read its list
 constexpr uint64_t kRowWaitNs = 2000000000ull;
 
@@ -604,8 +595,9 @@ constexpr uint64_t kRowWaitNs = 2000000000ull;
 struct RowShared {
   uint4 answer[2];                                            // of cluster launch control
   uint64_t answer_full[2], answer_empty[2];
-  uint64_t unit_full[kAheadRows], unit_empty[kAheadRows];
-  int unit[kAheadRows];                                       // the rows taken over
+  uint64_t row_full[kAheadRows], row_empty[kAheadRows];
+  int row[kAheadRows];                                        // the rows to take, -1: no more
+  int row_off[kAheadRows];                                    // those that are not read
   uint64_t full[kMaxSlots], empty[kMaxSlots];
   uint64_t head_full[kMaxHeads], head_empty[kMaxHeads];
   uint64_t together;                                          // all consumer warps
@@ -616,8 +608,9 @@ struct RowShared {
   int failed;                                                 // a wait ran out of time
 };
 
-// Rows whose targets are held at a time, their lists, and a table per target
-// warp.
+// Rows whose targets are held at a time (with two, 64 targets a row took 387
+// us for 8,192 rows of 65,536 instead of 337; long lists leave no room for
+// four), their lists, and a table per target warp.
 __host__ __device__ constexpr inline int row_heads(int k) { return k <= 256 ? kMaxHeads : 2; }
 __host__ __device__ constexpr inline size_t row_list_bytes(int k) {
   return align_up(static_cast<size_t>(k) * 12, 16);
@@ -736,11 +729,10 @@ __device__ __forceinline__ int next_cta(const uint4* answer) {
   return ok != 0 ? static_cast<int>(x) : -1;
 }
 
-template <int TYPE, int OP, int MODE>
-__global__ void __launch_bounds__(kRowThreads, 1) row_loss_ring_kernel(const RowLossArgs a,
-                                                                    const int split,
-                                                                    const int ring_slots,
-                                                                    const bool steal) {
+template <int TYPE, int OP>
+__global__ void __launch_bounds__(kRowThreads, 1)
+    row_loss_ring_kernel(const RowLossArgs a, const int split, const int ring_slots,
+                         const bool steal) {
   using S = Score<TYPE>;
   using Raw = typename S::Raw;
   using V = ScoreVec<TYPE>;
@@ -758,12 +750,9 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_ring_kernel(const Row
   const int heads = row_heads(a.k);
   const int tid = static_cast<int>(threadIdx.x), warp = tid / kWarp;
   const int lane = static_cast<int>(lane_id());
-  // kLossBwd has nothing to exchange: its CTAs are launched without clusters,
-  // one per segment of a row
-  const bool clustered = MODE != kLossBwd && split > 1;
+  const int rank = static_cast<int>(blockIdx.x) % split;  // in the cluster
   // vectors per CTA, whatever the row's first address
   const int per = (static_cast<int>(a.cols + 2 * (V::kCount - 1)) / V::kCount + split - 1) / split;
-  const int keep_slots = ring_slots - LSDRS_RING_AHEAD;  // chunks of a row that stay for the second pass
   if (tid == 0) {
     for (int i = 0; i < ring_slots; ++i) {
       mbar_init(&sh->full[i], 1);
@@ -775,75 +764,68 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_ring_kernel(const Row
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh->answer_full[i], 1);
-      mbar_init(&sh->answer_empty[i], clustered ? split : 1);
+      mbar_init(&sh->answer_empty[i], split);
     }
     for (int i = 0; i < kAheadRows; ++i) {
-      mbar_init(&sh->unit_full[i], 1);
-      mbar_init(&sh->unit_empty[i], kRowReaders);
+      mbar_init(&sh->row_full[i], 1);
+      mbar_init(&sh->row_empty[i], kRowReaders);
     }
     mbar_init(&sh->together, kRowWarps);
     mbar_init(&sh->peers, split);
     sh->failed = 0;
   }
-  if (clustered)
+  if (split > 1)
     cluster_sync();
   else
     __syncthreads();
   grid_dependency_sync();
 
-  // One warp's way through the units (a row's segment each): its own first,
-  // then those that the scheduler took over.
+  // One warp's way through the scheduler's list: the next row, or -1.
   struct Way {
     int slot;
     uint32_t phase;
+    bool off;  // the row is not read
   };
-  auto next_unit = [&](Way& way) {
-    if (!steal) return -1;
-    const bool ok = warp_wait(&sh->unit_full[way.slot], way.phase, &sh->failed);
-    const int unit = ok ? sh->unit[way.slot] : -1;
+  auto next_row = [&](Way& way) {
+    const bool ok = warp_wait(&sh->row_full[way.slot], way.phase, &sh->failed);
+    const int row = ok ? sh->row[way.slot] : -1;
+    way.off = sh->row_off[way.slot] != 0;
     __syncwarp();
-    if (lane == 0) mbar_arrive(&sh->unit_empty[way.slot]);
+    if (lane == 0) mbar_arrive(&sh->row_empty[way.slot]);
     if (++way.slot == kAheadRows) {
       way.slot = 0;
       way.phase ^= 1;
     }
-    return unit;
+    return row;
   };
-  const int first_unit = static_cast<int>(blockIdx.x);
-  const int cluster_rank = first_unit % split;
-  auto rank_of = [&](int unit) { return clustered ? cluster_rank : unit % split; };
-
+  // This CTA's segment of a row: vectors [begin, end), in chunks, the last
+  // `keep` of which stay in the ring for the second pass.
   struct Segment {
     const Raw* x;
     RowVecs<TYPE> vecs;
     int begin, end, chunks, keep;
   };
-  auto segment = [&](int unit) {
-    const int64_t row = unit / split;
-    const int rank = rank_of(unit);
+  auto segment = [&](int64_t row) {
     const Raw* x = static_cast<const Raw*>(a.logits) + row * a.stride;
     Segment s{x, RowVecs<TYPE>(x, static_cast<int>(a.cols)), 0, 0, 0, 0};
     s.begin = min(rank * per, s.vecs.count);
     s.end = min(s.begin + per, s.vecs.count);
     s.chunks = (s.end - s.begin + kChunkVecs - 1) / kChunkVecs;
-    s.keep = MODE == kLossGrad ? min(s.chunks, keep_slots) : 0;
+    s.keep = min(s.chunks, ring_slots - 1);
     return s;
   };
 
   if (warp == kProducerWarp) {
     int slot = 0;
     uint32_t use = 0;  // times round the ring
-    Way way{0, 0};
-    int unit = first_unit;
-    bool off = row_off<OP>(a, unit / split);
-    while (unit >= 0) {
-      const int next = next_unit(way);
-      const bool next_off = next >= 0 && row_off<OP>(a, next / split);
-      if (!off && lane == 0) {
-        const Segment s = segment(unit);
-        const int loads = MODE == kLossGrad ? 2 * s.chunks - s.keep : s.chunks;
+    Way way{0, 0, false};
+    for (int row; (row = next_row(way)) >= 0;) {
+      if (way.off) continue;
+      if (lane == 0) {
+        const Segment s = segment(row);
         const uint4* xv = reinterpret_cast<const uint4*>(s.x - s.vecs.lead);
-        for (int i = 0; i < loads; ++i) {
+        // every chunk, then those that do not stay once more
+        for (int i = 0; i < 2 * s.chunks - s.keep; ++i) {
           if (use > 0 && !row_wait(&sh->empty[slot], (use - 1) & 1, &sh->failed)) break;
           const int first = s.begin + (i < s.chunks ? i : i - s.chunks) * kChunkVecs;
           const int b = max(first, s.vecs.whole_begin());
@@ -860,63 +842,64 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_ring_kernel(const Row
         }
       }
       __syncwarp();
-      if (sh->failed) break;
-      unit = next;
-      off = next_off;
     }
     if (sh->failed && lane == 0)  // copies in flight end before the CTA does
       for (int i = 0; i < ring_slots; ++i)
         if (i < slot || use > 0)
           mbar_wait_bounded(&sh->full[i], (i < slot ? use : use - 1) & 1, kCopyDrainNs);
   } else if (warp == kSchedulerWarp) {
-    if (lane == 0 && steal) {
-      // The cluster's first CTA asks, and not before the last answer was a
-      // success; every CTA arms its own barrier for the shared answer and
-      // tells the first CTA when it has read it.
-      const bool asks = !clustered || cluster_rank == 0;
-      int unit = 0;
-      for (uint32_t n = 0; unit >= 0; ++n) {
+    if (lane == 0) {
+      // The cluster's first CTA asks for the next launch to cancel, and not
+      // before the last answer was a success; every CTA arms its own barrier
+      // for the shared answer and tells the first CTA when it has read it.
+      int row = static_cast<int>(blockIdx.x) / split;
+      for (uint32_t n = 0;; ++n) {
+        const int at = n % kAheadRows;
+        const int off = row >= 0 && row_off<OP>(a, row);
+        if (n >= kAheadRows &&
+            !row_wait(&sh->row_empty[at], (n / kAheadRows - 1) & 1, &sh->failed))
+          break;
+        sh->row[at] = row;
+        sh->row_off[at] = off;
+        mbar_arrive(&sh->row_full[at]);
+        if (row < 0) break;
+        row = -1;
+        if (!steal) continue;
         const int s = n & 1;
-        if (asks && n >= 2 &&
+        if (rank == 0 && n >= 2 &&
             !row_wait_cluster(&sh->answer_empty[s], ((n >> 1) - 1) & 1, &sh->failed))
           break;
         mbar_arrive_expect_tx(&sh->answer_full[s], 16);
-        if (asks) ask_next(&sh->answer[s], &sh->answer_full[s], clustered);
+        if (rank == 0) ask_next(&sh->answer[s], &sh->answer_full[s], split > 1);
         if (!row_wait(&sh->answer_full[s], (n >> 1) & 1, &sh->failed)) break;
-        unit = next_cta(&sh->answer[s]);
-        if (clustered)
+        const int cta = next_cta(&sh->answer[s]);
+        if (cta >= 0) row = cta / split;
+        if (split > 1)
           mbar_arrive_cluster(peer_addr(smem_addr(&sh->answer_empty[s]), 0));
         else
           mbar_arrive(&sh->answer_empty[s]);
-        const int at = n % kAheadRows;
-        if (n >= kAheadRows &&
-            !row_wait(&sh->unit_empty[at], (n / kAheadRows - 1) & 1, &sh->failed))
-          break;
-        sh->unit[at] = unit;
-        mbar_arrive(&sh->unit_full[at]);
       }
     }
   } else if (warp >= kFirstTargetWarp) {  // every kTargetWarps-th row each
     int* table = reinterpret_cast<int*>(lists + heads * row_list_bytes(a.k)) +
                  (warp - kFirstTargetWarp) * target_slots(a.k);
-    Way way{0, 0};
-    uint32_t n = 0;  // the row's number in this CTA
-    for (int unit = first_unit; unit >= 0; unit = next_unit(way), ++n) {
-      if (static_cast<int>(n % kTargetWarps) != warp - kFirstTargetWarp) continue;
-      const int i = n % heads;
-      if (n >= static_cast<uint32_t>(heads) &&
-          !warp_wait(&sh->head_empty[i], (n / heads - 1) & 1, &sh->failed))
-        break;
-      load_targets<TYPE, OP, MODE>(a, unit / split, targets(i), table, &sh->head[i]);
+    Way way{0, 0, false};
+    uint32_t n = 0;  // the row's number among those of this CTA that are read
+    for (int row; (row = next_row(way)) >= 0;) {
+      if (way.off) continue;
+      const uint32_t i = n % heads, use = n / heads;
+      if (static_cast<int>(n++ % kTargetWarps) != warp - kFirstTargetWarp) continue;
+      if (use > 0 && !warp_wait(&sh->head_empty[i], (use - 1) & 1, &sh->failed)) break;
+      load_targets<TYPE, OP, kLossGrad>(a, row, targets(i), table, &sh->head[i]);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->head_full[i]);
     }
   } else {  // ---- consumers
     const float scale2 = a.inv_tau * kLog2e;
     int slot = 0, hi = 0;
-    uint32_t phase = 0, head_phase = 0, peer_phase = 0, together_phase = 0;
-    // the chunk's vector u of this thread, from its slot (or, at an edge of
-    // the row, score by score from memory)
+    uint32_t phase = 0, head_phase = 0, parity = 0;  // parity: of the rows read
+    // a chunk's vectors of this thread, from their slot (or, at an edge of the
+    // row, score by score from memory)
     auto fetch = [&](const Segment& s, int at, int first, bool inner, uint4 (&r)[kChunkUnits]) {
       const uint4* from = reinterpret_cast<const uint4*>(ring + at * kChunkBytes) + tid;
       if (inner) {
@@ -935,34 +918,13 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_ring_kernel(const Row
           r[u] = s.vecs.load_edge(s.x, v);
       }
     };
-    // every consumer warp has come here (a bounded wait, unlike bar.sync)
-    auto together = [&] {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->together);
-      warp_wait(&sh->together, together_phase, &sh->failed);
-      together_phase ^= 1;
-    };
     auto release = [&](int at) {
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->empty[at]);
     };
-    Way way{0, 0};
-    for (int unit = first_unit; unit >= 0; unit = next_unit(way)) {
-      const int64_t row = unit / split;
-      const int rank = rank_of(unit);
-      const bool got_head = warp_wait(&sh->head_full[hi], head_phase, &sh->failed);
-      const Head h = sh->head[hi];
-      const Targets t = targets(hi);
-      const int head_slot = hi;
-      if (++hi == heads) {
-        hi = 0;
-        head_phase ^= 1;
-      }
-      const Segment s = segment(unit);
-      // chunks [inner0, inner1) lie in the segment and inside the row entirely
-      const int inner0 = s.begin < s.vecs.whole_begin();
-      const int inner1 = max(inner0, (min(s.end, s.vecs.whole_end()) - s.begin) / kChunkVecs);
-      const int early = s.chunks - s.keep;  // chunks that do not stay
+    Way way{0, 0, false};
+    for (int row; (row = next_row(way)) >= 0;) {
+      const Segment s = segment(row);
       Raw* g = static_cast<Raw*>(a.grad) + row * a.grad_stride;
       uint4* gv = reinterpret_cast<uint4*>(g - s.vecs.lead);
       const bool same = reinterpret_cast<uintptr_t>(gv) % 16 == 0;
@@ -972,117 +934,118 @@ __global__ void __launch_bounds__(kRowThreads, 1) row_loss_ring_kernel(const Row
         else
           s.vecs.store_scores(g, v, y);
       };
-      if (got_head && h.off) {
-        if (MODE != kLossBwd && rank == 0 && tid == 0)
-          store_result<OP>(a, row, RowResult{0, 0, 0, 0});
-        if (MODE != kLossFwd)
-          for (int v = s.begin + tid; v < s.end; v += kRowConsumers)
-            put(v, make_uint4(0, 0, 0, 0));
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->head_empty[head_slot]);
+      if (way.off) {
+        if (rank == 0 && tid == 0) store_result<OP>(a, row, RowResult{0, 0, 0, 0});
+        for (int v = s.begin + tid; v < s.end; v += kRowConsumers) put(v, make_uint4(0, 0, 0, 0));
         continue;
       }
-      Softmax st{-INFINITY, 0.0f};
+      // chunks [inner0, inner1) lie in the segment and inside the row entirely
+      const int inner0 = s.begin < s.vecs.whole_begin();
+      const int inner1 = max(inner0, (min(s.end, s.vecs.whole_end()) - s.begin) / kChunkVecs);
+      const int early = s.chunks - s.keep;  // chunks that do not stay
       const int slot0 = slot;
       const uint32_t phase0 = phase;
-      if (MODE == kLossBwd) {
-        st = {a.lse[row] * a.tau, 1.0f};
-      } else {
-        RunningSoftmax<TYPE> run(scale2);
-        for (int c = 0; c < s.chunks; ++c) {
-          uint4 r[kChunkUnits];
-          row_wait(&sh->full[slot], phase, &sh->failed);
-          fetch(s, slot, s.begin + c * kChunkVecs, c >= inner0 && c < inner1, r);
-          if (MODE == kLossFwd || c < early) release(slot);
-          if (++slot == ring_slots) {
-            slot = 0;
-            phase ^= 1;
-          }
-          run.add(r);
+      // ---- the maximum and the sum
+      RunningSoftmax<TYPE> run(scale2);
+      for (int c = 0; c < s.chunks; ++c) {
+        uint4 r[kChunkUnits];
+        row_wait(&sh->full[slot], phase, &sh->failed);
+        fetch(s, slot, s.begin + c * kChunkVecs, c >= inner0 && c < inner1, r);
+        if (c < early) release(slot);
+        if (++slot == ring_slots) {
+          slot = 0;
+          phase ^= 1;
         }
-        st = run.result();
-        st = warp_join(st, scale2);
-        Softmax* part = sh->part[peer_phase];
-        if (lane == 0) part[warp] = st;
-        together();
-        st = warp_join(lane < kRowWarps ? part[lane] : Softmax{-INFINITY, 0.0f}, scale2);
-        if (split > 1) {
-          if (tid < split) {  // thread i hands this CTA's part to CTA i
-            store_peer(&sh->peer[peer_phase][rank], tid, st);
-            mbar_arrive_cluster(peer_addr(smem_addr(&sh->peers), tid));
-          }
-          __all_sync(kFull, row_wait_cluster(&sh->peers, peer_phase, &sh->failed));
-          st = warp_join(lane < split ? sh->peer[peer_phase][lane] : Softmax{-INFINITY, 0.0f},
-                         scale2);
-        }
-        peer_phase ^= 1;
+        run.add(r);
       }
-      RowResult res = row_result<OP, MODE>(a, h, st.m, st.sum);
+      Softmax st = warp_join(run.result(), scale2);
+      Softmax* part = sh->part[parity];
+      if (lane == 0) {
+        part[warp] = st;
+        mbar_arrive(&sh->together);
+      }
+      // every consumer warp has come here (a bounded wait, unlike bar.sync)
+      warp_wait(&sh->together, parity, &sh->failed);
+      st = warp_join(lane < kRowWarps ? part[lane] : Softmax{-INFINITY, 0.0f}, scale2);
+      if (split > 1) {
+        if (tid < split) {  // thread i hands this CTA's part to CTA i
+          store_peer(&sh->peer[parity][rank], tid, st);
+          mbar_arrive_cluster(peer_addr(smem_addr(&sh->peers), tid));
+        }
+        __all_sync(kFull, row_wait_cluster(&sh->peers, parity, &sh->failed));
+        st = warp_join(lane < split ? sh->peer[parity][lane] : Softmax{-INFINITY, 0.0f}, scale2);
+      }
+      parity ^= 1;
+      // ---- the coefficient
+      const bool got_head = warp_wait(&sh->head_full[hi], head_phase, &sh->failed);
+      const Targets t = targets(hi);
+      RowResult res = row_result<OP, kLossGrad>(a, sh->head[hi], st.m, st.sum);
       if (sh->failed) res = RowResult{NAN, NAN, NAN, NAN};
-      if (MODE != kLossBwd && rank == 0 && tid == 0) store_result<OP>(a, row, res);
-      if (MODE != kLossFwd) {
-        const float o = origin(st.m), f = res.c / st.sum;
-        const Exponent e(o, scale2);
-        const uint64_t ff = pack2(f * e.mend, f * e.mend);
-        // the resident chunks, then those copied again
-        int at = slot0 + (MODE == kLossGrad ? early : 0);
-        uint32_t ph = phase0;
-        while (at >= ring_slots) {
-          at -= ring_slots;
+      if (rank == 0 && tid == 0) store_result<OP>(a, row, res);
+      // ---- the gradient: the chunks that stayed, then those copied again
+      const float o = origin(st.m), f = res.c / st.sum;
+      const Exponent e(o, scale2);
+      const uint64_t ff = pack2(f * e.mend, f * e.mend);
+      int at = slot0 + early;
+      uint32_t ph = phase0;
+      while (at >= ring_slots) {
+        at -= ring_slots;
+        ph ^= 1;
+      }
+      for (int i = 0; i < s.chunks; ++i) {
+        const int c = i < s.keep ? early + i : i - s.keep;
+        const int begin = s.begin + c * kChunkVecs;
+        const bool inner = c >= inner0 && c < inner1;
+        // a chunk that stayed was waited for in the first pass
+        const bool ok = i < s.keep || row_wait(&sh->full[at], ph, &sh->failed);
+        const uint64_t fc = ok ? ff : pack2(NAN, NAN);
+        uint4 r[kChunkUnits];
+        fetch(s, at, begin, inner, r);
+        release(at);
+        if (++at == ring_slots) {
+          at = 0;
           ph ^= 1;
         }
-        for (int i = 0; i < s.chunks; ++i) {
-          const int c = MODE == kLossGrad ? (i < s.keep ? early + i : i - s.keep) : i;
-          const int begin = s.begin + c * kChunkVecs;
-          const bool inner = c >= inner0 && c < inner1;
-          // a resident chunk was waited for in the first pass
-          const bool ok = (MODE == kLossGrad && i < s.keep) ||
-                          row_wait(&sh->full[at], ph, &sh->failed);
-          const uint64_t fc = ok ? ff : pack2(NAN, NAN);
-          uint4 r[kChunkUnits];
-          fetch(s, at, begin, inner, r);
-          release(at);
-          if (++at == ring_slots) {
-            at = 0;
-            ph ^= 1;
-          }
-          if (res.c == 0.0f) {  // also where the row holds NaN
+        if (res.c == 0.0f) {  // also where the row holds NaN
 #pragma unroll
-            for (int u = 0; u < kChunkUnits; ++u) r[u] = make_uint4(0, 0, 0, 0);
-          } else {
+          for (int u = 0; u < kChunkUnits; ++u) r[u] = make_uint4(0, 0, 0, 0);
+        } else {
 #pragma unroll
-            for (int u = 0; u < kChunkUnits; ++u) r[u] = vec_grad<TYPE>(r[u], e, fc);
-          }
-          if (inner && same) {
-#pragma unroll
-            for (int u = 0; u < kChunkUnits; ++u) gv[begin + tid + u * kRowConsumers] = r[u];
-          } else {
-#pragma unroll
-            for (int u = 0; u < kChunkUnits; ++u) {
-              const int v = begin + tid + u * kRowConsumers;
-              if (v < s.end) put(v, r[u]);
-            }
-          }
+          for (int u = 0; u < kChunkUnits; ++u) r[u] = vec_grad<TYPE>(r[u], e, fc);
         }
-        slot = at;
-        phase = ph;
-        together();  // the targets' columns are written last
-        if (res.c != 0.0f && got_head) {
-          const int64_t b = static_cast<int64_t>(s.begin) * V::kCount - s.vecs.lead;
-          const int64_t e = static_cast<int64_t>(s.end) * V::kCount - s.vecs.lead;
-          for (int k = tid; k < a.k; k += kRowConsumers) {
-            const int col = t.col[k];
-            if (col >= 0 && col >= b && col < e)
-              g[col] = S::store(exp2_approx((t.x[k] - o) * scale2) * f - res.c * t.p[k]);
+        if (inner && same) {
+#pragma unroll
+          for (int u = 0; u < kChunkUnits; ++u) gv[begin + tid + u * kRowConsumers] = r[u];
+        } else {
+#pragma unroll
+          for (int u = 0; u < kChunkUnits; ++u) {
+            const int v = begin + tid + u * kRowConsumers;
+            if (v < s.end) put(v, r[u]);
           }
         }
       }
+      slot = at;
+      phase = ph;
+      // ---- the targets' columns, each by the warp that wrote its vector
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->head_empty[head_slot]);
+      if (res.c != 0.0f && got_head) {
+        for (int k = lane; k < a.k; k += kWarp) {
+          const int col = t.col[k];
+          const int v = (col + s.vecs.lead) / V::kCount - s.begin;  // among the CTA's vectors
+          if (col >= 0 && v >= 0 && v < s.end - s.begin && v / kWarp % kRowWarps == warp)
+            g[col] = S::store(exp2_approx((t.x[k] - o) * scale2) * f - res.c * t.p[k]);
+        }
+        __syncwarp();
+      }
+      if (lane == 0) mbar_arrive(&sh->head_empty[hi]);
+      if (++hi == heads) {
+        hi = 0;
+        head_phase ^= 1;
+      }
     }
   }
   // no CTA ends while another may still write into its shared memory
-  if (clustered) {
+  if (split > 1) {
     __syncwarp();
     cluster_sync();
   }
@@ -1145,31 +1108,26 @@ cudaError_t launch_stream(const RowLossArgs& a, int split, size_t smem, cudaStre
   }
 }
 
-template <int TYPE, int OP, int MODE>
+template <int TYPE, int OP>
 cudaError_t launch_ring(const RowLossArgs& a, int sms, int64_t bytes, cudaStream_t s) {
   const int slots = row_ring_slots(a.k);
   int split = 1;
-  if (MODE == kLossGrad)
-    while (split < 8 && bytes > int64_t(split) * slots * kChunkBytes * LSDRS_RING_OVER) split *= 2;
+  while (split < 8 && bytes > int64_t(split) * 2 * slots * kChunkBytes) split *= 2;
   while (split < kMaxCluster && a.rows * split * 2 <= sms && bytes >= int64_t(split) * 2 * 8192)
     split *= 2;
-  // over its own logits the backward call of the policy loss must not write a
-  // segment before every segment has read the action's score
-  if (MODE == kLossBwd && OP == kOpPolicy && a.grad == a.logits) split = 1;
   while (a.rows * split >= (int64_t(1) << 31)) split /= 2;  // CTA numbers are 31 bits
-  auto kern = row_loss_ring_kernel<TYPE, OP, MODE>;
-  const size_t smem = row_ring_smem(a.k, slots);
+  auto kern = row_loss_ring_kernel<TYPE, OP>;
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow(kern, true, true, &done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.rows * split));
   cfg.blockDim = dim3(kRowThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = row_ring_smem(a.k, slots);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   cfg.attrs = attr;
-  cfg.numAttrs = add_attributes(attr, MODE == kLossBwd ? 1 : split);
+  cfg.numAttrs = add_attributes(attr, split);
   return cudaLaunchKernelEx(&cfg, kern, a, split, slots, a.rows * split > sms);
 }
 
@@ -1187,7 +1145,7 @@ cudaError_t launch_row_loss_as(const RowLossArgs& a, cudaStream_t s) {
     return launch_kernel(row_loss_short_kernel<TYPE, OP, MODE, 256, 8>,
                          dim3(static_cast<unsigned>(a.rows)), dim3(256), lists, s, a);
   const int sms = device_sm_count();
-  if constexpr (MODE != kLossGrad && !((LSDRS_RING_MODES >> MODE) & 1)) {
+  if constexpr (MODE != kLossGrad) {
     // segments of at least 16 KB, until there are two for every place
     int split = 1;
     while (split < kMaxCluster &&
@@ -1200,7 +1158,7 @@ cudaError_t launch_row_loss_as(const RowLossArgs& a, cudaStream_t s) {
     while (a.rows * split >= (int64_t(1) << 31)) split /= 2;  // CTA numbers are 31 bits
     return launch_stream<TYPE, OP, MODE>(a, split, lists, s);
   } else {
-    return launch_ring<TYPE, OP, MODE>(a, sms, bytes, s);
+    return launch_ring<TYPE, OP>(a, sms, bytes, s);
   }
 }
 
