@@ -286,19 +286,12 @@ __global__ void __launch_bounds__(kThreads, LSDRS_SHORT_WARPS / (kThreads / kWar
   Raw* g = static_cast<Raw*>(a.grad) + row * a.grad_stride;
   const RowVecs<TYPE> vecs(x, static_cast<int>(a.cols));
   const uint4* xv = reinterpret_cast<const uint4*>(x - vecs.lead);
-  uint4* gv = reinterpret_cast<uint4*>(g - vecs.lead);
-  const bool same = reinterpret_cast<uintptr_t>(gv) % 16 == 0;
+  const RowOut<TYPE> out(g, vecs);
   const float scale2 = a.inv_tau * kLog2e;
-  auto put = [&](int v, const uint4& y) {
-    if (same && vecs.whole(v))
-      gv[v] = y;
-    else
-      vecs.store_scores(g, v, y);
-  };
   if (row_off<OP>(a, row)) {
     if (MODE != kLossBwd && tid == 0) store_result<OP>(a, row, RowResult{0, 0, 0, 0});
     if (MODE != kLossFwd)
-      for (int v = tid; v < vecs.count; v += kThreads) put(v, make_uint4(0, 0, 0, 0));
+      for (int v = tid; v < vecs.count; v += kThreads) out.store(vecs, v, make_uint4(0, 0, 0, 0));
     return;
   }
   uint4 r[VECS];
@@ -335,8 +328,7 @@ __global__ void __launch_bounds__(kThreads, LSDRS_SHORT_WARPS / (kThreads / kWar
   for (int u = 0; u < VECS; ++u) {
     const int v = tid + u * kThreads;
     if (v < vecs.count)
-      put(v, res.c == 0.0f ? make_uint4(0, 0, 0, 0)
-                           : vec_grad<TYPE>(r[u], e, ff));
+      out.store(vecs, v, res.c == 0.0f ? make_uint4(0, 0, 0, 0) : vec_grad<TYPE>(r[u], e, ff));
   }
   if (res.c == 0.0f) return;
   __syncthreads();
@@ -498,22 +490,24 @@ __global__ void __launch_bounds__(kStreamThreads + kWarp, LSDRS_STREAM_CTAS)
   const RowVecs<TYPE> vecs(x, static_cast<int>(a.cols));
   const int per = (vecs.count + split - 1) / split;
   const int begin = min(rank * per, vecs.count), end = min(begin + per, vecs.count);
-  uint4* gv = reinterpret_cast<uint4*>(g - vecs.lead);
-  const bool same = reinterpret_cast<uintptr_t>(gv) % 16 == 0;
+  const RowOut<TYPE> out(g, vecs);
   const int inner_end = min(end, vecs.whole_end());
   auto put = [&](int v0, const uint4(&r)[kStreamBatch]) {
-    if (same && v0 >= vecs.whole_begin() && v0 + (kStreamBatch - 1) * kStreamThreads < inner_end) {
+    // the same for all lanes of the warp
+    const int first = v0 - static_cast<int>(lane_id());
+    const bool inner = first >= vecs.whole_begin() &&
+                       first + (kStreamBatch - 1) * kStreamThreads + kWarp <= inner_end;
+    if (inner && out.shift == 0) {
 #pragma unroll
-      for (int u = 0; u < kStreamBatch; ++u) __stcs(gv + v0 + u * kStreamThreads, r[u]);
+      for (int u = 0; u < kStreamBatch; ++u) __stcs(out.vec0 + v0 + u * kStreamThreads, r[u]);
+    } else if (inner) {
+#pragma unroll
+      for (int u = 0; u < kStreamBatch; ++u) out.store_shifted(v0 + u * kStreamThreads, r[u]);
     } else {
 #pragma unroll
       for (int u = 0; u < kStreamBatch; ++u) {
         const int v = v0 + u * kStreamThreads;
-        if (v >= end) break;
-        if (same && vecs.whole(v))
-          __stcs(gv + v, r[u]);
-        else
-          vecs.store_scores(g, v, r[u]);
+        if (v < end) out.store(vecs, v, r[u]);
       }
     }
   };
@@ -926,17 +920,11 @@ __global__ void __launch_bounds__(kRowThreads, 1)
     for (int row; (row = next_row(way)) >= 0;) {
       const Segment s = segment(row);
       Raw* g = static_cast<Raw*>(a.grad) + row * a.grad_stride;
-      uint4* gv = reinterpret_cast<uint4*>(g - s.vecs.lead);
-      const bool same = reinterpret_cast<uintptr_t>(gv) % 16 == 0;
-      auto put = [&](int v, const uint4& y) {
-        if (same && s.vecs.whole(v))
-          gv[v] = y;
-        else
-          s.vecs.store_scores(g, v, y);
-      };
+      const RowOut<TYPE> out(g, s.vecs);
       if (way.off) {
         if (rank == 0 && tid == 0) store_result<OP>(a, row, RowResult{0, 0, 0, 0});
-        for (int v = s.begin + tid; v < s.end; v += kRowConsumers) put(v, make_uint4(0, 0, 0, 0));
+        for (int v = s.begin + tid; v < s.end; v += kRowConsumers)
+          out.store(s.vecs, v, make_uint4(0, 0, 0, 0));
         continue;
       }
       // chunks [inner0, inner1) lie in the segment and inside the row entirely
@@ -1013,14 +1001,18 @@ __global__ void __launch_bounds__(kRowThreads, 1)
 #pragma unroll
           for (int u = 0; u < kChunkUnits; ++u) r[u] = vec_grad<TYPE>(r[u], e, fc);
         }
-        if (inner && same) {
+        if (inner && out.shift == 0) {
 #pragma unroll
-          for (int u = 0; u < kChunkUnits; ++u) gv[begin + tid + u * kRowConsumers] = r[u];
+          for (int u = 0; u < kChunkUnits; ++u) out.vec0[begin + tid + u * kRowConsumers] = r[u];
+        } else if (inner) {
+#pragma unroll
+          for (int u = 0; u < kChunkUnits; ++u)
+            out.store_shifted(begin + tid + u * kRowConsumers, r[u]);
         } else {
 #pragma unroll
           for (int u = 0; u < kChunkUnits; ++u) {
             const int v = begin + tid + u * kRowConsumers;
-            if (v < s.end) put(v, r[u]);
+            if (v < s.end) out.store(s.vecs, v, r[u]);
           }
         }
       }

@@ -386,4 +386,62 @@ struct RowVecs {
   }
 };
 
+// Where a row of results goes that is computed as the vectors of a RowVecs:
+// the same vectors of memory if both rows begin at the same place in their 16
+// bytes, else `shift` scores later.
+template <int TYPE>
+struct RowOut {
+  using Raw = typename Score<TYPE>::Raw;
+  static constexpr int kN = ScoreVec<TYPE>::kCount;
+  Raw* row;
+  uint4* vec0;  // the 16 bytes that vector 0 begins in
+  int shift;
+
+  __device__ __forceinline__ RowOut(Raw* row_, const RowVecs<TYPE>& vecs)
+      : row(row_),
+        vec0(reinterpret_cast<uint4*>(reinterpret_cast<uintptr_t>(row_ - vecs.lead) &
+                                      ~static_cast<uintptr_t>(15))),
+        shift(static_cast<int>(reinterpret_cast<uintptr_t>(row_ - vecs.lead) % 16 / sizeof(Raw))) {}
+
+  // Consecutive lanes store consecutive vectors v, all of them whole, shift
+  // != 0: 16 bytes of memory hold the end of one lane's vector and the
+  // beginning of the next one's.  (Score by score, a misaligned f32 gradient
+  // of 1,021 x 50,001 took 83 us instead of 71.)
+  __device__ __forceinline__ void store_shifted(int v, const uint4& x) const {
+    const uint32_t lane = lane_id();
+    uint32_t c[8] = {x.x, x.y, x.z, x.w, x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = __shfl_up_sync(kFull, c[i], 1);
+    const int bytes = shift * static_cast<int>(sizeof(Raw));
+    const bool two = bytes & 8, one = bytes & 4, half = bytes & 2;
+    uint32_t a[6], b[5];  // words -2 .. 3 and -1 .. 3 of the result
+#pragma unroll
+    for (int k = 0; k < 6; ++k) a[k] = two ? c[k] : c[k + 2];
+#pragma unroll
+    for (int k = 0; k < 5; ++k) b[k] = one ? a[k] : a[k + 1];
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = half ? __funnelshift_l(b[k], b[k + 1], 16) : b[k + 1];
+    if (lane != 0) __stcs(vec0 + v, make_uint4(w[0], w[1], w[2], w[3]));
+    Raw* first = reinterpret_cast<Raw*>(vec0 + v) + shift;  // of this lane's own vector
+    const uint32_t own[4] = {x.x, x.y, x.z, x.w};
+    if (lane == 0 || lane == kWarp - 1) {
+#pragma unroll
+      for (int i = 0; i < kN; ++i) {
+        const uint32_t word = own[i * sizeof(Raw) / 4];
+        const Raw r = static_cast<Raw>(sizeof(Raw) == 4 ? word : word >> (16 * (i & 1)));
+        if (lane == 0 ? i < kN - shift : i >= kN - shift) first[i] = r;
+      }
+    }
+  }
+
+  // Any vector of the row, whole or not.
+  __device__ __forceinline__ void store(const RowVecs<TYPE>& vecs, int v, const uint4& x) const {
+    if (shift == 0 && vecs.whole(v))
+      vec0[v] = x;
+    else
+      vecs.store_scores(row, v, x);
+  }
+};
+
 }  // namespace lsdrs
