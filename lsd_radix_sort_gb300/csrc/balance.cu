@@ -54,7 +54,7 @@ cudaError_t launch_balance_counts(const BalanceArgs& a, int clusters, cudaStream
 }
 
 size_t balance_temp(int64_t tokens, int experts) {
-  if (tokens * experts <= LSDRS_BAL_SINGLE) return 0;
+  if (tokens * experts <= kBalSingle) return 0;
   return bal_header_bytes(experts) +
          align_up(static_cast<size_t>(kBalMaxHists) * (experts + 1) * sizeof(int), 256);
 }

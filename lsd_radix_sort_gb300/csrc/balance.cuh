@@ -28,20 +28,21 @@
 
 namespace lsdrs {
 
-#ifndef LSDRS_BAL_THREADS
-#define LSDRS_BAL_THREADS 256
-#define LSDRS_BAL_CTAS 2
-#endif
-constexpr int kBalThreads = LSDRS_BAL_THREADS;
+// Two CTAs of 8 warps per SM, two tokens per lane under way: with three CTAs,
+// one token each, bf16 gradients of 262,144 tokens and 256 experts took 80 us
+// instead of 68, with one token and two CTAs 76; 43 us is the time of the
+// bytes.  What bounds it is latency: about 20 instructions per score, a
+// quarter of them shuffles, at half the issue rate.
+constexpr int kBalThreads = 256;
+constexpr int kBalCtas = 2;               // per SM
 constexpr int kBalWarps = kBalThreads / kWarp;
-constexpr int kBalCluster = 8;
+constexpr int kBalTurns = 4;              // warps that add to one row of sums
+constexpr int kBalCluster = 8;            // CTAs of a cluster, at most
 constexpr int kBalMaxHists = 19;          // clusters of the counting launch
 constexpr int kCountThreads = 1024;       // its threads per CTA
-// Scores up to which one cluster does the whole call.
-#ifndef LSDRS_BAL_SINGLE
-#define LSDRS_BAL_SINGLE (1 << 18)
-#endif
-constexpr int kBalTurns = 4;              // warps that add to one row of sums
+// Scores up to which one cluster does the whole call (8,192 tokens of 64
+// experts: 14.6 us in one cluster, 9.7 in two launches; 32 of 8: 4.9 and 9.2).
+constexpr int64_t kBalSingle = int64_t(1) << 18;
 
 // Scratch: what the counting launch clears (the ticket, a flag for NaN, the
 // experts' sums of probabilities), then its clusters' histograms (experts
@@ -185,7 +186,8 @@ struct BalVec {
   }
   // a lane's words as pairs of floats
   template <int VECS>
-  static __device__ __forceinline__ void pairs(const Word (&w)[VECS], uint64_t (&p)[VECS * kN / 2]) {
+  static __device__ __forceinline__ void pairs(const Word (&w)[VECS],
+                                               uint64_t (&p)[VECS * kN / 2]) {
 #pragma unroll
     for (int j = 0; j < VECS * kN / 2; ++j) {
       const int a = 2 * j, b = 2 * j + 1;
@@ -265,7 +267,7 @@ __device__ __forceinline__ void sum_rows(const T* from, int n, int64_t pitch, in
 // `hists` clusters of the counting launch left their histograms in the
 // scratch (kLossBwd: the counts are given).
 template <int TYPE, int MODE, int WIDTH, int VECS>
-__global__ void __launch_bounds__(kBalThreads, VECS * BalVec<TYPE, WIDTH>::kN <= 16 ? LSDRS_BAL_CTAS : 512 / kBalThreads)
+__global__ void __launch_bounds__(kBalThreads, kBalCtas)
     balance_kernel(const BalanceArgs a, const int group, const bool single, const int hists) {
   using B = BalVec<TYPE, WIDTH>;
   using Raw = typename B::Raw;
@@ -324,7 +326,8 @@ __global__ void __launch_bounds__(kBalThreads, VECS * BalVec<TYPE, WIDTH>::kN <=
   for (int e = tid; e < all_vecs * kN; e += kBalThreads) {
     const bool real = e < a.experts;
     if (MODE != kLossFwd)
-      share_at(e / kN, e % kN / kFour)[e % kFour] = real ? static_cast<float>(hist[e]) * each : 0.0f;
+      share_at(e / kN, e % kN / kFour)[e % kFour] =
+          real ? static_cast<float>(hist[e]) * each : 0.0f;
     if (MODE != kLossBwd && blockIdx.x == 0 && real) a.counts[e] = hist[e];
   }
   if (MODE != kLossBwd && blockIdx.x == 0 && tid == 0) *a.n_tokens = tokens_kept;
@@ -469,86 +472,85 @@ __global__ void __launch_bounds__(kBalThreads, VECS * BalVec<TYPE, WIDTH>::kN <=
 #pragma unroll
   for (int j = 0; j < kPairs; ++j) unpack2(acc2[j], acc[2 * j], acc[2 * j + 1]);
   if constexpr (MODE != kLossBwd) {
-
-  // ---- the sums over tokens
+    // ---- the sums over tokens
 #pragma unroll
-  for (int j = 0; j < VECS * kN; ++j)
-    for (int o = group; o < kWarp; o <<= 1) acc[j] += __shfl_xor_sync(kFull, acc[j], o);
-  constexpr int kRows = kBalWarps / kBalTurns;
-  for (int turn = 0; turn < kBalTurns; ++turn) {
-    if (warp / kRows == turn && lane < group) {
-      float* row = sums + (warp % kRows) * a.experts;
+    for (int j = 0; j < VECS * kN; ++j)
+      for (int o = group; o < kWarp; o <<= 1) acc[j] += __shfl_xor_sync(kFull, acc[j], o);
+    constexpr int kRows = kBalWarps / kBalTurns;
+    for (int turn = 0; turn < kBalTurns; ++turn) {
+      if (warp / kRows == turn && lane < group) {
+        float* row = sums + (warp % kRows) * a.experts;
 #pragma unroll
-      for (int u = 0; u < VECS; ++u)
+        for (int u = 0; u < VECS; ++u)
 #pragma unroll
-        for (int i = 0; i < kN; ++i) {
-          const int e = (u * group + sub) * kN + i;
-          if (e < a.experts) row[e] = turn == 0 ? acc[u * kN + i] : row[e] + acc[u * kN + i];
-        }
-    }
-    __syncthreads();
-  }
-  for (int e = tid; e < a.experts; e += kBalThreads) {
-    float p = 0.0f;
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) p += sums[r * a.experts + e];
-    sums[e] = p;
-  }
-  float loss = 0.0f;
-  if (single) {
-    const int size = static_cast<int>(gridDim.x);
-    if (size > 1)
-      bal_cluster_sync();
-    else
+          for (int i = 0; i < kN; ++i) {
+            const int e = (u * group + sub) * kN + i;
+            if (e < a.experts) row[e] = turn == 0 ? acc[u * kN + i] : row[e] + acc[u * kN + i];
+          }
+      }
       __syncthreads();
-    if (blockIdx.x == 0) {  // the first CTA adds up, in rank order
+    }
+    for (int e = tid; e < a.experts; e += kBalThreads) {
+      float p = 0.0f;
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) p += sums[r * a.experts + e];
+      sums[e] = p;
+    }
+    float loss = 0.0f;
+    if (single) {
+      const int size = static_cast<int>(gridDim.x);
+      if (size > 1)
+        bal_cluster_sync();
+      else
+        __syncthreads();
+      if (blockIdx.x == 0) {  // the first CTA adds up, in rank order
+        for (int e = tid; e < a.experts; e += kBalThreads) {
+          float p = sums[e];
+          for (int r = 1; r < size; ++r) p += __uint_as_float(peer_word(sums + e, r));
+          p /= n;
+          a.mean_probs[e] = p;
+          loss += static_cast<float>(hist[e]) * each * p;
+        }
+      }
+      if (size > 1) bal_cluster_sync();  // no CTA ends while its sums are read
+      if (blockIdx.x != 0) return;
+    } else {
+      __syncthreads();
+      BalHeader* to = static_cast<BalHeader*>(a.temp);
+      // p <= tokens < 2^bits, so sums of p 2^shift stay below 2^62
+      const int shift = 62 - (32 - __clz(tokens_kept | 1));
+      const float up = ldexpf(1.0f, shift);
+      bool nan = false;
       for (int e = tid; e < a.experts; e += kBalThreads) {
-        float p = sums[e];
-        for (int r = 1; r < size; ++r) p += __uint_as_float(peer_word(sums + e, r));
-        p /= n;
+        const float p = sums[e];
+        if (isnan(p))
+          nan = true;
+        else
+          atomicAdd(&to->sums[e], static_cast<unsigned long long>(__float2ll_rn(p * up)));
+      }
+      if (nan) atomicOr(&to->nan, 1u);
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) last = atomicAdd(&to->ticket, 1u) == gridDim.x - 1;
+      __syncthreads();
+      if (!last) return;
+      __threadfence();
+      const bool any_nan = __ldcg(&to->nan) != 0;
+      for (int e = tid; e < a.experts; e += kBalThreads) {
+        const float total = __ull2float_rn(__ldcg(&to->sums[e]));
+        const float p = any_nan ? NAN : total / up / n;
         a.mean_probs[e] = p;
         loss += static_cast<float>(hist[e]) * each * p;
       }
     }
-    if (size > 1) bal_cluster_sync();  // no CTA ends while its sums are read
-    if (blockIdx.x != 0) return;
-  } else {
+    loss = warp_sum(loss);
+    if (lane == 0) warp_part[warp] = loss;
     __syncthreads();
-    BalHeader* to = static_cast<BalHeader*>(a.temp);
-    // p <= tokens < 2^bits, so sums of p 2^shift stay below 2^62
-    const int shift = 62 - (32 - __clz(tokens_kept | 1));
-    const float up = ldexpf(1.0f, shift);
-    bool nan = false;
-    for (int e = tid; e < a.experts; e += kBalThreads) {
-      const float p = sums[e];
-      if (isnan(p))
-        nan = true;
-      else
-        atomicAdd(&to->sums[e], static_cast<unsigned long long>(__float2ll_rn(p * up)));
+    if (tid == 0) {
+      loss = 0.0f;
+      for (int i = 0; i < kBalWarps; ++i) loss += warp_part[i];
+      *a.loss = loss;
     }
-    if (nan) atomicOr(&to->nan, 1u);
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) last = atomicAdd(&to->ticket, 1u) == gridDim.x - 1;
-    __syncthreads();
-    if (!last) return;
-    __threadfence();
-    const bool any_nan = __ldcg(&to->nan) != 0;
-    for (int e = tid; e < a.experts; e += kBalThreads) {
-      const float total = __ull2float_rn(__ldcg(&to->sums[e]));
-      const float p = any_nan ? NAN : total / up / n;
-      a.mean_probs[e] = p;
-      loss += static_cast<float>(hist[e]) * each * p;
-    }
-  }
-  loss = warp_sum(loss);
-  if (lane == 0) warp_part[warp] = loss;
-  __syncthreads();
-  if (tid == 0) {
-    loss = 0.0f;
-    for (int i = 0; i < kBalWarps; ++i) loss += warp_part[i];
-    *a.loss = loss;
-  }
   }
 }
 
@@ -625,13 +627,13 @@ cudaError_t launch_balance_as(const BalanceArgs& a, int* launched, cudaStream_t 
   if (MODE == kLossBwd) {
     const int64_t most = int64_t(device_sm_count()) * 4;
     ctas = static_cast<int>(ctas_for < most ? ctas_for : most);
-  } else if (a.tokens * a.experts <= LSDRS_BAL_SINGLE) {
+  } else if (a.tokens * a.experts <= kBalSingle) {
     single = true;
     while (cluster < kBalCluster && cluster < ctas_for) cluster *= 2;
     ctas = cluster;
   } else {
     // a warp takes two batches at least before there is another CTA
-    const int64_t most = int64_t(device_sm_count()) * LSDRS_BAL_CTAS, half = (ctas_for + 1) / 2;
+    const int64_t most = int64_t(device_sm_count()) * kBalCtas, half = (ctas_for + 1) / 2;
     ctas = static_cast<int>(half < 1 ? 1 : half < most ? half : most);
     const int64_t each = int64_t(kCountThreads) * kBalCluster * 4;
     const int64_t want = (a.tokens * a.k + each - 1) / each;

@@ -2,7 +2,8 @@
 #include "balance.cuh"
 
 namespace lsdrs {
-cudaError_t launch_balance_bf16(LossMode mode, const BalanceArgs& a, int* launched, cudaStream_t s) {
+cudaError_t launch_balance_bf16(LossMode mode, const BalanceArgs& a, int* launched,
+                                cudaStream_t s) {
   return launch_balance_of<RS_SCORE_BF16>(mode, a, launched, s);
 }
 }  // namespace lsdrs

@@ -62,7 +62,8 @@ struct BalanceArgs {
 
 // type: an rs_score_type
 cudaError_t launch_row_loss(RowLossOp op, int type, LossMode mode, const RowLossArgs& a,
-                            int* launched, cudaStream_t s);
+                            cudaStream_t s);
+// *launched: 1, raised to the number of kernels
 cudaError_t launch_balance(int type, LossMode mode, const BalanceArgs& a, int* launched,
                            cudaStream_t s);
 // Scratch of a call; 0 where one cluster does all of it.

@@ -115,8 +115,8 @@ rs_status distill(const rs_distill_args* p, const float* grad_losses, LossMode m
   a.index_stride = p->top_indices_stride;
   a.k = p->top;
   return enqueue(8, static_cast<uint64_t>(p->rows) * p->cols, stream,
-                 [&](int* n, cudaStream_t s) {
-                   return launch_row_loss(kOpDistill, p->logits_type, mode, a, n, s);
+                 [&](int*, cudaStream_t s) {
+                   return launch_row_loss(kOpDistill, p->logits_type, mode, a, s);
                  });
 }
 
@@ -160,8 +160,8 @@ rs_status policy(const rs_policy_args* p, const float* grad_losses, LossMode mod
   a.clip_high = 1.0f + p->clip_high;
   a.kl_coef = p->kl_coef;
   return enqueue(8, static_cast<uint64_t>(p->rows) * p->cols, stream,
-                 [&](int* n, cudaStream_t s) {
-                   return launch_row_loss(kOpPolicy, p->logits_type, mode, a, n, s);
+                 [&](int*, cudaStream_t s) {
+                   return launch_row_loss(kOpPolicy, p->logits_type, mode, a, s);
                  });
 }
 

@@ -11,7 +11,7 @@ cudaError_t launch_row_loss_bf16(RowLossOp, LossMode, const RowLossArgs&, cudaSt
 cudaError_t launch_row_loss_f32(RowLossOp, LossMode, const RowLossArgs&, cudaStream_t);
 
 cudaError_t launch_row_loss(RowLossOp op, int type, LossMode mode, const RowLossArgs& a,
-                            int* /*launched*/, cudaStream_t s) {
+                            cudaStream_t s) {
   switch (type) {
     case RS_SCORE_F16: return launch_row_loss_f16(op, mode, a, s);
     case RS_SCORE_BF16: return launch_row_loss_bf16(op, mode, a, s);

@@ -259,13 +259,15 @@ __device__ __forceinline__ void store_result(const RowLossArgs& a, int64_t row,
 }
 
 // ---------------------------------------------------------------- short rows
-#ifndef LSDRS_SHORT_WARPS
-#define LSDRS_SHORT_WARPS 32
-#endif
 // One CTA per row, the row in registers: rows of at most kThreads * VECS
-// 16-byte vectors.  Many CTAs per SM hide each other's loads and reductions.
+// 16-byte vectors (8 KB and 32 KB).  Many CTAs per SM hide each other's loads
+// and reductions, so registers are held to what 32 warps per SM leave: bf16
+// gradients of 16,384 x 16,000 took 190 us, 199 with 24 warps and 239 with
+// 16.  What bounds it is the chain of a CTA (targets, maximum, sum, gradient)
+// against the few KB it moves; 157 us is the time of the bytes.
+constexpr int kShortWarps = 32;
 template <int TYPE, int OP, int MODE, int kThreads, int VECS>
-__global__ void __launch_bounds__(kThreads, LSDRS_SHORT_WARPS / (kThreads / kWarp))
+__global__ void __launch_bounds__(kThreads, kShortWarps / (kThreads / kWarp))
     row_loss_short_kernel(const RowLossArgs a) {
   grid_dependency_sync();
   using S = Score<TYPE>;
@@ -340,19 +342,20 @@ __global__ void __launch_bounds__(kThreads, LSDRS_SHORT_WARPS / (kThreads / kWar
 // -------------------------------------------- long rows, one pass over a row
 // The losses alone, and the backward call, read a row once and keep nothing
 // of it: plain wide loads, a batch of them always ahead of the arithmetic,
-// with three CTAs per SM.  A row is cut into `split` segments when there are
-// too few rows.  One more warp reads the row's targets meanwhile.
+// with three CTAs per SM (batches of 4 vectors; 3 with four CTAs took 101 us
+// instead of 83 for a bf16 forward of 2,048 x 131,072, 8 with two 85; the
+// ring of the one-call form below 88 to 92).  One more warp reads the row's
+// targets meanwhile.  A row is cut into `split` segments of at least 16 KB
+// until there are two CTAs for every place on the GPU: four times as many
+// CTAs gain nothing (each pays for its targets), sixteen cost 30% and more.
+// What bounds them is HBM (70 us for the bytes of that forward), and the last
+// CTAs of a grid, which have the GPU to themselves.
 constexpr int kStreamThreads = 256;
 constexpr int kStreamWarps = kStreamThreads / kWarp;
-#ifndef LSDRS_STREAM_BATCH
-#define LSDRS_STREAM_BATCH 4
-#define LSDRS_STREAM_CTAS 3
-#endif
-#ifndef LSDRS_STREAM_WAVES
-#define LSDRS_STREAM_WAVES 2
-#define LSDRS_STREAM_LEAST 16384
-#endif
-constexpr int kStreamBatch = LSDRS_STREAM_BATCH;
+constexpr int kStreamBatch = 4;   // vectors per thread under way
+constexpr int kStreamCtas = 3;    // per SM
+constexpr int kStreamWaves = 2;
+constexpr int64_t kStreamLeast = 16384;
 constexpr int kMaxCluster = 16;
 
 __device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
@@ -424,7 +427,7 @@ struct Stream {
 };
 
 template <int TYPE, int OP>
-__global__ void __launch_bounds__(kStreamThreads + kWarp, LSDRS_STREAM_CTAS)
+__global__ void __launch_bounds__(kStreamThreads + kWarp, kStreamCtas)
     row_loss_forward_kernel(const RowLossArgs a, const int split) {
   using Raw = typename Score<TYPE>::Raw;
   extern __shared__ __align__(16) unsigned char smem[];
@@ -470,7 +473,7 @@ __global__ void __launch_bounds__(kStreamThreads + kWarp, LSDRS_STREAM_CTAS)
 }
 
 template <int TYPE, int OP>
-__global__ void __launch_bounds__(kStreamThreads + kWarp, LSDRS_STREAM_CTAS)
+__global__ void __launch_bounds__(kStreamThreads + kWarp, kStreamCtas)
     row_loss_backward_kernel(const RowLossArgs a, const int split) {
   using S = Score<TYPE>;
   using Raw = typename S::Raw;
@@ -1128,7 +1131,7 @@ cudaError_t launch_row_loss_as(const RowLossArgs& a, cudaStream_t s) {
   constexpr int kEs = sizeof(typename Score<TYPE>::Raw);
   const int64_t bytes = a.cols * kEs;
   const size_t lists = static_cast<size_t>(a.k) * 12 + static_cast<size_t>(target_slots(a.k)) * 4;
-  // a row's vectors: one more than its bytes hold where it begins unaligned
+  // vectors of a row, wherever it begins
   const int64_t vecs = (a.cols + 2 * (ScoreVec<TYPE>::kCount - 1)) / ScoreVec<TYPE>::kCount;
   if (vecs <= 128 * 4)
     return launch_kernel(row_loss_short_kernel<TYPE, OP, MODE, 128, 4>,
@@ -1138,11 +1141,9 @@ cudaError_t launch_row_loss_as(const RowLossArgs& a, cudaStream_t s) {
                          dim3(static_cast<unsigned>(a.rows)), dim3(256), lists, s, a);
   const int sms = device_sm_count();
   if constexpr (MODE != kLossGrad) {
-    // segments of at least 16 KB, until there are two for every place
     int split = 1;
-    while (split < kMaxCluster &&
-           a.rows * split < int64_t(sms) * LSDRS_STREAM_CTAS * LSDRS_STREAM_WAVES &&
-           bytes >= int64_t(split) * 2 * LSDRS_STREAM_LEAST)
+    while (split < kMaxCluster && a.rows * split < int64_t(sms) * kStreamCtas * kStreamWaves &&
+           bytes >= split * 2 * kStreamLeast)
       split *= 2;
     // over its own logits the backward call of the policy loss must not write
     // a segment before every segment has read the action's score

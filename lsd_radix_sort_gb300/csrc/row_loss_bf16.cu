@@ -2,7 +2,8 @@
 #include "row_loss_launch.cuh"
 
 namespace lsdrs {
-cudaError_t launch_row_loss_bf16(RowLossOp op, LossMode mode, const RowLossArgs& a, cudaStream_t s) {
+cudaError_t launch_row_loss_bf16(RowLossOp op, LossMode mode, const RowLossArgs& a,
+                                 cudaStream_t s) {
   return launch_row_loss_of<RS_SCORE_BF16>(op, mode, a, s);
 }
 }  // namespace lsdrs

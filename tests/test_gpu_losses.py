@@ -417,6 +417,83 @@ def test_cuda_graph(rs):
         assert all(torch.equal(a, b) for a, b in zip(gb, rs.balance_loss_grad(router, ids)))
 
 
+def test_graph_of_long_rows(rs):
+    """Rows taken over from unlaunched CTAs, replayed: more rows than SMs."""
+    x, xd, g = rows_of(400, 33000, torch.bfloat16, 17)
+    actions, old, ref, adv = (t.cuda() for t in policy_inputs(x, 1.0, g))
+    rs.policy_loss_grad(xd, actions, old, adv, ref, kl_coef=0.1)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = rs.policy_loss_grad(xd, actions, old, adv, ref, kl_coef=0.1)
+    for _ in range(3):
+        xd.mul_(0.75)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = rs.policy_loss_grad(xd, actions, old, adv, ref, kl_coef=0.1)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 90000), (5, 90000), (200, 90000), (3, 400000), (160, 400000)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rows_beyond_the_ring(rs, rows, cols, dtype):
+    """Rows that one CTA cannot hold, alone and as many as there are SMs,
+    against the gradient of plain double arithmetic."""
+    g = torch.Generator(device="cuda").manual_seed(rows + cols)
+    x = (torch.randn(rows, cols, generator=g, device="cuda") * 3).to(dtype)
+    values, indices = torch.topk(x.float() + torch.randn(x.shape, generator=g, device="cuda"), 40, dim=1)
+    weights = torch.rand(rows, generator=g, device="cuda")
+    weights[::7] = 0
+    losses, lse, grad = rs.distill_loss_grad(x, values, indices, weights=weights)
+    back = rs.distill_loss_backward(None, x, lse, values, indices, weights=weights)
+    err = lo.row_error(torch.tensor([[-16.0, 16.0]]).expand(1, 2), 1.0)[0] + lo.U32 * cols / 32
+    u, tiny = lo.ROUND[dtype]
+    for r in range(rows):
+        z = x[r].double()
+        logq = z - torch.logsumexp(z, 0)
+        logp = torch.log_softmax(values[r].double(), 0)
+        w = weights[r].double()
+        target = torch.zeros_like(z).index_add_(0, indices[r], logp.exp())
+        want = w * (logq.exp() - target)
+        bound = w * (logq.exp() + target) * (2 * float(err) + 16 * lo.U32) + want.abs() * u * 1.01 + tiny
+        for got in (grad[r], back[r]):
+            assert bool(((got.double() - want).abs() <= bound).all()), (r, "gradient")
+        loss = w * (logp.exp() * (logp - logq[indices[r]])).sum()
+        assert abs(losses[r].double() - loss) <= 4 * float(err) * (1 + abs(loss)), (r, "loss")
+
+
+@pytest.mark.parametrize("k", [300, 1024])
+def test_long_lists_of_long_rows(rs, k):
+    """Long lists leave less of the ring; some columns are named twice."""
+    x, xd, g = rows_of(6, 70001, torch.bfloat16, k)
+    values, indices = distill_case(x, k, g)
+    indices[1, 1::2] = indices[1, 0::2]
+    indices[4, k // 2] = indices[4, 0]
+    check_distill(rs, x, xd, values, indices)
+
+
+def test_int32_actions_and_indices(rs):
+    x, xd, g = rows_of(5, 4000, torch.float16, 19)
+    actions, old, ref, adv = policy_inputs(x, 1.0, g)
+    actions[2] = -1
+    check_policy(rs, x, xd, actions.int(), old, adv, ref, 0.1)
+
+
+def test_the_example_trains(rs):
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "train_step.py")
+    spec = importlib.util.spec_from_file_location("train_step", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    history = example.main(steps=12)
+    assert history["distill"][-1] < 0.8 * history["distill"][0]
+    assert 0.9 < history["balance"][-1] < 3.0
+    assert history["reward"][-1] >= history["reward"][0] - 0.05
+    assert all(math.isfinite(v) for series in history.values() for v in series)
+
+
 # --------------------------------------------------------------- balance
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("tokens,experts,k", [
