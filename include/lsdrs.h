@@ -465,6 +465,16 @@ rs_status rs_policy_loss(const rs_policy_args* args, void* stream);
 rs_status rs_policy_loss_backward(const rs_policy_args* args, const float* grad_losses,
                                   void* stream);
 
+/* Failure-detection check of the row losses: the kernels of long rows wait
+ * for their copies and for each other on barriers, each wait for 2 s at most;
+ * one that runs out gives the rows that were left NaN losses and gradients.
+ * This runs that wait, with the given limit (1 ns .. 60 s), on a barrier on
+ * which nothing arrives, synchronises `stream` and writes the status it
+ * produced (RS_ERR_LOOKBACK_TIMEOUT when it expired) to *result.
+ * word: (device) one u32 scratch word, overwritten. */
+rs_status rs_row_wait_timeout_probe(uint32_t* word, uint64_t timeout_ns, void* stream,
+                                    rs_status* result);
+
 /* A router's load-balancing loss and its per-expert counts.  With p = the
  * softmax of a token's scores, over the N tokens that the mask keeps, c_e the
  * number of their expert ids equal to e and P_e = 1/N sum_t p_te:

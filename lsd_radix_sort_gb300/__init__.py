@@ -36,6 +36,7 @@ __all__ = [
     "BoundsViolation", "distill_loss", "distill_loss_grad", "distill_loss_backward",
     "policy_loss", "policy_loss_grad", "policy_loss_backward", "balance_loss",
     "balance_loss_grad", "balance_loss_backward", "balance_temp_bytes",
+    "row_wait_timeout_probe",
 ]
 
 RS_OK, RS_ERR_INVALID, RS_ERR_TEMP_TOO_SMALL, RS_ERR_CUDA, RS_ERR_LOOKBACK_TIMEOUT = range(5)
@@ -64,6 +65,7 @@ EXPORTED_SYMBOLS = (
     "rs_checked_build", "radix_sort_checked_violations",
     "rs_distill_loss", "rs_distill_loss_backward", "rs_policy_loss", "rs_policy_loss_backward",
     "rs_balance_loss", "rs_balance_loss_backward", "rs_balance_temp_bytes",
+    "rs_row_wait_timeout_probe",
 )
 
 
@@ -148,6 +150,7 @@ def load_library() -> ctypes.CDLL:
             "rs_balance_loss": [P, P],
             "rs_balance_loss_backward": [P, P, P],
             "rs_balance_temp_bytes": [i64, i, P],
+            "rs_row_wait_timeout_probe": [P, u64, P, P],
         }
         for name, args in sig.items():
             f = getattr(lib, name)
@@ -521,4 +524,4 @@ def noalloc_timeout_probe(timeout_ns: int, stream=None) -> int:
 from .losses import (  # noqa: E402  (the losses use the helpers above)
     balance_loss, balance_loss_backward, balance_loss_grad, balance_temp_bytes, distill_loss,
     distill_loss_backward, distill_loss_grad, policy_loss, policy_loss_backward,
-    policy_loss_grad)
+    policy_loss_grad, row_wait_timeout_probe)

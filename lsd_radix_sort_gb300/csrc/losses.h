@@ -66,6 +66,7 @@ cudaError_t launch_row_loss(RowLossOp op, int type, LossMode mode, const RowLoss
 // *launched: 1, raised to the number of kernels
 cudaError_t launch_balance(int type, LossMode mode, const BalanceArgs& a, int* launched,
                            cudaStream_t s);
+cudaError_t launch_row_wait_probe(uint32_t* error, uint64_t limit_ns, cudaStream_t s);
 // Scratch of a call; 0 where one cluster does all of it.
 size_t balance_temp(int64_t tokens, int experts);
 

@@ -11,6 +11,7 @@ using namespace lsdrs;
 
 namespace {
 
+constexpr uint64_t kMaxWaitNs = 60000000000ull;
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
 
 int score_bytes(int type) { return type == RS_SCORE_F32 ? 4 : 2; }
@@ -237,6 +238,24 @@ rs_status rs_policy_loss(const rs_policy_args* args, void* stream) {
 rs_status rs_policy_loss_backward(const rs_policy_args* args, const float* grad_losses,
                                   void* stream) {
   return policy(args, grad_losses, kLossBwd, stream);
+}
+
+rs_status rs_row_wait_timeout_probe(uint32_t* word, uint64_t timeout_ns, void* stream,
+                                    rs_status* result) {
+  if (!given(word, 4) || !result || timeout_ns == 0 || timeout_ns > kMaxWaitNs)
+    return RS_ERR_INVALID;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (cudaMemsetAsync(word, 0, 4, s) != cudaSuccess) return RS_ERR_CUDA;
+  const rs_status st = enqueue(4, 1, stream, [&](int*, cudaStream_t on) {
+    return launch_row_wait_probe(word, timeout_ns, on);
+  });
+  if (st != RS_OK) return st;
+  uint32_t err = 0;
+  if (cudaMemcpyAsync(&err, word, 4, cudaMemcpyDeviceToHost, s) != cudaSuccess)
+    return RS_ERR_CUDA;
+  if (cudaStreamSynchronize(s) != cudaSuccess) return RS_ERR_CUDA;
+  *result = static_cast<rs_status>(err);
+  return RS_OK;
 }
 
 rs_status rs_balance_temp_bytes(int64_t tokens, int experts, size_t* bytes) {

@@ -633,7 +633,8 @@ __host__ constexpr inline int row_ring_slots(int k) {
 // shared-memory ports of those that work (a 4096 x 131072 bf16 gradient took
 // 500 us so, 441 with a read of the clock between polls).
 template <bool CLUSTER>
-__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* failed) {
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* failed,
+                                           uint64_t limit_ns = kRowWaitNs) {
   constexpr uint32_t kSleepNs = 1000000;
   auto done = [&] {
     uint32_t ok;
@@ -659,7 +660,7 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volat
   const uint64_t t0 = global_timer_ns();
   while (!done()) {
     if (*failed) return false;
-    if (global_timer_ns() - t0 > kRowWaitNs) {
+    if (global_timer_ns() - t0 > limit_ns) {
       *failed = 1;
       return false;
     }

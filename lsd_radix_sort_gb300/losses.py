@@ -30,7 +30,8 @@ from . import _check, _lib_of
 __all__ = [
     "distill_loss", "distill_loss_grad", "distill_loss_backward", "policy_loss",
     "policy_loss_grad", "policy_loss_backward", "balance_loss", "balance_loss_grad",
-    "balance_loss_backward", "balance_temp_bytes", "MAX_TOP", "MAX_EXPERTS",
+    "balance_loss_backward", "balance_temp_bytes", "row_wait_timeout_probe", "MAX_TOP",
+    "MAX_EXPERTS",
 ]
 
 MAX_TOP = 1024
@@ -431,6 +432,19 @@ def balance_loss_backward(grad_loss, scores, counts, n_tokens, top_k: int, token
     _check(_lib_of().rs_balance_loss_backward(ctypes.byref(args), _ptr(grad_loss), s),
            "rs_balance_loss_backward")
     return grad
+
+
+def row_wait_timeout_probe(timeout_ns: int, stream=None) -> int:
+    """Run the long-row kernels' bounded wait on a barrier on which nothing
+    arrives (rs_row_wait_timeout_probe); return its status."""
+    torch = _torch or _load()
+    word = torch.empty(1, dtype=torch.int32, device="cuda")
+    result = ctypes.c_int(-1)
+    s = _raw_stream(word.get_device()) if stream is None else stream.cuda_stream
+    _check(_lib_of().rs_row_wait_timeout_probe(word.data_ptr(), int(timeout_ns), s,
+                                               ctypes.byref(result)),
+           "rs_row_wait_timeout_probe")
+    return result.value
 
 
 # --------------------------------------------------------------- autograd

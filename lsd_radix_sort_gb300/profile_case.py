@@ -1,4 +1,4 @@
-"""Run one sort workload a fixed number of times, for profiling.
+"""Run one sort (or loss) workload a fixed number of times, for profiling.
 
     python -m lsd_radix_sort_gb300.profile_case CASE [--log2 N] [--bits B]
                                                 [--sorts K] [--warmup W]
@@ -11,6 +11,9 @@ CASE is one of
   rows_f16    (R, C) fp16 rows (the standard-normal mix), ascending; by
               default (1024, 65536)
   rows_bf16   the same rows in bf16
+  distill     losses and gradient of (R, C) bf16 logits against 64 targets each
+  policy      losses and gradient of (R, C) bf16 logits and one action each
+  balance     loss, counts and gradient of (R, C) bf16 router scores, 8 ids each
 
 Each sort is timed with CUDA events around every kernel the library enqueues
 (on the launching stream) and the script prints one JSON line with the
@@ -29,7 +32,7 @@ import numpy as np
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("case", choices=["pairs_u32", "keys_u32", "pairs_u64", "rows_f16",
-                                     "rows_bf16"])
+                                     "rows_bf16", "distill", "policy", "balance"])
     ap.add_argument("--log2", type=int, default=25)
     ap.add_argument("--bits", type=int, default=8)
     ap.add_argument("--end-bit", type=int, default=None)
@@ -77,6 +80,28 @@ def main():
         def sort():
             rs.radix_sort_pairs(keys, vals, ko, vo, 0, end, args.bits, temp=temp)
         units = n
+    elif args.case in ("distill", "policy", "balance"):
+        rows, cols = args.rows, args.cols
+        torch.manual_seed(0)
+        x = (torch.randn(rows, cols, device=dev) * 2.5).to(torch.bfloat16)
+        grad = torch.empty_like(x)
+        temp = torch.zeros(1024, dtype=torch.uint8, device=dev)  # no status of their own
+        if args.case == "policy":
+            actions = torch.randint(0, cols, (rows,), device=dev)
+            zeros = torch.zeros(rows, device=dev)
+
+            def sort():
+                rs.policy_loss_grad(x, actions, zeros - 10, zeros + 1, grad_out=grad)
+        else:
+            k = 64 if args.case == "distill" else 8
+            values, indices = (t.contiguous() for t in torch.topk(x, k, dim=1))
+
+            def sort():
+                if args.case == "distill":
+                    rs.distill_loss_grad(x, values, indices, grad_out=grad)
+                else:
+                    rs.balance_loss_grad(x, indices, grad_out=grad)
+        units = rows * cols
     else:
         kind = "f16" if args.case == "rows_f16" else "bf16"
         rows, cols = args.rows, args.cols

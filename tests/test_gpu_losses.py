@@ -472,6 +472,13 @@ def test_long_lists_of_long_rows(rs, k):
     check_distill(rs, x, xd, values, indices)
 
 
+def test_a_wait_that_runs_out_is_reported(rs):
+    assert rs.row_wait_timeout_probe(3_000_000) == rs.RS_ERR_LOOKBACK_TIMEOUT
+    x, xd, g = rows_of(3, 40000, torch.bfloat16, 18)  # and the next call is right
+    values, indices = distill_case(x, 4, g)
+    check_distill(rs, x, xd, values, indices)
+
+
 def test_int32_actions_and_indices(rs):
     x, xd, g = rows_of(5, 4000, torch.float16, 19)
     actions, old, ref, adv = policy_inputs(x, 1.0, g)

@@ -158,6 +158,14 @@ def test_no_rows_is_no_work(lib):
     assert lib.rs_balance_loss_backward(ctypes.byref(balance_args(tokens=0, scores=None, grad=None)), None, None) == 0
 
 
+def test_wait_probe_refuses(lib):
+    out = ctypes.c_int(0)
+    for word, limit in ((None, 1), (ctypes.c_void_p(BASE + 2), 1), (ctypes.c_void_p(BASE), 0),
+                        (ctypes.c_void_p(BASE), 61_000_000_000)):
+        assert lib.rs_row_wait_timeout_probe(word, limit, None, ctypes.byref(out)) == 1
+    assert lib.rs_row_wait_timeout_probe(ctypes.c_void_p(BASE), 1, None, None) == 1
+
+
 def test_balance_scratch_size(lib):
     out = ctypes.c_size_t(0)
     for bad in ((-1, 8), (10, 0), (10, 1025)):
