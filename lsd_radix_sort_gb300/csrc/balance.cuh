@@ -266,9 +266,10 @@ __device__ __forceinline__ void sum_rows(const T* from, int n, int64_t pitch, in
 // single: the grid is one cluster, which counts the ids itself.  Otherwise
 // `hists` clusters of the counting launch left their histograms in the
 // scratch (kLossBwd: the counts are given).
-template <int TYPE, int MODE, int WIDTH, int VECS>
+template <int TYPE, int MODE, int WIDTH, int VECS, int GROUP>
 __global__ void __launch_bounds__(kBalThreads, kBalCtas)
-    balance_kernel(const BalanceArgs a, const int group, const bool single, const int hists) {
+    balance_kernel(const BalanceArgs a, const int group_, const bool single, const int hists) {
+  const int group = GROUP != 0 ? GROUP : group_;
   using B = BalVec<TYPE, WIDTH>;
   using Raw = typename B::Raw;
   constexpr int kN = B::kN;
@@ -560,7 +561,7 @@ inline size_t bal_smem(int experts) {
   return (size_t(RS_MAX_EXPERTS) + experts + 1 + (sums > kBalThreads ? sums : kBalThreads)) * 4;
 }
 
-template <int TYPE, int MODE, int WIDTH, int VECS>
+template <int TYPE, int MODE, int WIDTH, int VECS, int GROUP>
 cudaError_t launch_balance_shape(const BalanceArgs& a, int group, bool single, int ctas,
                                  int cluster, int hists, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
@@ -582,7 +583,8 @@ cudaError_t launch_balance_shape(const BalanceArgs& a, int group, bool single, i
   }
   cfg.attrs = attr;
   cfg.numAttrs = n;
-  return cudaLaunchKernelEx(&cfg, balance_kernel<TYPE, MODE, WIDTH, VECS>, a, group, single, hists);
+  return cudaLaunchKernelEx(&cfg, balance_kernel<TYPE, MODE, WIDTH, VECS, GROUP>, a, group, single,
+                            hists);
 }
 
 cudaError_t launch_balance_counts(const BalanceArgs& a, int clusters, cudaStream_t s);
@@ -642,15 +644,22 @@ cudaError_t launch_balance_as(const BalanceArgs& a, int* launched, cudaStream_t 
     if (e != cudaSuccess) return e;
     *launched = 2;
   }
-  auto go = [&](auto w, auto v) {
-    return launch_balance_shape<TYPE, MODE, decltype(w)::value, decltype(v)::value>(
-        a, group, single, ctas, cluster, hists, s);
+  // the lanes per token are known at compile time for 16-byte vectors
+  auto shape = [&](auto w, auto v, auto g) {
+    return launch_balance_shape<TYPE, MODE, decltype(w)::value, decltype(v)::value,
+                                decltype(g)::value>(a, group, single, ctas, cluster, hists, s);
+  };
+  auto go = [&](auto w, auto v) { return shape(w, v, ScoreTag<0>{}); };
+  auto wide = [&](auto v) {
+    if (group == 8) return shape(ScoreTag<16>{}, v, ScoreTag<8>{});
+    if (group == 16) return shape(ScoreTag<16>{}, v, ScoreTag<16>{});
+    return go(ScoreTag<16>{}, v);
   };
   constexpr int k4 = 4 / kEs;  // 16-byte vectors hold half as many 32-bit scores
   if (width == 16) {
-    if (best == 1) return go(ScoreTag<16>{}, ScoreTag<1>{});
-    if (best == 2) return go(ScoreTag<16>{}, ScoreTag<2>{});
-    if (best == 4) return go(ScoreTag<16>{}, ScoreTag<4>{});
+    if (best == 1) return wide(ScoreTag<1>{});
+    if (best == 2) return wide(ScoreTag<2>{});
+    if (best == 4) return wide(ScoreTag<4>{});
     if constexpr (k4 == 1)
       if (best == 8) return go(ScoreTag<16>{}, ScoreTag<8>{});
   } else if (width == kEs) {

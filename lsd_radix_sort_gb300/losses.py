@@ -21,6 +21,7 @@ synchronises; results are allocated by torch on that stream unless given.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import types
@@ -144,12 +145,12 @@ def _grad_stride(x, grad_out):
     return _matrix(grad_out, "grad_out")[2]
 
 
-def _allocate(stream, make):
-    """make(), its allocations belonging to the stream that the work runs on."""
-    if stream is None:
-        return make()
-    with _torch.cuda.stream(stream):
-        return make()
+_CURRENT = contextlib.nullcontext()
+
+
+def _on(stream):
+    """A context whose allocations belong to the stream that the work runs on."""
+    return _CURRENT if stream is None else _torch.cuda.stream(stream)
 
 
 def _ptr(t):
@@ -180,14 +181,14 @@ def _distill(logits, top_values, top_indices, temperature, weights, losses, lse,
     grad_stride = cols if grad is None else _grad_stride(logits, grad)
     index = _device(logits, top_values, top_indices, weights, losses, lse, grad, grad_losses)
 
-    def make():
+    with _on(stream):
         device = logits.device
-        stat = lse if lse is not None else torch.empty(rows, dtype=torch.float32, device=device)
-        return (losses if losses is not None or backward else torch.empty_like(stat), stat,
-                grad if grad is not None or not with_grad else
-                torch.empty((rows, cols), dtype=logits.dtype, device=device))
-
-    losses, lse, grad = make() if stream is None else _allocate(stream, make)
+        if lse is None:
+            lse = torch.empty((rows,), dtype=torch.float32, device=device)
+        if losses is None and not backward:
+            losses = torch.empty((rows,), dtype=torch.float32, device=device)
+        if grad is None and with_grad:
+            grad = torch.empty((rows, cols), dtype=logits.dtype, device=device)
     args = DistillArgs(logits.data_ptr(), stride, rows, cols, top_values.data_ptr(), values_stride,
                        top_indices.data_ptr(), indices_stride, _ptr(weights), _ptr(losses),
                        lse.data_ptr(), _ptr(grad), grad_stride, kind, top_kind, ib, k, temperature)
@@ -262,15 +263,16 @@ def _policy(logits, actions, old, advantages, ref, clip_low, clip_high, kl_coef,
     index = _device(logits, actions, old, advantages, ref, weights, losses, logprobs, lse, grad,
                     grad_losses)
 
-    def make():
+    with _on(stream):
         device = logits.device
-        stat = lse if lse is not None else torch.empty(rows, dtype=torch.float32, device=device)
-        return (losses if losses is not None or backward else torch.empty_like(stat),
-                logprobs if logprobs is not None or backward else torch.empty_like(stat), stat,
-                grad if grad is not None or not with_grad else
-                torch.empty((rows, cols), dtype=logits.dtype, device=device))
-
-    losses, logprobs, lse, grad = make() if stream is None else _allocate(stream, make)
+        if lse is None:
+            lse = torch.empty((rows,), dtype=torch.float32, device=device)
+        if losses is None and not backward:
+            losses = torch.empty((rows,), dtype=torch.float32, device=device)
+        if logprobs is None and not backward:
+            logprobs = torch.empty((rows,), dtype=torch.float32, device=device)
+        if grad is None and with_grad:
+            grad = torch.empty((rows, cols), dtype=logits.dtype, device=device)
     args = PolicyArgs(logits.data_ptr(), stride, rows, cols, actions.data_ptr(), old.data_ptr(),
                       advantages.data_ptr(), _ptr(ref), _ptr(weights), _ptr(losses),
                       _ptr(logprobs), lse.data_ptr(), _ptr(grad), grad_stride, kind, ib, clip_low,
@@ -359,19 +361,16 @@ def _balance(scores, ids, mask, scale, grad, with_grad, temp, stream):
     grad_stride = experts if grad is None else _grad_stride(scores, grad)
     index = _device(scores, ids, mask, grad, temp)
     need = balance_temp_bytes(tokens, experts)
-
-    def make():
+    with _on(stream):
         device = scores.device
-        return (temp if temp is not None or not need else
-                torch.empty(need, dtype=torch.uint8, device=device),
-                torch.empty((), dtype=torch.float32, device=device),
-                torch.empty(experts, dtype=torch.float32, device=device),
-                torch.empty(experts, dtype=torch.int32, device=device),
-                torch.empty(1, dtype=torch.int32, device=device),
-                grad if grad is not None or not with_grad else
-                torch.empty((tokens, experts), dtype=scores.dtype, device=device))
-
-    temp, loss, mean, counts, n, grad = make() if stream is None else _allocate(stream, make)
+        loss = torch.empty((), dtype=torch.float32, device=device)
+        mean = torch.empty((experts,), dtype=torch.float32, device=device)
+        counts = torch.empty((experts,), dtype=torch.int32, device=device)
+        n = torch.empty((1,), dtype=torch.int32, device=device)
+        if temp is None and need:
+            temp = torch.empty((need,), dtype=torch.uint8, device=device)
+        if grad is None and with_grad:
+            grad = torch.empty((tokens, experts), dtype=scores.dtype, device=device)
     args = BalanceArgs(scores.data_ptr(), stride, tokens, ids.data_ptr(), ids_stride, _ptr(mask),
                        loss.data_ptr(), mean.data_ptr(), counts.data_ptr(), n.data_ptr(),
                        _ptr(grad), grad_stride, _ptr(temp),
@@ -423,8 +422,10 @@ def balance_loss_backward(grad_loss, scores, counts, n_tokens, top_k: int, token
         _mask(token_mask, tokens)
     grad_stride = experts if grad_out is None else _grad_stride(scores, grad_out)
     index = _device(scores, counts, n_tokens, grad_loss, token_mask, grad_out)
-    grad = grad_out if grad_out is not None else _allocate(
-        stream, lambda: torch.empty((tokens, experts), dtype=scores.dtype, device=scores.device))
+    grad = grad_out
+    if grad is None:
+        with _on(stream):
+            grad = torch.empty((tokens, experts), dtype=scores.dtype, device=scores.device)
     args = BalanceArgs(scores.data_ptr(), stride, tokens, None, 0, _ptr(token_mask), None, None,
                        counts.data_ptr(), n_tokens.data_ptr(), grad.data_ptr(), grad_stride, None,
                        0, kind, experts, 0, top_k, 1.0)
