@@ -156,25 +156,31 @@ __device__ __forceinline__ void load_targets(const RowLossArgs& a, int64_t row, 
   if (MODE != kLossBwd) acc = warp_sum(acc);
   // A column named twice: its first entry gets the sum, in the entries'
   // order, and the others are dropped.  Lists of a sort name none twice, so
-  // the columns are first looked up in a table; only a list that does repeat
-  // one is compared entry by entry.
+  // the columns are first matched across the warp, or looked up in a table;
+  // only a list that does repeat one is compared entry by entry.
   if (MODE != kLossFwd && a.k > 1) {
-    const int n = target_slots(a.k);
-    for (int i = lane; i < n; i += kWarp) slots[i] = -1;
-    __syncwarp();
     bool twice = false;
-    for (int k = lane; k < a.k; k += kWarp) {
-      const int col = t.col[k];
-      if (col < 0) continue;
-      int at = static_cast<int>((static_cast<uint32_t>(col) * 2654435769u) >> 7) & (n - 1);
-      for (int probe = 0; probe < n; ++probe) {  // the table is at most half full
-        const int was = atomicCAS(&slots[at], -1, col);
-        if (was == -1) break;
-        if (was == col) {
-          twice = true;
-          break;
+    if (a.k <= kWarp) {
+      const int col = lane < a.k ? t.col[lane] : -1;
+      const unsigned same = __match_any_sync(kFull, col);
+      twice = col >= 0 && (same & (same - 1)) != 0;
+    } else {
+      const int n = target_slots(a.k);
+      for (int i = lane; i < n; i += kWarp) slots[i] = -1;
+      __syncwarp();
+      for (int k = lane; k < a.k; k += kWarp) {
+        const int col = t.col[k];
+        if (col < 0) continue;
+        int at = static_cast<int>((static_cast<uint32_t>(col) * 2654435769u) >> 7) & (n - 1);
+        for (int probe = 0; probe < n; ++probe) {  // the table is at most half full
+          const int was = atomicCAS(&slots[at], -1, col);
+          if (was == -1) break;
+          if (was == col) {
+            twice = true;
+            break;
+          }
+          at = (at + 1) & (n - 1);
         }
-        at = (at + 1) & (n - 1);
       }
     }
     if (__any_sync(kFull, twice)) {
@@ -260,12 +266,14 @@ __device__ __forceinline__ void store_result(const RowLossArgs& a, int64_t row,
 
 // ---------------------------------------------------------------- short rows
 // One CTA per row, the row in registers: rows of at most kThreads * VECS
-// 16-byte vectors (8 KB and 32 KB).  Many CTAs per SM hide each other's loads
-// and reductions, so registers are held to what 32 warps per SM leave: bf16
-// gradients of 16,384 x 16,000 took 190 us, 199 with 24 warps and 239 with
-// 16.  What bounds it is the chain of a CTA (targets, maximum, sum, gradient)
-// against the few KB it moves; 157 us is the time of the bytes.
-constexpr int kShortWarps = 32;
+// 16-byte vectors.  Many CTAs per SM hide each other's loads and reductions:
+// as few threads per row as 8 vectors each allow, and registers held to what
+// 24 warps per SM leave (bf16 policy gradients of 8,000 x 7,000 took 50 us; 56
+// with 20 warps, 52 with 32, and 78 by 256 threads per row; 16,384 x 16,000
+// 191 us, 236 with 20 warps).  What bounds it is the chain of a CTA (targets,
+// maximum, sum, gradient) against the few KB it moves: 34 and 157 us are the
+// times of the bytes.
+constexpr int kShortWarps = 24;
 template <int TYPE, int OP, int MODE, int kThreads, int VECS>
 __global__ void __launch_bounds__(kThreads, kShortWarps / (kThreads / kWarp))
     row_loss_short_kernel(const RowLossArgs a) {
@@ -1134,12 +1142,17 @@ cudaError_t launch_row_loss_as(const RowLossArgs& a, cudaStream_t s) {
   const size_t lists = static_cast<size_t>(a.k) * 12 + static_cast<size_t>(target_slots(a.k)) * 4;
   // vectors of a row, wherever it begins
   const int64_t vecs = (a.cols + 2 * (ScoreVec<TYPE>::kCount - 1)) / ScoreVec<TYPE>::kCount;
-  if (vecs <= 128 * 4)
-    return launch_kernel(row_loss_short_kernel<TYPE, OP, MODE, 128, 4>,
-                         dim3(static_cast<unsigned>(a.rows)), dim3(128), lists, s, a);
+  const dim3 each(static_cast<unsigned>(a.rows));
+  if (vecs <= 64 * 4)
+    return launch_kernel(row_loss_short_kernel<TYPE, OP, MODE, 64, 4>, each, dim3(64), lists, s, a);
+  if (vecs <= 64 * 8)
+    return launch_kernel(row_loss_short_kernel<TYPE, OP, MODE, 64, 8>, each, dim3(64), lists, s, a);
+  if (vecs <= 128 * 8)
+    return launch_kernel(row_loss_short_kernel<TYPE, OP, MODE, 128, 8>, each, dim3(128), lists, s,
+                         a);
   if (vecs <= 256 * 8)
-    return launch_kernel(row_loss_short_kernel<TYPE, OP, MODE, 256, 8>,
-                         dim3(static_cast<unsigned>(a.rows)), dim3(256), lists, s, a);
+    return launch_kernel(row_loss_short_kernel<TYPE, OP, MODE, 256, 8>, each, dim3(256), lists, s,
+                         a);
   const int sms = device_sm_count();
   if constexpr (MODE != kLossGrad) {
     int split = 1;
