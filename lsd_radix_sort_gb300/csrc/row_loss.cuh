@@ -275,7 +275,7 @@ __device__ __forceinline__ void store_result(const RowLossArgs& a, int64_t row,
 // times of the bytes.
 constexpr int kShortWarps = 24;
 template <int TYPE, int OP, int MODE, int kThreads, int VECS>
-__global__ void __launch_bounds__(kThreads, kShortWarps / (kThreads / kWarp))
+__global__ void __launch_bounds__(kThreads, VECS == 16 ? 2 : kShortWarps / (kThreads / kWarp))
     row_loss_short_kernel(const RowLossArgs a) {
   grid_dependency_sync();
   using S = Score<TYPE>;
@@ -684,6 +684,12 @@ __device__ __forceinline__ bool row_wait_cluster(uint64_t* bar, uint32_t parity,
   return wait_phase<true>(bar, parity, failed);
 }
 
+__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)),
+               "r"(bytes)
+               : "memory");
+}
+
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
@@ -825,29 +831,44 @@ __global__ void __launch_bounds__(kRowThreads, 1)
     int slot = 0;
     uint32_t use = 0;  // times round the ring
     Way way{0, 0, false};
-    for (int row; (row = next_row(way)) >= 0;) {
+    bool going = true;
+    for (int row; going && (row = next_row(way)) >= 0;) {
       if (way.off) continue;
-      if (lane == 0) {
-        const Segment s = segment(row);
-        const uint4* xv = reinterpret_cast<const uint4*>(s.x - s.vecs.lead);
-        // every chunk, then those that do not stay once more
-        for (int i = 0; i < 2 * s.chunks - s.keep; ++i) {
-          if (use > 0 && !row_wait(&sh->empty[slot], (use - 1) & 1, &sh->failed)) break;
-          const int first = s.begin + (i < s.chunks ? i : i - s.chunks) * kChunkVecs;
-          const int b = max(first, s.vecs.whole_begin());
-          const int e = min(min(first + kChunkVecs, s.end), s.vecs.whole_end());
-          const uint32_t bytes = e > b ? static_cast<uint32_t>(e - b) * 16u : 0u;
-          mbar_arrive_expect_tx(&sh->full[slot], bytes);
-          if (bytes != 0)
-            bulk_copy_g2s(ring + slot * kChunkBytes + (b - first) * 16, xv + b, bytes,
+      const Segment s = segment(row);
+      const uint4* xv = reinterpret_cast<const uint4*>(s.x - s.vecs.lead);
+      const int tail = s.vecs.count - 1;  // the last vector, and whether it is part of the row
+      const bool ragged_tail = s.vecs.whole_end() < s.vecs.count;
+      // every chunk, then those that do not stay once more
+      for (int i = 0; i < 2 * s.chunks - s.keep; ++i) {
+        const int first = s.begin + (i < s.chunks ? i : i - s.chunks) * kChunkVecs;
+        const int last = min(first + kChunkVecs, s.end);
+        const int b = max(first, s.vecs.whole_begin()), e = min(last, s.vecs.whole_end());
+        unsigned char* to = ring + slot * kChunkBytes;
+        bool ok = true;
+        if (lane == 0) {
+          if (use > 0) ok = row_wait(&sh->empty[slot], (use - 1) & 1, &sh->failed);
+          if (ok && e > b) {
+            mbar_expect_tx(&sh->full[slot], static_cast<uint32_t>(e - b) * 16u);
+            bulk_copy_g2s(to + (b - first) * 16, xv + b, static_cast<uint32_t>(e - b) * 16u,
                           &sh->full[slot]);
-          if (++slot == ring_slots) {
-            slot = 0;
-            ++use;
           }
         }
+        going = __shfl_sync(kFull, ok, 0);
+        if (!going) break;
+        // Vectors at the row's ends that are not whole are put together here,
+        // one lane per score, ahead of the warps that would wait for each load
+        // (3,000 bf16 rows of 49,153 took 153 us so, 49,152 took 116).
+        if (s.vecs.lead != 0 && first == 0)
+          s.vecs.copy_edge(s.x, 0, to, lane);
+        if (ragged_tail && tail >= first && tail < last && (tail != 0 || s.vecs.lead == 0))
+          s.vecs.copy_edge(s.x, tail, to + (tail - first) * 16, lane);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->full[slot]);
+        if (++slot == ring_slots) {
+          slot = 0;
+          ++use;
+        }
       }
-      __syncwarp();
     }
     if (sh->failed && lane == 0)  // copies in flight end before the CTA does
       for (int i = 0; i < ring_slots; ++i)
@@ -904,29 +925,32 @@ __global__ void __launch_bounds__(kRowThreads, 1)
     const float scale2 = a.inv_tau * kLog2e;
     int slot = 0, hi = 0;
     uint32_t phase = 0, head_phase = 0, parity = 0;  // parity: of the rows read
-    // a chunk's vectors of this thread, from their slot (or, at an edge of the
-    // row, score by score from memory)
-    auto fetch = [&](const Segment& s, int at, int first, bool inner, uint4 (&r)[kChunkUnits]) {
+    // A chunk's vectors of this thread from their slot: all of them, or one
+    // (-inf past the segment's end).
+    auto fetch = [&](int at, uint4 (&r)[kChunkUnits]) {
       const uint4* from = reinterpret_cast<const uint4*>(ring + at * kChunkBytes) + tid;
-      if (inner) {
 #pragma unroll
-        for (int u = 0; u < kChunkUnits; ++u) r[u] = from[u * kRowConsumers];
-        return;
-      }
-#pragma unroll
-      for (int u = 0; u < kChunkUnits; ++u) {
-        const int v = first + tid + u * kRowConsumers;
-        if (v >= s.end)
-          r[u] = make_uint4(V::kMinusInf, V::kMinusInf, V::kMinusInf, V::kMinusInf);
-        else if (s.vecs.whole(v))
-          r[u] = from[u * kRowConsumers];
-        else
-          r[u] = s.vecs.load_edge(s.x, v);
-      }
+      for (int u = 0; u < kChunkUnits; ++u) r[u] = from[u * kRowConsumers];
     };
-    auto release = [&](int at) {
+    auto fetch_one = [&](const Segment& s, int at, int u, int v) {
+      if (v >= s.end) return make_uint4(V::kMinusInf, V::kMinusInf, V::kMinusInf, V::kMinusInf);
+      return reinterpret_cast<const uint4*>(ring + at * kChunkBytes)[tid + u * kRowConsumers];
+    };
+    // Gives a slot back once every lane holds what it read from it.  Arriving
+    // on the barrier does not wait for reads that are still queued (behind
+    // stores that memory holds up, for microseconds), and the next copy would
+    // overtake them; so which lane arrives depends on the data themselves:
+    // `read` joins the ends of every vector read.
+    auto release = [&](int at, uint32_t read) {
+      const int who = __any_sync(kFull, read == 0x7FADC0DEu) ? 1 : 0;  // either will do
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->empty[at]);
+      if (lane == who) mbar_arrive(&sh->empty[at]);
+    };
+    auto join = [](const uint4 (&r)[kChunkUnits]) {
+      uint32_t w = r[0].x ^ r[0].w;
+#pragma unroll
+      for (int u = 1; u < kChunkUnits; ++u) w ^= r[u].x ^ r[u].w;
+      return w;
     };
     Way way{0, 0, false};
     for (int row; (row = next_row(way)) >= 0;) {
@@ -939,7 +963,8 @@ __global__ void __launch_bounds__(kRowThreads, 1)
           out.store(s.vecs, v, make_uint4(0, 0, 0, 0));
         continue;
       }
-      // chunks [inner0, inner1) lie in the segment and inside the row entirely
+      const int full_chunks = (s.end - s.begin) / kChunkVecs;
+      // of which chunks [inner0, inner1) consist of whole vectors
       const int inner0 = s.begin < s.vecs.whole_begin();
       const int inner1 = max(inner0, (min(s.end, s.vecs.whole_end()) - s.begin) / kChunkVecs);
       const int early = s.chunks - s.keep;  // chunks that do not stay
@@ -948,15 +973,27 @@ __global__ void __launch_bounds__(kRowThreads, 1)
       // ---- the maximum and the sum
       RunningSoftmax<TYPE> run(scale2);
       for (int c = 0; c < s.chunks; ++c) {
-        uint4 r[kChunkUnits];
         row_wait(&sh->full[slot], phase, &sh->failed);
-        fetch(s, slot, s.begin + c * kChunkVecs, c >= inner0 && c < inner1, r);
-        if (c < early) release(slot);
+        if (c < full_chunks) {
+          uint4 r[kChunkUnits];
+          fetch(slot, r);
+          if (c < early) release(slot, join(r));
+          run.add(r);
+        } else {
+          const int v = s.begin + c * kChunkVecs + tid;
+          uint32_t read = 0;
+#pragma unroll 1
+          for (int u = 0; u < kChunkUnits && v - lane + u * kRowConsumers < s.end; ++u) {
+            const uint4 r[1] = {fetch_one(s, slot, u, v + u * kRowConsumers)};
+            run.add(r);
+            read ^= r[0].x ^ r[0].w;
+          }
+          if (c < early) release(slot, read);
+        }
         if (++slot == ring_slots) {
           slot = 0;
           phase ^= 1;
         }
-        run.add(r);
       }
       Softmax st = warp_join(run.result(), scale2);
       Softmax* part = sh->part[parity];
@@ -999,33 +1036,42 @@ __global__ void __launch_bounds__(kRowThreads, 1)
         // a chunk that stayed was waited for in the first pass
         const bool ok = i < s.keep || row_wait(&sh->full[at], ph, &sh->failed);
         const uint64_t fc = ok ? ff : pack2(NAN, NAN);
-        uint4 r[kChunkUnits];
-        fetch(s, at, begin, inner, r);
-        release(at);
+        auto result = [&](const uint4& x) {  // zero also where the row holds NaN
+          return res.c == 0.0f ? make_uint4(0, 0, 0, 0) : vec_grad<TYPE>(x, e, fc);
+        };
+        if (inner) {
+          uint4 r[kChunkUnits];
+          fetch(at, r);
+          release(at, join(r));
+#pragma unroll
+          for (int u = 0; u < kChunkUnits; ++u) r[u] = result(r[u]);
+          if (out.shift == 0) {
+#pragma unroll
+            for (int u = 0; u < kChunkUnits; ++u) out.vec0[begin + tid + u * kRowConsumers] = r[u];
+          } else {
+#pragma unroll
+            for (int u = 0; u < kChunkUnits; ++u)
+              out.store_shifted(begin + tid + u * kRowConsumers, r[u]);
+          }
+        } else {
+          const int lo = s.vecs.whole_begin(), up = min(s.end, s.vecs.whole_end());
+          uint32_t read = 0;
+#pragma unroll 1
+          for (int u = 0; u < kChunkUnits; ++u) {
+            const int v = begin + tid + u * kRowConsumers, v0 = v - lane;  // v0: of the warp
+            if (v0 >= s.end) break;
+            const uint4 x = fetch_one(s, at, u, v), y = result(x);
+            read ^= x.x ^ x.w;
+            if (out.shift != 0 && v0 >= lo && v0 + kWarp <= up)
+              out.store_shifted(v, y);
+            else if (v < s.end)
+              out.store(s.vecs, v, y);
+          }
+          release(at, read);
+        }
         if (++at == ring_slots) {
           at = 0;
           ph ^= 1;
-        }
-        if (res.c == 0.0f) {  // also where the row holds NaN
-#pragma unroll
-          for (int u = 0; u < kChunkUnits; ++u) r[u] = make_uint4(0, 0, 0, 0);
-        } else {
-#pragma unroll
-          for (int u = 0; u < kChunkUnits; ++u) r[u] = vec_grad<TYPE>(r[u], e, fc);
-        }
-        if (inner && out.shift == 0) {
-#pragma unroll
-          for (int u = 0; u < kChunkUnits; ++u) out.vec0[begin + tid + u * kRowConsumers] = r[u];
-        } else if (inner) {
-#pragma unroll
-          for (int u = 0; u < kChunkUnits; ++u)
-            out.store_shifted(begin + tid + u * kRowConsumers, r[u]);
-        } else {
-#pragma unroll
-          for (int u = 0; u < kChunkUnits; ++u) {
-            const int v = begin + tid + u * kRowConsumers;
-            if (v < s.end) out.store(s.vecs, v, r[u]);
-          }
         }
       }
       slot = at;
@@ -1140,8 +1186,11 @@ cudaError_t launch_row_loss_as(const RowLossArgs& a, cudaStream_t s) {
   constexpr int kEs = sizeof(typename Score<TYPE>::Raw);
   const int64_t bytes = a.cols * kEs;
   const size_t lists = static_cast<size_t>(a.k) * 12 + static_cast<size_t>(target_slots(a.k)) * 4;
-  // vectors of a row, wherever it begins
-  const int64_t vecs = (a.cols + 2 * (ScoreVec<TYPE>::kCount - 1)) / ScoreVec<TYPE>::kCount;
+  // vectors of a row: one more where rows begin inside one
+  constexpr int kN = ScoreVec<TYPE>::kCount;
+  const bool aligned = reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 &&
+                       (a.rows == 1 || a.stride % kN == 0);
+  const int64_t vecs = (a.cols + (aligned ? 1 : 2) * (kN - 1)) / kN;
   const dim3 each(static_cast<unsigned>(a.rows));
   if (vecs <= 64 * 4)
     return launch_kernel(row_loss_short_kernel<TYPE, OP, MODE, 64, 4>, each, dim3(64), lists, s, a);
@@ -1154,6 +1203,13 @@ cudaError_t launch_row_loss_as(const RowLossArgs& a, cudaStream_t s) {
     return launch_kernel(row_loss_short_kernel<TYPE, OP, MODE, 256, 8>, each, dim3(256), lists, s,
                          a);
   const int sms = device_sm_count();
+  // Rows of 32 to 64 KB, where there are enough of them for two CTAs per SM:
+  // f16 policy gradients of 2,000 x 30,011 took 63 us so and 89 us in the ring,
+  // 300 x 30,000 7.8 and 11.4.  (The forms that read a row once need not keep
+  // it.)
+  if (MODE == kLossGrad && vecs <= 256 * 16 && a.rows >= 300)
+    return launch_kernel(row_loss_short_kernel<TYPE, OP, MODE, 256, 16>, each, dim3(256), lists, s,
+                         a);
   if constexpr (MODE != kLossGrad) {
     int split = 1;
     while (split < kMaxCluster && a.rows * split < int64_t(sms) * kStreamCtas * kStreamWaves &&

@@ -353,6 +353,16 @@ struct RowVecs {
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
 
+  // The same to 16 bytes of shared memory, one lane per score.
+  __device__ __forceinline__ void copy_edge(const Raw* row, int v, void* to, int lane) const {
+    if (lane < kN) {
+      const int64_t j = static_cast<int64_t>(v) * kN - lead + lane;
+      static_cast<Raw*>(to)[lane] = j >= 0 && j < cols
+                                        ? row[j]
+                                        : static_cast<Raw>(ScoreVec<TYPE>::kMinusInf);
+    }
+  }
+
   // Any vector, score by score.
   __device__ __forceinline__ void store_scores(Raw* row, int v, const uint4& x) const {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};

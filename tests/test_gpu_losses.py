@@ -472,6 +472,21 @@ def test_long_lists_of_long_rows(rs, k):
     check_distill(rs, x, xd, values, indices)
 
 
+@pytest.mark.parametrize("rows,cols,dtype", [(1000, 65536, torch.bfloat16), (1000, 100003, torch.float16),
+                                             (160, 400000, torch.float32)])
+def test_long_rows_give_the_same_bits_under_load(rs, rows, cols, dtype):
+    """Copies run ahead of the threads that read the slots: a slot that is given
+    back too early would show as a line of another row's gradient, now and then
+    and only while memory is busy."""
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    x = (torch.randn(rows, cols, generator=g, device="cuda") * 3).to(dtype)
+    values, indices = torch.topk(x, 40, dim=1)
+    first = rs.distill_loss_grad(x, values, indices)
+    for _ in range(40):
+        again = rs.distill_loss_grad(x, values, indices)
+        assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
 def test_a_wait_that_runs_out_is_reported(rs):
     assert rs.row_wait_timeout_probe(3_000_000) == rs.RS_ERR_LOOKBACK_TIMEOUT
     x, xd, g = rows_of(3, 40000, torch.bfloat16, 18)  # and the next call is right
