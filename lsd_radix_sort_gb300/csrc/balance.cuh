@@ -130,10 +130,20 @@ __device__ __forceinline__ void count_ids(const BalanceArgs& a, int* hist, int64
   }
 }
 
+// A word at the same place in every CTA of the cluster (0 past its size), all
+// of the reads under way together.
+__device__ __forceinline__ void peer_words(const void* p, int size, uint32_t (&w)[kBalCluster]) {
+#pragma unroll
+  for (int r = 0; r < kBalCluster; ++r) w[r] = r < size ? peer_word(p, r) : 0u;
+}
+
 // The sum of a word of every CTA's histogram.
 __device__ __forceinline__ int cluster_count(const int* hist, int e, int size) {
+  uint32_t w[kBalCluster];
+  peer_words(hist + e, size, w);
   int n = 0;
-  for (int r = 0; r < size; ++r) n += static_cast<int>(peer_word(hist + e, r));
+#pragma unroll
+  for (int r = 0; r < kBalCluster; ++r) n += static_cast<int>(w[r]);
   return n;
 }
 
@@ -506,8 +516,11 @@ __global__ void __launch_bounds__(kBalThreads, kBalCtas)
         __syncthreads();
       if (blockIdx.x == 0) {  // the first CTA adds up, in rank order
         for (int e = tid; e < a.experts; e += kBalThreads) {
-          float p = sums[e];
-          for (int r = 1; r < size; ++r) p += __uint_as_float(peer_word(sums + e, r));
+          uint32_t w[kBalCluster];
+          peer_words(sums + e, size, w);
+          float p = 0.0f;
+#pragma unroll
+          for (int r = 0; r < kBalCluster; ++r) p += __uint_as_float(w[r]);
           p /= n;
           a.mean_probs[e] = p;
           loss += static_cast<float>(hist[e]) * each * p;
