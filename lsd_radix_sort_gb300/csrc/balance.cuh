@@ -30,9 +30,11 @@ namespace lsdrs {
 
 // Two CTAs of 8 warps per SM, two tokens per lane under way: with three CTAs,
 // one token each, bf16 gradients of 262,144 tokens and 256 experts took 80 us
-// instead of 68, with one token and two CTAs 76; 43 us is the time of the
-// bytes.  What bounds it is latency: about 20 instructions per score, a
-// quarter of them shuffles, at half the issue rate.
+// instead of 68, with one token and two CTAs 76; lanes per token known at
+// compile time took 2 us off that, and a pass among others takes 60 now, 8 of
+// them the counts.  43 us is the time of the bytes.  What bounds it is
+// latency: 13.5 instructions per score, of which the reductions over a
+// token's lanes are paid per 16 scores, at half the issue rate.
 constexpr int kBalThreads = 256;
 constexpr int kBalCtas = 2;               // per SM
 constexpr int kBalWarps = kBalThreads / kWarp;
@@ -41,7 +43,7 @@ constexpr int kBalCluster = 8;            // CTAs of a cluster, at most
 constexpr int kBalMaxHists = 19;          // clusters of the counting launch
 constexpr int kCountThreads = 1024;       // its threads per CTA
 // Scores up to which one cluster does the whole call (8,192 tokens of 64
-// experts: 14.6 us in one cluster, 9.7 in two launches; 32 of 8: 4.9 and 9.2).
+// experts: 14.6 us in one cluster, 9 in two launches; 32 of 8: 5 and 9).
 constexpr int64_t kBalSingle = int64_t(1) << 18;
 
 // Scratch: what the counting launch clears (the ticket, a flag for NaN, the

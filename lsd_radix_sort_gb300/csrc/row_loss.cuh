@@ -573,7 +573,13 @@ __global__ void __launch_bounds__(kStreamThreads + kWarp, kStreamCtas)
 // that keep everything, 326 us as single CTAs that copy 96 of 256 KB again.
 // Chunks of 16 KB, every wait and release twice as often, took 361 us for
 // 8,192 rows of 65,536 instead of 339; per-warp rings of 2 KB copies 437,
-// per-thread cp.async rings 434.
+// per-thread cp.async rings 434 (each pair measured in one run).
+//
+// What bounds it is HBM: 335 us for the distillation loss and gradient of
+// 4,096 x 131,072 with an eighth of the rows masked (90% of the measured copy
+// bandwidth), 322 us for the policy loss of 8,192 x 65,536 (93%).  Rows of
+// little more than a chunk or two pay for the exchange between their passes
+// (3,000 x 49,152: 116 us, 76%).
 //
 // Rows cost unequally (a masked row is not read), so they are not dealt out
 // beforehand: the grid has a CTA (cluster) per row, and a running one takes
