@@ -23,6 +23,7 @@ struct RowLossArgs {
   float* losses;
   float* lse;                      // written, or read by kLossBwd
   float inv_tau, tau;
+  float scale2, scale2_low;        // log2(e) / tau: rounded, and what that leaves
   // distill
   const void* top_values;
   int top_type;

@@ -78,6 +78,14 @@ rs_status rows_check(const void* logits, int64_t stride, int64_t rows, int64_t c
   return RS_OK;
 }
 
+void set_temperature(RowLossArgs* a, float t) {
+  const double scale = 1.4426950408889634074 / t;
+  a->tau = t;
+  a->inv_tau = 1.0f / t;
+  a->scale2 = static_cast<float>(scale);
+  a->scale2_low = static_cast<float>(scale - static_cast<double>(a->scale2));
+}
+
 rs_status distill(const rs_distill_args* p, const float* grad_losses, LossMode mode,
                   void* stream) {
   if (p == nullptr) return RS_ERR_INVALID;
@@ -106,8 +114,7 @@ rs_status distill(const rs_distill_args* p, const float* grad_losses, LossMode m
   a.grad_losses = grad_losses;
   a.losses = p->losses;
   a.lse = p->lse;
-  a.tau = p->temperature;
-  a.inv_tau = 1.0f / p->temperature;
+  set_temperature(&a, p->temperature);
   a.top_values = p->top_values;
   a.top_type = p->top_values_type;
   a.top_stride = p->top_values_stride;
@@ -148,8 +155,7 @@ rs_status policy(const rs_policy_args* p, const float* grad_losses, LossMode mod
   a.grad_losses = grad_losses;
   a.losses = p->losses;
   a.lse = p->lse;
-  a.tau = p->temperature;
-  a.inv_tau = 1.0f / p->temperature;
+  set_temperature(&a, p->temperature);
   a.actions = p->actions;
   a.index_bytes = p->index_bytes;
   a.k = 1;

@@ -90,7 +90,7 @@ __device__ __forceinline__ void load_targets(const RowLossArgs& a, int64_t row, 
     if (lane == 0) h->off = 1;
     return;
   }
-  const float scale2 = a.inv_tau * kLog2e;
+  const float scale2 = a.scale2;
   float vm = -INFINITY, xm = -INFINITY;
   // Columns and values of up to 256 entries are in flight together, then
   // their scores: two trips to memory, whatever the length up to there.
@@ -220,7 +220,7 @@ struct RowResult {
   float loss, logp, lse, c;
 };
 
-// kLossBwd: m is t * lse, sum is 1.
+// kLossBwd: m is the saved lse, sum is 1.
 template <int OP, int MODE>
 __device__ __forceinline__ RowResult row_result(const RowLossArgs& a, const Head& h, float m,
                                                 float sum) {
@@ -234,7 +234,9 @@ __device__ __forceinline__ RowResult row_result(const RowLossArgs& a, const Head
     r.loss = none ? 0.0f : a.tau * a.tau * h.w * (h.a + ((m - h.ref) * a.inv_tau + log_sum));
     r.c = none ? 0.0f : h.up * a.tau;
   } else {
-    const float logp = empty ? -INFINITY : (h.x0 - m) * a.inv_tau - log_sum;
+    const float logp = empty               ? -INFINITY
+                       : MODE == kLossBwd ? h.x0 / a.tau - m
+                                          : (h.x0 - m) * a.inv_tau - log_sum;
     const float adv = h.adv;
     const float ratio = expf(logp - h.old);
     const bool held = (adv > 0.0f && ratio > a.clip_high) || (adv < 0.0f && ratio < a.clip_low);
@@ -254,6 +256,15 @@ __device__ __forceinline__ RowResult row_result(const RowLossArgs& a, const Head
     r.c = empty ? 0.0f : -h.up * g * a.inv_tau;
   }
   return r;
+}
+
+// The exponentials of a row from its maximum, or (kLossBwd) its saved lse.
+template <int TYPE, int MODE>
+__device__ __forceinline__ auto exponent(const RowLossArgs& a, float m) {
+  if constexpr (MODE == kLossBwd)
+    return ExponentOfLse<TYPE == RS_SCORE_F32>(origin(m), a.tau, a.scale2, a.scale2_low);
+  else
+    return Exponent(origin(m), a.scale2);
 }
 
 template <int OP>
@@ -297,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, VECS == 16 ? 2 : kShortWarps / (kThr
   const RowVecs<TYPE> vecs(x, static_cast<int>(a.cols));
   const uint4* xv = reinterpret_cast<const uint4*>(x - vecs.lead);
   const RowOut<TYPE> out(g, vecs);
-  const float scale2 = a.inv_tau * kLog2e;
+  const float scale2 = a.scale2;
   if (row_off<OP>(a, row)) {
     if (MODE != kLossBwd && tid == 0) store_result<OP>(a, row, RowResult{0, 0, 0, 0});
     if (MODE != kLossFwd)
@@ -317,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, VECS == 16 ? 2 : kShortWarps / (kThr
   if (warp == kWarps - 1) load_targets<TYPE, OP, MODE>(a, row, t, slots, &head);
   Softmax s;
   if (MODE == kLossBwd) {
-    s = {a.lse[row] * a.tau, 1.0f};
+    s = {a.lse[row], 1.0f};
     __syncthreads();
   } else {
     RunningSoftmax<TYPE> run(scale2);
@@ -331,8 +342,8 @@ __global__ void __launch_bounds__(kThreads, VECS == 16 ? 2 : kShortWarps / (kThr
   const RowResult res = row_result<OP, MODE>(a, head, s.m, s.sum);
   if (MODE != kLossBwd && tid == 0) store_result<OP>(a, row, res);
   if (MODE == kLossFwd) return;
-  const float o = origin(s.m), f = res.c / s.sum;
-  const Exponent e(o, scale2);
+  const float f = res.c / s.sum;
+  const auto e = exponent<TYPE, MODE>(a, s.m);
   const uint64_t ff = pack2(f * e.mend, f * e.mend);
 #pragma unroll
   for (int u = 0; u < VECS; ++u) {
@@ -344,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, VECS == 16 ? 2 : kShortWarps / (kThr
   __syncthreads();
   for (int k = tid; k < a.k; k += kThreads)
     if (t.col[k] >= 0)
-      g[t.col[k]] = S::store(exp2_approx((t.x[k] - o) * scale2) * f - res.c * t.p[k]);
+      g[t.col[k]] = S::store(e.one(t.x[k]) * f - res.c * t.p[k]);
 }
 
 // -------------------------------------------- long rows, one pass over a row
@@ -454,7 +465,7 @@ __global__ void __launch_bounds__(kStreamThreads + kWarp, kStreamCtas)
     if (rank == 0 && tid == 0) store_result<OP>(a, row, RowResult{0, 0, 0, 0});
     return;
   }
-  const float scale2 = a.inv_tau * kLog2e;
+  const float scale2 = a.scale2;
   if (warp == kStreamWarps) {
     if (rank == 0) load_targets<TYPE, OP, kLossFwd>(a, row, t, nullptr, &head);
   } else {
@@ -527,16 +538,15 @@ __global__ void __launch_bounds__(kStreamThreads + kWarp, kStreamCtas)
     load_targets<TYPE, OP, kLossBwd>(a, row, t, reinterpret_cast<int*>(t.x + a.k), &head);
   // the first loads are under way before the targets are known
   Stream<TYPE> stream(x, vecs, begin, off || warp == kStreamWarps ? begin : end, tid);
-  const float m = off ? 0.0f : a.lse[row] * a.tau;
+  const float m = off ? 0.0f : a.lse[row];
   __syncthreads();
   const float c = off ? 0.0f : row_result<OP, kLossBwd>(a, head, m, 1.0f).c;
-  const float o = origin(m), scale2 = a.inv_tau * kLog2e;
+  const auto e = exponent<TYPE, kLossBwd>(a, m);
   if (warp < kStreamWarps) {
     if (c == 0.0f) {  // nothing of the row is read
       const uint4 zero[kStreamBatch] = {};
       for (int v = begin + tid; v < end; v += kStreamThreads * kStreamBatch) put(v, zero);
     } else {
-      const Exponent e(o, scale2);
       const uint64_t f = pack2(c * e.mend, c * e.mend);
       stream.run([&](int v, uint4(&r)[kStreamBatch]) {
 #pragma unroll
@@ -552,7 +562,7 @@ __global__ void __launch_bounds__(kStreamThreads + kWarp, kStreamCtas)
   for (int k = tid; k < a.k; k += kStreamThreads + kWarp) {
     const int col = t.col[k];
     if (col >= 0 && col >= b && col < last)
-      g[col] = S::store(exp2_approx((t.x[k] - o) * scale2) * c - c * t.p[k]);
+      g[col] = S::store(e.one(t.x[k]) * c - c * t.p[k]);
   }
 }
 
@@ -928,7 +938,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
       if (lane == 0) mbar_arrive(&sh->head_full[i]);
     }
   } else {  // ---- consumers
-    const float scale2 = a.inv_tau * kLog2e;
+    const float scale2 = a.scale2;
     int slot = 0, hi = 0;
     uint32_t phase = 0, head_phase = 0, parity = 0;  // parity: of the rows read
     // A chunk's vectors of this thread from their slot: all of them, or one
@@ -1026,8 +1036,8 @@ __global__ void __launch_bounds__(kRowThreads, 1)
       if (sh->failed) res = RowResult{NAN, NAN, NAN, NAN};
       if (rank == 0 && tid == 0) store_result<OP>(a, row, res);
       // ---- the gradient: the chunks that stayed, then those copied again
-      const float o = origin(st.m), f = res.c / st.sum;
-      const Exponent e(o, scale2);
+      const float f = res.c / st.sum;
+      const Exponent e(origin(st.m), scale2);
       const uint64_t ff = pack2(f * e.mend, f * e.mend);
       int at = slot0 + early;
       uint32_t ph = phase0;
@@ -1089,7 +1099,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
           const int col = t.col[k];
           const int v = (col + s.vecs.lead) / V::kCount - s.begin;  // among the CTA's vectors
           if (col >= 0 && v >= 0 && v < s.end - s.begin && v / kWarp % kRowWarps == warp)
-            g[col] = S::store(exp2_approx((t.x[k] - o) * scale2) * f - res.c * t.p[k]);
+            g[col] = S::store(e.one(t.x[k]) * f - res.c * t.p[k]);
         }
         __syncwarp();
       }

@@ -9,7 +9,7 @@
 namespace lsdrs {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLog2eLow = static_cast<float>(1.4426950408889634 - static_cast<double>(kLog2e));
 
 // One score type: its raw word in memory and its conversions.
 template <int TYPE>
@@ -237,20 +237,57 @@ __device__ __forceinline__ uint4 vec_of(const uint64_t (&p)[ScoreVec<TYPE>::kCou
 // then, and below 2^65 by the least temperature) scores are at least 2^40
 // apart or equal, so any scale gives the same 0 or 1: 1 does.
 struct Exponent {
-  uint64_t scale2, neg_os2;
-  float mend;
+  float scale, os2, mend;
 
-  __device__ __forceinline__ Exponent(float o, float scale) {
-    float os2 = o * scale;
+  __device__ __forceinline__ Exponent(float o, float scale_) : scale(scale_), os2(o * scale_) {
     const bool far = isinf(os2) && !isinf(o);
-    os2 = far ? o : os2;
-    const float used = far ? 1.0f : scale;
-    scale2 = pack2(used, used);
-    neg_os2 = pack2(-os2, -os2);
+    if (far) {
+      os2 = o;
+      scale = 1.0f;
+    }
     mend = far ? 1.0f : exp2_approx(__fmaf_rn(-o, scale, os2));
   }
+  // the exponential of one score, put right
+  __device__ __forceinline__ float one(float x) const {
+    return exp2_approx(__fmaf_rn(x, scale, -os2)) * mend;
+  }
   __device__ __forceinline__ uint64_t of(uint64_t x) const {
-    return exp2_2(fma2(x, scale2, neg_os2));
+    return exp2_2(fma2(x, pack2(scale, scale), pack2(-os2, -os2)));
+  }
+};
+
+// exp2(x scale - lse log2 e) for a saved lse, which came from the temperature
+// itself: the rounding of scale would not cancel against it as it does against
+// a sum taken with the same scale, and is off by |x| scale 2^-24 in the
+// exponent.  So scale = hi + lo, and both products are added for 32-bit
+// scores (LOW; 16-bit results are rounded far above that).
+template <bool LOW>
+struct ExponentOfLse {
+  float hi, lo, os2, mend;
+
+  __device__ __forceinline__ ExponentOfLse(float lse, float tau, float hi_, float lo_)
+      : hi(hi_), lo(lo_), os2(lse * kLog2e) {
+    const float o = lse * tau;
+    if (isinf(os2) || isinf(o * hi)) {  // as above (or no score at all)
+      os2 = o;
+      hi = 1.0f;
+      lo = 0.0f;
+      mend = 1.0f;
+    } else {
+      mend = exp2_approx(__fmaf_rn(-lse, kLog2e, os2) - lse * kLog2eLow);
+    }
+  }
+  // -os2, with the low product (of a finite score: -inf * lo might be +inf)
+  __device__ __forceinline__ float rest(float x) const {
+    return LOW ? __fmaf_rn(fmaxf(x, -3.0e38f), lo, -os2) : -os2;
+  }
+  __device__ __forceinline__ float one(float x) const {
+    return exp2_approx(__fmaf_rn(x, hi, rest(x))) * mend;
+  }
+  __device__ __forceinline__ uint64_t of(uint64_t x) const {
+    float a, b;
+    unpack2(x, a, b);
+    return exp2_2(fma2(x, pack2(hi, hi), pack2(rest(a), rest(b))));
   }
 };
 
@@ -266,8 +303,8 @@ __device__ __forceinline__ void vec_exp_sum(const uint4& v, const Exponent& e,
 }
 
 // f times the exponentials of a vector, rounded to the scores' type.
-template <int TYPE>
-__device__ __forceinline__ uint4 vec_grad(const uint4& v, const Exponent& e, uint64_t f) {
+template <int TYPE, class E>
+__device__ __forceinline__ uint4 vec_grad(const uint4& v, const E& e, uint64_t f) {
   uint64_t p[ScoreVec<TYPE>::kCount / 2];
   vec_pairs<TYPE>(v, p);
 #pragma unroll
