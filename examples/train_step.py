@@ -30,7 +30,8 @@ class Student(torch.nn.Module):
         super().__init__()
 
         def weights(*shape):
-            return torch.nn.Parameter(torch.randn(*shape, generator=gen, device="cuda") * WIDTH ** -0.5)
+            drawn = torch.randn(*shape, generator=gen, device="cuda")
+            return torch.nn.Parameter(drawn * WIDTH ** -0.5)
 
         self.router = weights(WIDTH, EXPERTS)
         self.experts = weights(EXPERTS, WIDTH, WIDTH)
@@ -52,7 +53,8 @@ class Student(torch.nn.Module):
             at = order[begin:begin + n].long()
             begin += n
             token = at // TOP_K
-            out = out.index_add(0, token, torch.tanh(x[token] @ self.experts[expert]) * gates[at, None])
+            done = torch.tanh(x[token] @ self.experts[expert])
+            out = out.index_add(0, token, done * gates[at, None])
         return out @ self.head, balance, counts
 
 

@@ -31,9 +31,9 @@ namespace lsdrs {
 // Two CTAs of 8 warps per SM, two tokens per lane under way: with three CTAs,
 // one token each, bf16 gradients of 262,144 tokens and 256 experts took 80 us
 // instead of 68, with one token and two CTAs 76; lanes per token known at
-// compile time took 2 us off that, and a pass among others takes 60 now, 8 of
-// them the counts.  43 us is the time of the bytes.  What bounds it is
-// latency: 13.5 instructions per score, of which the reductions over a
+// compile time took 2 us off that, first scores under way during the counts
+// three, and a pass among others takes 57 now, some 6 of them the counts.  43 us is the time of the bytes.  What bounds it is
+// latency: 14.2 instructions per score, of which the reductions over a
 // token's lanes are paid per 16 scores, at half the issue rate.
 constexpr int kBalThreads = 256;
 constexpr int kBalCtas = 2;               // per SM
@@ -41,9 +41,13 @@ constexpr int kBalWarps = kBalThreads / kWarp;
 constexpr int kBalTurns = 4;              // warps that add to one row of sums
 constexpr int kBalCluster = 8;            // CTAs of a cluster, at most
 constexpr int kBalMaxHists = 19;          // clusters of the counting launch
-constexpr int kCountThreads = 1024;       // its threads per CTA
+// Its threads per CTA: their registers leave room for one CTA of the launch
+// that comes next, which then has its first scores when the counts are there
+// (bf16 gradients of 262,144 tokens and 256 experts: 62.4 us, 65.4 with 1,024
+// threads, 65.1 with 256, back to back; 8,192 tokens of 64: 7.9, 8.8 and 8.3).
+constexpr int kCountThreads = 512;
 // Scores up to which one cluster does the whole call (8,192 tokens of 64
-// experts: 14.6 us in one cluster, 9 in two launches; 32 of 8: 5 and 9).
+// experts: 14.6 us in one cluster, 8 in two launches; 32 of 8: 4.8 and 8).
 constexpr int64_t kBalSingle = int64_t(1) << 18;
 
 // Scratch: what the counting launch clears (the ticket, a flag for NaN, the
@@ -301,7 +305,56 @@ __global__ void __launch_bounds__(kBalThreads, kBalCtas)
   float* sums = reinterpret_cast<float*>(hist + a.experts + 1);  // kBalWarps / kBalTurns rows
   const int tid = static_cast<int>(threadIdx.x), lane = static_cast<int>(lane_id());
   const int warp = tid / kWarp;
+  const int sub = lane & (group - 1), in_warp = kWarp / group;
+  // A warp's tokens: batches of kTokens times in_warp, `step` apart.  The
+  // tokens' numbers fit 31 bits; pointers go along.
+  const int tokens = static_cast<int>(a.tokens);
+  const int64_t step = int64_t(gridDim.x) * kBalWarps * in_warp;
+  const int64_t first = (blockIdx.x * int64_t(kBalWarps) + warp) * in_warp + lane / group;
+  const Raw* x = static_cast<const Raw*>(a.logits) + first * a.stride + sub * kN;
+  Raw* g = static_cast<Raw*>(a.grad) + first * a.grad_stride + sub * kN;
+  const int64_t x_step = step * a.stride, g_step = step * a.grad_stride;
+  bool on[VECS];  // the lane's vectors that hold experts; the others stay -inf
+  typename B::Word raw[kTokens][VECS];
+#pragma unroll
+  for (int u = 0; u < VECS; ++u) {
+    on[u] = (u * group + sub) * kN < a.experts;
+#pragma unroll
+    for (int q = 0; q < kTokens; ++q) raw[q][u] = B::none();
+  }
+  // the batch at t: all of its tokens count (whole), or some may not
+  auto load = [&](int64_t t, bool whole) {
+#pragma unroll
+    for (int q = 0; q < kTokens; ++q) {
+      bool kept = true;
+      if (!whole) {
+        const int64_t at = t + q * step;
+        kept = at < tokens && (a.mask == nullptr || a.mask[at]);
+        if (!kept) {  // a token that the mask drops is one without scores
+#pragma unroll
+          for (int u = 0; u < VECS; ++u) raw[q][u] = B::none();
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < VECS; ++u)
+        if (kept && on[u]) raw[q][u] = B::load(x + u * group * kN);
+      x += x_step;
+    }
+  };
+  // past the last batch of which every lane's tokens exist (the same for the
+  // whole warp)
+  const int64_t warp_first = first - lane / group;
+  const int64_t whole_end =
+      a.mask == nullptr ? int64_t(tokens) - (in_warp - 1) - (kTokens - 1) * step : -1;
+  // The first batch is on its way while the counts come.  After a counting
+  // launch it is asked for before that launch has ended: the launch lets this
+  // one start only once all of its CTAs have waited for what came before it,
+  // the scores and the mask among that, and it writes neither.  (The backward
+  // call has little to wait for: 8.4 us with its loads after the counts for
+  // 32,767 f16 tokens of 160 experts, 9.1 before.)
+  if (MODE != kLossBwd && !single) load(first, warp_first < whole_end);
   grid_dependency_sync();
+  if (MODE != kLossBwd && single) load(first, warp_first < whole_end);
 
   // ---- the counts
   int tokens_kept;
@@ -349,7 +402,6 @@ __global__ void __launch_bounds__(kBalThreads, kBalCtas)
   // ---- the tokens
   float scale = a.scale / n;
   if (MODE == kLossBwd && a.grad_loss != nullptr) scale *= *a.grad_loss;
-  const int sub = lane & (group - 1), in_warp = kWarp / group;
   constexpr int kPairs = VECS * kN / 2;
   uint64_t acc2[kPairs];
 #pragma unroll
@@ -372,48 +424,8 @@ __global__ void __launch_bounds__(kBalThreads, kBalCtas)
       }
     }
   };
-  // A warp's tokens: batches of kTokens times in_warp, `step` apart.  The
-  // tokens' numbers fit 31 bits; pointers go along.
-  const int tokens = static_cast<int>(a.tokens);
-  const int64_t step = int64_t(gridDim.x) * kBalWarps * in_warp;
-  const int64_t first = (blockIdx.x * int64_t(kBalWarps) + warp) * in_warp + lane / group;
-  const Raw* x = static_cast<const Raw*>(a.logits) + first * a.stride + sub * kN;
-  Raw* g = static_cast<Raw*>(a.grad) + first * a.grad_stride + sub * kN;
-  const int64_t x_step = step * a.stride, g_step = step * a.grad_stride;
-  bool on[VECS];  // the lane's vectors that hold experts; the others stay -inf
-  typename B::Word raw[kTokens][VECS];
-#pragma unroll
-  for (int u = 0; u < VECS; ++u) {
-    on[u] = (u * group + sub) * kN < a.experts;
-#pragma unroll
-    for (int q = 0; q < kTokens; ++q) raw[q][u] = B::none();
-  }
-  // the batch at t: all of its tokens count (whole), or some may not
-  auto load = [&](int64_t t, bool whole) {
-#pragma unroll
-    for (int q = 0; q < kTokens; ++q) {
-      bool kept = true;
-      if (!whole) {
-        const int64_t at = t + q * step;
-        kept = at < tokens && (a.mask == nullptr || a.mask[at]);
-        if (!kept) {  // a token that the mask drops is one without scores
-#pragma unroll
-          for (int u = 0; u < VECS; ++u) raw[q][u] = B::none();
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < VECS; ++u)
-        if (kept && on[u]) raw[q][u] = B::load(x + u * group * kN);
-      x += x_step;
-    }
-  };
-  // past the last batch of which every lane's tokens exist (the same for the
-  // whole warp)
-  const int64_t warp_first = first - lane / group;
-  const int64_t whole_end =
-      a.mask == nullptr ? int64_t(tokens) - (in_warp - 1) - (kTokens - 1) * step : -1;
   int64_t at = warp_first;
-  load(first, at < whole_end);
+  if (MODE == kLossBwd) load(first, at < whole_end);
   for (; at < tokens; at += step * kTokens) {
     uint64_t v[kTokens][kPairs];
     float m[kTokens], sum[kTokens], dot[kTokens];

@@ -587,7 +587,7 @@ __global__ void __launch_bounds__(kStreamThreads + kWarp, kStreamCtas)
 //
 // What bounds it is HBM: 335 us for the distillation loss and gradient of
 // 4,096 x 131,072 with an eighth of the rows masked (90% of the measured copy
-// bandwidth), 322 us for the policy loss of 8,192 x 65,536 (93%).  Rows of
+// bandwidth), 319 us for the policy loss of 8,192 x 65,536 (94%).  Rows of
 // little more than a chunk or two pay for the exchange between their passes
 // (3,000 x 49,152: 116 us, 76%).
 //

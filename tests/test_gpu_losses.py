@@ -564,6 +564,36 @@ def test_balance_masked_scores_and_empty(rs):
     assert out[4].shape == (0, 20) and out[0].item() == 0
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_balance_reads_what_the_call_before_wrote(rs, dtype):
+    """The scores are asked for while the expert ids are still being counted:
+    they have to be those that the work queued before the call leaves."""
+    tokens, experts, k = 40001, 64, 4
+    g = torch.Generator(device="cuda").manual_seed(3)
+    sources = [(torch.randn(tokens, experts, generator=g, device="cuda") * 2).to(dtype) for _ in range(6)]
+    ids = torch.randint(0, experts, (tokens, k), generator=g, device="cuda")
+    mask = torch.rand(tokens, generator=g, device="cuda") < 0.8
+    up = torch.tensor([1e4], device="cuda")
+    _, counts, _, n = rs.balance_loss(sources[0], ids)
+    writes = [lambda to, s: to.copy_(s),
+              lambda to, s: rs.balance_loss_backward(up, s, counts, n, k, grad_out=to)]
+    for token_mask in (None, mask):
+        for write in writes:
+            want = []
+            for s in sources:
+                x = torch.empty_like(s)
+                write(x, s)
+                torch.cuda.synchronize()
+                want.append(rs.balance_loss_grad(x, ids, token_mask=token_mask))
+                torch.cuda.synchronize()
+            x, got = torch.empty_like(sources[0]), []
+            for s in sources:
+                write(x, s)
+                got.append(rs.balance_loss_grad(x, ids, token_mask=token_mask))
+            for a, b in zip(want, got):
+                assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
 def test_balance_nan_stays_in_its_gradient_row(rs):
     x, xd, g = rows_of(40, 20, torch.float32, 7)
     x[7, 3] = math.nan
