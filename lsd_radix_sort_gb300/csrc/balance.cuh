@@ -32,9 +32,10 @@ namespace lsdrs {
 // one token each, bf16 gradients of 262,144 tokens and 256 experts took 80 us
 // instead of 68, with one token and two CTAs 76; lanes per token known at
 // compile time took 2 us off that, first scores under way during the counts
-// three, and a pass among others takes 57 now, some 6 of them the counts.  43 us is the time of the bytes.  What bounds it is
-// latency: 14.2 instructions per score, of which the reductions over a
-// token's lanes are paid per 16 scores, at half the issue rate.
+// three, and a pass among others takes 57 now, the counts among them.  43 us
+// is the time of the bytes.  What bounds it is latency: 14.2 instructions per
+// score, of which the reductions over a token's lanes are paid per 16 scores,
+// at half the issue rate.
 constexpr int kBalThreads = 256;
 constexpr int kBalCtas = 2;               // per SM
 constexpr int kBalWarps = kBalThreads / kWarp;
