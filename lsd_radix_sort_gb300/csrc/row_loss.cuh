@@ -389,6 +389,15 @@ __device__ __forceinline__ void store_peer(Softmax* at, uint32_t rank, const Sof
                : "memory");
 }
 
+// The two halves of a cluster's barrier, where it only has to be known that
+// every CTA has begun: another CTA's shared memory must not be touched before.
+__device__ __forceinline__ void cluster_begun() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
@@ -465,6 +474,7 @@ __global__ void __launch_bounds__(kStreamThreads + kWarp, kStreamCtas)
     if (rank == 0 && tid == 0) store_result<OP>(a, row, RowResult{0, 0, 0, 0});
     return;
   }
+  if (split > 1) cluster_begun();
   const float scale2 = a.scale2;
   if (warp == kStreamWarps) {
     if (rank == 0) load_targets<TYPE, OP, kLossFwd>(a, row, t, nullptr, &head);
@@ -483,6 +493,7 @@ __global__ void __launch_bounds__(kStreamThreads + kWarp, kStreamCtas)
   Softmax s{-INFINITY, 0.0f};
   if (warp == 0) s = warp_join(lane < kStreamWarps ? part[lane] : s, scale2);
   if (split > 1) {
+    cluster_wait();
     if (tid == 0) store_peer(&peer[rank], 0, s);
     cluster_sync();
     if (rank != 0) return;

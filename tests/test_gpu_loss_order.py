@@ -1,0 +1,54 @@
+"""The order of memory operations inside one call of a loss: CTAs of a cluster
+that begin apart, gradients written over the scores that others still read,
+copies that overtake reads.  Each call is repeated under load and compared bit
+by bit with a first one."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+def rows_of(rows, cols, dtype, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(rows, cols, generator=g, device="cuda") * 3).to(dtype), g
+
+
+def policy_of(x, g):
+    rows, cols = x.shape
+    actions = torch.randint(0, cols, (rows,), generator=g, device="cuda")
+    logp = torch.log_softmax(x.float(), 1).gather(1, actions[:, None])[:, 0]
+    old = logp + 0.1 * torch.randn(rows, generator=g, device="cuda")
+    return actions, old, torch.randn(rows, generator=g, device="cuda")
+
+
+class Load:
+    """Copies on a stream of their own, which keep memory and SMs busy."""
+
+    def __init__(self):
+        self.stream = torch.cuda.Stream()
+        self.a = torch.zeros(1 << 26, dtype=torch.int32, device="cuda")
+        self.b = torch.empty_like(self.a)
+        torch.cuda.synchronize()
+
+    def more(self, n=1):
+        with torch.cuda.stream(self.stream):
+            for _ in range(n):
+                self.b.copy_(self.a)
+
+
+def same(a, b):
+    return all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 65536), (7, 131072), (40, 50001), (70, 300000)])
+def test_losses_of_clusters_that_begin_apart(rs, rows, cols):
+    x, g = rows_of(rows, cols, torch.bfloat16)
+    actions, old, adv = policy_of(x, g)
+    values, indices = torch.topk(x, 20, dim=1)
+    first = rs.policy_loss(x, actions, old, adv), rs.distill_loss(x, values, indices)
+    load = Load()
+    for _ in range(30):
+        load.more()
+        assert same(first[0], rs.policy_loss(x, actions, old, adv))
+        assert same(first[1], rs.distill_loss(x, values, indices))
+    torch.cuda.synchronize()
