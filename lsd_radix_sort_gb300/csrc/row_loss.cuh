@@ -1031,6 +1031,11 @@ __global__ void __launch_bounds__(kRowThreads, 1)
       // every consumer warp has come here (a bounded wait, unlike bar.sync)
       warp_wait(&sh->together, parity, &sh->failed);
       st = warp_join(lane < kRowWarps ? part[lane] : Softmax{-INFINITY, 0.0f}, scale2);
+      // This CTA has read its targets before any CTA of the cluster learns the
+      // row's sum: the gradient may lie over the logits, and a CTA's targets
+      // are scores of all the others' segments.  (They are read rows ahead:
+      // the wait is over as a rule.)
+      const bool got_head = warp_wait(&sh->head_full[hi], head_phase, &sh->failed);
       if (split > 1) {
         if (tid < split) {  // thread i hands this CTA's part to CTA i
           store_peer(&sh->peer[parity][rank], tid, st);
@@ -1041,7 +1046,6 @@ __global__ void __launch_bounds__(kRowThreads, 1)
       }
       parity ^= 1;
       // ---- the coefficient
-      const bool got_head = warp_wait(&sh->head_full[hi], head_phase, &sh->failed);
       const Targets t = targets(hi);
       RowResult res = row_result<OP, kLossGrad>(a, sh->head[hi], st.m, st.sum);
       if (sh->failed) res = RowResult{NAN, NAN, NAN, NAN};

@@ -52,3 +52,49 @@ def test_losses_of_clusters_that_begin_apart(rs, rows, cols):
         assert same(first[0], rs.policy_loss(x, actions, old, adv))
         assert same(first[1], rs.distill_loss(x, values, indices))
     torch.cuda.synchronize()
+
+
+# rows too few for the SMs and rows of more than twice the ring are shared by a
+# cluster; the others are a CTA's each, in registers or in the ring
+IN_PLACE = [(1, 65536, torch.bfloat16), (3, 30000, torch.float16), (9, 50001, torch.float32),
+            (37, 131072, torch.bfloat16), (70, 65536, torch.bfloat16), (12, 400000, torch.float32),
+            (90, 400000, torch.float32), (200, 40000, torch.bfloat16), (320, 12000, torch.float32)]
+
+
+@pytest.mark.parametrize("rows,cols,dtype", IN_PLACE)
+def test_gradient_over_the_logits_under_load(rs, rows, cols, dtype):
+    """Every CTA of a cluster reads the targets' scores of the whole row: none
+    of them may be a gradient yet."""
+    x, g = rows_of(rows, cols, dtype, 1)
+    actions, old, adv = policy_of(x, g)
+    ref = old + 0.1
+    values, indices = torch.topk(x, 300, dim=1)  # a long list takes long to read
+    calls = [lambda y, out: rs.policy_loss_grad(y, actions, old, adv, ref, kl_coef=0.1, grad_out=out),
+             lambda y, out: rs.distill_loss_grad(y, values, indices, grad_out=out),
+             lambda y, out: rs.distill_loss_grad(y, values[:, :1], indices[:, :1], grad_out=out)]
+    want = [call(x, None) for call in calls]
+    load, y = Load(), torch.empty_like(x)
+    for _ in range(40):
+        load.more()
+        for call, expected in zip(calls, want):
+            y.copy_(x)
+            assert same(call(y, y), expected)
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("rows,cols,dtype", IN_PLACE)
+def test_backward_over_the_logits_under_load(rs, rows, cols, dtype):
+    x, g = rows_of(rows, cols, dtype, 2)
+    actions, old, adv = policy_of(x, g)
+    values, indices = torch.topk(x, 300, dim=1)
+    lse = rs.policy_loss(x, actions, old, adv)[2]
+    calls = [lambda y, out: rs.policy_loss_backward(None, y, lse, actions, old, adv, grad_out=out),
+             lambda y, out: rs.distill_loss_backward(None, y, lse, values, indices, grad_out=out)]
+    want = [call(x, None) for call in calls]
+    load, y = Load(), torch.empty_like(x)
+    for _ in range(20):
+        load.more()
+        for call, expected in zip(calls, want):
+            y.copy_(x)
+            assert torch.equal(call(y, y), expected)
+    torch.cuda.synchronize()
