@@ -856,7 +856,8 @@ __global__ void __launch_bounds__(kRowThreads, 1)
 
   if (warp == kProducerWarp) {
     int slot = 0;
-    uint32_t use = 0;  // times round the ring
+    uint32_t use = 0;        // times round the ring
+    uint32_t put_by_us = 0;  // slots (bits) that hold scores stored by this warp
     Way way{0, 0, false};
     bool going = true;
     for (int row; going && (row = next_row(way)) >= 0;) {
@@ -875,6 +876,9 @@ __global__ void __launch_bounds__(kRowThreads, 1)
         if (lane == 0) {
           if (use > 0) ok = row_wait(&sh->empty[slot], (use - 1) & 1, &sh->failed);
           if (ok && e > b) {
+            // plain stores to a slot come before the bulk copy over it, which
+            // is of another proxy
+            if (put_by_us >> slot & 1) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             mbar_expect_tx(&sh->full[slot], static_cast<uint32_t>(e - b) * 16u);
             bulk_copy_g2s(to + (b - first) * 16, xv + b, static_cast<uint32_t>(e - b) * 16u,
                           &sh->full[slot]);
@@ -885,10 +889,15 @@ __global__ void __launch_bounds__(kRowThreads, 1)
         // Vectors at the row's ends that are not whole are put together here,
         // one lane per score, ahead of the warps that would wait for each load
         // (3,000 bf16 rows of 49,153 took 153 us so, 49,152 took 116).
-        if (s.vecs.lead != 0 && first == 0)
+        if (e > b) put_by_us &= ~(1u << slot);
+        if (s.vecs.lead != 0 && first == 0) {
           s.vecs.copy_edge(s.x, 0, to, lane);
-        if (ragged_tail && tail >= first && tail < last && (tail != 0 || s.vecs.lead == 0))
+          put_by_us |= 1u << slot;
+        }
+        if (ragged_tail && tail >= first && tail < last && (tail != 0 || s.vecs.lead == 0)) {
           s.vecs.copy_edge(s.x, tail, to + (tail - first) * 16, lane);
+          put_by_us |= 1u << slot;
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->full[slot]);
         if (++slot == ring_slots) {

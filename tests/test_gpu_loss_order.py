@@ -98,3 +98,26 @@ def test_backward_over_the_logits_under_load(rs, rows, cols, dtype):
             y.copy_(x)
             assert torch.equal(call(y, y), expected)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("rows,cols,dtype", [(1000, 65537, torch.bfloat16), (600, 50003, torch.float32),
+                                             (1000, 70003, torch.float16)])
+def test_ragged_rows_give_the_same_bits_under_load(rs, rows, cols, dtype):
+    """The ends of rows that are no whole vectors are stored to their ring slots
+    by a warp, and the next bulk copy lands on them."""
+    x, g = rows_of(rows, cols, dtype, 3)
+    actions, old, adv = policy_of(x, g)
+    values, indices = torch.topk(x, 9, dim=1)
+    first = rs.policy_loss_grad(x, actions, old, adv), rs.distill_loss_grad(x, values, indices)
+    # the ends, against plain arithmetic: the last and first eight columns
+    q = torch.softmax(x.float(), 1)
+    target = torch.zeros_like(q).scatter_add_(1, indices, torch.softmax(values.float(), 1))
+    for part in (slice(0, 8), slice(cols - 8, cols)):
+        want = (q - target)[:, part]
+        u = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 0}[dtype]
+        # two 32-bit evaluations, each of at most 4e-4 relative (cols / 32 additions)
+        assert bool(((first[1][2][:, part].float() - want).abs()
+                     <= u * want.abs() + 8e-4 * (q + target)[:, part] + 2.0 ** -24).all())
+    for _ in range(30):
+        assert same(first[0], rs.policy_loss_grad(x, actions, old, adv))
+        assert same(first[1], rs.distill_loss_grad(x, values, indices))
