@@ -31,9 +31,8 @@ namespace lsdrs {
 // Two CTAs of 8 warps per SM, two tokens per lane under way: with three CTAs,
 // one token each, bf16 gradients of 262,144 tokens and 256 experts took 80 us
 // instead of 68, with one token and two CTAs 76; lanes per token known at
-// compile time took 2 us off that, first scores under way during the counts
-// three, and a pass among others takes 57 now, the counts among them.  43 us
-// is the time of the bytes.  What bounds it is latency: 14.2 instructions per
+// compile time took 2 us off that, and a pass among others takes 57 now, the
+// counts among them.  42 us is the time of the bytes.  What bounds it is latency: 14.2 instructions per
 // score, of which the reductions over a token's lanes are paid per 16 scores,
 // at half the issue rate.
 constexpr int kBalThreads = 256;
@@ -43,9 +42,10 @@ constexpr int kBalTurns = 4;              // warps that add to one row of sums
 constexpr int kBalCluster = 8;            // CTAs of a cluster, at most
 constexpr int kBalMaxHists = 19;          // clusters of the counting launch
 // Its threads per CTA: their registers leave room for one CTA of the launch
-// that comes next, which then has its first scores when the counts are there
-// (bf16 gradients of 262,144 tokens and 256 experts: 62.4 us, 65.4 with 1,024
-// threads, 65.1 with 256, back to back; 8,192 tokens of 64: 7.9, 8.8 and 8.3).
+// that comes next, which then has its first scores in L2 when the counts are
+// there (bf16 gradients of 262,144 tokens and 256 experts: 57.1 us, 58.1
+// without the prefetch; with scores read before the counts 62.4 back to back,
+// 65.4 with 1,024 threads here, 65.1 with 256).
 constexpr int kCountThreads = 512;
 // Scores up to which one cluster does the whole call (8,192 tokens of 64
 // experts: 14.6 us in one cluster, 8 in two launches; 32 of 8: 4.8 and 8).
@@ -348,14 +348,21 @@ __global__ void __launch_bounds__(kBalThreads, kBalCtas)
   const int64_t whole_end =
       a.mask == nullptr ? int64_t(tokens) - (in_warp - 1) - (kTokens - 1) * step : -1;
   // The first batch is on its way while the counts come.  After a counting
-  // launch it is asked for before that launch has ended: the launch lets this
-  // one start only once all of its CTAs have waited for what came before it,
-  // the scores and the mask among that, and it writes neither.  (The backward
-  // call has little to wait for: 8.4 us with its loads after the counts for
-  // 32,767 f16 tokens of 160 experts, 9.1 before.)
-  if (MODE != kLossBwd && !single) load(first, warp_first < whole_end);
+  // launch this one may begin before that has ended, and what was queued
+  // before it need not be visible yet: until the wait the scores are only
+  // brought to L2, where later writes to them are seen too, and read after it.
+  // (The backward call has little to wait for: 8.4 us with its loads after the
+  // counts for 32,767 f16 tokens of 160 experts, 9.1 before.)
+  if (MODE != kLossBwd && !single) {
+#pragma unroll
+    for (int q = 0; q < kTokens; ++q) {
+#pragma unroll
+      for (int u = 0; u < VECS; ++u)
+        if (first + q * step < tokens && on[u]) prefetch_l2(x + q * x_step + u * group * kN);
+    }
+  }
   grid_dependency_sync();
-  if (MODE != kLossBwd && single) load(first, warp_first < whole_end);
+  if (MODE != kLossBwd) load(first, warp_first < whole_end);
 
   // ---- the counts
   int tokens_kept;

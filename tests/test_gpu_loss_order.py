@@ -121,3 +121,40 @@ def test_ragged_rows_give_the_same_bits_under_load(rs, rows, cols, dtype):
     for _ in range(30):
         assert same(first[0], rs.policy_loss_grad(x, actions, old, adv))
         assert same(first[1], rs.distill_loss_grad(x, values, indices))
+
+
+def test_balance_reads_nothing_before_its_wait():
+    """The source of the balance kernel: no score and no mask byte is loaded
+    ahead of the wait for what was queued before it (a prefetch to L2 is no
+    read); a stale read would show only now and then."""
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                        "lsd_radix_sort_gb300", "csrc", "balance.cuh")
+    with open(path) as f:
+        source = f.read()
+    body = source[source.index("    balance_kernel(const BalanceArgs a"):]
+    before = body[:body.index("grid_dependency_sync();")]
+    calls = [line for line in before.split("\n") if "load(" in line and "auto load" not in line]
+    assert calls == ["        if (kept && on[u]) raw[q][u] = B::load(x + u * group * kN);"]  # load's own
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_balance_after_a_mask_was_written(rs, dtype):
+    """The mask and the scores are overwritten right before each call."""
+    tokens, experts, k = 50000, 64, 4
+    g = torch.Generator(device="cuda").manual_seed(4)
+    sources = [(torch.randn(tokens, experts, generator=g, device="cuda") * 2).to(dtype) for _ in range(5)]
+    masks = [torch.rand(tokens, generator=g, device="cuda") < 0.5 for _ in range(5)]
+    ids = torch.randint(0, experts, (tokens, k), generator=g, device="cuda")
+    want = []
+    for s, m in zip(sources, masks):
+        want.append(rs.balance_loss_grad(s, ids, token_mask=m))
+        torch.cuda.synchronize()
+    x, mask = torch.empty_like(sources[0]), torch.empty_like(masks[0])
+    for _ in range(10):
+        got = []
+        for s, m in zip(sources, masks):
+            x.copy_(s)
+            mask.copy_(m)
+            got.append(rs.balance_loss_grad(x, ids, token_mask=mask))
+        assert all(same(a, b) for a, b in zip(want, got))
