@@ -229,23 +229,33 @@ __device__ __forceinline__ uint4 vec_of(const uint64_t (&p)[ScoreVec<TYPE>::kCou
   return v;
 }
 
+// For an origin whose product with the scale is 2^30 or more (scores of -1e30
+// that mask, or a very small temperature): neighbouring scores are then at
+// least 2^6 apart in the exponent, so that only those equal to the origin
+// count, and the product is rounded by 2^7 and more, too far to be put right
+// by a factor.  Any scale gives the same 1 or 0 that keeps neighbours apart;
+// the power of two that takes the origin to [2^33, 2^34) does (2^9 at least
+// between neighbours), and its product with the origin is exact.
+__device__ __forceinline__ bool far_origin(float o, float os2) {
+  return !(fabsf(os2) < 1073741824.0f) && !isinf(o);
+}
+__device__ __forceinline__ float far_scale(float o) {
+  return __uint_as_float(((127u + 127u + 33u) << 23) - (__float_as_uint(o) & 0x7F800000u));
+}
+
 // exp2((x - o) scale) of pairs of scores.  One multiply-add per score takes
 // x * scale - os2 with os2 = o * scale rounded: the product is exact inside,
 // so the result is that of a slightly other origin, and `mend` = the factor
-// 2^(os2 - o scale) puts it right, once per sum.  Where o * scale overflows
-// (a row that holds nothing above the type's lowest value, say; scale > 1
-// then, and below 2^65 by the least temperature) scores are at least 2^40
-// apart or equal, so any scale gives the same 0 or 1: 1 does.
+// 2^(os2 - o scale) puts it right, once per sum.
 struct Exponent {
   float scale, os2, mend;
 
   __device__ __forceinline__ Exponent(float o, float scale_) : scale(scale_), os2(o * scale_) {
-    const bool far = isinf(os2) && !isinf(o);
-    if (far) {
-      os2 = o;
-      scale = 1.0f;
+    if (far_origin(o, os2)) {
+      scale = far_scale(o);
+      os2 = o * scale;
     }
-    mend = far ? 1.0f : exp2_approx(__fmaf_rn(-o, scale, os2));
+    mend = exp2_approx(__fmaf_rn(-o, scale, os2));
   }
   // the exponential of one score, put right
   __device__ __forceinline__ float one(float x) const {
@@ -268,7 +278,7 @@ struct ExponentOfLse {
   __device__ __forceinline__ ExponentOfLse(float lse, float tau, float hi_, float lo_)
       : hi(hi_), lo(lo_), os2(lse * kLog2e) {
     const float o = lse * tau;
-    if (isinf(os2) || isinf(o * hi)) {  // as above (or no score at all)
+    if (isinf(os2) || isinf(o * hi)) {  // (or no score at all)
       os2 = o;
       hi = 1.0f;
       lo = 0.0f;
@@ -314,8 +324,10 @@ __device__ __forceinline__ uint4 vec_grad(const uint4& v, const E& e, uint64_t f
 
 // A thread's softmax in progress over many vectors.  The origin is the
 // largest score of some vectors past; it moves only when a score exceeds it
-// by more than 2^60 would (so no sum overflows), which keeps the maximum off
-// the path of the exponentials.
+// by more than 2^30 would (so no sum overflows), which keeps the maximum off
+// the path of the exponentials.  (30 is less than half of what neighbouring
+// scores of a far origin are apart, so that the limit is then the origin
+// itself.)
 template <int TYPE>
 struct RunningSoftmax {
   float scale, o, limit;
@@ -334,7 +346,7 @@ struct RunningSoftmax {
   __device__ __forceinline__ void move(float m) {
     const float sum = total() * exp2_approx((o - m) * scale);
     o = m;
-    limit = m + 60.0f / scale;
+    limit = m + 30.0f / scale;
     e = Exponent(m, scale);
     acc[0] = pack2(sum / e.mend, 0.0f);
     acc[1] = 0;

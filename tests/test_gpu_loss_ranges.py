@@ -1,0 +1,132 @@
+"""The losses over the whole range of finite scores and temperatures: masks of
+-1e10, -1e30 and the type's lowest value, in part of a row and in all of it,
+large positive scores, small temperatures; every path of the row losses."""
+
+import pytest
+import torch
+
+from tests import loss_bounds as lb
+
+pytestmark = pytest.mark.gpu
+
+# registers of one CTA (short, odd, 32 to 64 KB), and rows beyond: clusters,
+# one CTA per row, few very long rows
+SHAPES = [(16, 3000), (16, 2051), (304, 12000), (304, 30000), (16, 40000), (160, 40000), (8, 400003)]
+FILLED = [(torch.bfloat16, (-1e10, -1e30, torch.finfo(torch.bfloat16).min)),
+          (torch.float32, (-1e10, -1e30, torch.finfo(torch.float32).min))]
+
+
+def scores(rows, cols, dtype, seed=0, spread=3.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(rows, cols, generator=g, device="cuda") * spread).to(dtype), g
+
+
+def masked(x, fill):
+    """Eight patterns of a finite mask, row after row; columns that stay."""
+    cols = x.shape[1]
+    kept = torch.ones_like(x, dtype=torch.bool)
+    kept[0::8, :cols // 2] = False
+    kept[1::8] = False                # the whole row
+    kept[2::8, :1024] = False         # the first vectors of every thread, or of many
+    kept[3::8, cols - 1024:] = False
+    kept[4::8] = False
+    kept[4::8, cols // 3] = True      # all but one
+    kept[5::8, ::2] = False
+    kept[6::8, 8:16] = False          # one vector
+    return torch.where(kept, x, torch.full_like(x, fill)), kept
+
+
+def some_columns(kept, k, g):
+    """k columns that the mask leaves (any, where it leaves none); entries that
+    would name a masked one are dropped."""
+    draw = torch.rand(kept.shape, generator=g, device="cuda") + kept
+    indices = draw.topk(k, dim=1).indices
+    alive = kept.gather(1, indices) | ~kept.any(1, keepdim=True)
+    return torch.where(alive, indices, torch.full_like(indices, -1))
+
+
+def check_distill(rs, x, tau, indices, g, backward=False, grad_out=None, weights=None, rows=None):
+    rows = lb.Rows(x, tau) if rows is None else rows
+    values = torch.randn(indices.shape, generator=g, device="cuda") * min(tau, 1.0)
+    losses, loss_bound, grad, bound = lb.distill(rows, x, values, indices, weights)
+    kw = {"temperature": tau, "weights": weights}
+    lse_bound = rows.lse_error()
+    fl, fs = rs.distill_loss(x, values, indices, **kw)
+    if backward:
+        lb.within(rs.distill_loss_backward(None, x, fs, values, indices, **kw), grad, bound, "backward")
+    gl, gs, gg = rs.distill_loss_grad(x, values, indices, grad_out=grad_out, **kw)
+    lb.within(fl, losses, loss_bound, "losses")
+    lb.within(gl, losses, loss_bound, "losses with gradient")
+    on = torch.ones_like(rows.lse) if weights is None else (weights != 0).double()
+    lb.within(fs, (rows.lse * on).float(), lse_bound, "lse")
+    lb.within(gs, (rows.lse * on).float(), lse_bound, "lse with gradient")
+    lb.within(gg, grad, bound, "gradient")
+
+
+def check_policy(rs, x, tau, actions, g, backward=False, weights=None, rows=None,
+                 kl=0.1):
+    rows = lb.Rows(x, tau) if rows is None else rows
+    n = x.shape[0]
+    logp = -rows.dist.gather(1, actions.long()[:, None])[:, 0] - rows.log_sum
+    old = (logp + torch.tensor([0.0, 0.1, -0.1, 0.5, -0.5], device="cuda").repeat(n)[:n]).float()
+    ref = (logp + 0.3 * torch.randn(n, generator=g, device="cuda")).float()
+    adv = torch.randn(n, generator=g, device="cuda")
+    losses, loss_bound, logp, logp_bound, grad, bound = lb.policy(rows, x, actions, old, adv, ref, kl=kl,
+                                                                        weights=weights)
+    kw = {"ref_logprobs": ref, "clip_low": 0.2, "clip_high": 0.28, "kl_coef": kl, "temperature": tau,
+          "weights": weights}
+    fl, fp, fs = rs.policy_loss(x, actions, old, adv, **kw)
+    if backward:
+        lb.within(rs.policy_loss_backward(None, x, fs, actions, old, adv, **kw), grad, bound, "backward")
+    gl, gp, gs, gg = rs.policy_loss_grad(x, actions, old, adv, **kw)
+    lb.within(fl, losses, loss_bound, "losses")
+    lb.within(gl, losses, loss_bound, "losses with gradient")
+    lb.within(fp, logp, logp_bound, "log-probabilities")
+    lb.within(gp, logp, logp_bound, "log-probabilities with gradient")
+    lb.within(fs, rows.lse.float(), rows.lse_error(), "lse")
+    lb.within(gs, rows.lse.float(), rows.lse_error(), "lse with gradient")
+    lb.within(gg, grad, bound, "gradient")
+
+
+@pytest.mark.parametrize("dtype,fills", FILLED)
+@pytest.mark.parametrize("tau", [0.7, 1.0, 2.0, 4.0])
+@pytest.mark.parametrize("n,cols", SHAPES)
+def test_finite_masks(rs, n, cols, tau, dtype, fills):
+    for fill in fills:
+        x, g = scores(n, cols, dtype, cols)
+        x, kept = masked(x, fill)
+        indices = some_columns(kept, 4, g)
+        check_distill(rs, x, tau, indices, g)
+        check_policy(rs, x, tau, indices.amax(1), g)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n,cols", [(16, 3000), (304, 12000), (16, 40000), (160, 40000)])
+def test_large_scores(rs, n, cols, dtype):
+    """Rows of one large value, and rows with one above the others."""
+    for size in (1e7, 1e9, 1e10, 1e20, 1e30):
+        x, g = scores(n, cols, dtype, 1)
+        x[0::3] = size
+        x[1::3] = -size
+        x[2::3, cols // 2] = size
+        indices = torch.randint(0, cols, (n, 4), generator=g, device="cuda")
+        indices[2::3] = cols // 2
+        indices[2::3, 1:] = -1
+        for tau in (0.5, 1.0, 3.0):
+            check_distill(rs, x, tau, indices, g)
+            check_policy(rs, x, tau, indices[:, 0].contiguous(), g)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("n,cols", [(16, 3000), (304, 12000), (16, 40000), (160, 40000)])
+def test_small_temperatures(rs, n, cols, dtype):
+    """Ordinary scores where only the largest counts."""
+    for tau in (1e-3, 1e-6, 1e-9, 1e-15, 6e-20):
+        x, g = scores(n, cols, dtype, 2)
+        rows = lb.Rows(x, tau)
+        indices = rows.q.topk(2, dim=1).indices
+        indices[:, 1] = -1
+        # gradients of the order of 1, which every type holds
+        check_distill(rs, x, tau, indices, g, rows=rows, weights=torch.full((n,), 1 / tau, device="cuda"))
+        check_policy(rs, x, tau, indices[:, 0].contiguous(), g, rows=rows,
+                     weights=torch.full((n,), tau, device="cuda"))
