@@ -447,12 +447,13 @@ __global__ void __launch_bounds__(kBalThreads, kBalCtas)
     group_reduce(m, group, [](float p, float r) { return fmaxf(p, r); });
 #pragma unroll
     for (int q = 0; q < kTokens; ++q) {
-      // exp2(x log2 e - o2), the rounding of o2 being the same for the whole
-      // token; where o2 overflows, scores are equal or far apart: any scale does
-      float o = origin(m[q]), o2 = o * kLog2e, s1 = kLog2e;
-      if (TYPE != RS_SCORE_F16 && isinf(o2) && !isinf(o)) {
-        o2 = o;
-        s1 = 1.0f;
+      // exp2(x log2 e - o2), the rounding of o2 (at most 2^5 but for a far
+      // origin) being the same for the whole token; f16 has no far scores
+      const float o = origin(m[q]);
+      float o2 = o * kLog2e, s1 = kLog2e;
+      if (TYPE != RS_SCORE_F16 && far_origin(o, o2)) {
+        s1 = far_scale(o);
+        o2 = o * s1;
       }
       const uint64_t neg_o2 = pack2(-o2, -o2), s2 = pack2(s1, s1);
       uint64_t total = 0, with = 0, sh2[kPairs];
@@ -473,7 +474,7 @@ __global__ void __launch_bounds__(kBalThreads, kBalCtas)
     if (MODE != kLossFwd) group_reduce(dot, group, [](float p, float r) { return p + r; });
 #pragma unroll
     for (int q = 0; q < kTokens; ++q) {
-      // 1 <= sum <= experts, NaN, or 0 for a token without scores
+      // 2^-32 <= sum <= 2^32 experts, NaN, or 0 for a token without scores
       const float inv = sum[q] == 0.0f ? 0.0f : __frcp_rn(sum[q]);
       if (MODE != kLossBwd) {
         const uint64_t inv2 = pack2(inv, inv);

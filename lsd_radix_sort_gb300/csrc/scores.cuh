@@ -232,8 +232,8 @@ __device__ __forceinline__ uint4 vec_of(const uint64_t (&p)[ScoreVec<TYPE>::kCou
 // For an origin whose product with the scale is 2^30 or more (scores of -1e30
 // that mask, or a very small temperature): neighbouring scores are then at
 // least 2^6 apart in the exponent, so that only those equal to the origin
-// count, and the product is rounded by 2^7 and more, too far to be put right
-// by a factor.  Any scale gives the same 1 or 0 that keeps neighbours apart;
+// count, and the product is rounded by 2^6 and more, soon too far to be put
+// right by a factor.  Any scale gives the same 1 or 0 that keeps neighbours apart;
 // the power of two that takes the origin to [2^33, 2^34) does (2^9 at least
 // between neighbours), and its product with the origin is exact.
 __device__ __forceinline__ bool far_origin(float o, float os2) {

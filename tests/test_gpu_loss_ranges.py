@@ -130,3 +130,53 @@ def test_small_temperatures(rs, n, cols, dtype):
         check_distill(rs, x, tau, indices, g, rows=rows, weights=torch.full((n,), 1 / tau, device="cuda"))
         check_policy(rs, x, tau, indices[:, 0].contiguous(), g, rows=rows,
                      weights=torch.full((n,), tau, device="cuda"))
+
+
+def balance64(x, ids, mask=None):
+    """(loss, mean probabilities, gradient, scale of its terms) in 64 bits."""
+    n, experts = x.shape
+    kept = torch.ones(n, dtype=torch.bool, device="cuda") if mask is None else mask
+    z = x.double()
+    p = (z - z.amax(1, keepdim=True)).exp()
+    p = p / p.sum(1, keepdim=True) * kept[:, None]
+    tokens = max(int(kept.sum()), 1)
+    counts = torch.bincount(ids[kept].reshape(-1), minlength=experts).double()
+    share = counts * experts / (ids.shape[1] * tokens)
+    mean = p.sum(0) / tokens
+    dot = (p @ share)[:, None]
+    return share @ mean, mean, p * (share - dot) / tokens, p * (share + dot) / tokens
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("tokens,experts", [(40, 20), (37, 8), (300, 64), (5000, 60), (6000, 128), (999, 257)])
+def test_balance_of_large_finite_scores(rs, tokens, experts, dtype):
+    """Tokens of equal scores are spread evenly, masked experts get nothing, and
+    no token drops out, however large the finite scores are."""
+    lowest = torch.finfo(dtype).min
+    for size in (-1e9, -1e10, -1e15, -1e20, -1e30, 1e10, 1e30, lowest, -lowest, -40000.0):
+        if abs(size) > -lowest:
+            continue
+        x, g = scores(tokens, experts, dtype, experts, 2.0)
+        x[0::5] = size                       # equal scores
+        x[1::5, experts // 2:] = min(size, -size)
+        x[2::5, 1:] = min(size, -size)
+        x[3::5, experts // 3] = max(size, -size)
+        ids = torch.randint(0, experts, (tokens, 2), generator=g, device="cuda")
+        mask = torch.rand(tokens, generator=g, device="cuda") < 0.8
+        for kept in (None, mask):
+            loss, mean, grad, terms = balance64(x, ids, kept)
+            out = rs.balance_loss_grad(x, ids, token_mask=kept)
+            back = rs.balance_loss_backward(None, x, out[1], out[3], 2, token_mask=kept)
+            only = rs.balance_loss(x, ids, token_mask=kept)
+            # a probability: its exponent's rounding over a spread of 16 nats,
+            # or over the 2^6 by which a large origin's product may be off;
+            # sums of up to 32 per lane and 5 steps; then sums over tokens
+            u = 2.0 ** -24 * (2 * 64 + 64 + 40)
+            for got in (out, only):
+                lb.within(got[2], mean, mean * (u + 2.0 ** -24 * (tokens / 8 + 64)) + 2.0 ** -60, "mean_probs")
+                lb.within(got[0], loss, loss * (u + 2.0 ** -24 * (tokens / 8 + experts + 64)), "loss")
+            round_to, tiny = {torch.bfloat16: (2.0 ** -8, 0), torch.float16: (2.0 ** -11, 2.0 ** -24),
+                              torch.float32: (2.0 ** -24, 0)}[dtype]
+            bound = terms * (2 * u + 32 * 2.0 ** -24) + grad.abs() * round_to * 1.01 + tiny + 2.0 ** -60
+            lb.within(out[4], grad, bound, "gradient")
+            lb.within(back, grad, bound, "backward")
