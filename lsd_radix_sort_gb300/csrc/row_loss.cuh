@@ -25,12 +25,18 @@ struct Targets {
   float* x;    // its score
 };
 
+// A distillation loss is added up in units of scores, a quarter of it at a
+// time: a target masked by the type's lowest value is twice that from the
+// largest score there may be, more than a float holds, and so is the lowest
+// value over a temperature below 1; weight and temperature come last.
+constexpr float kPart = 0.25f;
+
 // What the target warp hands to the threads that hold the row.
 struct Head {
   int off;       // weight 0 (or no action): the row is not read
   int live;      // 0: the row has no target
   float w, up;   // weight; weight times the upstream gradient
-  float a;       // distill: sum p (log p - (x - ref) / t)
+  float a;       // distill: t sum p (log p - (x - ref) / t), kPart of it
   float ref;     // the score that `a` is taken from: the largest target's,
                  // which is near the row's maximum, so that the loss is a sum
                  // of small terms instead of a difference of large ones
@@ -150,7 +156,7 @@ __device__ __forceinline__ void load_targets(const RowLossArgs& a, int64_t row, 
     const float v = t.p[k] - vm;
     const float p = sum == 0.0f ? 0.0f : exp2_approx(v * scale2) / sum;
     if (MODE != kLossBwd && p != 0.0f)
-      acc += p * (v * a.inv_tau - log_sum - (t.x[k] - xm) * a.inv_tau);
+      acc += p * (kPart * v - kPart * a.tau * log_sum - (kPart * t.x[k] - kPart * xm));
     t.p[k] = p;
   }
   if (MODE != kLossBwd) acc = warp_sum(acc);
@@ -231,7 +237,9 @@ __device__ __forceinline__ RowResult row_result(const RowLossArgs& a, const Head
   if (OP == kOpDistill) {
     const bool none = empty || !h.live;
     r.logp = 0.0f;
-    r.loss = none ? 0.0f : a.tau * a.tau * h.w * (h.a + ((m - h.ref) * a.inv_tau + log_sum));
+    r.loss = none ? 0.0f
+                  : a.tau * h.w / kPart *
+                        (h.a + (kPart * m - kPart * h.ref + kPart * a.tau * log_sum));
     r.c = none ? 0.0f : h.up * a.tau;
   } else {
     const float logp = empty               ? -INFINITY

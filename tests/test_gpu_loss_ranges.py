@@ -180,3 +180,25 @@ def test_balance_of_large_finite_scores(rs, tokens, experts, dtype):
             bound = terms * (2 * u + 32 * 2.0 ** -24) + grad.abs() * round_to * 1.01 + tiny + 2.0 ** -60
             lb.within(out[4], grad, bound, "gradient")
             lb.within(back, grad, bound, "backward")
+
+
+@pytest.mark.parametrize("dtype,fills", FILLED)
+@pytest.mark.parametrize("n,cols", [(16, 3000), (304, 12000), (16, 40000), (160, 40000)])
+def test_targets_on_masked_columns(rs, n, cols, dtype, fills):
+    """A teacher's entry on a column that the student masks: its loss is as
+    large as the mask, and infinite only where a float cannot hold it."""
+    for fill in fills:
+        x, g = scores(n, cols, dtype, 5)
+        x, kept = masked(x, fill)
+        indices = torch.rand(n, cols, generator=g, device="cuda").topk(4, dim=1).indices
+        indices[0::8, 0] = 3          # masked
+        indices[0::8, 1:] = -1        # nothing but it
+        for tau in (0.1, 0.25, 0.7, 1.0, 3.0, 1e20):
+            rows = lb.Rows(x, tau)
+            weights = torch.full((n,), 0.125 / min(tau, 1e19), device="cuda")
+            values = torch.randn(n, 4, generator=g, device="cuda")
+            want, bound, _, _ = lb.distill(rows, x, values, indices, weights)
+            kw = {"temperature": tau, "weights": weights}
+            for got in (rs.distill_loss(x, values, indices, **kw)[0],
+                        rs.distill_loss_grad(x, values, indices, **kw)[0]):
+                lb.within(got, want.float(), bound, f"losses at {fill}, {tau}")
