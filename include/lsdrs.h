@@ -365,6 +365,11 @@ rs_status rs_noalloc_timeout_probe(uint64_t timeout_ns, void* stream, rs_status*
  *    stride); any other overlap of a gradient with the logits is rejected.
  *  - Statistics, sums and losses are 32-bit floats whatever the scores'
  *    type; a gradient has the scores' type and is rounded to it once.
+ *  - Every finite score takes part, however large: a finite mask of -1e30 or
+ *    of the type's lowest value has probability 0 beside ordinary scores, and
+ *    a row of nothing else is uniform.  (An lse beyond what a float holds is
+ *    +-inf.  A backward call reads a row whose saved lse is 1024 or more in
+ *    size, or none, once more: so large an lse has lost the row's sum.)
  *  - -inf scores take no part (their probability is 0).  A row without any
  *    score above -inf has loss 0 and gradient 0, its lse is -inf.  NaN, or
  *    +inf, makes its row's results NaN and no other row's (a balance loss is

@@ -226,12 +226,12 @@ struct RowResult {
   float loss, logp, lse, c;
 };
 
-// kLossBwd: m is the saved lse, sum is 1.
+// kLossBwd: m is the saved lse (none that far_lse() names), sum is 1.
 template <int OP, int MODE>
 __device__ __forceinline__ RowResult row_result(const RowLossArgs& a, const Head& h, float m,
                                                 float sum) {
   RowResult r;
-  const bool empty = MODE == kLossBwd ? m == -INFINITY : sum == 0.0f;
+  const bool empty = MODE != kLossBwd && sum == 0.0f;
   const float log_sum = MODE == kLossBwd ? 0.0f : logf(sum);
   r.lse = empty ? -INFINITY : m * a.inv_tau + log_sum;
   if (OP == kOpDistill) {
@@ -266,13 +266,16 @@ __device__ __forceinline__ RowResult row_result(const RowLossArgs& a, const Head
   return r;
 }
 
-// The exponentials of a row from its maximum, or (kLossBwd) its saved lse.
+// The exponentials of a row from its maximum, or (kLossBwd, unless the row's
+// statistics were taken again) its saved lse.
 template <int TYPE, int MODE>
-__device__ __forceinline__ auto exponent(const RowLossArgs& a, float m) {
-  if constexpr (MODE == kLossBwd)
-    return ExponentOfLse<TYPE == RS_SCORE_F32>(origin(m), a.tau, a.scale2, a.scale2_low);
-  else
+__device__ __forceinline__ auto exponent(const RowLossArgs& a, float m, bool again) {
+  if constexpr (MODE == kLossBwd) {
+    using E = ExponentOfLse<TYPE == RS_SCORE_F32>;
+    return again ? E(Exponent(origin(m), a.scale2)) : E(m, a.scale2, a.scale2_low);
+  } else {
     return Exponent(origin(m), a.scale2);
+  }
 }
 
 template <int OP>
@@ -334,9 +337,10 @@ __global__ void __launch_bounds__(kThreads, VECS == 16 ? 2 : kShortWarps / (kThr
                             : make_uint4(V::kMinusInf, V::kMinusInf, V::kMinusInf, V::kMinusInf);
   }
   if (warp == kWarps - 1) load_targets<TYPE, OP, MODE>(a, row, t, slots, &head);
-  Softmax s;
-  if (MODE == kLossBwd) {
-    s = {a.lse[row], 1.0f};
+  Softmax s{-INFINITY, 1.0f};
+  if (MODE == kLossBwd) s.m = a.lse[row];
+  const bool again = MODE == kLossBwd && far_lse(s.m);
+  if (MODE == kLossBwd && !again) {
     __syncthreads();
   } else {
     RunningSoftmax<TYPE> run(scale2);
@@ -347,11 +351,12 @@ __global__ void __launch_bounds__(kThreads, VECS == 16 ? 2 : kShortWarps / (kThr
     s = lane_id() < kWarps ? part[lane_id()] : Softmax{-INFINITY, 0.0f};
     s = warp_join(s, scale2);
   }
-  const RowResult res = row_result<OP, MODE>(a, head, s.m, s.sum);
+  const RowResult res = again ? row_result<OP, kLossGrad>(a, head, s.m, s.sum)
+                              : row_result<OP, MODE>(a, head, s.m, s.sum);
   if (MODE != kLossBwd && tid == 0) store_result<OP>(a, row, res);
   if (MODE == kLossFwd) return;
   const float f = res.c / s.sum;
-  const auto e = exponent<TYPE, MODE>(a, s.m);
+  const auto e = exponent<TYPE, MODE>(a, s.m, again);
   const uint64_t ff = pack2(f * e.mend, f * e.mend);
 #pragma unroll
   for (int u = 0; u < VECS; ++u) {
@@ -428,19 +433,19 @@ struct Stream {
   __device__ __forceinline__ Stream(const Raw* x_, const RowVecs<TYPE>& vecs_, int begin, int end_,
                                     int tid)
       : x(x_), vecs(vecs_), end(end_), v(begin + tid) {
-    if (v < end) load(v, r);
+    if (v < end) load(v, end, r);
   }
-  __device__ __forceinline__ void load(int v0, uint4 (&to)[kStreamBatch]) const {
+  __device__ __forceinline__ void load(int v0, int last, uint4 (&to)[kStreamBatch]) const {
     const uint4* xv = reinterpret_cast<const uint4*>(x - vecs.lead);
     const int v1 = v0 + (kStreamBatch - 1) * kStreamThreads;
-    if (v0 >= vecs.whole_begin() && v1 < min(end, vecs.whole_end())) {
+    if (v0 >= vecs.whole_begin() && v1 < min(last, vecs.whole_end())) {
 #pragma unroll
       for (int u = 0; u < kStreamBatch; ++u) to[u] = __ldcs(xv + v0 + u * kStreamThreads);
     } else {
 #pragma unroll
       for (int u = 0; u < kStreamBatch; ++u) {
         const int w = v0 + u * kStreamThreads;
-        if (w >= end)
+        if (w >= last)
           to[u] = make_uint4(V::kMinusInf, V::kMinusInf, V::kMinusInf, V::kMinusInf);
         else if (vecs.whole(w))
           to[u] = __ldcs(xv + w);
@@ -454,7 +459,7 @@ struct Stream {
   __device__ __forceinline__ void run(F&& body) {
     uint4 ahead[kStreamBatch];
     for (; v < end; v += kStep) {
-      if (v + kStep < end) load(v + kStep, ahead);
+      if (v + kStep < end) load(v + kStep, end, ahead);
       body(v, r);
 #pragma unroll
       for (int u = 0; u < kStreamBatch; ++u) r[u] = ahead[u];
@@ -512,11 +517,12 @@ __global__ void __launch_bounds__(kStreamThreads + kWarp, kStreamCtas)
 
 template <int TYPE, int OP>
 __global__ void __launch_bounds__(kStreamThreads + kWarp, kStreamCtas)
-    row_loss_backward_kernel(const RowLossArgs a, const int split) {
+    row_loss_backward_kernel(const RowLossArgs a, const int split, const bool together) {
   using S = Score<TYPE>;
   using Raw = typename S::Raw;
   using V = ScoreVec<TYPE>;
   extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ Softmax part[kStreamWarps];
   __shared__ Head head;
   grid_dependency_sync();
   Targets t;
@@ -557,16 +563,39 @@ __global__ void __launch_bounds__(kStreamThreads + kWarp, kStreamCtas)
     load_targets<TYPE, OP, kLossBwd>(a, row, t, reinterpret_cast<int*>(t.x + a.k), &head);
   // the first loads are under way before the targets are known
   Stream<TYPE> stream(x, vecs, begin, off || warp == kStreamWarps ? begin : end, tid);
-  const float m = off ? 0.0f : a.lse[row];
+  Softmax s{off ? 0.0f : a.lse[row], 1.0f};
+  const bool again = far_lse(s.m);
   __syncthreads();
-  const float c = off ? 0.0f : row_result<OP, kLossBwd>(a, head, m, 1.0f).c;
-  const auto e = exponent<TYPE, kLossBwd>(a, m);
+  if (again) {  // every CTA of the row reads all of it
+    s = Softmax{-INFINITY, 0.0f};
+    if (warp < kStreamWarps) {
+      RunningSoftmax<TYPE> run(a.scale2);
+      for (int v = tid; v < vecs.count; v += Stream<TYPE>::kStep) {
+        stream.load(v, vecs.count, stream.r);
+        run.add(stream.r);
+      }
+      s = warp_join(run.result(), a.scale2);
+      if (lane_id() == 0) part[warp] = s;
+    }
+    __syncthreads();
+    s = lane_id() < kStreamWarps ? part[lane_id()] : Softmax{-INFINITY, 0.0f};
+    s = warp_join(s, a.scale2);
+    if (warp < kStreamWarps && stream.v < end) stream.load(stream.v, end, stream.r);
+  }
+  const float c = off     ? 0.0f
+                  : again ? row_result<OP, kLossGrad>(a, head, s.m, s.sum).c
+                          : row_result<OP, kLossBwd>(a, head, s.m, 1.0f).c;
+  const float per_sum = c / s.sum;
+  const auto e = exponent<TYPE, kLossBwd>(a, s.m, again);
+  // over its own logits no CTA of the row may write before all of them have
+  // read the action's score, and the row where its statistics were taken again
+  if (together && !off) cluster_sync();
   if (warp < kStreamWarps) {
     if (c == 0.0f) {  // nothing of the row is read
       const uint4 zero[kStreamBatch] = {};
       for (int v = begin + tid; v < end; v += kStreamThreads * kStreamBatch) put(v, zero);
     } else {
-      const uint64_t f = pack2(c * e.mend, c * e.mend);
+      const uint64_t f = pack2(per_sum * e.mend, per_sum * e.mend);
       stream.run([&](int v, uint4(&r)[kStreamBatch]) {
 #pragma unroll
         for (int u = 0; u < kStreamBatch; ++u) r[u] = vec_grad<TYPE>(r[u], e, f);
@@ -581,7 +610,7 @@ __global__ void __launch_bounds__(kStreamThreads + kWarp, kStreamCtas)
   for (int k = tid; k < a.k; k += kStreamThreads + kWarp) {
     const int col = t.col[k];
     if (col >= 0 && col >= b && col < last)
-      g[col] = S::store(e.one(t.x[k]) * c - c * t.p[k]);
+      g[col] = S::store(e.one(t.x[k]) * per_sum - c * t.p[k]);
   }
 }
 
@@ -1192,18 +1221,22 @@ cudaError_t launch_stream(const RowLossArgs& a, int split, size_t smem, cudaStre
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   cfg.attrs = attr;
-  cfg.numAttrs = add_attributes(attr, MODE == kLossFwd ? split : 1);
-  if constexpr (MODE == kLossFwd) {
-    auto kern = row_loss_forward_kernel<TYPE, OP>;
-    static std::atomic<uint64_t> done{0};
-    if (split > 8) {
+  // the CTAs of a row wait for each other in the forward call, and in the
+  // backward one over its own logits
+  const bool together = split > 1 && (MODE == kLossFwd || a.grad == a.logits);
+  cfg.numAttrs = add_attributes(attr, together ? split : 1);
+  static std::atomic<uint64_t> done{0};
+  auto go = [&](auto kern, auto... args) {
+    if (together && split > 8) {
       const cudaError_t e = allow(kern, false, true, &done);
       if (e != cudaSuccess) return e;
     }
-    return cudaLaunchKernelEx(&cfg, kern, a, split);
-  } else {
-    return cudaLaunchKernelEx(&cfg, row_loss_backward_kernel<TYPE, OP>, a, split);
-  }
+    return cudaLaunchKernelEx(&cfg, kern, a, args...);
+  };
+  if constexpr (MODE == kLossFwd)
+    return go(row_loss_forward_kernel<TYPE, OP>, split);
+  else
+    return go(row_loss_backward_kernel<TYPE, OP>, split, together);
 }
 
 template <int TYPE, int OP>
@@ -1263,9 +1296,6 @@ cudaError_t launch_row_loss_as(const RowLossArgs& a, cudaStream_t s) {
     while (split < kMaxCluster && a.rows * split < int64_t(sms) * kStreamCtas * kStreamWaves &&
            bytes >= split * 2 * kStreamLeast)
       split *= 2;
-    // over its own logits the backward call of the policy loss must not write
-    // a segment before every segment has read the action's score
-    if (MODE == kLossBwd && OP == kOpPolicy && a.grad == a.logits) split = 1;
     while (a.rows * split >= (int64_t(1) << 31)) split /= 2;  // CTA numbers are 31 bits
     return launch_stream<TYPE, OP, MODE>(a, split, lists, s);
   } else {

@@ -266,6 +266,13 @@ struct Exponent {
   }
 };
 
+// From here on (and for an lse that is none, or that a float does not hold) a
+// saved lse carries too little of its row: it is rounded by up to 2^-15 at
+// 1024, which a probability then is off by; at 2^24 the sum of a row is lost
+// altogether.  The backward call takes the statistics of such a row again.
+constexpr float kFarLse = 1024.0f;
+__device__ __forceinline__ bool far_lse(float lse) { return fabsf(lse) >= kFarLse; }
+
 // exp2(x scale - lse log2 e) for a saved lse, which came from the temperature
 // itself: the rounding of scale would not cancel against it as it does against
 // a sum taken with the same scale, and is off by |x| scale 2^-24 in the
@@ -273,23 +280,22 @@ struct Exponent {
 // scores (LOW; 16-bit results are rounded far above that).
 template <bool LOW>
 struct ExponentOfLse {
-  float hi, lo, os2, mend;
+  float hi, lo, least, os2, mend;
 
-  __device__ __forceinline__ ExponentOfLse(float lse, float tau, float hi_, float lo_)
-      : hi(hi_), lo(lo_), os2(lse * kLog2e) {
-    const float o = lse * tau;
-    if (isinf(os2) || isinf(o * hi)) {  // (or no score at all)
-      os2 = o;
-      hi = 1.0f;
-      lo = 0.0f;
-      mend = 1.0f;
-    } else {
-      mend = exp2_approx(__fmaf_rn(-lse, kLog2e, os2) - lse * kLog2eLow);
-    }
+  __device__ __forceinline__ ExponentOfLse(float lse, float hi_, float lo_)
+      : hi(hi_),
+        lo(lo_),
+        least(fmaxf((lse * kLog2e - 300.0f) / hi_, -3.0e38f)),
+        os2(lse * kLog2e) {
+    mend = exp2_approx(__fmaf_rn(-lse, kLog2e, os2) - lse * kLog2eLow);
   }
-  // -os2, with the low product (of a finite score: -inf * lo might be +inf)
+  // from the row's own largest score
+  __device__ __forceinline__ explicit ExponentOfLse(const Exponent& e)
+      : hi(e.scale), lo(0.0f), least(-3.0e38f), os2(e.os2), mend(e.mend) {}
+  // -os2, with the low product; that of a score whose exponential is 0 anyway
+  // must not be infinite (for lo < 0 it would be +inf)
   __device__ __forceinline__ float rest(float x) const {
-    return LOW ? __fmaf_rn(fmaxf(x, -3.0e38f), lo, -os2) : -os2;
+    return LOW ? __fmaf_rn(fmaxf(x, least), lo, -os2) : -os2;
   }
   __device__ __forceinline__ float one(float x) const {
     return exp2_approx(__fmaf_rn(x, hi, rest(x))) * mend;

@@ -37,6 +37,13 @@ class Rows:
         self.off = (self.top[:, 0].abs() * 1.5 * 2.0 ** -24).clamp(max=64)
         self.sum_error = U32 * (2 * (math.log(cols) + LAG) + self.off + cols / 1024 + 96)
 
+    def saved_error(self):
+        """What a saved lse adds to a probability of the backward call: its own
+        rounding, and that of the scores' products, where it is below 1024;
+        the statistics of other rows are taken again."""
+        near = self.lse.abs() < 1100
+        return torch.where(near, U32 * 6 * self.lse.abs(), torch.zeros_like(self.lse))
+
     def q_error(self):
         return self.sum_error[:, None] + U32 * 2 * self.dist.clamp(max=200)
 
@@ -64,8 +71,9 @@ def within(got, want, bound, what):
 
 
 def distill(rows, x, values, indices, weights=None, up=None):
-    """(losses, bound, gradient, bound) of a distillation; every row has a live
-    entry of finite value on a column of finite score."""
+    """(losses, bound, gradient, bound, what the backward call adds to that) of
+    a distillation; every row has a live entry of finite value on a column of
+    finite score."""
     n, cols = x.shape
     tau, w = rows.tau, dev64(weights, n)
     live = (indices >= 0) & (indices < cols)
@@ -92,11 +100,13 @@ def distill(rows, x, values, indices, weights=None, up=None):
     u, tiny = ROUND[x.dtype]
     bound = (c.abs()[:, None] * (rows.q * rows.q_error() + target_error + 4 * U32 * (rows.q + target))
              + grad.abs() * u * 1.01 + tiny + rows.least(c))
-    return losses, loss_bound, grad, bound
+    saved = c.abs()[:, None] * rows.q * rows.saved_error()[:, None]
+    return losses, loss_bound, grad, bound, saved
 
 
 def policy(rows, x, actions, old, adv, ref=None, low=0.2, high=0.28, kl=0.0, weights=None, up=None):
-    """(losses, bound, log-probabilities, bound, gradient, bound)."""
+    """(losses, bound, log-probabilities, bound, gradient, bound, what the
+    backward call adds to that)."""
     n = x.shape[0]
     w, adv, old = dev64(weights, n), adv.double(), old.double()
     a = actions.long()[:, None]
@@ -123,4 +133,7 @@ def policy(rows, x, actions, old, adv, ref=None, low=0.2, high=0.28, kl=0.0, wei
     u, tiny = ROUND[x.dtype]
     bound = (c_bound[:, None] * (taken + rows.q) + c.abs()[:, None] * rows.q * rows.q_error()
              + 4 * U32 * c.abs()[:, None] * (rows.q + taken) + grad.abs() * u * 1.01 + tiny + rows.least(c))
-    return w * loss, loss_bound, logp, logp_error, grad, bound
+    more = (rows.saved_error() + 4 * U32 * dist.clamp(max=1e4))[:, None]
+    saved = ((w * dev64(up, n)).abs() / rows.tau * size)[:, None] * 2 * more * (taken + rows.q)
+    saved = saved + c.abs()[:, None] * rows.q * more
+    return w * loss, loss_bound, logp, logp_error, grad, bound, saved

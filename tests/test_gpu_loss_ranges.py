@@ -48,12 +48,15 @@ def some_columns(kept, k, g):
 def check_distill(rs, x, tau, indices, g, backward=False, grad_out=None, weights=None, rows=None):
     rows = lb.Rows(x, tau) if rows is None else rows
     values = torch.randn(indices.shape, generator=g, device="cuda") * min(tau, 1.0)
-    losses, loss_bound, grad, bound = lb.distill(rows, x, values, indices, weights)
+    losses, loss_bound, grad, bound, saved = lb.distill(rows, x, values, indices, weights)
     kw = {"temperature": tau, "weights": weights}
     lse_bound = rows.lse_error()
     fl, fs = rs.distill_loss(x, values, indices, **kw)
     if backward:
-        lb.within(rs.distill_loss_backward(None, x, fs, values, indices, **kw), grad, bound, "backward")
+        got = rs.distill_loss_backward(None, x, fs, values, indices, **kw)
+        lb.within(got, grad, bound + saved, "backward")
+        over = x.clone()
+        assert torch.equal(rs.distill_loss_backward(None, over, fs, values, indices, grad_out=over, **kw), got)
     gl, gs, gg = rs.distill_loss_grad(x, values, indices, grad_out=grad_out, **kw)
     lb.within(fl, losses, loss_bound, "losses")
     lb.within(gl, losses, loss_bound, "losses with gradient")
@@ -71,13 +74,16 @@ def check_policy(rs, x, tau, actions, g, backward=False, weights=None, rows=None
     old = (logp + torch.tensor([0.0, 0.1, -0.1, 0.5, -0.5], device="cuda").repeat(n)[:n]).float()
     ref = (logp + 0.3 * torch.randn(n, generator=g, device="cuda")).float()
     adv = torch.randn(n, generator=g, device="cuda")
-    losses, loss_bound, logp, logp_bound, grad, bound = lb.policy(rows, x, actions, old, adv, ref, kl=kl,
+    losses, loss_bound, logp, logp_bound, grad, bound, saved = lb.policy(rows, x, actions, old, adv, ref, kl=kl,
                                                                         weights=weights)
     kw = {"ref_logprobs": ref, "clip_low": 0.2, "clip_high": 0.28, "kl_coef": kl, "temperature": tau,
           "weights": weights}
     fl, fp, fs = rs.policy_loss(x, actions, old, adv, **kw)
     if backward:
-        lb.within(rs.policy_loss_backward(None, x, fs, actions, old, adv, **kw), grad, bound, "backward")
+        got = rs.policy_loss_backward(None, x, fs, actions, old, adv, **kw)
+        lb.within(got, grad, bound + saved, "backward")
+        over = x.clone()
+        assert torch.equal(rs.policy_loss_backward(None, over, fs, actions, old, adv, grad_out=over, **kw), got)
     gl, gp, gs, gg = rs.policy_loss_grad(x, actions, old, adv, **kw)
     lb.within(fl, losses, loss_bound, "losses")
     lb.within(gl, losses, loss_bound, "losses with gradient")
@@ -197,8 +203,38 @@ def test_targets_on_masked_columns(rs, n, cols, dtype, fills):
             rows = lb.Rows(x, tau)
             weights = torch.full((n,), 0.125 / min(tau, 1e19), device="cuda")
             values = torch.randn(n, 4, generator=g, device="cuda")
-            want, bound, _, _ = lb.distill(rows, x, values, indices, weights)
+            want, bound, _, _, _ = lb.distill(rows, x, values, indices, weights)
             kw = {"temperature": tau, "weights": weights}
             for got in (rs.distill_loss(x, values, indices, **kw)[0],
                         rs.distill_loss_grad(x, values, indices, **kw)[0]):
                 lb.within(got, want.float(), bound, f"losses at {fill}, {tau}")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n,cols", SHAPES + [(1, 200000)])
+def test_backward_of_rows_whose_lse_says_too_little(rs, n, cols, dtype):
+    """A saved lse of -1e10 has lost the logarithm of the sum, one of the type's
+    lowest value over a temperature below 1 is -inf: the gradient is right all
+    the same, also over the logits."""
+    lowest = torch.finfo(dtype).min
+    for fill, tau in ((-1e10, 1.0), (-1e30, 2.0), (lowest, 0.7), (lowest, 1.0), (lowest, 4.0), (-3000.0, 1.0),
+                      (-300.0, 0.25)):
+        x, g = scores(n, cols, dtype, cols)
+        x, kept = masked(x, fill)
+        indices = some_columns(kept, 4, g)
+        check_distill(rs, x, tau, indices, g, backward=True)
+        check_policy(rs, x, tau, indices.amax(1), g, backward=True)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("n,cols", [(16, 3000), (304, 12000), (16, 40000), (160, 40000), (2, 300007)])
+def test_backward_at_small_temperatures(rs, n, cols, dtype):
+    for tau in (1e-3, 1e-6, 1e-15, 6e-20):
+        x, g = scores(n, cols, dtype, 2)
+        x[1::4, ::5] = torch.finfo(dtype).min
+        rows = lb.Rows(x, tau)
+        indices = rows.q.topk(2, dim=1).indices
+        indices[:, 1] = -1
+        check_distill(rs, x, tau, indices, g, True, rows=rows, weights=torch.full((n,), 1 / tau, device="cuda"))
+        check_policy(rs, x, tau, indices[:, 0].contiguous(), g, True, rows=rows,
+                     weights=torch.full((n,), tau, device="cuda"))
