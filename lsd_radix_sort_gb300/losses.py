@@ -176,6 +176,8 @@ def _distill(logits, top_values, top_indices, temperature, weights, losses, lse,
         _vector(losses, rows, "losses_out")
     if lse is not None:
         _vector(lse, rows, "lse" if backward else "lse_out")
+    elif backward:
+        raise ValueError("the backward call needs the forward call's lse")
     if grad_losses is not None:
         _vector(grad_losses, rows, "grad_losses")
     grad_stride = cols if grad is None else _grad_stride(logits, grad)
@@ -257,6 +259,8 @@ def _policy(logits, actions, old, advantages, ref, clip_low, clip_high, kl_coef,
         _vector(logprobs, rows, "logprobs_out")
     if lse is not None:
         _vector(lse, rows, "lse" if backward else "lse_out")
+    elif backward:
+        raise ValueError("the backward call needs the forward call's lse")
     if grad_losses is not None:
         _vector(grad_losses, rows, "grad_losses")
     grad_stride = cols if grad is None else _grad_stride(logits, grad)
