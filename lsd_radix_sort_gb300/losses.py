@@ -128,14 +128,20 @@ def _vector(t, n, what, dtype=None):
         raise ValueError(f"{what} must be contiguous")
 
 
-def _device(x, *ts):
-    """The index of the one CUDA device that all tensors are on."""
+def _device(stream, x, *ts):
+    """The index of the one CUDA device that all tensors are on, which must be
+    the current one (the library launches there) and the stream's."""
     index = x.get_device()
     if index < 0:
         raise ValueError("tensors must be on a CUDA device")
     for t in ts:
         if t is not None and t.get_device() != index:
             raise ValueError("tensors must be on one CUDA device")
+    if index != _torch.cuda.current_device():
+        raise ValueError(f"tensors must be on the current CUDA device, got cuda:{index} while "
+                         f"cuda:{_torch.cuda.current_device()} is current")
+    if stream is not None and stream.device_index != index:
+        raise ValueError(f"the stream must be one of cuda:{index}, the tensors' device")
     return index
 
 
@@ -181,7 +187,8 @@ def _distill(logits, top_values, top_indices, temperature, weights, losses, lse,
     if grad_losses is not None:
         _vector(grad_losses, rows, "grad_losses")
     grad_stride = cols if grad is None else _grad_stride(logits, grad)
-    index = _device(logits, top_values, top_indices, weights, losses, lse, grad, grad_losses)
+    index = _device(stream, logits, top_values, top_indices, weights, losses, lse, grad,
+                    grad_losses)
 
     with _on(stream):
         device = logits.device
@@ -264,8 +271,8 @@ def _policy(logits, actions, old, advantages, ref, clip_low, clip_high, kl_coef,
     if grad_losses is not None:
         _vector(grad_losses, rows, "grad_losses")
     grad_stride = cols if grad is None else _grad_stride(logits, grad)
-    index = _device(logits, actions, old, advantages, ref, weights, losses, logprobs, lse, grad,
-                    grad_losses)
+    index = _device(stream, logits, actions, old, advantages, ref, weights, losses, logprobs, lse,
+                    grad, grad_losses)
 
     with _on(stream):
         device = logits.device
@@ -363,7 +370,7 @@ def _balance(scores, ids, mask, scale, grad, with_grad, temp, stream):
     if mask is not None:
         _mask(mask, tokens)
     grad_stride = experts if grad is None else _grad_stride(scores, grad)
-    index = _device(scores, ids, mask, grad, temp)
+    index = _device(stream, scores, ids, mask, grad, temp)
     need = balance_temp_bytes(tokens, experts)
     with _on(stream):
         device = scores.device
@@ -425,7 +432,7 @@ def balance_loss_backward(grad_loss, scores, counts, n_tokens, top_k: int, token
     if token_mask is not None:
         _mask(token_mask, tokens)
     grad_stride = experts if grad_out is None else _grad_stride(scores, grad_out)
-    index = _device(scores, counts, n_tokens, grad_loss, token_mask, grad_out)
+    index = _device(stream, scores, counts, n_tokens, grad_loss, token_mask, grad_out)
     grad = grad_out
     if grad is None:
         with _on(stream):

@@ -19,3 +19,35 @@ def test_backward_calls_without_lse():
         rs.distill_loss_backward(None, f(4, 9), None, f(4, 2), i(4, 2))
     with pytest.raises(ValueError, match="needs the forward call's lse"):
         rs.policy_loss_backward(None, f(4, 9), None, i(4), f(4), f(4))
+
+
+CALLS = {
+    "distill_loss": lambda **kw: rs.distill_loss(f(4, 9), f(4, 2), i(4, 2), **kw),
+    "distill_loss_grad": lambda **kw: rs.distill_loss_grad(f(4, 9), f(4, 2), i(4, 2), **kw),
+    "distill_loss_backward": lambda **kw: rs.distill_loss_backward(None, f(4, 9), f(4), f(4, 2), i(4, 2), **kw),
+    "policy_loss": lambda **kw: rs.policy_loss(f(4, 9), i(4), f(4), f(4), **kw),
+    "policy_loss_grad": lambda **kw: rs.policy_loss_grad(f(4, 9), i(4), f(4), f(4), **kw),
+    "policy_loss_backward": lambda **kw: rs.policy_loss_backward(None, f(4, 9), f(4), i(4), f(4), f(4), **kw),
+    "balance_loss": lambda **kw: rs.balance_loss(f(4, 9), i(4, 2), **kw),
+    "balance_loss_grad": lambda **kw: rs.balance_loss_grad(f(4, 9), i(4, 2), **kw),
+    "balance_loss_backward": lambda **kw: rs.balance_loss_backward(
+        None, f(4, 9), i(9).int(), i(1).int(), 2, **kw),
+}
+
+
+class OtherStream:
+    device_index = 0
+    cuda_stream = 0
+
+
+@pytest.mark.parametrize("name", sorted(CALLS))
+def test_tensors_of_a_device_that_is_not_current(monkeypatch, name):
+    """Device indices are stubbed: the tensors say that they are on the second
+    device while the first is current."""
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 1)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    with pytest.raises(ValueError, match="current CUDA device, got cuda:1 while cuda:0"):
+        CALLS[name]()
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(ValueError, match="the stream must be one of cuda:1"):
+        CALLS[name](stream=OtherStream())
