@@ -330,18 +330,21 @@ __device__ __forceinline__ uint4 vec_grad(const uint4& v, const E& e, uint64_t f
 
 // A thread's softmax in progress over many vectors.  The origin is the
 // largest score of some vectors past; it moves only when a score exceeds it
-// by more than 2^30 would (so no sum overflows), which keeps the maximum off
-// the path of the exponentials.  (30 is less than half of what neighbouring
-// scores of a far origin are apart, so that the limit is then the origin
-// itself.)
+// by more than 2^8 would (so no sum overflows), which keeps the maximum off
+// the path of the exponentials.  (Exponents up to 8 are rounded by 2^-22 at
+// most, as exponentials are anyway; and 8 is less than half of what
+// neighbouring scores of a far origin are apart, so that the limit is then
+// the origin itself.)  The result is taken from the largest score of all: the
+// logarithm of the sum is then small where one score outweighs the others, and
+// a loss near 0 no difference of two large numbers.
 template <int TYPE>
 struct RunningSoftmax {
-  float scale, o, limit;
+  float scale, slack, o, limit, top;
   Exponent e;
   uint64_t acc[2];
 
   __device__ __forceinline__ explicit RunningSoftmax(float scale2)
-      : scale(scale2), o(-INFINITY), limit(-INFINITY), e(0.0f, scale2) {
+      : scale(scale2), slack(8.0f / scale2), o(-INFINITY), limit(-INFINITY), top(-INFINITY), e(0.0f, scale2) {
     acc[0] = acc[1] = 0;
   }
   __device__ __forceinline__ float total() const {
@@ -352,19 +355,23 @@ struct RunningSoftmax {
   __device__ __forceinline__ void move(float m) {
     const float sum = total() * exp2_approx((o - m) * scale);
     o = m;
-    limit = m + 30.0f / scale;
+    limit = m + slack;
     e = Exponent(m, scale);
-    acc[0] = pack2(sum / e.mend, 0.0f);
+    acc[0] = pack2(__fdividef(sum, e.mend), 0.0f);
     acc[1] = 0;
   }
   template <int VECS>
   __device__ __forceinline__ void add(const uint4 (&v)[VECS]) {
     const float m = vec_max<TYPE>(v);
+    top = fmaxf(top, m);
     if (m > limit) move(m);
 #pragma unroll
     for (int u = 0; u < VECS; ++u) vec_exp_sum<TYPE>(v[u], e, acc);
   }
-  __device__ __forceinline__ Softmax result() const { return {o, total()}; }
+  __device__ __forceinline__ Softmax result() const {
+    const float sum = total();
+    return {top, top > o ? sum * exp2_approx((o - top) * scale) : sum};
+  }
 };
 
 // A row of scores as 16-byte vectors of memory: vector 0 begins at the row's

@@ -238,3 +238,25 @@ def test_backward_at_small_temperatures(rs, n, cols, dtype):
         check_distill(rs, x, tau, indices, g, True, rows=rows, weights=torch.full((n,), 1 / tau, device="cuda"))
         check_policy(rs, x, tau, indices[:, 0].contiguous(), g, True, rows=rows,
                      weights=torch.full((n,), tau, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n,cols", [(64, 65536), (200, 65536), (64, 3000), (12, 400000)])
+def test_losses_near_zero(rs, n, cols, dtype):
+    """One score far above the others and far behind the first, which the
+    target names: the loss is some 1e-5, and off by the rounding of numbers
+    near 1 (16 units: two exponentials of 2 ulp, sums, a logarithm), however far
+    the scores before it lie below."""
+    x, g = scores(n, cols, dtype, 7, 1.0)
+    at = torch.randint(cols * 3 // 4, cols, (n, 1), generator=g, device="cuda")
+    height = 10.4 + torch.logsumexp(x.double(), 1, keepdim=True)
+    x.scatter_(1, at, (height + torch.rand(n, 1, generator=g, device="cuda")).to(dtype))
+    want = torch.logsumexp(x.double(), 1) - x.double().gather(1, at)[:, 0]
+    assert 5e-6 < float(want.min()) and float(want.max()) < 1e-4
+    bound = torch.full_like(want, 16 * 2.0 ** -24)
+    values = torch.zeros(n, 1, device="cuda")
+    zeros = torch.zeros(n, device="cuda")
+    for got in (rs.distill_loss(x, values, at)[0], rs.distill_loss_grad(x, values, at)[0],
+                -rs.policy_loss(x, at[:, 0], zeros, zeros)[1],
+                -rs.policy_loss_grad(x, at[:, 0], zeros, zeros)[1]):
+        lb.within(got, want, bound, "losses")
