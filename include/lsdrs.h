@@ -402,7 +402,13 @@ typedef enum rs_score_type { RS_SCORE_F16 = 0, RS_SCORE_BF16 = 1, RS_SCORE_F32 =
  *   temperature >= RS_MIN_TEMPERATURE, finite
  *   losses, lse rows floats
  *   grad        rows x cols of the logits' type; rs_distill_loss: may be
- *               NULL (losses only), else the gradient of the sum of losses */
+ *               NULL (losses only), else the gradient of the sum of losses
+ *   wait_timeout_ns, status  of the call that writes losses and gradient: the
+ *               kernel of its long rows waits for copies and for the CTAs that
+ *               share a row, each wait for wait_timeout_ns at most (0: 2 s, up
+ *               to 60 s).  Where one runs out, every row that is not finished
+ *               gets NaN losses, lse and gradients, and status (NULL, or one
+ *               u32 that the caller has cleared) RS_ERR_LOOKBACK_TIMEOUT */
 typedef struct rs_distill_args {
   const void* logits;
   int64_t logits_stride, rows, cols;
@@ -417,6 +423,8 @@ typedef struct rs_distill_args {
   int64_t grad_stride;
   int logits_type, top_values_type, index_bytes, top;
   float temperature;
+  uint64_t wait_timeout_ns;
+  uint32_t* status;
 } rs_distill_args;
 
 /* The losses and, where args->grad is given, the gradient of their sum. */
@@ -460,6 +468,8 @@ typedef struct rs_policy_args {
   int64_t grad_stride;
   int logits_type, index_bytes;
   float clip_low, clip_high, kl_coef, temperature;
+  uint64_t wait_timeout_ns;
+  uint32_t* status;
 } rs_policy_args;
 
 /* The losses and, where args->grad is given, the gradient of their sum. */
@@ -470,10 +480,8 @@ rs_status rs_policy_loss(const rs_policy_args* args, void* stream);
 rs_status rs_policy_loss_backward(const rs_policy_args* args, const float* grad_losses,
                                   void* stream);
 
-/* Failure-detection check of the row losses: the kernels of long rows wait
- * for their copies and for each other on barriers, each wait for 2 s at most;
- * one that runs out gives the rows that were left NaN losses and gradients.
- * This runs that wait, with the given limit (1 ns .. 60 s), on a barrier on
+/* Failure-detection check of the row losses: runs the wait that
+ * wait_timeout_ns limits, with the given limit (1 ns .. 60 s), on a barrier on
  * which nothing arrives, synchronises `stream` and writes the status it
  * produced (RS_ERR_LOOKBACK_TIMEOUT when it expired) to *result.
  * word: (device) one u32 scratch word, overwritten. */

@@ -24,6 +24,8 @@ struct RowLossArgs {
   float* lse;                      // written, or read by kLossBwd
   float inv_tau, tau;
   float scale2, scale2_low;        // log2(e) / tau: rounded, and what that leaves
+  uint64_t wait_ns;                // limit on one wait of the long rows' kernel
+  uint32_t* status;                // null, or set when such a wait ran out
   // distill
   const void* top_values;
   int top_type;

@@ -12,6 +12,7 @@ using namespace lsdrs;
 namespace {
 
 constexpr uint64_t kMaxWaitNs = 60000000000ull;
+constexpr uint64_t kDefaultWaitNs = 2000000000ull;
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
 
 int score_bytes(int type) { return type == RS_SCORE_F32 ? 4 : 2; }
@@ -64,8 +65,10 @@ rs_status enqueue(int kernel, uint64_t units, void* stream, F&& launch) {
 // What the row losses share: the logits, the row arrays, the mode's outputs.
 rs_status rows_check(const void* logits, int64_t stride, int64_t rows, int64_t cols, int type,
                      const float* weights, const float* losses, const float* lse, void* grad,
-                     int64_t grad_stride, float temperature, LossMode mode) {
+                     int64_t grad_stride, float temperature, uint64_t wait_ns,
+                     const uint32_t* status, LossMode mode) {
   if (!known_type(type)) return RS_ERR_INVALID;
+  if (wait_ns > kMaxWaitNs || !aligned(status, 4)) return RS_ERR_INVALID;
   const int es = score_bytes(type);
   if (rows < 0 || rows > kMaxRows || cols < 1 || cols > RS_MAX_ROW_KEYS) return RS_ERR_INVALID;
   if (!matrix_ok(rows, cols, stride, es)) return RS_ERR_INVALID;
@@ -91,7 +94,7 @@ rs_status distill(const rs_distill_args* p, const float* grad_losses, LossMode m
   if (p == nullptr) return RS_ERR_INVALID;
   rs_status st = rows_check(p->logits, p->logits_stride, p->rows, p->cols, p->logits_type,
                             p->weights, p->losses, p->lse, p->grad, p->grad_stride,
-                            p->temperature, mode);
+                            p->temperature, p->wait_timeout_ns, p->status, mode);
   if (st != RS_OK) return st;
   if (!known_type(p->top_values_type) || p->top < 1 || p->top > RS_MAX_TOP) return RS_ERR_INVALID;
   if (p->index_bytes != 4 && p->index_bytes != 8) return RS_ERR_INVALID;
@@ -115,6 +118,8 @@ rs_status distill(const rs_distill_args* p, const float* grad_losses, LossMode m
   a.losses = p->losses;
   a.lse = p->lse;
   set_temperature(&a, p->temperature);
+  a.wait_ns = p->wait_timeout_ns != 0 ? p->wait_timeout_ns : kDefaultWaitNs;
+  a.status = p->status;
   a.top_values = p->top_values;
   a.top_type = p->top_values_type;
   a.top_stride = p->top_values_stride;
@@ -132,7 +137,7 @@ rs_status policy(const rs_policy_args* p, const float* grad_losses, LossMode mod
   if (p == nullptr) return RS_ERR_INVALID;
   rs_status st = rows_check(p->logits, p->logits_stride, p->rows, p->cols, p->logits_type,
                             p->weights, p->losses, p->lse, p->grad, p->grad_stride,
-                            p->temperature, mode);
+                            p->temperature, p->wait_timeout_ns, p->status, mode);
   if (st != RS_OK) return st;
   if (p->index_bytes != 4 && p->index_bytes != 8) return RS_ERR_INVALID;
   if (!(p->clip_low >= 0.0f) || !std::isfinite(p->clip_low) || !(p->clip_high >= 0.0f) ||
@@ -156,6 +161,8 @@ rs_status policy(const rs_policy_args* p, const float* grad_losses, LossMode mod
   a.losses = p->losses;
   a.lse = p->lse;
   set_temperature(&a, p->temperature);
+  a.wait_ns = p->wait_timeout_ns != 0 ? p->wait_timeout_ns : kDefaultWaitNs;
+  a.status = p->status;
   a.actions = p->actions;
   a.index_bytes = p->index_bytes;
   a.k = 1;

@@ -27,7 +27,7 @@ __global__ void row_wait_probe_kernel(uint32_t* error, uint64_t limit_ns) {
   __shared__ int failed;
   failed = 0;
   mbar_init(&bar, 1);
-  if (!wait_phase<false>(&bar, 0, &failed, limit_ns) && failed) *error = kErrLookback;
+  if (wait_phase<false>(&bar, 0, &failed, limit_ns, 1000000) == kWaitRanOut) *error = kErrLookback;
 }
 
 }  // namespace

@@ -12,6 +12,7 @@
 // a pass that writes c q_j, and a last step that rewrites the target columns.
 #pragma once
 #include <atomic>
+#include <climits>
 
 #include "losses.h"
 #include "scores.cuh"
@@ -643,8 +644,15 @@ __global__ void __launch_bounds__(kStreamThreads + kWarp, kStreamCtas)
 // beforehand: the grid has a CTA (cluster) per row, and a running one takes
 // over the rows of CTAs that have not been launched yet, one row after
 // another, by cancelling their launch (cluster launch control).  One thread
-// per CTA (the scheduler) does so a few rows ahead and lists them for the
-// other warps.
+// per CTA (the scheduler; the first CTA's asks and tells the others') does so
+// a few rows ahead and lists them for the other warps.
+//
+// Every wait has a limit.  One that runs out marks the whole cluster as
+// failed; its warps then finish the row they are in, on whatever data, and
+// leave.  Copies and answers under way are waited for; nothing is in flight
+// when a CTA ends.  The rows taken over are no other CTA's any more, so those
+// that some warp has not finished in good order get NaN, all of them, and the
+// caller's status word is set.
 constexpr int kRowConsumers = 512;
 constexpr int kRowWarps = kRowConsumers / kWarp;
 constexpr int kTargetWarps = 2;
@@ -656,17 +664,30 @@ constexpr int kChunkVecs = kRowConsumers * kChunkUnits;
 constexpr int kChunkBytes = kChunkVecs * 16;
 constexpr int kMaxSlots = 6;                                  // most ring slots
 constexpr int kMaxHeads = 4;                                  // rows whose targets are held
-constexpr int kAheadRows = 8;                                 // rows that the scheduler is ahead
+// Rows that the scheduler is ahead: enough for the targets, and not more, or
+// the last rows pile up at few CTAs (8: bf16 4,096 x 131,072 with 64 targets
+// 337 us instead of 330, 300 x 400,000 106 instead of 98).
+constexpr int kAheadRows = 4;
 constexpr int kRowReaders = kRowWarps + 1 + kTargetWarps;     // warps that read its list
-constexpr uint64_t kRowWaitNs = 2000000000ull;
+// Rows that are remembered.  A scheduler lists row n once every warp of its CTA
+// has begun row n - kAheadRows, and the first CTA's remembers row n for all
+// once the others' have read row n - kTold, or n - kTold - 1 where that wait
+// gives up: no row before n - kAheadRows - kTold - 2 is unfinished then.
+constexpr int kTold = 2;
+constexpr int kRowHistory = 16;
+static_assert(kRowHistory >= kAheadRows + kTold + 3 && kRowHistory % kAheadRows == 0);
 
 // Barriers and small arrays behind the ring.
 struct RowShared {
-  uint4 answer[2];                                            // of cluster launch control
-  uint64_t answer_full[2], answer_empty[2];
+  uint4 answer;                                               // of cluster launch control
+  uint64_t answer_full;
+  uint64_t told_full[kTold], told_empty[kTold];
   uint64_t row_full[kAheadRows], row_empty[kAheadRows];
-  int row[kAheadRows];                                        // the rows to take, -1: no more
-  int row_off[kAheadRows];                                    // those that are not read
+  int2 row[kRowHistory];  // row n at n % kRowHistory: its number (-1: no more), and whether it
+                          // is not read
+  int taken;              // rows taken so far by the cluster
+  int done[kRowWarps];    // rows that a consumer warp has finished
+  int first_bad;          // the least of these in the cluster
   uint64_t full[kMaxSlots], empty[kMaxSlots];
   uint64_t head_full[kMaxHeads], head_empty[kMaxHeads];
   uint64_t together;                                          // all consumer warps
@@ -674,7 +695,7 @@ struct RowShared {
   Softmax part[2][kRowWarps];
   Softmax peer[2][kMaxCluster];
   Head head[kMaxHeads];
-  int failed;                                                 // a wait ran out of time
+  int failed;                                                 // a wait of the cluster ran out
 };
 
 // Rows whose targets are held at a time (with two, 64 targets a row took 387
@@ -697,56 +718,102 @@ __host__ constexpr inline int row_ring_slots(int k) {
 }
 
 // Waits for a phase of a barrier, with CLUSTER for one on which other CTAs
-// arrive (what they wrote before is then seen after it).  After kRowWaitNs,
-// or once another wait of the CTA has run out, it gives up: the caller goes
-// on without using what it waited for, so that every thread still reaches
-// every barrier, and the rows it had left get NaN.  Each try names a time to
-// sleep: warps that poll in a tight loop take the issue slots and the
-// shared-memory ports of those that work (a 4096 x 131072 bf16 gradient took
-// 500 us so, 441 with a read of the clock between polls).
+// arrive (what they wrote before is then seen after it).  It gives up after
+// limit_ns, or once another wait has.  Each try names a time to sleep: warps
+// that poll in a tight loop take the issue slots and the shared-memory ports
+// of those that work (a 4096 x 131072 bf16 gradient took 500 us so, 441 with a
+// read of the clock between polls).
 template <bool CLUSTER>
-__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* failed,
-                                           uint64_t limit_ns = kRowWaitNs) {
-  constexpr uint32_t kSleepNs = 1000000;
-  auto done = [&] {
-    uint32_t ok;
-    if (CLUSTER)
-      asm volatile(
-          "{\n .reg .pred p;\n"
-          " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
-          " selp.u32 %0, 1, 0, p;\n}"
-          : "=r"(ok)
-          : "r"(smem_addr(bar)), "r"(parity), "r"(kSleepNs)
-          : "memory");
-    else
-      asm volatile(
-          "{\n .reg .pred p;\n"
-          " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
-          " selp.u32 %0, 1, 0, p;\n}"
-          : "=r"(ok)
-          : "r"(smem_addr(bar)), "r"(parity), "r"(kSleepNs)
-          : "memory");
-    return ok != 0;
-  };
-  if (done()) return true;
+__device__ __forceinline__ bool phase_done(uint64_t* bar, uint32_t parity, uint32_t sleep_ns) {
+  uint32_t ok;
+  if (CLUSTER)
+    asm volatile(
+        "{\n .reg .pred p;\n"
+        " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(sleep_ns)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n"
+        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(sleep_ns)
+        : "memory");
+  return ok != 0;
+}
+enum WaitResult { kWaitDone, kWaitFailedBefore, kWaitRanOut };
+template <bool CLUSTER>
+__device__ __forceinline__ WaitResult wait_phase(uint64_t* bar, uint32_t parity,
+                                                 const volatile int* failed, uint64_t limit_ns,
+                                                 uint32_t sleep_ns) {
   const uint64_t t0 = global_timer_ns();
-  while (!done()) {
-    if (*failed) return false;
-    if (global_timer_ns() - t0 > limit_ns) {
-      *failed = 1;
-      return false;
-    }
+  while (!phase_done<CLUSTER>(bar, parity, sleep_ns)) {
+    if (*failed) return kWaitFailedBefore;
+    if (global_timer_ns() - t0 > limit_ns) return kWaitRanOut;
   }
-  return true;
+  return kWaitDone;
 }
 
-__device__ __forceinline__ bool row_wait(uint64_t* bar, uint32_t parity, volatile int* failed) {
-  return wait_phase<false>(bar, parity, failed);
+__device__ __forceinline__ void store_peer(int* at, uint32_t rank, int v) {
+  asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(peer_addr(smem_addr(at), rank)), "r"(v)
+               : "memory");
 }
-__device__ __forceinline__ bool row_wait_cluster(uint64_t* bar, uint32_t parity,
-                                                 volatile int* failed) {
-  return wait_phase<true>(bar, parity, failed);
+__device__ __forceinline__ void store_peer(int2* at, uint32_t rank, int2 v) {
+  asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(peer_addr(smem_addr(at), rank)),
+               "r"(v.x), "r"(v.y)
+               : "memory");
 }
+__device__ __forceinline__ int load_peer(const int* at, uint32_t rank) {
+  int v;
+  asm volatile("ld.shared::cluster.b32 %0, [%1];"
+               : "=r"(v)
+               : "r"(peer_addr(smem_addr(at), rank))
+               : "memory");
+  return v;
+}
+
+// The rest of a wait whose first try did not end in time, out of the way of
+// the code around it (inlined everywhere it cost the policy case 2%).
+template <bool CLUSTER>
+__device__ __noinline__ bool wait_longer(RowShared* sh, uint64_t* bar, uint32_t parity,
+                                         uint64_t limit_ns, uint32_t sleep_ns, int split) {
+  const WaitResult w = wait_phase<CLUSTER>(bar, parity, &sh->failed, limit_ns, sleep_ns);
+  if (w == kWaitRanOut)  // for the whole cluster
+    for (int r = 0; r < split; ++r) store_peer(&sh->failed, r, 1);
+  return w == kWaitDone;
+}
+
+// One thread's waits in the ring kernel.
+struct RowWaits {
+  RowShared* sh;
+  uint64_t limit_ns;
+  uint32_t sleep_ns;
+  int split;
+
+  __device__ __forceinline__ RowWaits(RowShared* sh_, uint64_t limit, int split_)
+      : sh(sh_),
+        limit_ns(limit),
+        sleep_ns(limit < 1000000 ? static_cast<uint32_t>(limit) : 1000000u),
+        split(split_) {}
+  template <bool CLUSTER>
+  __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) const {
+    return phase_done<CLUSTER>(bar, parity, sleep_ns) ||
+           wait_longer<CLUSTER>(sh, bar, parity, limit_ns, sleep_ns, split);
+  }
+  __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
+    return wait<false>(bar, parity);
+  }
+  // all lanes of a warp, which agree on the outcome
+  __device__ __forceinline__ bool warp(uint64_t* bar, uint32_t parity) const {
+    return __all_sync(kFull, wait<false>(bar, parity));
+  }
+  __device__ __forceinline__ bool warp_cluster(uint64_t* bar, uint32_t parity) const {
+    return __all_sync(kFull, wait<true>(bar, parity));
+  }
+};
 
 __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
   asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)),
@@ -758,11 +825,6 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
-// A warp's wait: all of its lanes agree on the outcome.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* failed) {
-  return __all_sync(kFull, row_wait(bar, parity, failed));
-}
-
 // Arrives on a barrier of any CTA of the cluster.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr)
@@ -770,21 +832,13 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
 }
 
 // Asks for the launch of a CTA (cluster) that has not begun yet to be
-// cancelled; the answer (16 bytes) arrives in shared memory, with `everyone`
-// in that of every CTA of the cluster.
-__device__ __forceinline__ void ask_next(uint4* answer, uint64_t* bar, bool everyone) {
-  if (everyone)
-    asm volatile(
-        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes"
-        ".multicast::cluster::all.b128 [%0], [%1];" ::"r"(smem_addr(answer)),
-        "r"(smem_addr(bar))
-        : "memory");
-  else
-    asm volatile(
-        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128"
-        " [%0], [%1];" ::"r"(smem_addr(answer)),
-        "r"(smem_addr(bar))
-        : "memory");
+// cancelled; the answer (16 bytes) arrives in this CTA's shared memory.
+__device__ __forceinline__ void ask_next(uint4* answer, uint64_t* bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128"
+      " [%0], [%1];" ::"r"(smem_addr(answer)),
+      "r"(smem_addr(bar))
+      : "memory");
 }
 
 // The first CTA of the cancelled launch, or -1: nothing was left.
@@ -827,6 +881,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
   const int tid = static_cast<int>(threadIdx.x), warp = tid / kWarp;
   const int lane = static_cast<int>(lane_id());
   const int rank = static_cast<int>(blockIdx.x) % split;  // in the cluster
+  const RowWaits wait(sh, a.wait_ns, split);
   // vectors per CTA, whatever the row's first address
   const int per = (static_cast<int>(a.cols + 2 * (V::kCount - 1)) / V::kCount + split - 1) / split;
   if (tid == 0) {
@@ -838,17 +893,21 @@ __global__ void __launch_bounds__(kRowThreads, 1)
       mbar_init(&sh->head_full[i], 1);
       mbar_init(&sh->head_empty[i], kRowWarps);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh->answer_full[i], 1);
-      mbar_init(&sh->answer_empty[i], split);
-    }
+    mbar_init(&sh->answer_full, 1);
     for (int i = 0; i < kAheadRows; ++i) {
       mbar_init(&sh->row_full[i], 1);
       mbar_init(&sh->row_empty[i], kRowReaders);
     }
+    for (int i = 0; i < kTold; ++i) {
+      mbar_init(&sh->told_full[i], 1);
+      mbar_init(&sh->told_empty[i], split > 1 ? split - 1 : 1);
+    }
     mbar_init(&sh->together, kRowWarps);
     mbar_init(&sh->peers, split);
     sh->failed = 0;
+    sh->row[0] = make_int2(static_cast<int>(blockIdx.x) / split, 0);
+    sh->taken = 1;  // the row that the CTA was launched for
+    sh->first_bad = INT_MAX;
   }
   if (split > 1)
     cluster_sync();
@@ -858,21 +917,17 @@ __global__ void __launch_bounds__(kRowThreads, 1)
 
   // One warp's way through the scheduler's list: the next row, or -1.
   struct Way {
-    int slot;
-    uint32_t phase;
-    bool off;  // the row is not read
+    uint32_t n;  // rows so far
+    bool off;    // the row is not read
   };
   auto next_row = [&](Way& way) {
-    const bool ok = warp_wait(&sh->row_full[way.slot], way.phase, &sh->failed);
-    const int row = ok ? sh->row[way.slot] : -1;
-    way.off = sh->row_off[way.slot] != 0;
+    const uint32_t at = way.n % kAheadRows, phase = way.n / kAheadRows & 1;
+    if (!wait.warp(&sh->row_full[at], phase)) return -1;
+    const int2 row = sh->row[way.n++ % kRowHistory];
+    way.off = row.y != 0;
     __syncwarp();
-    if (lane == 0) mbar_arrive(&sh->row_empty[way.slot]);
-    if (++way.slot == kAheadRows) {
-      way.slot = 0;
-      way.phase ^= 1;
-    }
-    return row;
+    if (lane == 0) mbar_arrive(&sh->row_empty[at]);
+    return row.x;
   };
   // This CTA's segment of a row: vectors [begin, end), in chunks, the last
   // `keep` of which stay in the ring for the second pass.
@@ -895,7 +950,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
     int slot = 0;
     uint32_t use = 0;        // times round the ring
     uint32_t put_by_us = 0;  // slots (bits) that hold scores stored by this warp
-    Way way{0, 0, false};
+    Way way{0, false};
     bool going = true;
     for (int row; going && (row = next_row(way)) >= 0;) {
       if (way.off) continue;
@@ -911,7 +966,7 @@ __global__ void __launch_bounds__(kRowThreads, 1)
         unsigned char* to = ring + slot * kChunkBytes;
         bool ok = true;
         if (lane == 0) {
-          if (use > 0) ok = row_wait(&sh->empty[slot], (use - 1) & 1, &sh->failed);
+          if (use > 0) ok = wait(&sh->empty[slot], (use - 1) & 1);
           if (ok && e > b) {
             // plain stores to a slot come before the bulk copy over it, which
             // is of another proxy
@@ -943,53 +998,63 @@ __global__ void __launch_bounds__(kRowThreads, 1)
         }
       }
     }
-    if (sh->failed && lane == 0)  // copies in flight end before the CTA does
+    if (lane == 0)  // copies in flight end before the CTA does, whoever else has left
       for (int i = 0; i < ring_slots; ++i)
         if (i < slot || use > 0)
           mbar_wait_bounded(&sh->full[i], (i < slot ? use : use - 1) & 1, kCopyDrainNs);
   } else if (warp == kSchedulerWarp) {
     if (lane == 0) {
-      // The cluster's first CTA asks for the next launch to cancel, and not
-      // before the last answer was a success; every CTA arms its own barrier
-      // for the shared answer and tells the first CTA when it has read it.
-      int row = static_cast<int>(blockIdx.x) / split;
+      int2 row = make_int2(sh->row[0].x, 0);
+      row.y = row_off<OP>(a, row.x);
+      sh->row[0].y = row.y;
       for (uint32_t n = 0;; ++n) {
+        const uint32_t m = n - 1, told = m % kTold;  // from the second row on
+        if (n > 0 && rank > 0 && steal) {  // what the first CTA has remembered here
+          if (!wait.wait<true>(&sh->told_full[told], m / kTold & 1)) break;
+          row = sh->row[n % kRowHistory];
+          mbar_arrive_cluster(peer_addr(smem_addr(&sh->told_empty[told]), 0));
+        } else if (n > 0 && !steal) {
+          sh->row[n % kRowHistory] = row;
+        } else if (n > 0) {
+          // remembered whatever has happened: no other CTA has the row any more
+          const bool ok = m < kTold || split == 1 ||
+                          wait.wait<true>(&sh->told_empty[told], (m / kTold - 1) & 1);
+          for (int r = split - 1; r >= 0; --r) {
+            store_peer(&sh->row[n % kRowHistory], r, row);
+            if (row.x >= 0) store_peer(&sh->taken, r, static_cast<int>(n) + 1);
+            if (ok && r > 0) mbar_arrive_cluster(peer_addr(smem_addr(&sh->told_full[told]), r));
+          }
+          if (!ok) break;
+        }
         const int at = n % kAheadRows;
-        const int off = row >= 0 && row_off<OP>(a, row);
-        if (n >= kAheadRows &&
-            !row_wait(&sh->row_empty[at], (n / kAheadRows - 1) & 1, &sh->failed))
-          break;
-        sh->row[at] = row;
-        sh->row_off[at] = off;
+        if (n >= kAheadRows && !wait(&sh->row_empty[at], (n / kAheadRows - 1) & 1)) break;
         mbar_arrive(&sh->row_full[at]);
-        if (row < 0) break;
-        row = -1;
-        if (!steal) continue;
-        const int s = n & 1;
-        if (rank == 0 && n >= 2 &&
-            !row_wait_cluster(&sh->answer_empty[s], ((n >> 1) - 1) & 1, &sh->failed))
+        if (row.x < 0) break;
+        row = make_int2(-1, 0);
+        if (!steal || rank > 0 || *static_cast<volatile int*>(&sh->failed)) continue;
+        mbar_arrive_expect_tx(&sh->answer_full, 16);
+        ask_next(&sh->answer, &sh->answer_full);
+        if (!mbar_wait_bounded(&sh->answer_full, n & 1, kCopyDrainNs)) {
+          for (int r = 0; r < split; ++r) store_peer(&sh->failed, r, 1);
           break;
-        mbar_arrive_expect_tx(&sh->answer_full[s], 16);
-        if (rank == 0) ask_next(&sh->answer[s], &sh->answer_full[s], split > 1);
-        if (!row_wait(&sh->answer_full[s], (n >> 1) & 1, &sh->failed)) break;
-        const int cta = next_cta(&sh->answer[s]);
-        if (cta >= 0) row = cta / split;
-        if (split > 1)
-          mbar_arrive_cluster(peer_addr(smem_addr(&sh->answer_empty[s]), 0));
-        else
-          mbar_arrive(&sh->answer_empty[s]);
+        }
+        const int cta = next_cta(&sh->answer);
+        if (cta >= 0) {
+          row.x = cta / split;
+          row.y = row_off<OP>(a, row.x);
+        }
       }
     }
   } else if (warp >= kFirstTargetWarp) {  // every kTargetWarps-th row each
     int* table = reinterpret_cast<int*>(lists + heads * row_list_bytes(a.k)) +
                  (warp - kFirstTargetWarp) * target_slots(a.k);
-    Way way{0, 0, false};
+    Way way{0, false};
     uint32_t n = 0;  // the row's number among those of this CTA that are read
     for (int row; (row = next_row(way)) >= 0;) {
       if (way.off) continue;
       const uint32_t i = n % heads, use = n / heads;
       if (static_cast<int>(n++ % kTargetWarps) != warp - kFirstTargetWarp) continue;
-      if (use > 0 && !warp_wait(&sh->head_empty[i], (use - 1) & 1, &sh->failed)) break;
+      if (use > 0 && !wait.warp(&sh->head_empty[i], (use - 1) & 1)) break;
       load_targets<TYPE, OP, kLossGrad>(a, row, targets(i), table, &sh->head[i]);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->head_full[i]);
@@ -1025,8 +1090,9 @@ __global__ void __launch_bounds__(kRowThreads, 1)
       for (int u = 1; u < kChunkUnits; ++u) w ^= r[u].x ^ r[u].w;
       return w;
     };
-    Way way{0, 0, false};
-    for (int row; (row = next_row(way)) >= 0;) {
+    Way way{0, false};
+    int done = 0;
+    for (int row; (row = next_row(way)) >= 0; ++done) {
       const Segment s = segment(row);
       Raw* g = static_cast<Raw*>(a.grad) + row * a.grad_stride;
       const RowOut<TYPE> out(g, s.vecs);
@@ -1045,8 +1111,9 @@ __global__ void __launch_bounds__(kRowThreads, 1)
       const uint32_t phase0 = phase;
       // ---- the maximum and the sum
       RunningSoftmax<TYPE> run(scale2);
+      bool lost = false;  // a wait of this thread has run out
       for (int c = 0; c < s.chunks; ++c) {
-        row_wait(&sh->full[slot], phase, &sh->failed);
+        lost |= !wait(&sh->full[slot], phase);
         if (c < full_chunks) {
           uint4 r[kChunkUnits];
           fetch(slot, r);
@@ -1068,33 +1135,33 @@ __global__ void __launch_bounds__(kRowThreads, 1)
           phase ^= 1;
         }
       }
-      Softmax st = warp_join(run.result(), scale2);
+      // NaN tells every warp of the row to look whether a wait has run out
+      Softmax st = warp_join(lost ? Softmax{-INFINITY, NAN} : run.result(), scale2);
       Softmax* part = sh->part[parity];
       if (lane == 0) {
         part[warp] = st;
         mbar_arrive(&sh->together);
       }
       // every consumer warp has come here (a bounded wait, unlike bar.sync)
-      warp_wait(&sh->together, parity, &sh->failed);
+      bool bad = !wait.warp(&sh->together, parity);
       st = warp_join(lane < kRowWarps ? part[lane] : Softmax{-INFINITY, 0.0f}, scale2);
       // This CTA has read its targets before any CTA of the cluster learns the
       // row's sum: the gradient may lie over the logits, and a CTA's targets
       // are scores of all the others' segments.  (They are read rows ahead:
       // the wait is over as a rule.)
-      const bool got_head = warp_wait(&sh->head_full[hi], head_phase, &sh->failed);
+      const bool got_head = wait.warp(&sh->head_full[hi], head_phase);
       if (split > 1) {
         if (tid < split) {  // thread i hands this CTA's part to CTA i
           store_peer(&sh->peer[parity][rank], tid, st);
           mbar_arrive_cluster(peer_addr(smem_addr(&sh->peers), tid));
         }
-        __all_sync(kFull, row_wait_cluster(&sh->peers, parity, &sh->failed));
+        bad |= !wait.warp_cluster(&sh->peers, parity);
         st = warp_join(lane < split ? sh->peer[parity][lane] : Softmax{-INFINITY, 0.0f}, scale2);
       }
       parity ^= 1;
       // ---- the coefficient
       const Targets t = targets(hi);
-      RowResult res = row_result<OP, kLossGrad>(a, sh->head[hi], st.m, st.sum);
-      if (sh->failed) res = RowResult{NAN, NAN, NAN, NAN};
+      const RowResult res = row_result<OP, kLossGrad>(a, sh->head[hi], st.m, st.sum);
       if (rank == 0 && tid == 0) store_result<OP>(a, row, res);
       // ---- the gradient: the chunks that stayed, then those copied again
       const float f = res.c / st.sum;
@@ -1110,11 +1177,9 @@ __global__ void __launch_bounds__(kRowThreads, 1)
         const int c = i < s.keep ? early + i : i - s.keep;
         const int begin = s.begin + c * kChunkVecs;
         const bool inner = c >= inner0 && c < inner1;
-        // a chunk that stayed was waited for in the first pass
-        const bool ok = i < s.keep || row_wait(&sh->full[at], ph, &sh->failed);
-        const uint64_t fc = ok ? ff : pack2(NAN, NAN);
+        if (i >= s.keep) lost |= !wait(&sh->full[at], ph);  // the others: see above
         auto result = [&](const uint4& x) {  // zero also where the row holds NaN
-          return res.c == 0.0f ? make_uint4(0, 0, 0, 0) : vec_grad<TYPE>(x, e, fc);
+          return res.c == 0.0f ? make_uint4(0, 0, 0, 0) : vec_grad<TYPE>(x, e, ff);
         };
         if (inner) {
           uint4 r[kChunkUnits];
@@ -1169,13 +1234,38 @@ __global__ void __launch_bounds__(kRowThreads, 1)
         hi = 0;
         head_phase ^= 1;
       }
+      bad |= !got_head || isnan(st.sum);
+      if (early > 0) bad |= __any_sync(kFull, lost) != 0;
+      // where a wait of the row has run out (and not only a score is NaN) the
+      // row is not counted, and the warp leaves
+      if (bad && __any_sync(kFull, *static_cast<volatile int*>(&sh->failed))) break;
     }
+    if (lane == 0) sh->done[warp] = done;
   }
-  // no CTA ends while another may still write into its shared memory
-  if (split > 1) {
-    __syncwarp();
+  // No CTA ends while another may still write into its shared memory; from
+  // here on everyone knows whether a wait has run out.
+  __syncwarp();
+  if (split > 1)
     cluster_sync();
+  else
+    __syncthreads();
+  if (!sh->failed) return;
+  for (int i = tid; i < split * kRowWarps; i += kRowThreads)
+    atomicMin(&sh->first_bad, load_peer(&sh->done[i % kRowWarps], i / kRowWarps));
+  __syncthreads();
+  for (int n = sh->first_bad; n < sh->taken; ++n) {
+    const int row = sh->row[n % kRowHistory].x;
+    const Segment s = segment(row);
+    const RowOut<TYPE> out(static_cast<Raw*>(a.grad) + row * a.grad_stride, s.vecs);
+    uint64_t nan[V::kCount / 2];
+#pragma unroll
+    for (int i = 0; i < V::kCount / 2; ++i) nan[i] = pack2(NAN, NAN);
+    for (int v = s.begin + tid; v < s.end; v += kRowThreads)
+      out.store(s.vecs, v, vec_of<TYPE>(nan));
+    if (rank == 0 && tid == 0) store_result<OP>(a, row, RowResult{NAN, NAN, NAN, NAN});
   }
+  if (a.status != nullptr && rank == 0 && tid == 0) *a.status = kErrLookback;
+  if (split > 1) cluster_sync();  // nor while another reads it
 }
 
 // -------------------------------------------------------------------- launch

@@ -344,7 +344,12 @@ struct RunningSoftmax {
   uint64_t acc[2];
 
   __device__ __forceinline__ explicit RunningSoftmax(float scale2)
-      : scale(scale2), slack(8.0f / scale2), o(-INFINITY), limit(-INFINITY), top(-INFINITY), e(0.0f, scale2) {
+      : scale(scale2),
+        slack(8.0f / scale2),
+        o(-INFINITY),
+        limit(-INFINITY),
+        top(-INFINITY),
+        e(0.0f, scale2) {
     acc[0] = acc[1] = 0;
   }
   __device__ __forceinline__ float total() const {

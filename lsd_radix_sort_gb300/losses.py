@@ -38,8 +38,8 @@ __all__ = [
 MAX_TOP = 1024
 MAX_EXPERTS = 1024
 
-_P, _I64, _I, _F, _SZ = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float,
-                         ctypes.c_size_t)
+_P, _I64, _U64, _I, _F, _SZ = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_uint64, ctypes.c_int,
+                               ctypes.c_float, ctypes.c_size_t)
 
 
 class DistillArgs(ctypes.Structure):
@@ -48,7 +48,8 @@ class DistillArgs(ctypes.Structure):
                 ("top_values", _P), ("top_values_stride", _I64), ("top_indices", _P),
                 ("top_indices_stride", _I64), ("weights", _P), ("losses", _P), ("lse", _P),
                 ("grad", _P), ("grad_stride", _I64), ("logits_type", _I),
-                ("top_values_type", _I), ("index_bytes", _I), ("top", _I), ("temperature", _F)]
+                ("top_values_type", _I), ("index_bytes", _I), ("top", _I), ("temperature", _F),
+                ("wait_timeout_ns", _U64), ("status", _P)]
 
 
 class PolicyArgs(ctypes.Structure):
@@ -57,7 +58,8 @@ class PolicyArgs(ctypes.Structure):
                 ("actions", _P), ("old_logprobs", _P), ("advantages", _P), ("ref_logprobs", _P),
                 ("weights", _P), ("losses", _P), ("logprobs", _P), ("lse", _P), ("grad", _P),
                 ("grad_stride", _I64), ("logits_type", _I), ("index_bytes", _I),
-                ("clip_low", _F), ("clip_high", _F), ("kl_coef", _F), ("temperature", _F)]
+                ("clip_low", _F), ("clip_high", _F), ("kl_coef", _F), ("temperature", _F),
+                ("wait_timeout_ns", _U64), ("status", _P)]
 
 
 class BalanceArgs(ctypes.Structure):
@@ -165,7 +167,7 @@ def _ptr(t):
 
 # ------------------------------------------------------------ distillation
 def _distill(logits, top_values, top_indices, temperature, weights, losses, lse, grad, with_grad,
-             backward, grad_losses, stream):
+             backward, grad_losses, stream, wait_timeout_ns=0, status=None):
     torch = _torch or _load()
     kind, top_kind = _kind(logits, "logits"), _kind(top_values, "top_values")
     rows, cols, stride = _matrix(logits, "logits")
@@ -186,9 +188,11 @@ def _distill(logits, top_values, top_indices, temperature, weights, losses, lse,
         raise ValueError("the backward call needs the forward call's lse")
     if grad_losses is not None:
         _vector(grad_losses, rows, "grad_losses")
+    if status is not None:
+        _vector(status, 1, "status_out", torch.int32)
     grad_stride = cols if grad is None else _grad_stride(logits, grad)
     index = _device(stream, logits, top_values, top_indices, weights, losses, lse, grad,
-                    grad_losses)
+                    grad_losses, status)
 
     with _on(stream):
         device = logits.device
@@ -200,7 +204,8 @@ def _distill(logits, top_values, top_indices, temperature, weights, losses, lse,
             grad = torch.empty((rows, cols), dtype=logits.dtype, device=device)
     args = DistillArgs(logits.data_ptr(), stride, rows, cols, top_values.data_ptr(), values_stride,
                        top_indices.data_ptr(), indices_stride, _ptr(weights), _ptr(losses),
-                       lse.data_ptr(), _ptr(grad), grad_stride, kind, top_kind, ib, k, temperature)
+                       lse.data_ptr(), _ptr(grad), grad_stride, kind, top_kind, ib, k, temperature,
+                       wait_timeout_ns, _ptr(status))
     lib = _lib_of()
     s = _raw_stream(index) if stream is None else stream.cuda_stream
     if backward:
@@ -229,11 +234,15 @@ def distill_loss(logits, top_values, top_indices, temperature: float = 1.0, weig
 
 
 def distill_loss_grad(logits, top_values, top_indices, temperature: float = 1.0, weights=None,
-                      losses_out=None, lse_out=None, grad_out=None, stream=None):
+                      losses_out=None, lse_out=None, grad_out=None, stream=None,
+                      wait_timeout_ns: int = 0, status_out=None):
     """(losses, lse, grad): ``distill_loss`` and the gradient of the sum of its
-    losses.  ``grad_out`` may be ``logits`` itself."""
+    losses.  ``grad_out`` may be ``logits`` itself.  ``wait_timeout_ns`` limits
+    a wait inside the kernel of long rows (0: 2 s); where one runs out, rows
+    that are not finished get NaN and ``status_out`` (one int32 on the device,
+    zero beforehand) RS_ERR_LOOKBACK_TIMEOUT."""
     return _distill(logits, top_values, top_indices, temperature, weights, losses_out, lse_out,
-                    grad_out, True, False, None, stream)
+                    grad_out, True, False, None, stream, wait_timeout_ns, status_out)
 
 
 def distill_loss_backward(grad_losses, logits, lse, top_values, top_indices,
@@ -246,7 +255,8 @@ def distill_loss_backward(grad_losses, logits, lse, top_values, top_indices,
 
 # ------------------------------------------------------------- policy loss
 def _policy(logits, actions, old, advantages, ref, clip_low, clip_high, kl_coef, temperature,
-            weights, losses, logprobs, lse, grad, with_grad, backward, grad_losses, stream):
+            weights, losses, logprobs, lse, grad, with_grad, backward, grad_losses, stream,
+            wait_timeout_ns=0, status=None):
     torch = _torch or _load()
     kind = _kind(logits, "logits")
     rows, cols, stride = _matrix(logits, "logits")
@@ -270,9 +280,11 @@ def _policy(logits, actions, old, advantages, ref, clip_low, clip_high, kl_coef,
         raise ValueError("the backward call needs the forward call's lse")
     if grad_losses is not None:
         _vector(grad_losses, rows, "grad_losses")
+    if status is not None:
+        _vector(status, 1, "status_out", torch.int32)
     grad_stride = cols if grad is None else _grad_stride(logits, grad)
     index = _device(stream, logits, actions, old, advantages, ref, weights, losses, logprobs, lse,
-                    grad, grad_losses)
+                    grad, grad_losses, status)
 
     with _on(stream):
         device = logits.device
@@ -287,7 +299,7 @@ def _policy(logits, actions, old, advantages, ref, clip_low, clip_high, kl_coef,
     args = PolicyArgs(logits.data_ptr(), stride, rows, cols, actions.data_ptr(), old.data_ptr(),
                       advantages.data_ptr(), _ptr(ref), _ptr(weights), _ptr(losses),
                       _ptr(logprobs), lse.data_ptr(), _ptr(grad), grad_stride, kind, ib, clip_low,
-                      clip_high, kl_coef, temperature)
+                      clip_high, kl_coef, temperature, wait_timeout_ns, _ptr(status))
     lib = _lib_of()
     s = _raw_stream(index) if stream is None else stream.cuda_stream
     if backward:
@@ -321,12 +333,14 @@ def policy_loss(logits, actions, old_logprobs, advantages, ref_logprobs=None,
 def policy_loss_grad(logits, actions, old_logprobs, advantages, ref_logprobs=None,
                      clip_low: float = 0.2, clip_high: float = 0.2, kl_coef: float = 0.0,
                      temperature: float = 1.0, weights=None, losses_out=None, logprobs_out=None,
-                     lse_out=None, grad_out=None, stream=None):
+                     lse_out=None, grad_out=None, stream=None, wait_timeout_ns: int = 0,
+                     status_out=None):
     """(losses, logprobs, lse, grad): ``policy_loss`` and the gradient of the
-    sum of its losses.  ``grad_out`` may be ``logits`` itself."""
+    sum of its losses.  ``grad_out`` may be ``logits`` itself;
+    ``wait_timeout_ns`` and ``status_out`` as ``distill_loss_grad``."""
     return _policy(logits, actions, old_logprobs, advantages, ref_logprobs, clip_low, clip_high,
                    kl_coef, temperature, weights, losses_out, logprobs_out, lse_out, grad_out,
-                   True, False, None, stream)
+                   True, False, None, stream, wait_timeout_ns, status_out)
 
 
 def policy_loss_backward(grad_losses, logits, lse, actions, old_logprobs, advantages,

@@ -51,3 +51,16 @@ def test_tensors_of_a_device_that_is_not_current(monkeypatch, name):
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
     with pytest.raises(ValueError, match="the stream must be one of cuda:1"):
         CALLS[name](stream=OtherStream())
+
+
+@pytest.mark.parametrize("make,name", [("distill_args", "rs_distill_loss"), ("policy_args", "rs_policy_loss")])
+def test_wait_limits_and_status(make, name):
+    """By the C ABI: a limit above 60 s, a status word that is not aligned."""
+    import ctypes
+
+    from lsd_radix_sort_gb300 import build
+    from tests import test_loss_checks as checks
+    build.build()
+    call = getattr(rs.load_library(), name)
+    for change in (dict(wait_timeout_ns=60_000_000_001), dict(status=checks.BASE + 2)):
+        assert call(ctypes.byref(getattr(checks, make)(**change)), None) == rs.RS_ERR_INVALID
