@@ -267,16 +267,13 @@ __device__ __forceinline__ RowResult row_result(const RowLossArgs& a, const Head
   return r;
 }
 
-// The exponentials of a row from its maximum, or (kLossBwd, unless the row's
-// statistics were taken again) its saved lse.
+// The exponentials of a row from its maximum, or (kLossBwd) its saved lse.
 template <int TYPE, int MODE>
-__device__ __forceinline__ auto exponent(const RowLossArgs& a, float m, bool again) {
-  if constexpr (MODE == kLossBwd) {
-    using E = ExponentOfLse<TYPE == RS_SCORE_F32>;
-    return again ? E(Exponent(origin(m), a.scale2)) : E(m, a.scale2, a.scale2_low);
-  } else {
+__device__ __forceinline__ auto exponent(const RowLossArgs& a, float m) {
+  if constexpr (MODE == kLossBwd)
+    return ExponentOfLse<TYPE == RS_SCORE_F32>(m, a.scale2, a.scale2_low);
+  else
     return Exponent(origin(m), a.scale2);
-  }
 }
 
 template <int OP>
@@ -285,6 +282,86 @@ __device__ __forceinline__ void store_result(const RowLossArgs& a, int64_t row,
   a.losses[row] = r.loss;
   a.lse[row] = r.lse;
   if (OP == kOpPolicy) a.logprobs[row] = r.logp;
+}
+
+__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+
+__device__ __forceinline__ void store_peer(Softmax* at, uint32_t rank, const Softmax& v) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(peer_addr(smem_addr(at), rank)),
+               "f"(v.m), "f"(v.sum)
+               : "memory");
+}
+
+// The two halves of a cluster's barrier, where it only has to be known that
+// every CTA has begun: another CTA's shared memory must not be touched before.
+__device__ __forceinline__ void cluster_begun() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+
+// The backward call's gradient of vectors [begin, end) of a row whose saved lse
+// says too little: the first WARPS warps of the CTA take the statistics of all
+// of the row, then its threads write the gradient, one vector at a time.
+// Rare, and out of the way of the registers of the usual way (inlined, 8,000 x
+// 7,000 policy rows of ordinary lse took 38 us instead of 34).  together: other
+// CTAs read the row too, and the gradient goes over it.
+template <int TYPE, int OP, int WARPS>
+__device__ __noinline__ void backward_again(const RowLossArgs& a, int64_t row, int begin, int end,
+                                            Targets t, const Head& head, Softmax* part,
+                                            bool together) {
+  using S = Score<TYPE>;
+  using Raw = typename S::Raw;
+  using V = ScoreVec<TYPE>;
+  const Raw* x = static_cast<const Raw*>(a.logits) + row * a.stride;
+  Raw* g = static_cast<Raw*>(a.grad) + row * a.grad_stride;
+  const RowVecs<TYPE> vecs(x, static_cast<int>(a.cols));
+  const uint4* xv = reinterpret_cast<const uint4*>(x - vecs.lead);
+  const RowOut<TYPE> out(g, vecs);
+  const int tid = static_cast<int>(threadIdx.x), lane = static_cast<int>(lane_id());
+  if (tid < WARPS * kWarp) {
+    constexpr int kBatch = 2, kStep = WARPS * kWarp;  // more would take registers
+    RunningSoftmax<TYPE> run(a.scale2);
+#pragma unroll 1
+    for (int v0 = tid; v0 < vecs.count; v0 += kBatch * kStep) {
+      uint4 r[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) r[u] = vecs.load(xv, x, v0 + u * kStep);
+      run.add(r);
+    }
+    const Softmax s = warp_join(run.result(), a.scale2);
+    if (lane == 0) part[tid / kWarp] = s;
+  }
+  __syncthreads();
+  const Softmax s = warp_join(lane < WARPS ? part[lane] : Softmax{-INFINITY, 0.0f}, a.scale2);
+  const RowResult res = row_result<OP, kLossGrad>(a, head, s.m, s.sum);
+  if (together) cluster_sync();
+  const float f = res.c / s.sum;
+  const Exponent e(origin(s.m), a.scale2);
+  const uint64_t ff = pack2(f * e.mend, f * e.mend);
+#pragma unroll 1
+  for (int v = begin + tid; v < end; v += static_cast<int>(blockDim.x))
+    out.store(vecs, v, res.c == 0.0f ? make_uint4(0, 0, 0, 0)
+                                     : vec_grad<TYPE>(vecs.load(xv, x, v), e, ff));
+  if (res.c == 0.0f) return;
+  __syncthreads();
+  const int64_t first = static_cast<int64_t>(begin) * V::kCount - vecs.lead;
+  const int64_t last = static_cast<int64_t>(end) * V::kCount - vecs.lead;
+  for (int k = tid; k < a.k; k += static_cast<int>(blockDim.x)) {
+    const int col = t.col[k];
+    if (col >= 0 && col >= first && col < last)
+      g[col] = S::store(e.one(t.x[k]) * f - res.c * t.p[k]);
+  }
 }
 
 // ---------------------------------------------------------------- short rows
@@ -299,7 +376,7 @@ __device__ __forceinline__ void store_result(const RowLossArgs& a, int64_t row,
 constexpr int kShortWarps = 24;
 template <int TYPE, int OP, int MODE, int kThreads, int VECS>
 __global__ void __launch_bounds__(kThreads, VECS == 16 ? 2 : kShortWarps / (kThreads / kWarp))
-    row_loss_short_kernel(const RowLossArgs a) {
+    row_loss_short_kernel(const __grid_constant__ RowLossArgs a) {
   grid_dependency_sync();
   using S = Score<TYPE>;
   using Raw = typename S::Raw;
@@ -329,35 +406,26 @@ __global__ void __launch_bounds__(kThreads, VECS == 16 ? 2 : kShortWarps / (kThr
   }
   uint4 r[VECS];
 #pragma unroll
-  for (int u = 0; u < VECS; ++u) {
-    const int v = tid + u * kThreads;
-    if (vecs.whole(v))
-      r[u] = xv[v];
-    else
-      r[u] = v < vecs.count ? vecs.load_edge(x, v)
-                            : make_uint4(V::kMinusInf, V::kMinusInf, V::kMinusInf, V::kMinusInf);
-  }
+  for (int u = 0; u < VECS; ++u) r[u] = vecs.load(xv, x, tid + u * kThreads);
   if (warp == kWarps - 1) load_targets<TYPE, OP, MODE>(a, row, t, slots, &head);
-  Softmax s{-INFINITY, 1.0f};
-  if (MODE == kLossBwd) s.m = a.lse[row];
-  const bool again = MODE == kLossBwd && far_lse(s.m);
-  if (MODE == kLossBwd && !again) {
+  Softmax s;
+  if constexpr (MODE == kLossBwd) {
+    s = {a.lse[row], 1.0f};
     __syncthreads();
+    if (far_lse(s.m))
+      return backward_again<TYPE, OP, kWarps>(a, row, 0, vecs.count, t, head, part, false);
   } else {
-    RunningSoftmax<TYPE> run(scale2);
-    run.add(r);
-    s = warp_join(run.result(), scale2);
+    s = warp_join(softmax_of<TYPE>(r, scale2), scale2);
     if (lane_id() == 0) part[warp] = s;
     __syncthreads();
     s = lane_id() < kWarps ? part[lane_id()] : Softmax{-INFINITY, 0.0f};
     s = warp_join(s, scale2);
   }
-  const RowResult res = again ? row_result<OP, kLossGrad>(a, head, s.m, s.sum)
-                              : row_result<OP, MODE>(a, head, s.m, s.sum);
+  const RowResult res = row_result<OP, MODE>(a, head, s.m, s.sum);
   if (MODE != kLossBwd && tid == 0) store_result<OP>(a, row, res);
   if (MODE == kLossFwd) return;
   const float f = res.c / s.sum;
-  const auto e = exponent<TYPE, MODE>(a, s.m, again);
+  const auto e = exponent<TYPE, MODE>(a, s.m);
   const uint64_t ff = pack2(f * e.mend, f * e.mend);
 #pragma unroll
   for (int u = 0; u < VECS; ++u) {
@@ -391,32 +459,6 @@ constexpr int kStreamWaves = 2;
 constexpr int64_t kStreamLeast = 16384;
 constexpr int kMaxCluster = 16;
 
-__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
-  uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
-}
-
-__device__ __forceinline__ void store_peer(Softmax* at, uint32_t rank, const Softmax& v) {
-  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(peer_addr(smem_addr(at), rank)),
-               "f"(v.m), "f"(v.sum)
-               : "memory");
-}
-
-// The two halves of a cluster's barrier, where it only has to be known that
-// every CTA has begun: another CTA's shared memory must not be touched before.
-__device__ __forceinline__ void cluster_begun() {
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::
-                   : "memory");
-}
-
 // A thread's vectors of a segment [begin, end): begin + tid, + kStreamThreads,
 // ..., in batches of kStreamBatch, the next batch's loads under way while one
 // is worked on; vectors past the end are -inf.
@@ -434,19 +476,19 @@ struct Stream {
   __device__ __forceinline__ Stream(const Raw* x_, const RowVecs<TYPE>& vecs_, int begin, int end_,
                                     int tid)
       : x(x_), vecs(vecs_), end(end_), v(begin + tid) {
-    if (v < end) load(v, end, r);
+    if (v < end) load(v, r);
   }
-  __device__ __forceinline__ void load(int v0, int last, uint4 (&to)[kStreamBatch]) const {
+  __device__ __forceinline__ void load(int v0, uint4 (&to)[kStreamBatch]) const {
     const uint4* xv = reinterpret_cast<const uint4*>(x - vecs.lead);
     const int v1 = v0 + (kStreamBatch - 1) * kStreamThreads;
-    if (v0 >= vecs.whole_begin() && v1 < min(last, vecs.whole_end())) {
+    if (v0 >= vecs.whole_begin() && v1 < min(end, vecs.whole_end())) {
 #pragma unroll
       for (int u = 0; u < kStreamBatch; ++u) to[u] = __ldcs(xv + v0 + u * kStreamThreads);
     } else {
 #pragma unroll
       for (int u = 0; u < kStreamBatch; ++u) {
         const int w = v0 + u * kStreamThreads;
-        if (w >= last)
+        if (w >= end)
           to[u] = make_uint4(V::kMinusInf, V::kMinusInf, V::kMinusInf, V::kMinusInf);
         else if (vecs.whole(w))
           to[u] = __ldcs(xv + w);
@@ -460,7 +502,7 @@ struct Stream {
   __device__ __forceinline__ void run(F&& body) {
     uint4 ahead[kStreamBatch];
     for (; v < end; v += kStep) {
-      if (v + kStep < end) load(v + kStep, end, ahead);
+      if (v + kStep < end) load(v + kStep, ahead);
       body(v, r);
 #pragma unroll
       for (int u = 0; u < kStreamBatch; ++u) r[u] = ahead[u];
@@ -518,7 +560,8 @@ __global__ void __launch_bounds__(kStreamThreads + kWarp, kStreamCtas)
 
 template <int TYPE, int OP>
 __global__ void __launch_bounds__(kStreamThreads + kWarp, kStreamCtas)
-    row_loss_backward_kernel(const RowLossArgs a, const int split, const bool together) {
+    row_loss_backward_kernel(const __grid_constant__ RowLossArgs a, const int split,
+                             const bool together) {
   using S = Score<TYPE>;
   using Raw = typename S::Raw;
   using V = ScoreVec<TYPE>;
@@ -564,39 +607,21 @@ __global__ void __launch_bounds__(kStreamThreads + kWarp, kStreamCtas)
     load_targets<TYPE, OP, kLossBwd>(a, row, t, reinterpret_cast<int*>(t.x + a.k), &head);
   // the first loads are under way before the targets are known
   Stream<TYPE> stream(x, vecs, begin, off || warp == kStreamWarps ? begin : end, tid);
-  Softmax s{off ? 0.0f : a.lse[row], 1.0f};
-  const bool again = far_lse(s.m);
+  const float m = off ? 0.0f : a.lse[row];
   __syncthreads();
-  if (again) {  // every CTA of the row reads all of it
-    s = Softmax{-INFINITY, 0.0f};
-    if (warp < kStreamWarps) {
-      RunningSoftmax<TYPE> run(a.scale2);
-      for (int v = tid; v < vecs.count; v += Stream<TYPE>::kStep) {
-        stream.load(v, vecs.count, stream.r);
-        run.add(stream.r);
-      }
-      s = warp_join(run.result(), a.scale2);
-      if (lane_id() == 0) part[warp] = s;
-    }
-    __syncthreads();
-    s = lane_id() < kStreamWarps ? part[lane_id()] : Softmax{-INFINITY, 0.0f};
-    s = warp_join(s, a.scale2);
-    if (warp < kStreamWarps && stream.v < end) stream.load(stream.v, end, stream.r);
-  }
-  const float c = off     ? 0.0f
-                  : again ? row_result<OP, kLossGrad>(a, head, s.m, s.sum).c
-                          : row_result<OP, kLossBwd>(a, head, s.m, 1.0f).c;
-  const float per_sum = c / s.sum;
-  const auto e = exponent<TYPE, kLossBwd>(a, s.m, again);
+  if (far_lse(m))
+    return backward_again<TYPE, OP, kStreamWarps>(a, row, begin, end, t, head, part, together);
+  const float c = off ? 0.0f : row_result<OP, kLossBwd>(a, head, m, 1.0f).c;
+  const auto e = exponent<TYPE, kLossBwd>(a, m);
   // over its own logits no CTA of the row may write before all of them have
-  // read the action's score, and the row where its statistics were taken again
+  // read the action's score
   if (together && !off) cluster_sync();
   if (warp < kStreamWarps) {
     if (c == 0.0f) {  // nothing of the row is read
       const uint4 zero[kStreamBatch] = {};
       for (int v = begin + tid; v < end; v += kStreamThreads * kStreamBatch) put(v, zero);
     } else {
-      const uint64_t f = pack2(per_sum * e.mend, per_sum * e.mend);
+      const uint64_t f = pack2(c * e.mend, c * e.mend);
       stream.run([&](int v, uint4(&r)[kStreamBatch]) {
 #pragma unroll
         for (int u = 0; u < kStreamBatch; ++u) r[u] = vec_grad<TYPE>(r[u], e, f);
@@ -611,7 +636,7 @@ __global__ void __launch_bounds__(kStreamThreads + kWarp, kStreamCtas)
   for (int k = tid; k < a.k; k += kStreamThreads + kWarp) {
     const int col = t.col[k];
     if (col >= 0 && col >= b && col < last)
-      g[col] = S::store(e.one(t.x[k]) * per_sum - c * t.p[k]);
+      g[col] = S::store(e.one(t.x[k]) * c - c * t.p[k]);
   }
 }
 
@@ -1378,9 +1403,11 @@ cudaError_t launch_row_loss_as(const RowLossArgs& a, cudaStream_t s) {
   // f16 policy gradients of 2,000 x 30,011 took 63 us so and 89 us in the ring,
   // 300 x 30,000 7.8 and 11.4.  (The forms that read a row once need not keep
   // it.)
-  if (MODE == kLossGrad && vecs <= 256 * 16 && a.rows >= 300)
-    return launch_kernel(row_loss_short_kernel<TYPE, OP, MODE, 256, 16>, each, dim3(256), lists, s,
-                         a);
+  if constexpr (MODE == kLossGrad) {
+    if (vecs <= 256 * 16 && a.rows >= 300)
+      return launch_kernel(row_loss_short_kernel<TYPE, OP, MODE, 256, 16>, each, dim3(256), lists,
+                           s, a);
+  }
   if constexpr (MODE != kLossGrad) {
     int split = 1;
     while (split < kMaxCluster && a.rows * split < int64_t(sms) * kStreamCtas * kStreamWaves &&

@@ -289,9 +289,6 @@ struct ExponentOfLse {
         os2(lse * kLog2e) {
     mend = exp2_approx(__fmaf_rn(-lse, kLog2e, os2) - lse * kLog2eLow);
   }
-  // from the row's own largest score
-  __device__ __forceinline__ explicit ExponentOfLse(const Exponent& e)
-      : hi(e.scale), lo(0.0f), least(-3.0e38f), os2(e.os2), mend(e.mend) {}
   // -os2, with the low product; that of a score whose exponential is 0 anyway
   // must not be infinite (for lo < 0 it would be +inf)
   __device__ __forceinline__ float rest(float x) const {
@@ -379,6 +376,19 @@ struct RunningSoftmax {
   }
 };
 
+// The softmax of vectors that a thread holds all at once.
+template <int TYPE, int VECS>
+__device__ __forceinline__ Softmax softmax_of(const uint4 (&v)[VECS], float scale2) {
+  const float m = vec_max<TYPE>(v);
+  const Exponent e(origin(m), scale2);
+  uint64_t acc[2] = {0, 0};
+#pragma unroll
+  for (int u = 0; u < VECS; ++u) vec_exp_sum<TYPE>(v[u], e, acc);
+  float a, b;
+  unpack2(add2(acc[0], acc[1]), a, b);
+  return {m, (a + b) * e.mend};
+}
+
 // A row of scores as 16-byte vectors of memory: vector 0 begins at the row's
 // address rounded down to 16 bytes, so its first `lead` scores, and the last
 // vector's scores past the row, belong to others and are never touched.
@@ -420,7 +430,14 @@ struct RowVecs {
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
 
-  // The same to 16 bytes of shared memory, one lane per score.
+  // Any vector, -inf past the row; vec0: the 16 bytes that vector 0 begins in.
+  __device__ __forceinline__ uint4 load(const uint4* vec0, const Raw* row, int v) const {
+    if (whole(v)) return vec0[v];
+    constexpr uint32_t kNone = ScoreVec<TYPE>::kMinusInf;
+    return v < count ? load_edge(row, v) : make_uint4(kNone, kNone, kNone, kNone);
+  }
+
+  // The same of an edge to 16 bytes of shared memory, one lane per score.
   __device__ __forceinline__ void copy_edge(const Raw* row, int v, void* to, int lane) const {
     if (lane < kN) {
       const int64_t j = static_cast<int64_t>(v) * kN - lead + lane;
