@@ -1404,7 +1404,7 @@ cudaError_t launch_row_loss_as(const RowLossArgs& a, cudaStream_t s) {
   // 300 x 30,000 7.8 and 11.4.  (The forms that read a row once need not keep
   // it.)
   if constexpr (MODE == kLossGrad) {
-    if (vecs <= 256 * 16 && a.rows >= 300)
+    if (vecs <= 256 * 16 && a.rows >= 2 * sms)
       return launch_kernel(row_loss_short_kernel<TYPE, OP, MODE, 256, 16>, each, dim3(256), lists,
                            s, a);
   }

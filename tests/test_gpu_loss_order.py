@@ -158,3 +158,34 @@ def test_balance_after_a_mask_was_written(rs, dtype):
             mask.copy_(m)
             got.append(rs.balance_loss_grad(x, ids, token_mask=mask))
         assert all(same(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("rows,cols", [(40, 1003), (40, 7001), (310, 9001), (310, 30003), (40, 30003), (200, 50003)])
+def test_gradients_aligned_otherwise(rs, rows, cols, dtype):
+    """Logits in padded rows, the gradient in packed ones and in rows that begin
+    elsewhere in their 16 bytes: the bits of a gradient aligned as the logits,
+    and nothing beside it is written."""
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    wide = torch.randn(rows, cols + 21, generator=g, device="cuda").to(dtype)
+    x = wide[:, :cols]
+    actions = torch.randint(0, cols, (rows,), generator=g, device="cuda")
+    old = torch.full((rows,), -8.0, device="cuda")
+    adv = torch.randn(rows, generator=g, device="cuda")
+    values, indices = torch.topk(x, 6, dim=1)
+    lse = rs.policy_loss(x, actions, old, adv)[2]
+    calls = [lambda out: rs.policy_loss_grad(x, actions, old, adv, grad_out=out)[3],
+             lambda out: rs.distill_loss_grad(x, values, indices, grad_out=out)[2],
+             lambda out: rs.policy_loss_backward(None, x, lse, actions, old, adv, grad_out=out),
+             lambda out: rs.distill_loss_backward(None, x, lse, values, indices, grad_out=out)]
+    for call in calls:
+        like = torch.empty_like(wide)[:, :cols]
+        want = call(like).clone()
+        packed = call(torch.empty(rows, cols, dtype=dtype, device="cuda"))
+        assert torch.equal(packed, want)
+        for pad, shift in ((9, 1), (5, 3), (16, 8)):
+            buf = torch.full((rows * (cols + pad) + 64,), 7.0, dtype=dtype, device="cuda")
+            out = buf[shift:].as_strided((rows, cols), (cols + pad, 1), shift)
+            assert torch.equal(call(out), want)
+            out.fill_(7.0)
+            assert bool((buf == 7.0).all())
