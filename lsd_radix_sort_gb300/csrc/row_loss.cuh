@@ -1399,12 +1399,13 @@ cudaError_t launch_row_loss_as(const RowLossArgs& a, cudaStream_t s) {
     return launch_kernel(row_loss_short_kernel<TYPE, OP, MODE, 256, 8>, each, dim3(256), lists, s,
                          a);
   const int sms = device_sm_count();
-  // Rows of 32 to 64 KB, where there are enough of them for two CTAs per SM:
-  // f16 policy gradients of 2,000 x 30,011 took 63 us so and 89 us in the ring,
-  // 300 x 30,000 7.8 and 11.4.  (The forms that read a row once need not keep
-  // it.)
+  // Rows of 32 to 64 KB, where they outnumber the SMs (the ring holds one per
+  // SM, registers two): f16 policy gradients of 160 x 30,000 took 7.8 us so and
+  // 11.6 in the ring, 500 13.9 and 20.8; distillation with 16 targets of 160
+  // 9.0 and 11.9, of 152 8.5 and 8.0.  (The forms that read a row once need
+  // not keep it.)
   if constexpr (MODE == kLossGrad) {
-    if (vecs <= 256 * 16 && a.rows >= 2 * sms)
+    if (vecs <= 256 * 16 && a.rows > sms)
       return launch_kernel(row_loss_short_kernel<TYPE, OP, MODE, 256, 16>, each, dim3(256), lists,
                            s, a);
   }

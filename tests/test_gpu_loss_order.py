@@ -189,3 +189,18 @@ def test_gradients_aligned_otherwise(rs, rows, cols, dtype):
             assert torch.equal(call(out), want)
             out.fill_(7.0)
             assert bool((buf == 7.0).all())
+
+
+@pytest.mark.parametrize("rows", [151, 152, 153, 160, 299, 300, 304])
+def test_both_ways_of_middling_rows_agree(rs, rows):
+    """Rows of 32 to 64 KB are held in registers where they outnumber the SMs,
+    and in the ring otherwise: each row against the same row among few others."""
+    x, g = rows_of(rows, 20000, torch.bfloat16, 5)
+    actions, old, adv = policy_of(x, g)
+    out = rs.policy_loss_grad(x, actions, old, adv)
+    few = rs.policy_loss_grad(x[:5], actions[:5], old[:5], adv[:5])
+    for a, b in zip(out, few):
+        # the two ways add up in other orders: 20,000 / 32 additions, and a rounding to bf16
+        u = 2.0 ** -8 if b.dtype is torch.bfloat16 else 0
+        assert bool(((a[:5].double() - b.double()).abs()
+                     <= b.double().abs() * (u + 1e-4) + 1e-4 * (b.dim() == 1) + 1e-9).all())
