@@ -347,12 +347,13 @@ rs_status rs_noalloc_timeout_probe(uint64_t timeout_ns, void* stream, rs_status*
 /* ------------------------------------------------------------------------
  * Losses over rows of scores.
  *
- * What the sorts above order, these train on: rows of logits with the
+ * Two of them train on what the sorts above order: rows of logits with the
  * teacher's top values and columns that a descending row sort returns
- * (rs_distill_loss), rows of logits with the one column that was sampled
- * (rs_policy_loss), and rows of a router's scores with the expert ids chosen
+ * (rs_distill_loss), and rows of a router's scores with the expert ids chosen
  * in them (rs_balance_loss, whose counts are the segment lengths of the
- * (expert, token) pairs that radix_sort_pairs_u32 groups).
+ * (expert, token) pairs that radix_sort_pairs_u32 groups).  The third,
+ * rs_policy_loss, is the same pass over rows of logits with the one column
+ * that was sampled in each; it takes nothing from a sort.
  *
  * Shared by the three:
  *  - Every pointer of an argument struct is device memory of the current
@@ -362,7 +363,10 @@ rs_status rs_noalloc_timeout_probe(uint64_t timeout_ns, void* stream, rs_status*
  *  - Rows have unit stride inside and *_stride elements from one to the next
  *    (at least the row's length); no alignment beyond the element's own is
  *    needed.  A gradient may be written over the logits (same pointer and
- *    stride); any other overlap of a gradient with the logits is rejected.
+ *    stride); any other overlap of the memory from its first to its last
+ *    element with that of the logits is rejected (also of rows that lie
+ *    between each other's).  No other output may overlap an input or another
+ *    output; that is not checked.
  *  - Statistics, sums and losses are 32-bit floats whatever the scores'
  *    type; a gradient has the scores' type and is rounded to it once.
  *  - Every finite score takes part, however large: a finite mask of -1e30 or

@@ -370,9 +370,9 @@ __device__ __noinline__ void backward_again(const RowLossArgs& a, int64_t row, i
 // as few threads per row as 8 vectors each allow, and registers held to what
 // 24 warps per SM leave (bf16 policy gradients of 8,000 x 7,000 took 50 us; 56
 // with 20 warps, 52 with 32, and 78 by 256 threads per row; 16,384 x 16,000
-// 191 us, 236 with 20 warps).  What bounds it is the chain of a CTA (targets,
-// maximum, sum, gradient) against the few KB it moves: 34 and 157 us are the
-// times of the bytes.
+// 191 us, 236 with 20 warps; one after another they take 45 and 178).  What
+// bounds it is the chain of a CTA (targets, maximum, sum, gradient) against
+// the few KB it moves: 33 and 154 us are the times of the bytes.
 constexpr int kShortWarps = 24;
 template <int TYPE, int OP, int MODE, int kThreads, int VECS>
 __global__ void __launch_bounds__(kThreads, VECS == 16 ? 2 : kShortWarps / (kThreads / kWarp))
@@ -449,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, VECS == 16 ? 2 : kShortWarps / (kThr
 // targets meanwhile.  A row is cut into `split` segments of at least 16 KB
 // until there are two CTAs for every place on the GPU: four times as many
 // CTAs gain nothing (each pays for its targets), sixteen cost 30% and more.
-// What bounds them is HBM (70 us for the bytes of that forward), and the last
+// What bounds them is HBM (69 us for the bytes of that forward), and the last
 // CTAs of a grid, which have the GPU to themselves.
 constexpr int kStreamThreads = 256;
 constexpr int kStreamWarps = kStreamThreads / kWarp;
@@ -659,11 +659,11 @@ __global__ void __launch_bounds__(kStreamThreads + kWarp, kStreamCtas)
 // 8,192 rows of 65,536 instead of 339; per-warp rings of 2 KB copies 437,
 // per-thread cp.async rings 434 (each pair measured in one run).
 //
-// What bounds it is HBM: 335 us for the distillation loss and gradient of
+// What bounds it is HBM: 329 us for the distillation loss and gradient of
 // 4,096 x 131,072 with an eighth of the rows masked (90% of the measured copy
-// bandwidth), 319 us for the policy loss of 8,192 x 65,536 (94%).  Rows of
+// bandwidth), 320 us for the policy loss of 8,192 x 65,536 (93%).  Rows of
 // little more than a chunk or two pay for the exchange between their passes
-// (3,000 x 49,152: 116 us, 76%).
+// (3,000 x 49,152: 107 us, 81%).
 //
 // Rows cost unequally (a masked row is not read), so they are not dealt out
 // beforehand: the grid has a CTA (cluster) per row, and a running one takes
