@@ -543,6 +543,146 @@ rs_status rs_balance_loss(const rs_balance_args* args, void* stream);
 rs_status rs_balance_loss_backward(const rs_balance_args* args, const float* grad_loss,
                                    void* stream);
 
+/* ------------------------------------------------------------------------
+ * The two ends of a vocabulary: rows of logits scored by token, and rows of a
+ * table looked up by token.  What the losses above share (device memory, row
+ * strides, alignment, streams, errors) holds here too.
+ *
+ * Log probabilities.  With m the largest score of a row x, z = x / temperature,
+ * lse = log sum_j exp(z_j) and q_j = exp(z_j - lse):
+ *
+ *   logprobs[r][k] = z_{t_k} - lse   of the row's given tokens t_k (0 for a
+ *                    token outside [0, cols): a padded place)
+ *   entropy[r]     = -sum_j q_j log q_j
+ *   lse[r]
+ *   stats[r]       = m and lse - m / temperature, which the backward call takes
+ *                    (they hold a row of any finite scores; lse may not)
+ *   top_ids[r], top_logprobs[r]   the `top` columns of largest score, the best
+ *                    first, of equal scores (-0 and 0 are equal) the lower
+ *                    column first, and their log probabilities
+ *
+ * What they return serves the losses: logprobs are policy_loss's old and
+ * reference log probabilities, top_logprobs and top_ids a teacher's list for
+ * distillation (taken with temperature 1: a list's softmax does not change
+ * when the row's lse is taken from all of it).
+ *
+ * -inf scores have probability 0 and are no alternatives; where a row has
+ * fewer others than `top`, the places left get id -1 and -inf.  A row of
+ * nothing else has entropy 0, lse -inf, and -inf for every token.  NaN, or
+ * +inf, makes the row's results NaN, its top_ids -1.
+ *   logits      rows x cols scores; 0 <= rows < 2^31, 1 <= cols <= RS_MAX_ROW_KEYS
+ *   tokens      rows x n_tokens columns, int32 or int64 (index_bytes 4 or 8),
+ *               0 <= n_tokens <= RS_MAX_TOP; NULL with n_tokens 0
+ *   top         0 <= top <= RS_MAX_TOP (top may exceed cols)
+ *   temperature >= RS_MIN_TEMPERATURE, finite
+ *   logprobs    rows x n_tokens floats; entropy, lse rows floats; stats rows
+ *               x 2 floats, 8-byte aligned; top_logprobs rows x top floats,
+ *               top_ids rows x top int64 (dense, all of them) */
+typedef struct rs_logprobs_args {
+  const void* logits;
+  int64_t logits_stride, rows, cols;
+  const void* tokens;
+  int64_t tokens_stride;
+  float* logprobs;
+  float* entropy;
+  float* lse;
+  float* stats;
+  float* top_logprobs;
+  int64_t* top_ids;
+  void* grad;
+  int64_t grad_stride;
+  int logits_type, index_bytes, n_tokens, top;
+  float temperature;
+} rs_logprobs_args;
+
+/* The log probabilities, the entropy and the alternatives (args->grad is not
+ * used). */
+rs_status rs_token_logprobs(const rs_logprobs_args* args, void* stream);
+
+/* The gradient of
+ *
+ *   sum_rk grad_logprobs logprobs + sum_r grad_entropy entropy
+ *   + sum_r grad_lse lse + sum_rk grad_top top_logprobs
+ *
+ * in the logits (each upstream gradient dense floats, or NULL: zeros), with
+ * stats, entropy (needed with grad_entropy) and top_ids (needed with
+ * grad_top) as rs_token_logprobs wrote them; a column may be named any number
+ * of times.  logprobs, lse and top_logprobs are not used.  With s the sum of
+ * the row's grad_logprobs and grad_top (of live entries):
+ *
+ *   temperature * d / d x_j = q_j (grad_lse - s - grad_entropy (log q_j + entropy))
+ *                             + the sum of the entries' gradients at column j
+ *
+ * A row of nothing but -inf has gradient 0. */
+rs_status rs_token_logprobs_backward(const rs_logprobs_args* args, const float* grad_logprobs,
+                                     const float* grad_entropy, const float* grad_lse,
+                                     const float* grad_top, void* stream);
+
+/* Rows of a table by token: out[i] = scale * table[ids[i]], zeros for an id
+ * outside [0, vocab).  The product is taken in 32 bits and rounded once.
+ *   table       vocab x width of an rs_score_type; 1 <= vocab < 2^31,
+ *               1 <= width <= RS_MAX_ROW_KEYS
+ *   ids         tokens ids, int32 or int64; 0 <= tokens < 2^31
+ *   out         tokens x width of the same type, apart from the table
+ *   scale       finite */
+typedef struct rs_embedding_args {
+  const void* table;
+  int64_t table_stride, vocab, width;
+  const void* ids;
+  int64_t tokens;
+  void* out;
+  int64_t out_stride;
+  int type, index_bytes;
+  float scale;
+} rs_embedding_args;
+rs_status rs_embedding(const rs_embedding_args* args, void* stream);
+
+/* The gradient of an embedding in its table: with up the upstream gradients
+ *
+ *   row v = scale * sum over i with ids[i] = v of up[i]
+ *
+ * summed in 32 bits in an order that depends on ids alone, so that the results
+ * are the same bits in every run.  Tokens whose id is outside [0, vocab) or
+ * is padding_id take no part.  mode
+ *   RS_EMBED_TABLE  out = the gradient, vocab rows, zeros where no token is
+ *   RS_EMBED_ADD    out += the gradient, vocab rows: those that no token names
+ *                   are neither read nor written
+ *   RS_EMBED_ROWS   out = the rows that some token names, in ascending order
+ *                   of their ids; out has min(tokens, vocab) rows, as many
+ *                   places row_ids (int64); *count (int32) is their number;
+ *                   row_ids past it are -1, rows past it are left as they were
+ *   grad        tokens x width of grad_type
+ *   padding_id  an id, or -1 for none
+ *   out         of out_type: grad_type or RS_SCORE_F32; apart from grad
+ *   temp        scratch of rs_embedding_grad_temp_bytes(), 256-byte aligned
+ *   status      NULL, or one u32 that the caller has cleared: where a wait of
+ *               the sort inside runs out it gets RS_ERR_LOOKBACK_TIMEOUT, and
+ *               out is NaN (RS_EMBED_TABLE), as it was (RS_EMBED_ADD), or has
+ *               no rows (RS_EMBED_ROWS) */
+typedef enum rs_embedding_mode {
+  RS_EMBED_TABLE = 0, RS_EMBED_ADD = 1, RS_EMBED_ROWS = 2
+} rs_embedding_mode;
+typedef struct rs_embedding_grad_args {
+  const void* grad;
+  int64_t grad_stride, tokens, width, vocab;
+  const void* ids;
+  int64_t padding_id;
+  void* out;
+  int64_t out_stride;
+  int64_t* row_ids;
+  int* count;
+  void* temp;
+  size_t temp_bytes;
+  uint32_t* status;
+  int grad_type, out_type, index_bytes, mode;
+  float scale;
+} rs_embedding_grad_args;
+
+/* Scratch size of rs_embedding_grad (host only). */
+rs_status rs_embedding_grad_temp_bytes(int64_t tokens, int64_t vocab, int64_t width,
+                                       size_t* bytes);
+rs_status rs_embedding_grad(const rs_embedding_grad_args* args, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

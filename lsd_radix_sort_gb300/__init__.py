@@ -17,7 +17,9 @@ mode state, so calls on different threads or streams never affect each
 other.
 
 The losses over rows of scores (distillation from a teacher's top logits, the
-clipped policy loss, a router's balance loss) are in ``losses.py``.
+clipped policy loss, a router's balance loss) are in ``losses.py``; the two
+ends of a vocabulary (log probabilities of tokens with entropy and top
+alternatives, embedding lookup and its gradient) in ``vocab.py``.
 """
 from __future__ import annotations
 
@@ -36,7 +38,8 @@ __all__ = [
     "BoundsViolation", "distill_loss", "distill_loss_grad", "distill_loss_backward",
     "policy_loss", "policy_loss_grad", "policy_loss_backward", "balance_loss",
     "balance_loss_grad", "balance_loss_backward", "balance_temp_bytes",
-    "row_wait_timeout_probe",
+    "row_wait_timeout_probe", "TokenLogprobs", "token_logprobs", "token_logprobs_backward",
+    "embedding", "embedding_grad", "embedding_grad_rows", "embedding_grad_temp_bytes",
 ]
 
 RS_OK, RS_ERR_INVALID, RS_ERR_TEMP_TOO_SMALL, RS_ERR_CUDA, RS_ERR_LOOKBACK_TIMEOUT = range(5)
@@ -52,7 +55,8 @@ RS_OPT_PASS_SKIPPING, RS_OPT_TILE_OFFSETS, RS_OPT_NO_SMALL_SORT = 0x1, 0x2, 0x4
 SMALL_SORT_MAX_KEYS = 8192
 KERNEL_NAMES = {0: "upfront_hist", 1: "digit_scan", 2: "onesweep", 3: "copy_probe",
                 4: "timeout_probe", 5: "finish", 6: "tile_counts",
-                7: "small_sort", 8: "row_loss", 9: "balance_loss"}
+                7: "small_sort", 8: "row_loss", 9: "balance_loss", 10: "token_logprobs",
+                11: "embedding"}
 
 EXPORTED_SYMBOLS = (
     "radix_sort_keys_temp_bytes", "radix_sort_keys_u32", "radix_sort_keys_u64",
@@ -66,6 +70,8 @@ EXPORTED_SYMBOLS = (
     "rs_distill_loss", "rs_distill_loss_backward", "rs_policy_loss", "rs_policy_loss_backward",
     "rs_balance_loss", "rs_balance_loss_backward", "rs_balance_temp_bytes",
     "rs_row_wait_timeout_probe",
+    "rs_token_logprobs", "rs_token_logprobs_backward", "rs_embedding", "rs_embedding_grad",
+    "rs_embedding_grad_temp_bytes",
 )
 
 
@@ -151,6 +157,11 @@ def load_library() -> ctypes.CDLL:
             "rs_balance_loss_backward": [P, P, P],
             "rs_balance_temp_bytes": [i64, i, P],
             "rs_row_wait_timeout_probe": [P, u64, P, P],
+            "rs_token_logprobs": [P, P],
+            "rs_token_logprobs_backward": [P, P, P, P, P, P],
+            "rs_embedding": [P, P],
+            "rs_embedding_grad": [P, P],
+            "rs_embedding_grad_temp_bytes": [i64, i64, i64, P],
         }
         for name, args in sig.items():
             f = getattr(lib, name)
@@ -525,3 +536,6 @@ from .losses import (  # noqa: E402  (the losses use the helpers above)
     balance_loss, balance_loss_backward, balance_loss_grad, balance_temp_bytes, distill_loss,
     distill_loss_backward, distill_loss_grad, policy_loss, policy_loss_backward,
     policy_loss_grad, row_wait_timeout_probe)
+from .vocab import (  # noqa: E402
+    TokenLogprobs, embedding, embedding_grad, embedding_grad_rows, embedding_grad_temp_bytes,
+    token_logprobs, token_logprobs_backward)
