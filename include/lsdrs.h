@@ -577,7 +577,9 @@ rs_status rs_balance_loss_backward(const rs_balance_args* args, const float* gra
  *   temperature >= RS_MIN_TEMPERATURE, finite
  *   logprobs    rows x n_tokens floats; entropy, lse rows floats; stats rows
  *               x 2 floats, 8-byte aligned; top_logprobs rows x top floats,
- *               top_ids rows x top int64 (dense, all of them) */
+ *               top_ids rows x top int64 (dense, all of them)
+ *   temp, temp_bytes  scratch of rs_token_logprobs_temp_bytes(), 256-byte
+ *               aligned; the backward call needs none */
 typedef struct rs_logprobs_args {
   const void* logits;
   int64_t logits_stride, rows, cols;
@@ -591,9 +593,15 @@ typedef struct rs_logprobs_args {
   int64_t* top_ids;
   void* grad;
   int64_t grad_stride;
+  void* temp;
+  size_t temp_bytes;
   int logits_type, index_bytes, n_tokens, top;
   float temperature;
 } rs_logprobs_args;
+
+/* Scratch size of rs_token_logprobs on the current device (host only). */
+rs_status rs_token_logprobs_temp_bytes(int64_t rows, int64_t cols, int logits_type, int top,
+                                       size_t* bytes);
 
 /* The log probabilities, the entropy and the alternatives (args->grad is not
  * used). */

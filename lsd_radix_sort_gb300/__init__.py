@@ -38,7 +38,7 @@ __all__ = [
     "BoundsViolation", "distill_loss", "distill_loss_grad", "distill_loss_backward",
     "policy_loss", "policy_loss_grad", "policy_loss_backward", "balance_loss",
     "balance_loss_grad", "balance_loss_backward", "balance_temp_bytes",
-    "row_wait_timeout_probe", "TokenLogprobs", "token_logprobs", "token_logprobs_backward",
+    "row_wait_timeout_probe", "TokenLogprobs", "token_logprobs", "token_logprobs_temp_bytes", "token_logprobs_backward",
     "embedding", "embedding_grad", "embedding_grad_rows", "embedding_grad_temp_bytes",
 ]
 
@@ -70,7 +70,7 @@ EXPORTED_SYMBOLS = (
     "rs_distill_loss", "rs_distill_loss_backward", "rs_policy_loss", "rs_policy_loss_backward",
     "rs_balance_loss", "rs_balance_loss_backward", "rs_balance_temp_bytes",
     "rs_row_wait_timeout_probe",
-    "rs_token_logprobs", "rs_token_logprobs_backward", "rs_embedding", "rs_embedding_grad",
+    "rs_token_logprobs_temp_bytes", "rs_token_logprobs", "rs_token_logprobs_backward", "rs_embedding", "rs_embedding_grad",
     "rs_embedding_grad_temp_bytes",
 )
 
@@ -157,6 +157,7 @@ def load_library() -> ctypes.CDLL:
             "rs_balance_loss_backward": [P, P, P],
             "rs_balance_temp_bytes": [i64, i, P],
             "rs_row_wait_timeout_probe": [P, u64, P, P],
+            "rs_token_logprobs_temp_bytes": [i64, i64, i, i, P],
             "rs_token_logprobs": [P, P],
             "rs_token_logprobs_backward": [P, P, P, P, P, P],
             "rs_embedding": [P, P],
@@ -538,4 +539,4 @@ from .losses import (  # noqa: E402  (the losses use the helpers above)
     policy_loss_grad, row_wait_timeout_probe)
 from .vocab import (  # noqa: E402
     TokenLogprobs, embedding, embedding_grad, embedding_grad_rows, embedding_grad_temp_bytes,
-    token_logprobs, token_logprobs_backward)
+    token_logprobs, token_logprobs_backward, token_logprobs_temp_bytes)

@@ -6,6 +6,8 @@
 // entropy's sum are taken in one pass, both moved along whenever the origin
 // of the exponents moves.
 #pragma once
+#include <algorithm>
+
 #include "row_loss.cuh"
 #include "vocab.h"
 
@@ -43,45 +45,41 @@ __device__ __forceinline__ Stats warp_join(const Stats& v, float scale2) {
 // products of the exponentials and their exponents as well.
 template <int TYPE>
 struct RunningStats {
-  float scale, slack, o, limit, top;
-  Exponent e;
+  float o, limit, top, scale, os2;  // exponents are x * scale - os2: see Exponent
   uint64_t sum[2], dot[2];
 
   __device__ __forceinline__ explicit RunningStats(float scale2)
-      : scale(scale2),
-        slack(8.0f / scale2),
-        o(-INFINITY),
-        limit(-INFINITY),
-        top(-INFINITY),
-        e(0.0f, scale2) {
+      : o(-INFINITY), limit(-INFINITY), top(-INFINITY), scale(scale2), os2(0.0f) {
     sum[0] = sum[1] = dot[0] = dot[1] = 0;
   }
-  // what the exponents lack because e.os2 is rounded, e.mend = 2^lack
+  // what the exponents lack because os2 is rounded
   __device__ __forceinline__ float lack() const {
-    return o == -INFINITY ? 0.0f : __fmaf_rn(-o, e.scale, e.os2);
+    return o == -INFINITY ? 0.0f : __fmaf_rn(-o, scale, os2);
   }
   __device__ __forceinline__ Stats at_origin() const {
     float a, b, c, d;
     unpack2(add2(sum[0], sum[1]), a, b);
     unpack2(add2(dot[0], dot[1]), c, d);
-    return {o, (a + b) * e.mend, (c + d + lack() * (a + b)) * e.mend};
+    const float mend = exp2_approx(lack());
+    return {o, (a + b) * mend, (c + d + lack() * (a + b)) * mend};
   }
-  __device__ __forceinline__ void move(float m) {
-    const Stats s = moved(at_origin(), m, (o - m) * scale);
+  __device__ __forceinline__ void move(float m, float scale2) {
+    const Stats s = moved(at_origin(), m, (o - m) * scale2);
     o = m;
-    limit = m + slack;
-    e = Exponent(m, scale);
+    limit = m + 8.0f / scale2;
+    const Exponent e(m, scale2);
+    scale = e.scale;
+    os2 = e.os2;
     const float a = __fdividef(s.sum, e.mend);
     sum[0] = pack2(a, 0.0f);
     dot[0] = pack2(__fdividef(s.dot, e.mend) - lack() * a, 0.0f);
     sum[1] = dot[1] = 0;
   }
-  // Adds vectors; returns their largest score.
+  // Adds vectors, m being their largest score.
   template <int VECS>
-  __device__ __forceinline__ float add(const uint4 (&v)[VECS]) {
-    const float m = vec_max<TYPE>(v);
+  __device__ __forceinline__ void add(const uint4 (&v)[VECS], float m, float scale2) {
     top = fmaxf(top, m);
-    if (m > limit) move(m);
+    if (m > limit) move(m, scale2);
 #pragma unroll
     for (int u = 0; u < VECS; ++u) {
       uint64_t p[ScoreVec<TYPE>::kCount / 2];
@@ -89,18 +87,17 @@ struct RunningStats {
 #pragma unroll
       for (int i = 0; i < ScoreVec<TYPE>::kCount / 2; ++i) {
         float a, b;
-        unpack2(fma2(p[i], pack2(e.scale, e.scale), pack2(-e.os2, -e.os2)), a, b);
+        unpack2(fma2(p[i], pack2(scale, scale), pack2(-os2, -os2)), a, b);
         const uint64_t y = pack2(above_nothing(a), above_nothing(b));
         const uint64_t x = exp2_2(y);
         sum[i & 1] = add2(sum[i & 1], x);
         dot[i & 1] = fma2(x, y, dot[i & 1]);
       }
     }
-    return m;
   }
-  __device__ __forceinline__ Stats result() const {
+  __device__ __forceinline__ Stats result(float scale2) const {
     const Stats s = at_origin();
-    return top > o ? moved(s, top, (o - top) * scale) : s;
+    return top > o ? moved(s, top, (o - top) * scale2) : s;
   }
 };
 
@@ -125,86 +122,205 @@ __device__ __forceinline__ int entry_col(uint64_t e) {
   return static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(e));
 }
 
-constexpr int kLpThreads = kStreamThreads;
-constexpr int kLpWarps = kLpThreads / kWarp;
-constexpr int kLpCtas = 3;      // per SM
-constexpr int kLpSlots = 32;    // maxima that a thread keeps of its vectors
+// A call is two kernels.  The first reads the scores once, every warp segments
+// of rows of its own, without a pause between two of them, and leaves of each
+// segment its statistics and the largest score of every few vectors of a lane
+// (a group); it needs that maximum for the softmax anyway.  The second joins
+// them, a CTA per row, and finds the top alternatives: from the groups'
+// maxima a bound that `top` of them reach, so that no score below it can be
+// among the `top` best, and few others do (of 64 groups about 24 scores reach
+// 20th largest maximum); only groups that reach it are read again.
+constexpr int kLpBlock = 256;     // threads of the first kernel's CTAs
+constexpr int kLpCtas = 3;        // per SM
+constexpr int kLpStep = kWarp * kStreamBatch;  // vectors of a warp's batch
+constexpr int kLpSplit = 128;     // segments of a row at most
+constexpr int kLpGroups = 4096;   // of a row at most, for lists of up to kLpShort
+constexpr int kLpManyGroups = 8192;  // for longer ones
+constexpr int kLpFewGroups = 1024;   // that one warp holds
+constexpr int kLpShort = 128;     // longest list that is not a long one
 constexpr int kLpRadix = 256;
-constexpr int kLpCounted = 128; // candidates whose ranks are counted, not sorted
-constexpr int64_t kLpLists = 4096;  // entries that a cluster exchanges at most
 
-// Candidates held of a segment.
-__host__ __device__ constexpr inline int candidate_room(int top) { return top <= 128 ? 512 : 2048; }
-
-// Shared memory behind the static part: candidates, the cluster's lists, and
-// every thread's maxima.
-__host__ __device__ constexpr inline size_t logprobs_smem(int top, int split, int slots) {
-  return top == 0 ? 0
-                  : static_cast<size_t>(candidate_room(top)) * 8 +
-                        (split > 1 ? static_cast<size_t>(split) * top * 8 : 0) +
-                        static_cast<size_t>(slots) * kLpThreads * 2;
+// Candidates held of a row, and groups that may hold them.
+__host__ __device__ constexpr inline int candidate_room(int top) {
+  return top <= kLpShort ? 512 : 2048;
+}
+// Shared memory of a selecting CTA: candidates, then groups worth reading again.
+__host__ __device__ constexpr inline size_t select_smem(int top) {
+  return top == 0 ? 0 : static_cast<size_t>(candidate_room(top)) * 12;
 }
 
-struct alignas(16) TopShared {
-  uint32_t tops[kLpThreads];     // largest scores of groups of threads
-  uint32_t hist[kLpRadix];
-  uint32_t least;                // no candidate is below this
-  int count;                     // candidates
-  uint64_t prefix;               // exact selection: entries from here on are kept,
-  int above, reach;              // so many are above its digits, at or above them
+// A warp's batch is 2 KB in one piece.  A lane reads every other vector of half
+// a 128-byte line, so that its four vectors lie in one line (they are read
+// again together) and a load of the warp still takes whole sectors.
+__host__ __device__ constexpr inline int lane_vector(int lane) { return lane / 2 * 8 + lane % 2; }
+constexpr int kLaneStride = 2;
+
+// How a call's rows are divided: into `split` segments of `per` vectors; a group
+// is a lane's vectors of 2^shift batches, or (single) one vector; a segment has
+// `slots` of them (a multiple of 8).
+struct LpPlan {
+  int split, per, shift, slots;
+  bool single;
+  uint32_t magic;  // 2^32 / slots, rounded up
+  __host__ __device__ int groups() const { return split * slots; }
+  __device__ __forceinline__ int segment_of(int group) const {
+    return static_cast<int>(__umulhi(static_cast<uint32_t>(group), magic));
+  }
+  // a group's vectors, and the first of them, in its segment
+  __device__ __forceinline__ int log_members() const { return single ? 0 : 2 + shift; }
+  __device__ __forceinline__ int64_t member(int group, int i) const {
+    if (single) return group;
+    return ((static_cast<int64_t>(group / kWarp) << shift) + i / kStreamBatch) * kLpStep +
+           lane_vector(group % kWarp) + i % kStreamBatch * kLaneStride;
+  }
+  // the group of a segment's vector
+  __device__ __forceinline__ int group_of(int vec) const {
+    if (single) return vec;
+    return (vec / kLpStep >> shift) * kWarp + vec % kLpStep / 8 * 2 + vec % 2;
+  }
 };
 
-// A CTA's segment of a row as its threads have read it: every thread's
-// vectors begin + tid + i * kLpThreads in batches, 2^shift batches to a slot
-// of which it has kept the largest score (as the upper half of its order).
+// Scratch: every segment's statistics, then the groups' maxima (the upper
+// halves of their orders; 0 for those that a segment does not reach).
+__host__ __device__ inline size_t stats_bytes(int64_t rows, const LpPlan& p) {
+  return align_up(static_cast<size_t>(rows) * p.split * sizeof(float4), 256);
+}
+__device__ __forceinline__ uint16_t* row_groups(const LogprobArgs& a, const LpPlan& p,
+                                                int64_t row) {
+  return reinterpret_cast<uint16_t*>(static_cast<char*>(a.temp) + stats_bytes(a.rows, p)) +
+         row * p.groups();
+}
+
+// Segment `rank` of a row: vectors [begin, end).
 template <int TYPE>
 struct Segment {
   using Raw = typename Score<TYPE>::Raw;
   const Raw* x;
-  const RowVecs<TYPE>& vecs;
-  int begin, end, shift, slots;
-  const uint16_t* kept;
+  RowVecs<TYPE> vecs;
+  int begin, end;
 
-  // f(order, column) for this thread's scores of slots that reach `least`
-  template <class F>
-  __device__ __forceinline__ void each(uint32_t least, F&& f) const {
-    constexpr int kN = ScoreVec<TYPE>::kCount;
-    const int tid = static_cast<int>(threadIdx.x);
-    const uint4* xv = reinterpret_cast<const uint4*>(x - vecs.lead);
-    uint32_t hit = 0;
-    for (int s = 0; s < slots; ++s)
-      hit |= static_cast<uint32_t>(kept[s * kLpThreads + tid] >= least >> 16) << s;
-    while (hit != 0) {
-      const int s = __ffs(static_cast<int>(hit)) - 1;
-      hit &= hit - 1;
-      const int64_t first = begin + tid + (static_cast<int64_t>(s) << shift) * Stream<TYPE>::kStep;
-      const int64_t last =
-          min(static_cast<int64_t>(end),
-              first + (static_cast<int64_t>(Stream<TYPE>::kStep) << shift));
-      for (int64_t v0 = first; v0 < last; v0 += Stream<TYPE>::kStep) {
-        uint4 r[kStreamBatch];
+  __device__ __forceinline__ Segment(const LogprobArgs& a, int64_t row, int rank, int per)
+      : x(static_cast<const Raw*>(a.logits) + row * a.stride),
+        vecs(x, static_cast<int>(a.cols)) {
+    begin = min(rank * per, vecs.count);
+    end = min(begin + per, vecs.count);
+  }
+  __device__ __forceinline__ const uint4* vec0() const {
+    return reinterpret_cast<const uint4*>(x - vecs.lead);
+  }
+};
+
+// What the reading warp needs of a segment from batch to batch; the rest is
+// worked out again at a row's ragged ends.
+template <int TYPE>
+struct Reader {
+  const uint4* vec0;
+  int begin, end, inner_begin, inner_end;  // inner: whole vectors
+  uint32_t item;
+
+  __device__ __forceinline__ Reader(const LogprobArgs& a, uint32_t item_, const LpPlan& p)
+      : item(item_) {
+    const Segment<TYPE> seg = segment(a, p);
+    vec0 = seg.vec0();
+    begin = seg.begin;
+    end = seg.end;
+    inner_begin = seg.vecs.whole_begin();
+    inner_end = min(end, seg.vecs.whole_end());
+  }
+  __device__ __forceinline__ Segment<TYPE> segment(const LogprobArgs& a, const LpPlan& p) const {
+    const uint32_t row = item / static_cast<uint32_t>(p.split);
+    return Segment<TYPE>(a, row, static_cast<int>(item - row * p.split), p.per);
+  }
+  __device__ __forceinline__ int batches() const {
+    return max(1, (end - begin + kLpStep - 1) / kLpStep);
+  }
+  // a lane's batch: vectors v0 + u * kLaneStride, -inf past the end
+  __device__ __forceinline__ void load(const LogprobArgs& a, const LpPlan& p, int v0,
+                                       uint4 (&to)[kStreamBatch]) const {
+    constexpr uint32_t kNone = ScoreVec<TYPE>::kMinusInf;
+    if (v0 >= inner_begin && v0 + (kStreamBatch - 1) * kLaneStride < inner_end) {
 #pragma unroll
-        for (int u = 0; u < kStreamBatch; ++u) {
-          const int64_t v = v0 + u * kLpThreads;
-          constexpr uint32_t kNone = ScoreVec<TYPE>::kMinusInf;
-          r[u] = v < last ? vecs.load(xv, x, static_cast<int>(v))
-                          : make_uint4(kNone, kNone, kNone, kNone);
-        }
+      for (int u = 0; u < kStreamBatch; ++u) to[u] = __ldcs(vec0 + v0 + u * kLaneStride);
+    } else {
+      const Segment<TYPE> seg = segment(a, p);
 #pragma unroll
-        for (int u = 0; u < kStreamBatch; ++u) {
-          const uint32_t w[4] = {r[u].x, r[u].y, r[u].z, r[u].w};
-          const int col = static_cast<int>((v0 + u * kLpThreads) * kN - vecs.lead);
-#pragma unroll
-          for (int i = 0; i < kN; ++i) {
-            const Raw raw = static_cast<Raw>(kN == 4 ? w[i & 3] : w[i >> 1] >> (16 * (i & 1)));
-            const uint32_t o = order_of(Score<TYPE>::load(raw));
-            if (o >= least) f(o, col + i);
-          }
-        }
+      for (int u = 0; u < kStreamBatch; ++u) {
+        const int v = v0 + u * kLaneStride;
+        to[u] = v < end ? seg.vecs.load(vec0, seg.x, v) : make_uint4(kNone, kNone, kNone, kNone);
       }
     }
   }
 };
+
+__device__ __forceinline__ uint32_t upper_order(float x) { return order_of(x) >> 16; }
+
+template <int TYPE>
+__device__ __forceinline__ float max_of(const uint4& v) {
+  const uint4 one[1] = {v};
+  return vec_max<TYPE>(one);
+}
+
+// GROUPS: 0 none are kept, 1 of one vector, 4 of a lane's batches.
+template <int TYPE, int GROUPS>
+__global__ void __launch_bounds__(kLpBlock, kLpCtas)
+    logprobs_read_kernel(const __grid_constant__ LogprobArgs a,
+                         const __grid_constant__ LpPlan p, const uint32_t items) {
+  grid_dependency_sync();
+  const uint32_t step = gridDim.x * (kLpBlock / kWarp);
+  const uint32_t first = blockIdx.x * (kLpBlock / kWarp) + threadIdx.x / kWarp;
+  if (first >= items) return;
+  const int lane = static_cast<int>(lane_id()), own = lane_vector(lane);
+  auto groups_of = [&](uint32_t item) {  // of a segment
+    const uint32_t row = item / static_cast<uint32_t>(p.split);
+    return row_groups(a, p, row) + static_cast<int>(item - row * p.split) * p.slots;
+  };
+  Reader<TYPE> in(a, first, p);
+  uint4 r[kStreamBatch], ahead[kStreamBatch];
+  in.load(a, p, in.begin + own, r);
+  for (uint32_t item = first; item < items; item += step) {
+    RunningStats<TYPE> run(a.scale2);
+    uint16_t* kept = nullptr;  // this lane's next group
+    if (GROUPS != 0) kept = groups_of(item) + (GROUPS == 1 ? own : lane);
+    const int batches = in.batches();
+    int v = in.begin + own;
+    float m = -INFINITY;
+    for (int b = 1; b <= batches; ++b) {
+      v += kLpStep;
+      if (b < batches) {
+        in.load(a, p, v, ahead);
+      } else if (item + step < items) {  // the next segment's first
+        in = Reader<TYPE>(a, item + step, p);
+        in.load(a, p, in.begin + own, ahead);
+      }
+      const float top = vec_max<TYPE>(r);
+      if (GROUPS == 1) {
+#pragma unroll
+        for (int u = 0; u < kStreamBatch; ++u)
+          kept[u * kLaneStride] = static_cast<uint16_t>(upper_order(max_of<TYPE>(r[u])));
+        kept += kLpStep;
+      } else if (GROUPS != 0) {
+        m = fmaxf(m, top);
+        if ((b & ((1 << p.shift) - 1)) == 0 || b == batches) {
+          *kept = static_cast<uint16_t>(upper_order(m));
+          kept += kWarp;
+          m = -INFINITY;
+        }
+      }
+      run.add(r, top, a.scale2);
+#pragma unroll
+      for (int u = 0; u < kStreamBatch; ++u) r[u] = ahead[u];
+    }
+    if (GROUPS != 0) {  // groups that the segment does not reach
+      uint16_t* all = groups_of(item);
+      const int done =
+          GROUPS == 1 ? batches * kLpStep : (((batches - 1) >> p.shift) + 1) * kWarp;
+      for (int i = done + lane; i < p.slots; i += kWarp) all[i] = 0;
+    }
+    const Stats st = warp_join(run.result(a.scale2), a.scale2);
+    if (lane == 0)
+      static_cast<float4*>(a.temp)[item] = make_float4(st.m, st.sum, st.dot, 0.0f);
+  }
+}
 
 // Adds to a histogram; lanes with the same digit at once.
 __device__ __forceinline__ void count_digit(uint32_t* hist, uint32_t digit) {
@@ -214,80 +330,336 @@ __device__ __forceinline__ void count_digit(uint32_t* hist, uint32_t digit) {
     atomicAdd(&hist[digit], static_cast<uint32_t>(__popc(same)));
 }
 
+// From the counts of 256 digits: the largest one that `above` plus the counts
+// from it on reach `want`, or 0.  `above` becomes the number of those beyond
+// it, `reach` that with its own.
+__device__ __forceinline__ int pick_digit(const uint32_t* hist, int want, int& above, int& reach) {
+  const int lane = static_cast<int>(lane_id());
+  // lane 31 has the largest eight digits
+  int n[8], mine = 0;
+#pragma unroll
+  for (int i = 7; i >= 0; --i) {
+    mine += static_cast<int>(hist[lane * 8 + i]);
+    n[i] = mine;  // of this lane's digits, from i on
+  }
+  int beyond = mine;
+#pragma unroll
+  for (int o = 1; o < kWarp; o *= 2) {
+    const int v = __shfl_down_sync(kFull, beyond, o);
+    if (lane + o < kWarp) beyond += v;
+  }
+  beyond += above - mine;  // above, and of the lanes behind
+  const unsigned ok = __ballot_sync(kFull, beyond + mine >= want);
+  const int from = ok != 0 ? 31 - __clz(static_cast<int>(ok)) : 0;
+  int digit = 0, upto = beyond + mine;
+#pragma unroll
+  for (int i = 7; i > 0; --i) {
+    if (beyond + n[i] >= want) {
+      digit = i;
+      upto = beyond + n[i];
+      break;
+    }
+  }
+  const int over = upto - static_cast<int>(hist[lane * 8 + digit]);
+  above = __shfl_sync(kFull, over, from);
+  reach = __shfl_sync(kFull, upto, from);
+  return __shfl_sync(kFull, lane * 8 + digit, from);
+}
+
+// The `top`-th largest of N values of 16 bits per lane, or 0 if that many are
+// not above it: bit by bit from the first that they differ in.
+template <int N>
+__device__ __forceinline__ uint32_t largest_of(const uint32_t (&v)[N], int top) {
+  uint32_t all = v[0], any = v[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) {
+    all &= v[i];
+    any |= v[i];
+  }
+  all = __reduce_and_sync(kFull, all);
+  any = __reduce_or_sync(kFull, any);
+  const int bits = 32 - __clz(static_cast<int>(all ^ any));
+  uint32_t best = all >> bits << bits;  // (shared by all of them)
+#pragma unroll 1
+  for (uint32_t bit = 1u << bits >> 1; bit != 0; bit >>= 1) {
+    const uint32_t t = best | bit;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) n += __popc(__ballot_sync(kFull, v[i] >= t));
+    if (n >= top) best = t;
+  }
+  return best;
+}
+
+// ------------------------------------------------------------- a row, by a CTA
+struct RowSelected {
+  int hits, count;
+  uint32_t words[4][4][kWarp];   // maxima by word, warp, lane
+  uint32_t hist[kLpRadix];
+  uint64_t prefix;
+  int above, reach;
+};
+
+template <int WARPS>
+__device__ __forceinline__ void row_sync() {
+  if (WARPS == 1)
+    __syncwarp();
+  else
+    __syncthreads();
+}
+
+template <int TYPE, int WARPS>
+struct Selection {
+  static constexpr int kThreads = WARPS * kWarp;
+  const LogprobArgs& a;
+  const LpPlan& p;
+  int64_t row;
+  const uint16_t* kept;
+  int room;
+  uint64_t* cand;
+  uint32_t* work;         // groups
+  RowSelected* sh;
+
+  // A bound (the upper half of an order) that `top` scores reach, or 0: the
+  // `top`-th largest of 64 * WORDS maxima, of this thread's in g.
+  template <int WORDS>
+  __device__ __forceinline__ uint32_t bound_of(const uint32_t (&g)[4]) const {
+    const int lane = static_cast<int>(lane_id()), warp = static_cast<int>(threadIdx.x) / kWarp;
+    uint32_t w[WORDS], v[2 * WORDS];
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) w[i] = g[i];
+#pragma unroll
+    for (int i = WORDS; i < 4; ++i) w[i % WORDS] = __vmaxu2(w[i % WORDS], g[i]);
+    if constexpr (WARPS > 1) {
+#pragma unroll
+      for (int i = 0; i < WORDS; ++i) sh->words[i][warp][lane] = w[i];
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < WORDS; ++i)
+#pragma unroll
+        for (int j = 0; j < WARPS; ++j) w[i] = __vmaxu2(w[i], sh->words[i][j][lane]);
+    }
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) {
+      v[2 * i] = w[i] & 0xFFFFu;
+      v[2 * i + 1] = w[i] >> 16;
+    }
+    return largest_of(v, a.top);
+  }
+
+  // One digit of a selection by counts: sh->prefix, above, reach.
+  __device__ __forceinline__ void pick(uint64_t prefix, int shift, int above) const {
+    row_sync<WARPS>();
+    if (threadIdx.x < kWarp) {
+      int reach;
+      const int d = pick_digit(sh->hist, a.top, above, reach);
+      if (threadIdx.x == 0) {
+        sh->prefix = prefix | static_cast<uint64_t>(d) << shift;
+        sh->above = above;
+        sh->reach = reach;
+      }
+    }
+    row_sync<WARPS>();
+  }
+  __device__ __forceinline__ void clear_counts() const {
+    for (int i = static_cast<int>(threadIdx.x); i < kLpRadix; i += kThreads) sh->hist[i] = 0;
+    row_sync<WARPS>();
+  }
+
+  // For long lists every group counts: the digits of their maxima.
+  __device__ __forceinline__ uint32_t bound_of_all() const {
+    uint64_t prefix = 0;
+    int above = 0;
+    const int groups = p.groups();
+    for (int shift = 8; shift >= 0; shift -= 8) {
+      clear_counts();
+#pragma unroll 4
+      for (int i = static_cast<int>(threadIdx.x); i < groups; i += kThreads) {
+        const uint32_t k = kept[i];
+        if (shift == 8 || k >> 8 == prefix >> 8) count_digit(sh->hist, k >> shift & 0xFFu);
+      }
+      pick(prefix, shift, above);
+      prefix = sh->prefix;
+      above = sh->above;
+    }
+    return sh->reach < a.top ? 0 : static_cast<uint32_t>(prefix);
+  }
+
+  __device__ __forceinline__ void hit(int group) const {
+    const int at = atomicAdd(&sh->hits, 1);
+    if (at < room) work[at] = static_cast<uint32_t>(group);
+  }
+  // Lists those of 8 groups that reach the bound.
+  __device__ __forceinline__ void hits_of(int group, const uint4& w, uint32_t least) const {
+    const uint32_t below = (least - 1) * 0x10001u;  // (least is not 0)
+    if (__vmaxu2(__vmaxu2(__vmaxu2(w.x, w.y), __vmaxu2(w.z, w.w)), below) == below) return;
+    const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+    uint32_t reach = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t over = __vmaxu2(words[j], below) ^ below;
+      reach |= (over & 0xFFFFu ? 1u << 2 * j : 0u) | (over >> 16 ? 2u << 2 * j : 0u);
+    }
+    for (; reach != 0; reach &= reach - 1) hit(group + __ffs(static_cast<int>(reach)) - 1);
+  }
+
+  __device__ __forceinline__ void add(uint64_t e) const {
+    const int at = atomicAdd(&sh->count, 1);
+    if (at < room) cand[at] = e;
+  }
+
+  // Candidates: the scores of the listed groups that reach the bound.
+  __device__ __forceinline__ void collect(int hits, uint32_t least) const {
+    const int log = p.log_members();
+    static_assert(kStreamBatch == 4);
+    const float from = score_of(least << 16);
+    constexpr int kN = ScoreVec<TYPE>::kCount, kAhead = 2;
+    const int64_t units = static_cast<int64_t>(hits) << log;
+    const Segment<TYPE> whole(a, row, 0, 0);
+    for (int64_t u0 = threadIdx.x; u0 < units; u0 += kAhead * kThreads) {
+      uint4 r[kAhead];
+      int col[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int64_t u = u0 + i * kThreads;
+        constexpr uint32_t kNone = ScoreVec<TYPE>::kMinusInf;
+        r[i] = make_uint4(kNone, kNone, kNone, kNone);
+        col[i] = 0;
+        if (u >= units) continue;
+        const int g = static_cast<int>(work[u >> log]), rank = p.segment_of(g);
+        const int begin = rank * p.per;
+        const int64_t v = begin + p.member(g - rank * p.slots,
+                                           static_cast<int>(u) & ((1 << log) - 1));
+        if (v >= min(begin + p.per, whole.vecs.count)) continue;
+        r[i] = whole.vecs.load(whole.vec0(), whole.x, static_cast<int>(v));
+        col[i] = static_cast<int>(v) * kN - whole.vecs.lead;
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
+#pragma unroll
+        for (int j = 0; j < kN; ++j) {
+          using Raw = typename Score<TYPE>::Raw;
+          const float x = Score<TYPE>::load(
+              static_cast<Raw>(kN == 4 ? w[j & 3] : w[j >> 1] >> (16 * (j & 1))));
+          if (x >= from) add(entry_of(order_of(x), col[i] + j));
+        }
+      }
+    }
+  }
+
+  // f(order, column) for every score of the row that reaches the bound
+  template <class F>
+  __device__ __forceinline__ void each(uint32_t least, F&& f) const {
+    constexpr int kN = ScoreVec<TYPE>::kCount, kAhead = 4;
+    for (int rank = 0; rank < p.split; ++rank) {
+      const Segment<TYPE> seg(a, row, rank, p.per);
+      for (int64_t v0 = seg.begin + static_cast<int>(threadIdx.x); v0 < seg.end;
+           v0 += kAhead * kThreads) {
+        uint4 r[kAhead];
+        bool on[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          const int64_t v = v0 + u * kThreads;
+          const int off = static_cast<int>(min(v, static_cast<int64_t>(seg.end) - 1) - seg.begin);
+          on[u] = v < seg.end && kept[rank * p.slots + p.group_of(off)] >= least;
+          if (on[u]) r[u] = seg.vecs.load(seg.vec0(), seg.x, static_cast<int>(v));
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          if (!on[u]) continue;
+          const uint32_t w[4] = {r[u].x, r[u].y, r[u].z, r[u].w};
+          const int col = static_cast<int>(v0 + u * kThreads) * kN - seg.vecs.lead;
+#pragma unroll
+          for (int i = 0; i < kN; ++i) {
+            using Raw = typename Score<TYPE>::Raw;
+            const uint32_t o = order_of(Score<TYPE>::load(
+                static_cast<Raw>(kN == 4 ? w[i & 3] : w[i >> 1] >> (16 * (i & 1)))));
+            if (o >> 16 >= least) f(o, col + i);
+          }
+        }
+      }
+    }
+  }
+};
+
 // More candidates than there is room for (many equal scores, or a long list):
 // entries are narrowed down digit by digit, 8 bits from the top, by counting
 // those that share the digits so far, until what is at and above them fits.
 // Entries differ, so they do at last.
-template <int TYPE>
-__device__ __noinline__ void select_exactly(const Segment<TYPE>& seg, int top, int room,
-                                            TopShared* sh, uint64_t* cand) {
-  const int tid = static_cast<int>(threadIdx.x);
-  const uint32_t least = sh->least;
-  uint64_t prefix = 0;  // entries at or above it are kept, those of its digits divided further
+template <int TYPE, int WARPS>
+__device__ __noinline__ void select_exactly(const Selection<TYPE, WARPS>& sel, uint32_t least) {
+  uint64_t prefix = 0;  // entries from it on are kept, those of its digits divided further
   int shift = 64, above = 0;
   do {
     shift -= 8;
-    for (int i = tid; i < kLpRadix; i += kLpThreads) sh->hist[i] = 0;
-    __syncthreads();
-    seg.each(least, [&](uint32_t o, int col) {
+    sel.clear_counts();
+    sel.each(least, [&](uint32_t o, int col) {
       const uint64_t e = entry_of(o, col);
       if (shift == 56 || (e ^ prefix) >> (shift + 8) == 0)
-        count_digit(sh->hist, static_cast<uint32_t>(e >> shift) & 0xFFu);
+        count_digit(sel.sh->hist, static_cast<uint32_t>(e >> shift) & 0xFFu);
     });
-    __syncthreads();
-    if (tid == 0) {
-      int n = above, d = kLpRadix - 1;
-      while (d > 0 && n + static_cast<int>(sh->hist[d]) < top) n += static_cast<int>(sh->hist[d--]);
-      sh->prefix = prefix | static_cast<uint64_t>(d) << shift;
-      sh->above = n;
-      sh->reach = n + static_cast<int>(sh->hist[d]);
-    }
-    __syncthreads();
-    prefix = sh->prefix;
-    above = sh->above;
-  } while (sh->reach > room && shift > 0);
-  if (tid == 0) sh->count = 0;
-  __syncthreads();
-  seg.each(least, [&](uint32_t o, int col) {
+    sel.pick(prefix, shift, above);
+    prefix = sel.sh->prefix;
+    above = sel.sh->above;
+  } while (sel.sh->reach > sel.room && shift > 0);
+  if (threadIdx.x == 0) sel.sh->count = 0;
+  row_sync<WARPS>();
+  sel.each(least, [&](uint32_t o, int col) {
     const uint64_t e = entry_of(o, col);
-    if (e >= prefix) {
-      const int at = atomicAdd(&sh->count, 1);
-      if (at < room) cand[at] = e;
-    }
+    if (e >= prefix) sel.add(e);
   });
-  __syncthreads();
+  row_sync<WARPS>();
 }
 
-// Sorts n entries, the largest first; room for the next power of two.
-static __device__ __noinline__ void sort_entries(uint64_t* e, int n) {
+// Puts n entries in order: place(position, entry), the largest first.  There
+// is room for the next power of two.
+template <int WARPS, class F>
+__device__ __forceinline__ void in_order(uint64_t* e, int n, F&& place) {
+  constexpr int kThreads = WARPS * kWarp;
   const int tid = static_cast<int>(threadIdx.x);
-  int size = 2;
+  if (n <= kThreads) {  // positions are counted
+    if (tid < n) {
+      const uint64_t own = e[tid];
+      int better = 0;
+#pragma unroll 4
+      for (int i = 0; i < n; ++i) better += e[i] > own;
+      place(better, own);
+    }
+    return;
+  }
+  if (n <= 4 * kThreads) {
+    uint64_t own[4];
+    int better[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int u = 0; u < 4; ++u) own[u] = u * kThreads + tid < n ? e[u * kThreads + tid] : 0;
+    for (int i = 0; i < n; ++i) {
+      const uint64_t x = e[i];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) better[u] += x > own[u];
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (own[u] != 0) place(better[u], own[u]);
+    return;
+  }
+  int size = 4 * kThreads;
   while (size < n) size *= 2;
-  for (int i = n + tid; i < size; i += kLpThreads) e[i] = 0;
-  __syncthreads();
+  for (int i = n + tid; i < size; i += kThreads) e[i] = 0;
+  row_sync<WARPS>();
   for (int run = 2; run <= size; run *= 2)
     for (int step = run / 2; step > 0; step /= 2) {
-      for (int p = tid; p < size / 2; p += kLpThreads) {
-        const int i = (p & ~(step - 1)) * 2 + (p & (step - 1)), j = i + step;
-        const uint64_t a = e[i], b = e[j];
-        if ((a < b) == ((i & run) == 0)) {
-          e[i] = b;
-          e[j] = a;
+      for (int q = tid; q < size / 2; q += kThreads) {
+        const int i = (q & ~(step - 1)) * 2 + (q & (step - 1)), j = i + step;
+        const uint64_t x = e[i], y = e[j];
+        if ((x < y) == ((i & run) == 0)) {
+          e[i] = y;
+          e[j] = x;
         }
       }
-      __syncthreads();
+      row_sync<WARPS>();
     }
-}
-
-__device__ __forceinline__ void store_peer(uint64_t* at, uint32_t rank, uint64_t v) {
-  asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(peer_addr(smem_addr(at), rank)), "l"(v)
-               : "memory");
-}
-__device__ __forceinline__ void store_peer(Stats* at, uint32_t rank, const Stats& v) {
-  const uint32_t to = peer_addr(smem_addr(at), rank);
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(v.m) : "memory");
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 4), "f"(v.sum) : "memory");
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 8), "f"(v.dot) : "memory");
+  for (int i = tid; i < n; i += kThreads) place(i, e[i]);
 }
 
 // What the outputs of a row are computed from.
@@ -308,190 +680,131 @@ struct RowStats {
 
 __device__ __forceinline__ void store_top(const LogprobArgs& a, int64_t row, int at, uint64_t e,
                                           const RowStats& s) {
+  if (at >= a.top) return;
   a.top_logprobs[row * a.top + at] =
       s.nan ? NAN : s.logprob(score_of(entry_order(e)), a.tau);
   a.top_ids[row * a.top + at] = s.nan ? -1 : entry_col(e);
 }
 
-// One CTA, or a cluster of `split`, per row.  Its scores pass through once
-// (batches of 4 vectors per thread, the next one under way); the top
-// alternatives cost that pass nothing but a maximum per batch, which it needs
-// anyway: a slot per thread and some batches keeps it.  Afterwards the
-// largest scores of 64 to 256 groups of threads give a bound: `top` of them
-// reach it, so no score below it can be among the `top` best, and few others
-// reach it (of 64 groups about 24 scores for the best 20).  Only the batches
-// whose maximum reaches the bound are read again, from L2.
+// A thread's first token of a row, asked for before it is needed.
 template <int TYPE>
-__global__ void __launch_bounds__(kLpThreads, kLpCtas)
-    logprobs_kernel(const __grid_constant__ LogprobArgs a, const int split, const int slots,
-                    const int shift) {
-  using S = Score<TYPE>;
-  using Raw = typename S::Raw;
-  extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ Stats part[kLpWarps], peer[kMaxCluster];
-  __shared__ TopShared sh;
-  __shared__ int lengths[kMaxCluster];
-  const int top = a.top, room = candidate_room(top);
-  uint64_t* cand = reinterpret_cast<uint64_t*>(smem);
-  uint64_t* lists = cand + room;  // the cluster's, `top` entries each
-  uint16_t* kept = reinterpret_cast<uint16_t*>(lists + (split > 1 ? split * top : 0));
-  const int tid = static_cast<int>(threadIdx.x), warp = tid / kWarp;
-  const int lane = static_cast<int>(lane_id());
-  grid_dependency_sync();
-  if (split > 1) cluster_begun();
-  const int64_t row = blockIdx.x / split;
-  const int rank = static_cast<int>(blockIdx.x % split);
-  const Raw* x = static_cast<const Raw*>(a.logits) + row * a.stride;
-  const RowVecs<TYPE> vecs(x, static_cast<int>(a.cols));
-  const int per = (vecs.count + split - 1) / split;
-  const int begin = min(rank * per, vecs.count), end = min(begin + per, vecs.count);
-  const float scale2 = a.scale2;
+struct Token {
+  float x;
+  bool live;
 
-  // the first tokens' scores, under way with the row's
-  float x0 = 0.0f;
-  bool live0 = false;
-  if (rank == 0 && tid < a.k) {
-    const int64_t i = load_index(a.tokens, a.index_bytes, row * a.token_stride + tid);
-    live0 = i >= 0 && i < a.cols;
-    if (live0) x0 = S::load(x[i]);
+  __device__ __forceinline__ Token(const LogprobArgs& a, int64_t row, int k) : x(0.0f), live(false) {
+    if (k >= a.k) return;
+    const int64_t i = load_index(a.tokens, a.index_bytes, row * a.token_stride + k);
+    live = i >= 0 && i < a.cols;
+    if (live)
+      x = Score<TYPE>::load(
+          static_cast<const typename Score<TYPE>::Raw*>(a.logits)[row * a.stride + i]);
   }
-  RunningStats<TYPE> run(scale2);
-  Stream<TYPE> stream(x, vecs, begin, end, tid);
-  if (top == 0) {
-    stream.run([&](int, const uint4(&r)[kStreamBatch]) { run.add(r); });
-  } else {
-    for (int s = 0; s < slots; ++s) kept[s * kLpThreads + tid] = 0;
-    int batch = 0;
-    float m = -INFINITY;
-    stream.run([&](int, const uint4(&r)[kStreamBatch]) {
-      m = fmaxf(m, run.add(r));
-      if ((++batch & ((1 << shift) - 1)) == 0) {
-        kept[((batch - 1) >> shift) * kLpThreads + tid] =
-            static_cast<uint16_t>(order_of(m) >> 16);
-        m = -INFINITY;
-      }
-    });
-    if ((batch & ((1 << shift) - 1)) != 0)
-      kept[(batch >> shift) * kLpThreads + tid] = static_cast<uint16_t>(order_of(m) >> 16);
-  }
-  Stats s = warp_join(run.result(), scale2);
-  if (lane == 0) part[warp] = s;
+};
 
-  if (top > 0) {
-    // the bound: of 64, 128 or 256 groups the `top`-th largest maximum; in
-    // each group's order the last 8 bits make room for its number
-    const int fold = top <= 32 ? 4 : top <= 64 ? 2 : 1, groups = kLpThreads / fold;
-    float g = run.top;
-    if (fold > 1) g = fmaxf(g, __shfl_xor_sync(kFull, g, 1));
-    if (fold > 2) g = fmaxf(g, __shfl_xor_sync(kFull, g, 2));
-    if (tid % fold == 0) sh.tops[tid / fold] = (order_of(g) & ~0xFFu) | (tid / fold);
-    if (tid == 0) {
-      sh.count = 0;
-      sh.least = kOrderLeast;  // stays where the groups are too few, or -inf
-    }
-    __syncthreads();
-    if (top <= groups / 2 && tid < groups) {
-      const uint32_t own = sh.tops[tid];
-      int better = 0;
-      for (int i = 0; i < groups; i += 4) {
-        const uint4 t = *reinterpret_cast<const uint4*>(&sh.tops[i]);
-        better += (t.x > own) + (t.y > own) + (t.z > own) + (t.w > own);
-      }
-      if (better == top - 1) sh.least = max(own & ~0xFFu, kOrderLeast);
-    }
+// All of a row but its `found` alternatives.
+template <int TYPE>
+__device__ __forceinline__ void store_row(const LogprobArgs& a, int64_t row, const RowStats& s,
+                                          const Token<TYPE>& first, int found) {
+  const int tid = static_cast<int>(threadIdx.x), threads = static_cast<int>(blockDim.x);
+  for (int i = found + tid; i < a.top; i += threads) {  // fewer scores than asked for
+    a.top_logprobs[row * a.top + i] = s.nan ? NAN : -INFINITY;
+    a.top_ids[row * a.top + i] = -1;
   }
-  __syncthreads();
-  s = warp_join(lane < kLpWarps ? part[lane] : Stats{-INFINITY, 0.0f, 0.0f}, scale2);
-
-  int found = 0;
-  if (top > 0) {
-    const Segment<TYPE> seg{x, vecs, begin, end, shift, slots, kept};
-    seg.each(sh.least, [&](uint32_t o, int col) {
-      const int at = atomicAdd(&sh.count, 1);
-      if (at < room) cand[at] = entry_of(o, col);
-    });
-    __syncthreads();
-    if (sh.count > room) select_exactly<TYPE>(seg, top, room, &sh, cand);
-    found = min(sh.count, room);
-  }
-  if (split > 1) {
-    cluster_wait();  // all CTAs of the cluster have begun
-    if (tid < split) {
-      store_peer(&peer[rank], tid, s);
-      store_peer(&lengths[rank], tid, min(found, top));
-    }
-  }
-  const RowStats alone(s);
-  // of the segment's candidates the best go to the row's list, or every CTA's
-  auto place = [&](int at, uint64_t e) {
-    if (at >= top) return;
-    if (split == 1)
-      store_top(a, row, at, e, alone);
-    else
-      for (int r = 0; r < split; ++r) store_peer(&lists[rank * top + at], r, e);
-  };
-  if (found <= kLpCounted) {
-    if (tid < found) {
-      const uint64_t e = cand[tid];
-      int better = 0;
-      for (int i = 0; i < found; ++i) better += cand[i] > e;
-      place(better, e);
-    }
-  } else {
-    sort_entries(cand, found);
-    for (int i = tid; i < found; i += kLpThreads) place(i, cand[i]);
-  }
-  int total = found;
-  if (split > 1) {
-    cluster_sync();
-    s = warp_join(lane < split ? peer[lane] : Stats{-INFINITY, 0.0f, 0.0f}, scale2);
-    total = 0;
-    for (int r = 0; r < split; ++r) total += lengths[r];
-  }
-  const RowStats st(s);
-  if (split > 1 && top > 0) {
-    // an entry's place: those above it in each CTA's list, which is in order
-    const int mine = min(found, top);
-    for (int first = 0; first < mine; first += kLpThreads) {
-      const int n = min(mine - first, kLpThreads);
-      if (tid < n) sh.hist[tid] = 0;
-      __syncthreads();
-      for (int p = tid; p < n * split; p += kLpThreads) {
-        const int i = p / split, r = p % split;
-        const uint64_t e = lists[rank * top + first + i];
-        const uint64_t* list = lists + r * top;
-        int lo = 0, hi = lengths[r];
-        while (lo < hi) {
-          const int mid = (lo + hi) / 2;
-          if (list[mid] > e)
-            lo = mid + 1;
-          else
-            hi = mid;
-        }
-        if (lo > 0) atomicAdd(&sh.hist[i], static_cast<uint32_t>(lo));
-      }
-      __syncthreads();
-      if (tid < n && sh.hist[tid] < static_cast<uint32_t>(top))
-        store_top(a, row, static_cast<int>(sh.hist[tid]), lists[rank * top + first + tid], st);
-      __syncthreads();
-    }
-  }
-  if (rank != 0) return;
-  for (int i = total + tid; i < top; i += kLpThreads) {  // fewer scores than asked for
-    a.top_logprobs[row * top + i] = st.nan ? NAN : -INFINITY;
-    a.top_ids[row * top + i] = -1;
-  }
-  if (tid < a.k) a.logprobs[row * a.k + tid] = live0 ? st.logprob(x0, a.tau) : 0.0f;
-  for (int i = tid + kLpThreads; i < a.k; i += kLpThreads) {
-    const int64_t c = load_index(a.tokens, a.index_bytes, row * a.token_stride + i);
-    a.logprobs[row * a.k + i] =
-        c >= 0 && c < a.cols ? st.logprob(S::load(x[c]), a.tau) : 0.0f;
+  for (int i = tid; i < a.k; i += threads) {
+    const Token<TYPE> t = i == tid ? first : Token<TYPE>(a, row, i);
+    a.logprobs[row * a.k + i] = t.live ? s.logprob(t.x, a.tau) : 0.0f;
   }
   if (tid == 0) {
-    a.entropy[row] = st.entropy;
-    a.lse[row] = st.nan ? NAN : st.empty ? -INFINITY : st.m / a.tau + st.log_sum;
-    a.stats[row] = make_float2(st.nan ? NAN : st.m, st.log_sum);
+    a.entropy[row] = s.entropy;
+    a.lse[row] = s.nan ? NAN : s.empty ? -INFINITY : s.m / a.tau + s.log_sum;
+    a.stats[row] = make_float2(s.nan ? NAN : s.m, s.log_sum);
   }
+}
+
+// The second kernel.  Short lists: a thread's groups stay in its registers.
+template <int TYPE, int WARPS>
+__global__ void __launch_bounds__(WARPS* kWarp)
+    logprobs_rows_kernel(const __grid_constant__ LogprobArgs a, const __grid_constant__ LpPlan p) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ RowSelected sh;
+  constexpr int kThreads = WARPS * kWarp;
+  constexpr int kVecs = (WARPS == 1 ? kLpFewGroups : kLpGroups) / 8 / kThreads;
+  const int tid = static_cast<int>(threadIdx.x), lane = static_cast<int>(lane_id());
+  const int64_t row = blockIdx.x;
+  if (tid == 0) sh.hits = sh.count = 0;
+  grid_dependency_sync();
+  const int top = a.top, room = candidate_room(top), groups = p.groups();
+  const bool short_list = top > 0 && top <= kLpShort;
+  const uint16_t* kept = row_groups(a, p, row);
+  uint4 v[kVecs];
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const int g = (i * kThreads + tid) * 8;
+    v[i] = short_list && g < groups ? *reinterpret_cast<const uint4*>(kept + g)
+                                    : make_uint4(0, 0, 0, 0);
+  }
+  const float4* part = static_cast<const float4*>(a.temp) + row * p.split;
+  float4 parts[kLpSplit / kWarp];
+#pragma unroll
+  for (int i = 0; i < kLpSplit / kWarp; ++i)
+    parts[i] = i * kWarp + lane < p.split ? part[i * kWarp + lane]
+                                          : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+  const Token<TYPE> token(a, row, tid);
+
+  const Selection<TYPE, WARPS> sel{
+      a, p, row, kept, room, reinterpret_cast<uint64_t*>(smem),
+      reinterpret_cast<uint32_t*>(smem + static_cast<size_t>(room) * 8), &sh};
+  uint32_t least = 0;
+  if (short_list) {
+    uint32_t g[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      g[0] = __vmaxu2(g[0], v[i].x);
+      g[1] = __vmaxu2(g[1], v[i].y);
+      g[2] = __vmaxu2(g[2], v[i].z);
+      g[3] = __vmaxu2(g[3], v[i].w);
+    }
+    least = top <= 32   ? sel.template bound_of<1>(g)
+            : top <= 64 ? sel.template bound_of<2>(g)
+                        : sel.template bound_of<4>(g);
+    least = max(least, kOrderLeast >> 16);
+    if (WARPS == 1) __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) sel.hits_of((i * kThreads + tid) * 8, v[i], least);
+  } else if (top > 0) {
+    least = max(sel.bound_of_all(), kOrderLeast >> 16);
+    for (int g = tid; g < groups; g += kThreads)
+      if (kept[g] >= least) sel.hit(g);
+  }
+  if (top > 0) {
+    row_sync<WARPS>();
+    if (sh.hits <= room) sel.collect(sh.hits, least);
+  }
+  int found = 0;
+  if (top > 0) {
+    row_sync<WARPS>();
+    const bool fits = sh.hits <= room && sh.count <= room;
+    row_sync<WARPS>();
+    if (!fits) select_exactly(sel, least);
+    found = sh.count;
+    // warps without a result to write
+    if (found <= kThreads && tid - lane >= max(found, max(top - found, a.k))) return;
+  }
+  Stats st{-INFINITY, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < kLpSplit / kWarp; ++i) {  // of a lane
+    if (i * kWarp >= p.split) break;
+    const float m = fmaxf(st.m, parts[i].x), o = origin(m);
+    const Stats x = moved(st, m, (st.m - o) * a.scale2);
+    const Stats y = moved(Stats{parts[i].x, parts[i].y, parts[i].z}, m,
+                          (parts[i].x - o) * a.scale2);
+    st = Stats{m, x.sum + y.sum, x.dot + y.dot};
+  }
+  const RowStats s(warp_join(st, a.scale2));
+  if (top > 0)
+    in_order<WARPS>(sel.cand, found, [&](int i, uint64_t e) { store_top(a, row, i, e, s); });
+  store_row<TYPE>(a, row, s, token, found);
 }
 
 // -------------------------------------------------------------------- backward
@@ -502,6 +815,8 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas)
 // that is 2^y_j (c0 + c1 y_j) with y_j the exponent from the row's maximum, in
 // units of log 2: two multiply-adds and one exponential per score.  The
 // entries' columns are written last.
+constexpr int kLpThreads = kStreamThreads;
+constexpr int kLpWarps = kLpThreads / kWarp;
 struct Pull {
   float c0, c1;
 };
@@ -635,55 +950,73 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas)
 }
 
 // ---------------------------------------------------------------------- launch
-constexpr int kLpMaxSmem = 65536;  // candidates, lists and maxima at their most
-static_assert(logprobs_smem(1024, static_cast<int>(kLpLists) / 1024, kLpSlots) <= kLpMaxSmem);
-
-// Opts a kernel into its dynamic shared memory and clusters of 16, once per
-// device.
-template <class K>
-cudaError_t allow_smem(K kern, int bytes, std::atomic<uint64_t>* done) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = uint64_t(1) << (dev & 63);
-  if (dev < 64 && (done->load(std::memory_order_acquire) & bit)) return cudaSuccess;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_release);
-  return e;
+// The time of `split` segments to a row is that of as many rounds of all warps
+// as they take, each at its share of the measured bandwidth, batch by batch,
+// and what a segment's end costs.
+template <int TYPE>
+LpPlan logprobs_plan(int64_t rows, int64_t cols, int top) {
+  constexpr int kN = ScoreVec<TYPE>::kCount;
+  const int64_t warps = int64_t(device_sm_count()) * kLpCtas * (kLpBlock / kWarp);
+  const int64_t vecs = (cols + 2 * (kN - 1)) / kN;  // however the rows begin
+  LpPlan p{1, 0, 0, kWarp, false, 0};
+  const double ns_per_batch = 16.0 * kLpStep * static_cast<double>(warps) / 6791.0;
+  double best = 1e300;
+  for (int split = 1; split <= kLpSplit; ++split) {
+    const int64_t per = (vecs + split - 1) / split;
+    if (split > 1 && per < kLpStep / 2) break;
+    const int64_t rounds = (rows * split + warps - 1) / warps;
+    const double ns =
+        rounds * (static_cast<double>((per + kLpStep - 1) / kLpStep) * ns_per_batch + 500.0);
+    if (ns < best) {
+      best = ns;
+      p.split = split;
+    }
+  }
+  while (p.split > 1 && rows * p.split >= (int64_t(1) << 31)) --p.split;
+  p.per = static_cast<int>((vecs + p.split - 1) / p.split);
+  const int64_t batches = (p.per + kLpStep - 1) / kLpStep;
+  if (top > 0) {
+    // single vectors where there are few: the best of short rows are then
+    // bounded by several times `top` maxima
+    p.single = p.split * batches * kLpStep <= (top <= kLpShort ? kLpFewGroups : kLpManyGroups);
+    const int64_t most = top <= kLpShort ? kLpGroups : kLpManyGroups;
+    auto slots = [&] {
+      return p.single ? batches * kLpStep : (((batches - 1) >> p.shift) + 1) * kWarp;
+    };
+    while (p.split * slots() > most) ++p.shift;
+    p.slots = static_cast<int>(slots());
+  }
+  p.magic = static_cast<uint32_t>(((uint64_t(1) << 32) + p.slots - 1) / p.slots);
+  return p;
 }
 
 template <int TYPE>
-cudaError_t launch_logprobs_as(const LogprobArgs& a, cudaStream_t s) {
-  constexpr int kEs = sizeof(typename Score<TYPE>::Raw);
-  const int64_t bytes = a.cols * kEs;
-  const int sms = device_sm_count();
-  int split = 1;
-  while (split < kMaxCluster && a.rows * split < int64_t(sms) * kLpCtas * kStreamWaves &&
-         bytes >= split * 2 * kStreamLeast && int64_t(split) * 2 * a.top <= kLpLists)
-    split *= 2;
-  while (a.rows * split >= (int64_t(1) << 31)) split /= 2;  // CTA numbers are 31 bits
-  // batches of a segment, 2^shift of them to a slot
-  const int64_t vecs = (a.cols + 2 * (ScoreVec<TYPE>::kCount - 1)) / ScoreVec<TYPE>::kCount;
-  const int64_t batches =
-      ((vecs + split - 1) / split + Stream<TYPE>::kStep - 1) / Stream<TYPE>::kStep;
-  int shift = 0;
-  while (((batches - 1) >> shift) >= kLpSlots) ++shift;
-  const int slots = static_cast<int>((batches - 1) >> shift) + 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.rows * split));
-  cfg.blockDim = dim3(kLpThreads);
-  cfg.dynamicSmemBytes = logprobs_smem(a.top, split, slots);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  cfg.attrs = attr;
-  cfg.numAttrs = add_attributes(attr, split);
-  auto kern = logprobs_kernel<TYPE>;
-  static std::atomic<uint64_t> done{0};
-  const cudaError_t e = allow_smem(kern, kLpMaxSmem, &done);
+size_t logprobs_temp(int64_t rows, int64_t cols, int top) {
+  const LpPlan p = logprobs_plan<TYPE>(rows, cols, top);
+  return stats_bytes(rows, p) + (top == 0 ? 0 : static_cast<size_t>(rows) * p.groups() * 2);
+}
+
+template <int TYPE>
+cudaError_t launch_logprobs_as(const LogprobArgs& a, int* launched, cudaStream_t s) {
+  const LpPlan p = logprobs_plan<TYPE>(a.rows, a.cols, a.top);
+  constexpr int kEach = kLpBlock / kWarp;
+  const uint32_t items = static_cast<uint32_t>(a.rows * p.split);
+  const uint32_t ctas = std::min<uint32_t>((items + kEach - 1) / kEach,
+                                           static_cast<uint32_t>(device_sm_count() * kLpCtas));
+  auto read = a.top == 0     ? logprobs_read_kernel<TYPE, 0>
+              : p.single     ? logprobs_read_kernel<TYPE, 1>
+                             : logprobs_read_kernel<TYPE, 4>;
+  const cudaError_t e = launch_kernel(read, dim3(ctas), dim3(kLpBlock), 0, s, a, p, items);
   if (e != cudaSuccess) return e;
-  return cudaLaunchKernelEx(&cfg, kern, a, split, slots, shift);
+  *launched = 2;
+  static_assert(select_smem(1024) + sizeof(RowSelected) <= 48 * 1024);
+  const bool one_warp =
+      a.top == 0 || (a.top <= kLpShort && p.groups() <= kLpFewGroups && a.rows >= 1024);
+  const dim3 rows(static_cast<unsigned>(a.rows));
+  return one_warp ? launch_kernel(logprobs_rows_kernel<TYPE, 1>, rows, dim3(kWarp),
+                                  select_smem(a.top), s, a, p)
+                  : launch_kernel(logprobs_rows_kernel<TYPE, 4>, rows, dim3(4 * kWarp),
+                                  select_smem(a.top), s, a, p);
 }
 
 template <int TYPE>

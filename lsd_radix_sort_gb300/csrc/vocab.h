@@ -22,6 +22,7 @@ struct LogprobArgs {
   float2* stats;                   // a row's largest score and log-sum; likewise
   float* top_logprobs;
   int64_t* top_ids;                // likewise
+  void* temp;                      // of the forward call
   // the backward call; each upstream gradient may be null
   const float* grad_logprobs;
   const float* grad_entropy;
@@ -62,7 +63,9 @@ struct EmbedGradArgs {
 };
 
 // type: an rs_score_type
-cudaError_t launch_logprobs(int type, const LogprobArgs& a, cudaStream_t s);
+// Scratch of a forward call.
+size_t logprobs_temp_bytes(int type, int64_t rows, int64_t cols, int top);
+cudaError_t launch_logprobs(int type, const LogprobArgs& a, int* launched, cudaStream_t s);
 cudaError_t launch_logprobs_backward(int type, const LogprobArgs& a, cudaStream_t s);
 cudaError_t launch_embed(int type, const EmbedArgs& a, cudaStream_t s);
 // The gradient's steps: the tokens' sort keys, their sort, the runs of equal

@@ -91,15 +91,28 @@ rs_status embed_grad_check(const rs_embedding_grad_args* p) {
 
 extern "C" {
 
+rs_status rs_token_logprobs_temp_bytes(int64_t rows, int64_t cols, int logits_type, int top,
+                                       size_t* bytes) {
+  if (!bytes || rows < 0 || rows > kMaxRows || cols < 1 || cols > RS_MAX_ROW_KEYS ||
+      !known_type(logits_type) || top < 0 || top > RS_MAX_TOP)
+    return RS_ERR_INVALID;
+  *bytes = rows == 0 ? 0 : logprobs_temp_bytes(logits_type, rows, cols, top);
+  return RS_OK;
+}
+
 rs_status rs_token_logprobs(const rs_logprobs_args* p, void* stream) {
   const rs_status st = logprobs_check(p);
   if (st != RS_OK || p->rows == 0) return st;
   if (!given(p->entropy, 4) || !given(p->lse, 4)) return RS_ERR_INVALID;
   if (p->n_tokens > 0 && !given(p->logprobs, 4)) return RS_ERR_INVALID;
   if (p->top > 0 && (!given(p->top_logprobs, 4) || !given(p->top_ids, 8))) return RS_ERR_INVALID;
-  const LogprobArgs a = logprob_args(p);
+  const size_t need = logprobs_temp_bytes(p->logits_type, p->rows, p->cols, p->top);
+  if (!given(p->temp, 256)) return RS_ERR_INVALID;
+  if (p->temp_bytes < need) return RS_ERR_TEMP_TOO_SMALL;
+  LogprobArgs a = logprob_args(p);
+  a.temp = p->temp;
   return enqueue(kNameLogprobs, static_cast<uint64_t>(p->rows) * p->cols, stream,
-                 [&](int*, cudaStream_t s) { return launch_logprobs(p->logits_type, a, s); });
+                 [&](int* n, cudaStream_t s) { return launch_logprobs(p->logits_type, a, n, s); });
 }
 
 rs_status rs_token_logprobs_backward(const rs_logprobs_args* p, const float* grad_logprobs,

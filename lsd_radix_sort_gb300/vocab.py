@@ -28,7 +28,7 @@ from . import losses as _l
 from .losses import (_F, _I, _I64, _P, _SZ, MAX_TOP, _device, _grad_stride, _index_bytes, _kind,
                      _matrix, _on, _ptr, _vector, _wants_grad)
 
-__all__ = ["TokenLogprobs", "token_logprobs", "token_logprobs_backward", "embedding",
+__all__ = ["TokenLogprobs", "token_logprobs", "token_logprobs_temp_bytes", "token_logprobs_backward", "embedding",
            "embedding_grad", "embedding_grad_rows", "embedding_grad_temp_bytes"]
 
 EMBED_TABLE, EMBED_ADD, EMBED_ROWS = range(3)
@@ -39,8 +39,8 @@ class LogprobsArgs(ctypes.Structure):
     _fields_ = [("logits", _P), ("logits_stride", _I64), ("rows", _I64), ("cols", _I64),
                 ("tokens", _P), ("tokens_stride", _I64), ("logprobs", _P), ("entropy", _P),
                 ("lse", _P), ("stats", _P), ("top_logprobs", _P), ("top_ids", _P), ("grad", _P),
-                ("grad_stride", _I64), ("logits_type", _I), ("index_bytes", _I),
-                ("n_tokens", _I), ("top", _I), ("temperature", _F)]
+                ("grad_stride", _I64), ("temp", _P), ("temp_bytes", _SZ), ("logits_type", _I),
+                ("index_bytes", _I), ("n_tokens", _I), ("top", _I), ("temperature", _F)]
 
 
 class EmbeddingArgs(ctypes.Structure):
@@ -93,14 +93,25 @@ def _dense(t, shape, what, dtype=None):
                          f"{t.dtype} of {tuple(t.shape)}")
 
 
-def _logprobs(logits, tokens, top, temperature, stream):
+@functools.lru_cache(maxsize=256)
+def token_logprobs_temp_bytes(rows: int, cols: int, logits_type: int, top: int = 0) -> int:
+    """Scratch size of ``token_logprobs`` on the current device, for logits of
+    an rs_score_type (0 float16, 1 bfloat16, 2 float32)."""
+    n = ctypes.c_size_t(0)
+    _check(_lib_of().rs_token_logprobs_temp_bytes(rows, cols, logits_type, top, ctypes.byref(n)),
+           "rs_token_logprobs_temp_bytes")
+    return n.value
+
+
+def _logprobs(logits, tokens, top, temperature, temp, stream):
     torch = _l._torch or _l._load()
     kind = _kind(logits, "logits")
     rows, cols, stride = _matrix(logits, "logits")
     k, token_stride, ib = _tokens_of(tokens, rows)
     if not 0 <= top <= MAX_TOP:
         raise ValueError(f"0 to {MAX_TOP} top alternatives per row, got {top}")
-    index = _device(stream, logits, tokens)
+    index = _device(stream, logits, tokens, temp)
+    need = token_logprobs_temp_bytes(rows, cols, kind, top)
     with _on(stream):
         device, f32 = logits.device, torch.float32
         logprobs = None if tokens is None else torch.empty(tokens.shape, dtype=f32, device=device)
@@ -111,15 +122,20 @@ def _logprobs(logits, tokens, top, temperature, stream):
         if top:
             top_logprobs = torch.empty((rows, top), dtype=f32, device=device)
             top_ids = torch.empty((rows, top), dtype=torch.int64, device=device)
+        if temp is None:
+            temp = torch.empty((need,), dtype=torch.uint8, device=device)
     args = LogprobsArgs(logits.data_ptr(), stride, rows, cols, _ptr(tokens), token_stride,
                         _ptr(logprobs), entropy.data_ptr(), lse.data_ptr(), stats.data_ptr(),
-                        _ptr(top_logprobs), _ptr(top_ids), None, 0, kind, ib, k, top, temperature)
+                        _ptr(top_logprobs), _ptr(top_ids), None, 0,
+                        temp.data_ptr(), temp.numel() * temp.element_size(), kind, ib, k, top,
+                        temperature)
     s = _l._raw_stream(index) if stream is None else stream.cuda_stream
     _check(_lib_of().rs_token_logprobs(ctypes.byref(args), s), "rs_token_logprobs")
     return TokenLogprobs(logprobs, entropy, lse, top_logprobs, top_ids, stats)
 
 
-def token_logprobs(logits, tokens=None, top: int = 0, temperature: float = 1.0, stream=None):
+def token_logprobs(logits, tokens=None, top: int = 0, temperature: float = 1.0, temp=None,
+                   stream=None):
     """TokenLogprobs(logprobs, entropy, lse, top_logprobs, top_ids, stats) of rows of logits.
 
     ``logits`` is (rows, cols) float16/bfloat16/float32; ``tokens`` (int32/
@@ -129,10 +145,10 @@ def token_logprobs(logits, tokens=None, top: int = 0, temperature: float = 1.0, 
     many alternatives: the columns of largest score, the best first, of equal
     ones the lower.  All but ``top_ids`` and ``stats`` are differentiable in
     ``logits``."""
-    if _wants_grad(logits, stream):
+    if _wants_grad(logits, stream, temp):
         return TokenLogprobs(*_autograd().Logprobs.apply(logits, tokens, int(top),
                                                          float(temperature)))
-    return _logprobs(logits, tokens, top, temperature, stream)
+    return _logprobs(logits, tokens, top, temperature, temp, stream)
 
 
 def token_logprobs_backward(logits, stats, entropy=None, tokens=None, top_ids=None,
@@ -176,8 +192,8 @@ def token_logprobs_backward(logits, stats, entropy=None, tokens=None, top_ids=No
             grad = torch.empty((rows, cols), dtype=logits.dtype, device=logits.device)
     args = LogprobsArgs(logits.data_ptr(), stride, rows, cols, _ptr(tokens), token_stride, None,
                         _ptr(entropy), None, stats.data_ptr(), None,
-                        _ptr(top_ids) if top else None, grad.data_ptr(), grad_stride, kind, ib, k,
-                        top, temperature)
+                        _ptr(top_ids) if top else None, grad.data_ptr(), grad_stride, None, 0,
+                        kind, ib, k, top, temperature)
     s = _l._raw_stream(index) if stream is None else stream.cuda_stream
     _check(_lib_of().rs_token_logprobs_backward(
         ctypes.byref(args), _ptr(grad_logprobs) if k else None, _ptr(grad_entropy),
@@ -352,7 +368,7 @@ def _autograd():
     class Logprobs(torch.autograd.Function):
         @staticmethod
         def forward(ctx, logits, tokens, top, temperature):
-            got = _logprobs(logits, tokens, top, temperature, None)
+            got = _logprobs(logits, tokens, top, temperature, None, None)
             ctx.save_for_backward(logits, got.stats, got.entropy, tokens, got.top_ids)
             ctx.temperature = temperature
             ctx.set_materialize_grads(False)

@@ -131,7 +131,8 @@ def logprobs_args(**change):
     a = dict(logits=BASE, logits_stride=100, rows=4, cols=100, tokens=BASE + 0x100000,
              tokens_stride=2, logprobs=BASE + 0x200000, entropy=BASE + 0x210000,
              lse=BASE + 0x220000, stats=BASE + 0x230000, top_logprobs=BASE + 0x240000,
-             top_ids=BASE + 0x250000, grad=BASE + 0x400000, grad_stride=100, logits_type=1,
+             top_ids=BASE + 0x250000, grad=BASE + 0x400000, grad_stride=100, temp=BASE + 0x500000,
+             temp_bytes=1 << 30, logits_type=1,
              index_bytes=8, n_tokens=2, top=3, temperature=1.0)
     return vocab.LogprobsArgs(**{**a, **change})
 
@@ -147,7 +148,8 @@ SHARED = [dict(logits_type=3), dict(logits_type=-1), dict(rows=-1), dict(rows=1 
 
 @pytest.mark.parametrize("change", SHARED + [
     dict(logprobs=None), dict(logprobs=BASE + 2), dict(entropy=None), dict(lse=None),
-    dict(top_logprobs=None), dict(top_ids=None), dict(top_ids=BASE + 0x250004)])
+    dict(top_logprobs=None), dict(top_ids=None), dict(top_ids=BASE + 0x250004), dict(temp=None),
+    dict(temp=BASE + 0x500010)])
 def test_logprobs_refuses(lib, change):
     assert lib.rs_token_logprobs(ctypes.byref(logprobs_args(**change)), None) == rs.RS_ERR_INVALID
 
@@ -216,6 +218,10 @@ def test_no_work_and_no_arguments(lib):
 
 def test_scratch_size(lib):
     out = ctypes.c_size_t(0)
+    for bad in ((-1, 8, 1, 0), (1 << 31, 8, 1, 0), (10, 0, 1, 0), (10, 1 << 30, 1, 0), (10, 8, 3, 0),
+                (10, 8, 1, -1), (10, 8, 1, 1025)):
+        assert lib.rs_token_logprobs_temp_bytes(*bad, ctypes.byref(out)) == 1
+    assert lib.rs_token_logprobs_temp_bytes(10, 8, 1, 0, None) == 1
     for bad in ((-1, 8, 8), (1 << 31, 8, 8), (10, 0, 8), (10, 1 << 31, 8), (10, 8, 0)):
         assert lib.rs_embedding_grad_temp_bytes(*bad, ctypes.byref(out)) == 1
     assert lib.rs_embedding_grad_temp_bytes(10, 8, 8, None) == 1
