@@ -629,10 +629,11 @@ rs_status rs_token_logprobs_backward(const rs_logprobs_args* args, const float* 
 /* Rows of a table by token: out[i] = scale * table[ids[i]], zeros for an id
  * outside [0, vocab).  The product is taken in 32 bits and rounded once.
  *   table       vocab x width of an rs_score_type; 1 <= vocab < 2^31,
- *               1 <= width <= RS_MAX_ROW_KEYS
+ *               1 <= width <= RS_MAX_WIDTH
  *   ids         tokens ids, int32 or int64; 0 <= tokens < 2^31
  *   out         tokens x width of the same type, apart from the table
  *   scale       finite */
+#define RS_MAX_WIDTH (1 << 24)
 typedef struct rs_embedding_args {
   const void* table;
   int64_t table_stride, vocab, width;

@@ -3,21 +3,277 @@
 #include "embed.cuh"
 
 #include <algorithm>
+#include <atomic>
 
 #include "kernels.h"
 
 namespace lsdrs {
 namespace {
 
+// ---- the list of up to kClusterTokens tokens, by one cluster
+// 16 CTAs hold the tokens' (key, place) in shared memory and sort them there,
+// digit by digit from the least: a warp ranks its 32 * ITEMS neighbouring words
+// by ballots, the CTAs tell each other their digits' counts, and every word is
+// written to its place in the CTA that this lies in.  (The sort of whole keys
+// takes 7 launches, 31 us for 16,384 tokens.)  Two passes of 9 bits for a
+// vocabulary of 131,072.
+constexpr int kClusterCtas = 16;
+constexpr int kClusterThreads = 1024;
+constexpr int kClusterWarps = kClusterThreads / kWarp;
+constexpr int kMaxRadix = 512;
+constexpr int kClusterItems = 8;
+constexpr int64_t kClusterTokens = int64_t(kClusterCtas) * kClusterThreads * kClusterItems;
+
+struct ClusterShared {
+  uint16_t warp_count[kClusterWarps][kMaxRadix];  // then: of the warps before
+  uint32_t count[kClusterCtas][kMaxRadix];        // of each CTA
+  uint32_t base[kMaxRadix];                       // where this CTA's words of a digit go
+  uint32_t part[kWarp];
+  // of each CTA: runs that begin there, its live tokens, and the list's place
+  // of its first and last run (none: all ones, 0)
+  uint4 ends[kClusterCtas];
+};
+
+__device__ __forceinline__ uint32_t cluster_peer(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+
+// Sums of v over the threads before this one; all: over all of them.
+__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* part, uint32_t* all) {
+  const uint32_t lane = lane_id(), warp = threadIdx.x / kWarp;
+  uint32_t upto = v;
+#pragma unroll
+  for (int o = 1; o < kWarp; o *= 2) {
+    const uint32_t n = __shfl_up_sync(kFull, upto, o);
+    if (lane >= static_cast<uint32_t>(o)) upto += n;
+  }
+  __syncthreads();  // (what was there before has been read)
+  if (lane == kWarp - 1) part[warp] = upto;
+  __syncthreads();
+  const uint32_t n = part[lane];
+  *all = __reduce_add_sync(kFull, n);
+  return __reduce_add_sync(kFull, lane < warp ? n : 0) + upto - v;
+}
+__device__ __forceinline__ uint32_t block_max_before(uint32_t v, uint32_t* part, uint32_t* all) {
+  const uint32_t lane = lane_id(), warp = threadIdx.x / kWarp;
+  uint32_t upto = v;
+#pragma unroll
+  for (int o = 1; o < kWarp; o *= 2) {
+    const uint32_t n = __shfl_up_sync(kFull, upto, o);
+    if (lane >= static_cast<uint32_t>(o)) upto = max(upto, n);
+  }
+  uint32_t before = __shfl_up_sync(kFull, upto, 1);
+  if (lane == 0) before = 0;
+  __syncthreads();
+  if (lane == kWarp - 1) part[warp] = upto;
+  __syncthreads();
+  const uint32_t n = part[lane];
+  *all = __reduce_max_sync(kFull, n);
+  return max(before, __reduce_max_sync(kFull, lane < warp ? n : 0));
+}
+__device__ __forceinline__ uint32_t block_min_after(uint32_t v, uint32_t* part, uint32_t* all) {
+  const uint32_t lane = lane_id(), warp = threadIdx.x / kWarp;
+  uint32_t from = v;
+#pragma unroll
+  for (int o = 1; o < kWarp; o *= 2) {
+    const uint32_t n = __shfl_down_sync(kFull, from, o);
+    if (lane + o < kWarp) from = min(from, n);
+  }
+  uint32_t after = __shfl_down_sync(kFull, from, 1);
+  if (lane == kWarp - 1) after = 0xFFFFFFFFu;
+  __syncthreads();
+  if (lane == 0) part[warp] = from;
+  __syncthreads();
+  const uint32_t n = part[lane];
+  *all = __reduce_min_sync(kFull, n);
+  return min(after, __reduce_min_sync(kFull, lane > warp ? n : 0xFFFFFFFFu));
+}
+
+template <int ITEMS>
+__global__ void __launch_bounds__(kClusterThreads, 1)
+    embed_list_kernel(const __grid_constant__ EmbedGradArgs a, const __grid_constant__ GradPlan p,
+                      const int passes, const int bits) {
+  constexpr uint32_t kSlice = kClusterThreads * ITEMS;  // words of a CTA
+  extern __shared__ __align__(16) unsigned char smem[];
+  uint64_t* word = reinterpret_cast<uint64_t*>(smem);
+  ClusterShared& sh = *reinterpret_cast<ClusterShared*>(smem + kSlice * 8);
+  const uint32_t tid = threadIdx.x, warp = tid / kWarp, lane = lane_id();
+  const uint32_t rank = blockIdx.x;
+  const uint32_t tokens = static_cast<uint32_t>(a.tokens), vocab = static_cast<uint32_t>(a.vocab);
+  const uint32_t radix = 1u << bits;
+  grid_dependency_sync();
+  uint64_t w[ITEMS];
+  const uint32_t first = warp * kWarp * ITEMS + lane;  // this thread's words: every 32nd
+#pragma unroll
+  for (int u = 0; u < ITEMS; ++u) {
+    const uint32_t i = rank * kSlice + first + u * kWarp;
+    // behind the last token: past every key
+    w[u] = i < tokens ? static_cast<uint64_t>(key_of(a, i)) << 32 | i : ~uint64_t(0);
+  }
+  {
+    const int64_t words = static_cast<int64_t>(p.chunks) * p.blocks;
+    for (int64_t i = rank * kClusterThreads + tid; i < words; i += kClusterCtas * kClusterThreads)
+      p.arrived[i] = 0;
+  }
+  for (int pass = 0; pass < passes; ++pass) {
+    const int shift = 32 + pass * bits;
+    for (uint32_t i = lane; i < radix; i += kWarp) sh.warp_count[warp][i] = 0;
+    __syncwarp();
+    uint16_t place[ITEMS];  // among the warp's words of the digit
+#pragma unroll
+    for (int u = 0; u < ITEMS; ++u) {
+      const uint32_t d = static_cast<uint32_t>(w[u] >> shift) & (radix - 1);
+      unsigned same = kFull;
+      for (int b = 0; b < bits; ++b) {
+        const unsigned set = __ballot_sync(kFull, d >> b & 1);
+        same &= (d >> b & 1) != 0 ? set : ~set;
+      }
+      const uint16_t was = sh.warp_count[warp][d];
+      __syncwarp();
+      place[u] = static_cast<uint16_t>(was + __popc(same & lanemask_lt()));
+      if ((same & lanemask_lt()) == 0)
+        sh.warp_count[warp][d] = static_cast<uint16_t>(was + __popc(same));
+      __syncwarp();
+    }
+    __syncthreads();
+    uint32_t total = 0;
+    if (tid < radix) {
+#pragma unroll 8
+      for (int i = 0; i < kClusterWarps; ++i) {
+        const uint32_t n = sh.warp_count[i][tid];
+        sh.warp_count[i][tid] = static_cast<uint16_t>(total);
+        total += n;
+      }
+    }
+    if (pass == 0) cluster_barrier();  // all CTAs have begun
+    if (tid < radix)
+      for (uint32_t r = 0; r < kClusterCtas; ++r)
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(
+                         cluster_peer(smem_addr(&sh.count[rank][tid]), r)),
+                     "r"(total)
+                     : "memory");
+    cluster_barrier();
+    uint32_t digit = 0, before = 0;
+    if (tid < radix)
+      for (uint32_t r = 0; r < kClusterCtas; ++r) {
+        const uint32_t n = sh.count[r][tid];
+        digit += n;
+        if (r < rank) before += n;
+      }
+    uint32_t all;
+    const uint32_t smaller = block_scan(digit, sh.part, &all);
+    if (tid < radix) sh.base[tid] = smaller + before;
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < ITEMS; ++u) {
+      const uint32_t d = static_cast<uint32_t>(w[u] >> shift) & (radix - 1);
+      const uint32_t to = sh.base[d] + sh.warp_count[warp][d] + place[u];
+      asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(
+                       cluster_peer(smem_addr(&word[to % kSlice]), to / kSlice)),
+                   "l"(w[u])
+                   : "memory");
+    }
+    cluster_barrier();
+    if (pass + 1 < passes) {
+#pragma unroll
+      for (int u = 0; u < ITEMS; ++u) w[u] = word[first + u * kWarp];
+    }
+  }
+  // the runs: ITEMS neighbouring words per thread
+  const uint32_t base = tid * ITEMS, place0 = rank * kSlice + base;
+  uint64_t last_word = 0;
+  if (base > 0) {
+    last_word = word[base - 1];
+  } else if (rank > 0) {
+    asm volatile("ld.shared::cluster.u64 %0, [%1];"
+                 : "=l"(last_word)
+                 : "r"(cluster_peer(smem_addr(&word[kSlice - 1]), rank - 1))
+                 : "memory");
+  }
+  uint32_t heads = 0, live = 0, first_head = 0xFFFFFFFFu, last_head = 0;  // (places + 1)
+#pragma unroll
+  for (int u = 0; u < ITEMS; ++u) {
+    w[u] = word[base + u];
+    const uint32_t key = static_cast<uint32_t>(w[u] >> 32);
+    const bool on = place0 + u < tokens && key < vocab;
+    live += on;
+    const uint64_t was = u == 0 ? last_word : w[u > 0 ? u - 1 : 0];
+    if (on && (place0 + u == 0 || static_cast<uint32_t>(was >> 32) != key)) {
+      heads |= 1u << u;
+      first_head = min(first_head, place0 + u);
+      last_head = place0 + u + 1;
+    }
+  }
+  uint32_t all_heads, all_live, min_head, max_head;
+  const uint32_t runs_before = block_scan(__popc(heads), sh.part, &all_heads);
+  block_scan(live, sh.part, &all_live);
+  uint32_t start = block_max_before(last_head, sh.part, &max_head);
+  uint32_t end = block_min_after(first_head, sh.part, &min_head);
+  if (tid < kClusterCtas) {
+    const uint32_t to = cluster_peer(smem_addr(&sh.ends[rank]), tid);
+    asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(all_heads),
+                 "r"(all_live), "r"(min_head), "r"(max_head)
+                 : "memory");
+  }
+  cluster_barrier();
+  uint32_t run = runs_before, runs = 0, total_live = 0, next = 0xFFFFFFFFu;
+  for (uint32_t r = 0; r < kClusterCtas; ++r) {
+    const uint4 e = sh.ends[r];
+    runs += e.x;
+    total_live += e.y;
+    if (r < rank) {
+      run += e.x;
+      start = max(start, e.w);  // (those of this CTA are larger, if any)
+    }
+    if (r > rank) next = min(next, e.z);
+  }
+  end = min(min(end, next), total_live);
+  // ends from the right: of each word the next run's beginning
+  uint32_t ends[ITEMS];
+#pragma unroll
+  for (int u = ITEMS - 1; u >= 0; --u) {
+    ends[u] = end;
+    if (heads >> u & 1) end = place0 + u;
+  }
+#pragma unroll
+  for (int u = 0; u < ITEMS; ++u) {
+    const uint32_t i = place0 + u, key = static_cast<uint32_t>(w[u] >> 32);
+    if (heads >> u & 1) {
+      start = i + 1;
+      p.key[run] = key;
+      if (a.mode == kEmbedRows) a.row_ids[run] = key;
+      ++run;
+    }
+    if (i < total_live)
+      p.list[i] = Entry{static_cast<uint32_t>(w[u]), a.mode == kEmbedRows ? run - 1 : key,
+                        start - 1, ends[u]};
+  }
+  if (rank == 0 && tid == 0) {
+    p.header[kRunsCount] = runs;
+    p.header[kRunsLive] = total_live;
+    p.header[kRunsFailed] = 0;
+    if (a.mode == kEmbedRows) *a.count = static_cast<int>(runs);
+  }
+  if (a.mode == kEmbedRows) {
+    const int64_t rows = a.tokens < a.vocab ? a.tokens : a.vocab;
+    for (int64_t i = runs + static_cast<int64_t>(rank * kClusterThreads + tid); i < rows;
+         i += kClusterCtas * kClusterThreads)
+      a.row_ids[i] = -1;
+  }
+  // no CTA ends while another may still read its words
+  cluster_barrier();
+}
+
+// ---- the list of more tokens, by the sort of whole keys
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanItems = 4;
 constexpr int kPlanTile = kPlanThreads * kPlanItems;
-
-// A token's sort key: its id, or the table's length for one without a row.
-__device__ __forceinline__ uint32_t key_of(const EmbedGradArgs& a, int64_t i) {
-  const int64_t id = load_index(a.ids, a.index_bytes, i);
-  return static_cast<uint32_t>(id < 0 || id >= a.vocab || id == a.padding_id ? a.vocab : id);
-}
 
 __global__ void __launch_bounds__(kPlanThreads)
     embed_keys_kernel(const __grid_constant__ EmbedGradArgs a, const __grid_constant__ GradPlan p) {
@@ -29,7 +285,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     p.vals[i] = static_cast<uint32_t>(i);
   }
   const int64_t words = static_cast<int64_t>(p.chunks) * p.blocks;
-  for (int64_t i = first; i < words; i += step) p.scratch.arrived[i] = 0;
+  for (int64_t i = first; i < words; i += step) p.arrived[i] = 0;
 }
 
 // Whether a run of live tokens begins at sorted place i.
@@ -42,24 +298,11 @@ __global__ void __launch_bounds__(kPlanThreads)
   __shared__ uint32_t part[kPlanThreads / kWarp];
   grid_dependency_sync();
   const int64_t first = static_cast<int64_t>(blockIdx.x) * kPlanTile + threadIdx.x * kPlanItems;
-  uint32_t n = 0;
+  uint32_t n = 0, all;
 #pragma unroll
   for (int u = 0; u < kPlanItems; ++u) n += begins(a, p.sorted_keys, first + u);
-  n = __reduce_add_sync(kFull, n);
-  if (lane_id() == 0) part[threadIdx.x / kWarp] = n;
-  __syncthreads();
-  if (threadIdx.x < kWarp) {
-    n = __reduce_add_sync(kFull, part[threadIdx.x]);
-    if (threadIdx.x == 0) p.tile_heads[blockIdx.x] = n;
-  }
-}
-
-__device__ __forceinline__ uint32_t block_sum(uint32_t v, uint32_t* part) {
-  v = __reduce_add_sync(kFull, v);
-  __syncthreads();
-  if (lane_id() == 0) part[threadIdx.x / kWarp] = v;
-  __syncthreads();
-  return __reduce_add_sync(kFull, part[lane_id()]);
+  block_scan(n, part, &all);
+  if (threadIdx.x == 0) p.tile_heads[blockIdx.x] = all;
 }
 
 __global__ void __launch_bounds__(kPlanThreads)
@@ -68,7 +311,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   __shared__ uint32_t part[kWarp];
   grid_dependency_sync();
   // tokens that are not sorted are not looked at
-  const bool failed = p.sort_error != nullptr && *p.sort_error != kErrNone;
+  const bool failed = *p.sort_error != kErrNone;
   const int64_t tokens = failed ? 0 : a.tokens;
   // runs that begin in earlier tiles, and in all of them
   uint32_t before = 0, all = 0;
@@ -77,28 +320,19 @@ __global__ void __launch_bounds__(kPlanThreads)
     all += n;
     if (t < blockIdx.x) before += n;
   }
-  before = block_sum(before, part);
-  all = block_sum(all, part);
+  block_scan(before, part, &before);
+  block_scan(all, part, &all);
+  if (failed) all = 0;
   // and in this one, before this thread's places
   const int64_t first = static_cast<int64_t>(blockIdx.x) * kPlanTile + threadIdx.x * kPlanItems;
   bool head[kPlanItems];
-  uint32_t n = 0;
+  uint32_t n = 0, tile;
 #pragma unroll
   for (int u = 0; u < kPlanItems; ++u) {
     head[u] = begins(a, p.sorted_keys, first + u);
     n += head[u];
   }
-  uint32_t upto = n;
-#pragma unroll
-  for (int o = 1; o < kWarp; o *= 2) {
-    const uint32_t v = __shfl_up_sync(kFull, upto, o);
-    if (lane_id() >= static_cast<uint32_t>(o)) upto += v;
-  }
-  __syncthreads();
-  if (lane_id() == kWarp - 1) part[threadIdx.x / kWarp] = upto;
-  __syncthreads();
-  uint32_t run = before + upto - n +
-                 __reduce_add_sync(kFull, lane_id() < threadIdx.x / kWarp ? part[lane_id()] : 0);
+  uint32_t run = before + block_scan(n, part, &tile);
 #pragma unroll
   for (int u = 0; u < kPlanItems; ++u) {
     const int64_t i = first + u;
@@ -112,8 +346,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     }
     if (key < a.vocab) p.slot[i] = run - 1;
     // the live tokens end here
-    const bool last = key < a.vocab && (i + 1 == a.tokens || p.sorted_keys[i + 1] >= a.vocab);
-    if (last) {
+    if (key < a.vocab && (i + 1 == a.tokens || p.sorted_keys[i + 1] >= a.vocab)) {
       p.start[run] = static_cast<uint32_t>(i + 1);
       p.header[kRunsLive] = static_cast<uint32_t>(i + 1);
     }
@@ -131,6 +364,17 @@ __global__ void __launch_bounds__(kPlanThreads)
          i += static_cast<int64_t>(gridDim.x) * kPlanThreads)
       a.row_ids[i] = -1;
   }
+}
+
+__global__ void __launch_bounds__(kPlanThreads)
+    embed_entries_kernel(const __grid_constant__ EmbedGradArgs a,
+                         const __grid_constant__ GradPlan p) {
+  grid_dependency_sync();
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kPlanThreads + threadIdx.x;
+  if (i >= p.header[kRunsLive]) return;
+  const uint32_t slot = p.slot[i];
+  p.list[i] = Entry{p.sorted_vals[i], a.mode == kEmbedRows ? slot : p.sorted_keys[i],
+                    p.start[slot], p.start[slot + 1]};
 }
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -186,45 +430,100 @@ int key_bits(int64_t vocab) {
   return bits;
 }
 
-// Lays a call's scratch out from `temp`; returns its size.
+// Lays a call's scratch out from `temp`; returns its size.  sort: where that of
+// the sort of whole keys begins.
 size_t lay_out(int64_t tokens, int64_t width, void* temp, GradPlan* p, size_t* sort) {
   Parts parts;
   unsigned char* base = static_cast<unsigned char*>(temp);
   auto words = [&](int64_t n) { return reinterpret_cast<uint32_t*>(base + parts.take(n * 4)); };
-  const int64_t chunks = cdiv(tokens, kChunk);
   p->header = words(64);
-  p->scratch.arrived = words(chunks * cdiv(width, kWarp));
-  p->scratch.partial = reinterpret_cast<float*>(
+  *sort = parts.at;
+  if (tokens <= kFewTokens) return parts.at;
+  const int64_t chunks = cdiv(tokens, kChunk);
+  p->chunks = static_cast<int>(chunks);
+  p->arrived = words(chunks * cdiv(width, kWarp));
+  p->partial = reinterpret_cast<float*>(
       words(2 * chunks * static_cast<int64_t>(align_up(static_cast<size_t>(width), 256))));
+  p->list = reinterpret_cast<Entry*>(words(tokens * 4));
+  p->key = words(tokens);
+  *sort = parts.at;
+  if (tokens <= kClusterTokens) return parts.at;
   p->keys = words(tokens);
   p->vals = words(tokens);
   p->sorted_keys = words(tokens);
-  p->pos = words(tokens);
+  p->sorted_vals = words(tokens);
   p->slot = p->keys;  // the unsorted tokens are done with
-  p->key = p->vals;
   p->start = words(tokens + 1);
-  p->tile_heads = words(cdiv(tokens, kPlanTile) + 1);
-  p->chunks = static_cast<int>(chunks);
+  p->tile_heads = words(cdiv(tokens, kPlanTile));
   *sort = parts.at;
-  p->sort_error = tokens > 0 ? reinterpret_cast<const uint32_t*>(base + parts.at) : nullptr;
+  p->sort_error = reinterpret_cast<const uint32_t*>(base + parts.at);
   return parts.at;
 }
 
-template <int IN, int OUT, int VEC>
-cudaError_t grad_as(const EmbedGradArgs& a, GradPlan& p, int64_t sum_ctas, int64_t ctas,
-                    cudaStream_t s) {
-  return launch_kernel(embed_grad_kernel<IN, OUT, VEC>, dim3(static_cast<unsigned>(ctas)),
-                       dim3(kGradThreads), 0, s, a, p, sum_ctas);
+// One of the gradient's last kernels, by types and vector; f(types...).
+template <int IN, int OUT, class F>
+cudaError_t by_vector(int vec, F&& f) {
+  constexpr int kEs = sizeof(typename Score<IN>::Raw);
+  if (vec == 16 / kEs) return f(ScoreTag<IN>{}, ScoreTag<OUT>{}, ScoreTag<16 / kEs>{});
+  if constexpr (kEs == 2)
+    if (vec == 2) return f(ScoreTag<IN>{}, ScoreTag<OUT>{}, ScoreTag<2>{});
+  return f(ScoreTag<IN>{}, ScoreTag<OUT>{}, ScoreTag<1>{});
+}
+template <class F>
+cudaError_t by_types(int type, int out_type, int vec, F&& f) {
+  if (type == RS_SCORE_F32) return by_vector<RS_SCORE_F32, RS_SCORE_F32>(vec, f);
+  if (type == RS_SCORE_F16)
+    return out_type == RS_SCORE_F32 ? by_vector<RS_SCORE_F16, RS_SCORE_F32>(vec, f)
+                                    : by_vector<RS_SCORE_F16, RS_SCORE_F16>(vec, f);
+  return out_type == RS_SCORE_F32 ? by_vector<RS_SCORE_BF16, RS_SCORE_F32>(vec, f)
+                                  : by_vector<RS_SCORE_BF16, RS_SCORE_BF16>(vec, f);
 }
 
-template <int IN, int OUT>
-cudaError_t grad_of(const EmbedGradArgs& a, GradPlan& p, int vec, int64_t sum_ctas, int64_t ctas,
-                    cudaStream_t s) {
-  constexpr int kEs = sizeof(typename Score<IN>::Raw);
-  if (vec == 16 / kEs) return grad_as<IN, OUT, 16 / kEs>(a, p, sum_ctas, ctas, s);
-  if constexpr (kEs == 2)
-    if (vec == 2) return grad_as<IN, OUT, 2>(a, p, sum_ctas, ctas, s);
-  return grad_as<IN, OUT, 1>(a, p, sum_ctas, ctas, s);
+// Opts a kernel into its shared memory and clusters of 16, once per device.
+template <class K>
+cudaError_t allow(K kern, int bytes, std::atomic<uint64_t>* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (dev < 64 && (done->load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
+template <int ITEMS>
+cudaError_t list_as(const EmbedGradArgs& a, const GradPlan& p, cudaStream_t s) {
+  constexpr int kSmem = kClusterThreads * ITEMS * 8 + static_cast<int>(sizeof(ClusterShared));
+  static_assert(kSmem <= 232448);
+  static std::atomic<uint64_t> done{0};
+  auto kern = embed_list_kernel<ITEMS>;
+  const cudaError_t e = allow(kern, kSmem, &done);
+  if (e != cudaSuccess) return e;
+  const int bits = key_bits(a.vocab), passes = (bits + 8) / 9;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kClusterCtas);
+  cfg.blockDim = dim3(kClusterThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+#if LSDRS_PDL
+  attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[n++].val.programmaticStreamSerializationAllowed = 1;
+#endif
+  attr[n].id = cudaLaunchAttributeClusterDimension;
+  attr[n].val.clusterDim.x = kClusterCtas;
+  attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = n + 1;
+  return cudaLaunchKernelEx(&cfg, kern, a, p, passes, (bits + passes - 1) / passes);
+}
+
+int64_t zero_ctas(const EmbedGradArgs& a, int64_t rows) {
+  return a.mode == kEmbedTable ? cdiv(a.vocab, rows) : 0;
 }
 
 }  // namespace
@@ -240,71 +539,103 @@ cudaError_t launch_embed(int type, const EmbedArgs& a, cudaStream_t s) {
 
 size_t embed_grad_temp(int64_t tokens, int64_t vocab, int64_t width) {
   GradPlan p{};
-  size_t sort = 0;
-  size_t total = lay_out(tokens, width, nullptr, &p, &sort);
-  size_t sort_bytes = 0;
-  if (tokens > 0 && radix_sort_keys_temp_bytes(static_cast<size_t>(tokens), 4, 4, 0,
-                                               key_bits(vocab), 8, &sort_bytes) != RS_OK)
+  size_t sort = 0, sort_bytes = 0;
+  const size_t total = lay_out(tokens, width, nullptr, &p, &sort);
+  if (tokens > kClusterTokens &&
+      radix_sort_keys_temp_bytes(static_cast<size_t>(tokens), 4, 4, 0, key_bits(vocab), 8,
+                                 &sort_bytes) != RS_OK)
     return 0;
   return total + align_up(sort_bytes, 256);
 }
+
+bool embed_grad_sorts(int64_t tokens) { return tokens > kClusterTokens; }
 
 cudaError_t launch_embed_keys(const EmbedGradArgs& a, cudaStream_t s) {
   GradPlan p{};
   size_t sort;
   lay_out(a.tokens, a.width, a.temp, &p, &sort);
   p.blocks = static_cast<int>(cdiv(a.width, kWarp));  // any launch has no more
-  const int64_t ctas = std::min<int64_t>(
-      std::max<int64_t>(1, cdiv(a.tokens, kPlanThreads)), 4 * device_sm_count());
+  const int64_t ctas = std::min<int64_t>(cdiv(a.tokens, kPlanThreads), 4 * device_sm_count());
   return launch_kernel(embed_keys_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kPlanThreads), 0,
                        s, a, p);
 }
 
 rs_status sort_embed_keys(const EmbedGradArgs& a, void* stream) {
-  if (a.tokens == 0) return RS_OK;
   GradPlan p{};
   size_t sort, bytes = 0;
   lay_out(a.tokens, a.width, a.temp, &p, &sort);
   const size_t n = static_cast<size_t>(a.tokens);
   const rs_status st = radix_sort_keys_temp_bytes(n, 4, 4, 0, key_bits(a.vocab), 8, &bytes);
   if (st != RS_OK) return st;
-  return radix_sort_pairs_u32(p.keys, p.sorted_keys, p.vals, p.pos, n, 0, key_bits(a.vocab), 8,
-                              static_cast<unsigned char*>(a.temp) + sort, bytes, stream);
+  return radix_sort_pairs_u32(p.keys, p.sorted_keys, p.vals, p.sorted_vals, n, 0,
+                              key_bits(a.vocab), 8, static_cast<unsigned char*>(a.temp) + sort,
+                              bytes, stream);
 }
 
-cudaError_t launch_embed_runs(const EmbedGradArgs& a, int* launched, cudaStream_t s) {
-  GradPlan p{};
-  size_t sort;
-  lay_out(a.tokens, a.width, a.temp, &p, &sort);
-  const dim3 tiles(static_cast<unsigned>(std::max<int64_t>(1, cdiv(a.tokens, kPlanTile))));
-  const cudaError_t e = launch_kernel(embed_heads_kernel, tiles, dim3(kPlanThreads), 0, s, a, p);
-  if (e != cudaSuccess) return e;
-  *launched = 2;
-  return launch_kernel(embed_runs_kernel, tiles, dim3(kPlanThreads), 0, s, a, p);
-}
-
-cudaError_t launch_embed_grad(int type, int out_type, const EmbedGradArgs& a, cudaStream_t s) {
+cudaError_t launch_embed_grad(int type, int out_type, const EmbedGradArgs& a, int* launched,
+                              cudaStream_t s) {
   GradPlan p{};
   size_t sort;
   lay_out(a.tokens, a.width, a.temp, &p, &sort);
   const int es = score_bytes(type), out_es = score_bytes(out_type);
-  const int vec =
-      vector_of(a.width, es, a.grad, a.grad_stride, out_es, a.out, a.out_stride);
-  p.blocks = static_cast<int>(cdiv(a.width, static_cast<int64_t>(kWarp) * vec));
-  p.piece = 128;
-  static_assert(128 >= kChunk, "a chunk holds the beginnings of two pieces at most");
+  const int vec = vector_of(a.width, es, a.grad, a.grad_stride, out_es, a.out, a.out_stride);
+  const int64_t blocks = cdiv(a.width, static_cast<int64_t>(kWarp) * vec);
+  const int sms = device_sm_count();
+  if (a.tokens <= kFewTokens) {
+    // every CTA sorts: no more of them than two per SM, for the zeros too
+    const int64_t rows = std::min<int64_t>(kZeroMostRows, cdiv(a.vocab, 2 * sms));
+    const int64_t sums =
+        std::max<int64_t>(1, std::min<int64_t>(cdiv(a.tokens * blocks, kFewWarps), 2 * sms));
+    int size = 2, shift = 1;
+    while (size < a.tokens) {
+      size *= 2;
+      ++shift;
+    }
+    const dim3 ctas(static_cast<unsigned>(sums + zero_ctas(a, rows)));
+    return by_types(type, out_type, vec, [&](auto in, auto out, auto v) {
+      auto go = [&](auto word) {
+        using W = decltype(word);
+        constexpr size_t kSmem =
+            sizeof(FewShared<W>) + sizeof(float) * kFewThreads * decltype(v)::value;
+        static_assert(kSmem <= 48 * 1024);
+        return launch_kernel(embed_grad_few_kernel<decltype(in)::value, decltype(out)::value,
+                                                   decltype(v)::value, W>,
+                             ctas, dim3(kFewThreads), kSmem, s, a, size, shift,
+                             static_cast<int>(blocks), static_cast<int>(sums), rows);
+      };
+      return key_bits(a.vocab) + shift <= 32 ? go(uint32_t{}) : go(uint64_t{});
+    });
+  }
+  p.blocks = static_cast<int>(blocks);
+  cudaError_t e = cudaSuccess;
+  if (!embed_grad_sorts(a.tokens)) {
+    const int64_t each = cdiv(a.tokens, kClusterCtas * kClusterThreads);
+    static_assert(kClusterItems == 8);
+    e = each <= 1   ? list_as<1>(a, p, s)
+        : each <= 2 ? list_as<2>(a, p, s)
+        : each <= 4 ? list_as<4>(a, p, s)
+                    : list_as<8>(a, p, s);
+    *launched = 2;
+  } else {
+    const dim3 tiles(static_cast<unsigned>(cdiv(a.tokens, kPlanTile)));
+    e = launch_kernel(embed_heads_kernel, tiles, dim3(kPlanThreads), 0, s, a, p);
+    if (e == cudaSuccess) e = launch_kernel(embed_runs_kernel, tiles, dim3(kPlanThreads), 0, s, a, p);
+    if (e == cudaSuccess)
+      e = launch_kernel(embed_entries_kernel,
+                        dim3(static_cast<unsigned>(cdiv(a.tokens, kPlanThreads))),
+                        dim3(kPlanThreads), 0, s, a, p);
+    *launched = 4;
+  }
+  if (e != cudaSuccess) return e;
   const int64_t sum_ctas = cdiv(static_cast<int64_t>(p.chunks) * p.blocks, kGradWarps);
-  p.rows_per_zero = std::min<int64_t>(kZeroMostRows, std::max<int64_t>(1, 131072 / (a.width * out_es)));
-  const int64_t ctas = sum_ctas + (a.mode == kEmbedTable ? cdiv(a.vocab, p.rows_per_zero) : 0);
-  if (ctas == 0) return cudaSuccess;
-  if (type == RS_SCORE_F32) return grad_of<RS_SCORE_F32, RS_SCORE_F32>(a, p, vec, sum_ctas, ctas, s);
-  if (type == RS_SCORE_F16)
-    return out_type == RS_SCORE_F32
-               ? grad_of<RS_SCORE_F16, RS_SCORE_F32>(a, p, vec, sum_ctas, ctas, s)
-               : grad_of<RS_SCORE_F16, RS_SCORE_F16>(a, p, vec, sum_ctas, ctas, s);
-  return out_type == RS_SCORE_F32
-             ? grad_of<RS_SCORE_BF16, RS_SCORE_F32>(a, p, vec, sum_ctas, ctas, s)
-             : grad_of<RS_SCORE_BF16, RS_SCORE_BF16>(a, p, vec, sum_ctas, ctas, s);
+  p.rows_per_zero =
+      std::min<int64_t>(kZeroMostRows, std::max<int64_t>(1, 131072 / (a.width * out_es)));
+  const dim3 ctas(static_cast<unsigned>(sum_ctas + zero_ctas(a, p.rows_per_zero)));
+  return by_types(type, out_type, vec, [&](auto in, auto out, auto v) {
+    return launch_kernel(
+        embed_grad_kernel<decltype(in)::value, decltype(out)::value, decltype(v)::value>, ctas,
+        dim3(kGradThreads), 0, s, a, p, sum_ctas);
+  });
 }
 
 }  // namespace lsdrs

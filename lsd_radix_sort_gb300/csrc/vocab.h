@@ -68,12 +68,13 @@ size_t logprobs_temp_bytes(int type, int64_t rows, int64_t cols, int top);
 cudaError_t launch_logprobs(int type, const LogprobArgs& a, int* launched, cudaStream_t s);
 cudaError_t launch_logprobs_backward(int type, const LogprobArgs& a, cudaStream_t s);
 cudaError_t launch_embed(int type, const EmbedArgs& a, cudaStream_t s);
-// The gradient's steps: the tokens' sort keys, their sort, the runs of equal
-// ids, and the sums (and zeros).  out_type: the input's, or RS_SCORE_F32.
+// The gradient: its launches, after those of a sort of whole keys where there
+// are too many tokens for less.  out_type: the input's, or RS_SCORE_F32.
 size_t embed_grad_temp(int64_t tokens, int64_t vocab, int64_t width);
+bool embed_grad_sorts(int64_t tokens);
 cudaError_t launch_embed_keys(const EmbedGradArgs& a, cudaStream_t s);
 rs_status sort_embed_keys(const EmbedGradArgs& a, void* stream);
-cudaError_t launch_embed_runs(const EmbedGradArgs& a, int* launched, cudaStream_t s);
-cudaError_t launch_embed_grad(int type, int out_type, const EmbedGradArgs& a, cudaStream_t s);
+cudaError_t launch_embed_grad(int type, int out_type, const EmbedGradArgs& a, int* launched,
+                              cudaStream_t s);
 
 }  // namespace lsdrs

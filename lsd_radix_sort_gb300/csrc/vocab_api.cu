@@ -64,7 +64,7 @@ rs_status embed_grad_check(const rs_embedding_grad_args* p) {
     return RS_ERR_INVALID;
   if (p->index_bytes != 4 && p->index_bytes != 8) return RS_ERR_INVALID;
   if (p->tokens < 0 || p->tokens > kMaxRows || p->vocab < 1 || p->vocab > kMaxRows ||
-      p->width < 1 || p->width > RS_MAX_ROW_KEYS || p->padding_id < -1 || !std::isfinite(p->scale))
+      p->width < 1 || p->width > RS_MAX_WIDTH || p->padding_id < -1 || !std::isfinite(p->scale))
     return RS_ERR_INVALID;
   const int es = score_bytes(p->grad_type), out_es = score_bytes(p->out_type);
   const bool rows = p->mode == RS_EMBED_ROWS;
@@ -148,7 +148,7 @@ rs_status rs_embedding(const rs_embedding_args* p, void* stream) {
   if (p->index_bytes != 4 && p->index_bytes != 8) return RS_ERR_INVALID;
   const int es = score_bytes(p->type);
   if (p->tokens < 0 || p->tokens > kMaxRows || p->vocab < 1 || p->vocab > kMaxRows ||
-      p->width < 1 || p->width > RS_MAX_ROW_KEYS || !std::isfinite(p->scale))
+      p->width < 1 || p->width > RS_MAX_WIDTH || !std::isfinite(p->scale))
     return RS_ERR_INVALID;
   if (!matrix_ok(p->vocab, p->width, p->table_stride, es) ||
       !matrix_ok(p->tokens, p->width, p->out_stride, es))
@@ -177,7 +177,7 @@ rs_status rs_embedding(const rs_embedding_args* p, void* stream) {
 rs_status rs_embedding_grad_temp_bytes(int64_t tokens, int64_t vocab, int64_t width,
                                        size_t* bytes) {
   if (!bytes || tokens < 0 || tokens > kMaxRows || vocab < 1 || vocab > kMaxRows || width < 1 ||
-      width > RS_MAX_ROW_KEYS)
+      width > RS_MAX_WIDTH)
     return RS_ERR_INVALID;
   *bytes = embed_grad_temp(tokens, vocab, width);
   return RS_OK;
@@ -204,16 +204,15 @@ rs_status rs_embedding_grad(const rs_embedding_grad_args* p, void* stream) {
   a.status = p->status;
   a.temp = p->temp;
   const uint64_t units = static_cast<uint64_t>(p->tokens);
-  st = enqueue(kNameEmbed, units, stream,
-               [&](int*, cudaStream_t s) { return launch_embed_keys(a, s); });
-  if (st == RS_OK) st = sort_embed_keys(a, stream);
-  if (st == RS_OK)
+  if (embed_grad_sorts(p->tokens)) {
     st = enqueue(kNameEmbed, units, stream,
-                 [&](int* n, cudaStream_t s) { return launch_embed_runs(a, n, s); });
-  if (st == RS_OK)
-    st = enqueue(kNameEmbed, units, stream, [&](int*, cudaStream_t s) {
-      return launch_embed_grad(p->grad_type, p->out_type, a, s);
-    });
+                 [&](int*, cudaStream_t s) { return launch_embed_keys(a, s); });
+    if (st == RS_OK) st = sort_embed_keys(a, stream);
+    if (st != RS_OK) return st;
+  }
+  st = enqueue(kNameEmbed, units, stream, [&](int* n, cudaStream_t s) {
+    return launch_embed_grad(p->grad_type, p->out_type, a, n, s);
+  });
   return st;
 }
 

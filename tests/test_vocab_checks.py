@@ -222,7 +222,7 @@ def test_scratch_size(lib):
                 (10, 8, 1, -1), (10, 8, 1, 1025)):
         assert lib.rs_token_logprobs_temp_bytes(*bad, ctypes.byref(out)) == 1
     assert lib.rs_token_logprobs_temp_bytes(10, 8, 1, 0, None) == 1
-    for bad in ((-1, 8, 8), (1 << 31, 8, 8), (10, 0, 8), (10, 1 << 31, 8), (10, 8, 0)):
+    for bad in ((-1, 8, 8), (1 << 31, 8, 8), (10, 0, 8), (10, 1 << 31, 8), (10, 8, 0), (10, 8, (1 << 24) + 1)):
         assert lib.rs_embedding_grad_temp_bytes(*bad, ctypes.byref(out)) == 1
     assert lib.rs_embedding_grad_temp_bytes(10, 8, 8, None) == 1
     assert rs.embedding_grad_temp_bytes(100000, 1000, 64) > rs.embedding_grad_temp_bytes(1000, 1000, 64) > 0
