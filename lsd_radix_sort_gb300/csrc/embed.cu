@@ -20,7 +20,6 @@ namespace {
 constexpr int kClusterCtas = 16;
 constexpr int kClusterThreads = 1024;
 constexpr int kClusterWarps = kClusterThreads / kWarp;
-constexpr int kMaxRadix = 512;
 constexpr int kClusterItems = 8;
 constexpr int64_t kClusterTokens = int64_t(kClusterCtas) * kClusterThreads * kClusterItems;
 
@@ -44,22 +43,6 @@ __device__ __forceinline__ void cluster_barrier() {
                    : "memory");
 }
 
-// Sums of v over the threads before this one; all: over all of them.
-__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* part, uint32_t* all) {
-  const uint32_t lane = lane_id(), warp = threadIdx.x / kWarp;
-  uint32_t upto = v;
-#pragma unroll
-  for (int o = 1; o < kWarp; o *= 2) {
-    const uint32_t n = __shfl_up_sync(kFull, upto, o);
-    if (lane >= static_cast<uint32_t>(o)) upto += n;
-  }
-  __syncthreads();  // (what was there before has been read)
-  if (lane == kWarp - 1) part[warp] = upto;
-  __syncthreads();
-  const uint32_t n = part[lane];
-  *all = __reduce_add_sync(kFull, n);
-  return __reduce_add_sync(kFull, lane < warp ? n : 0) + upto - v;
-}
 __device__ __forceinline__ uint32_t block_max_before(uint32_t v, uint32_t* part, uint32_t* all) {
   const uint32_t lane = lane_id(), warp = threadIdx.x / kWarp;
   uint32_t upto = v;
@@ -108,6 +91,8 @@ __global__ void __launch_bounds__(kClusterThreads, 1)
   const uint32_t tokens = static_cast<uint32_t>(a.tokens), vocab = static_cast<uint32_t>(a.vocab);
   const uint32_t radix = 1u << bits;
   grid_dependency_sync();
+  // (waited for before another CTA's memory is written to)
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   uint64_t w[ITEMS];
   const uint32_t first = warp * kWarp * ITEMS + lane;  // this thread's words: every 32nd
 #pragma unroll
@@ -117,42 +102,19 @@ __global__ void __launch_bounds__(kClusterThreads, 1)
     w[u] = i < tokens ? static_cast<uint64_t>(key_of(a, i)) << 32 | i : ~uint64_t(0);
   }
   {
-    const int64_t words = static_cast<int64_t>(p.chunks) * p.blocks;
+    const int64_t words = 2 * static_cast<int64_t>(p.chunks) * p.blocks;
     for (int64_t i = rank * kClusterThreads + tid; i < words; i += kClusterCtas * kClusterThreads)
       p.arrived[i] = 0;
   }
   for (int pass = 0; pass < passes; ++pass) {
     const int shift = 32 + pass * bits;
-    for (uint32_t i = lane; i < radix; i += kWarp) sh.warp_count[warp][i] = 0;
-    __syncwarp();
-    uint16_t place[ITEMS];  // among the warp's words of the digit
-#pragma unroll
-    for (int u = 0; u < ITEMS; ++u) {
-      const uint32_t d = static_cast<uint32_t>(w[u] >> shift) & (radix - 1);
-      unsigned same = kFull;
-      for (int b = 0; b < bits; ++b) {
-        const unsigned set = __ballot_sync(kFull, d >> b & 1);
-        same &= (d >> b & 1) != 0 ? set : ~set;
-      }
-      const uint16_t was = sh.warp_count[warp][d];
-      __syncwarp();
-      place[u] = static_cast<uint16_t>(was + __popc(same & lanemask_lt()));
-      if ((same & lanemask_lt()) == 0)
-        sh.warp_count[warp][d] = static_cast<uint16_t>(was + __popc(same));
-      __syncwarp();
-    }
+    uint32_t place[ITEMS];
+    rank_words<ITEMS>(w, shift, bits, sh.warp_count[warp], place);
     __syncthreads();
-    uint32_t total = 0;
-    if (tid < radix) {
-#pragma unroll 8
-      for (int i = 0; i < kClusterWarps; ++i) {
-        const uint32_t n = sh.warp_count[i][tid];
-        sh.warp_count[i][tid] = static_cast<uint16_t>(total);
-        total += n;
-      }
-    }
-    if (pass == 0) cluster_barrier();  // all CTAs have begun
+    const uint32_t total = tid < radix ? sum_warps<kClusterWarps>(sh.warp_count, tid) : 0;
+    if (pass == 0) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     if (tid < radix)
+#pragma unroll
       for (uint32_t r = 0; r < kClusterCtas; ++r)
         asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(
                          cluster_peer(smem_addr(&sh.count[rank][tid]), r)),
@@ -161,13 +123,14 @@ __global__ void __launch_bounds__(kClusterThreads, 1)
     cluster_barrier();
     uint32_t digit = 0, before = 0;
     if (tid < radix)
+#pragma unroll
       for (uint32_t r = 0; r < kClusterCtas; ++r) {
         const uint32_t n = sh.count[r][tid];
         digit += n;
         if (r < rank) before += n;
       }
     uint32_t all;
-    const uint32_t smaller = block_scan(digit, sh.part, &all);
+    const uint32_t smaller = block_scan<kWarp>(digit, sh.part, &all);
     if (tid < radix) sh.base[tid] = smaller + before;
     __syncthreads();
 #pragma unroll
@@ -211,8 +174,8 @@ __global__ void __launch_bounds__(kClusterThreads, 1)
     }
   }
   uint32_t all_heads, all_live, min_head, max_head;
-  const uint32_t runs_before = block_scan(__popc(heads), sh.part, &all_heads);
-  block_scan(live, sh.part, &all_live);
+  const uint32_t runs_before = block_scan<kWarp>(__popc(heads), sh.part, &all_heads);
+  block_scan<kWarp>(live, sh.part, &all_live);
   uint32_t start = block_max_before(last_head, sh.part, &max_head);
   uint32_t end = block_min_after(first_head, sh.part, &min_head);
   if (tid < kClusterCtas) {
@@ -221,7 +184,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1)
                  "r"(all_live), "r"(min_head), "r"(max_head)
                  : "memory");
   }
-  cluster_barrier();
+  cluster_barrier();  // from here on no CTA reads another's memory
   uint32_t run = runs_before, runs = 0, total_live = 0, next = 0xFFFFFFFFu;
   for (uint32_t r = 0; r < kClusterCtas; ++r) {
     const uint4 e = sh.ends[r];
@@ -266,8 +229,6 @@ __global__ void __launch_bounds__(kClusterThreads, 1)
          i += kClusterCtas * kClusterThreads)
       a.row_ids[i] = -1;
   }
-  // no CTA ends while another may still read its words
-  cluster_barrier();
 }
 
 // ---- the list of more tokens, by the sort of whole keys
@@ -284,7 +245,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     p.keys[i] = key_of(a, i);
     p.vals[i] = static_cast<uint32_t>(i);
   }
-  const int64_t words = static_cast<int64_t>(p.chunks) * p.blocks;
+  const int64_t words = 2 * static_cast<int64_t>(p.chunks) * p.blocks;
   for (int64_t i = first; i < words; i += step) p.arrived[i] = 0;
 }
 
@@ -301,7 +262,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   uint32_t n = 0, all;
 #pragma unroll
   for (int u = 0; u < kPlanItems; ++u) n += begins(a, p.sorted_keys, first + u);
-  block_scan(n, part, &all);
+  block_scan<kWarp>(n, part, &all);
   if (threadIdx.x == 0) p.tile_heads[blockIdx.x] = all;
 }
 
@@ -320,8 +281,8 @@ __global__ void __launch_bounds__(kPlanThreads)
     all += n;
     if (t < blockIdx.x) before += n;
   }
-  block_scan(before, part, &before);
-  block_scan(all, part, &all);
+  block_scan<kWarp>(before, part, &before);
+  block_scan<kWarp>(all, part, &all);
   if (failed) all = 0;
   // and in this one, before this thread's places
   const int64_t first = static_cast<int64_t>(blockIdx.x) * kPlanTile + threadIdx.x * kPlanItems;
@@ -332,7 +293,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     head[u] = begins(a, p.sorted_keys, first + u);
     n += head[u];
   }
-  uint32_t run = before + block_scan(n, part, &tile);
+  uint32_t run = before + block_scan<kWarp>(n, part, &tile);
 #pragma unroll
   for (int u = 0; u < kPlanItems; ++u) {
     const int64_t i = first + u;
@@ -383,13 +344,13 @@ bool aligned(const void* p, int64_t stride, int64_t bytes, int es) {
   return reinterpret_cast<uintptr_t>(p) % bytes == 0 && stride * es % bytes == 0;
 }
 
-// The widest access, in elements, that every row of both sides allows: 16
-// bytes of the input, else 4, else one element.
-int vector_of(int64_t width, int in_es, const void* in, int64_t in_stride, int out_es,
+// The widest access, in elements, that every row of both sides allows: `most`
+// bytes of the input, 16, 4, or one element.
+int vector_of(int most, int64_t width, int in_es, const void* in, int64_t in_stride, int out_es,
               const void* out, int64_t out_stride) {
-  for (int vec : {16 / in_es, 4 / in_es})
+  for (int vec : {most / in_es, 16 / in_es, 4 / in_es})
     if (width % vec == 0 && aligned(in, in_stride, vec * in_es, in_es) &&
-        aligned(out, out_stride, std::min(16, vec * out_es), out_es))
+        aligned(out, out_stride, std::min(32, vec * out_es), out_es))
       return vec;
   return 1;
 }
@@ -405,7 +366,8 @@ cudaError_t embed_as(const EmbedArgs& a, cudaStream_t s) {
 template <int TYPE>
 cudaError_t embed_of(const EmbedArgs& a, cudaStream_t s) {
   constexpr int kEs = sizeof(typename Score<TYPE>::Raw);
-  const int vec = vector_of(a.width, kEs, a.table, a.table_stride, kEs, a.out, a.out_stride);
+  const int vec = vector_of(32, a.width, kEs, a.table, a.table_stride, kEs, a.out, a.out_stride);
+  if (vec == 32 / kEs) return embed_as<TYPE, 32 / kEs>(a, s);
   if (vec == 16 / kEs) return embed_as<TYPE, 16 / kEs>(a, s);
   if constexpr (kEs == 2)
     if (vec == 2) return embed_as<TYPE, 2>(a, s);
@@ -439,11 +401,14 @@ size_t lay_out(int64_t tokens, int64_t width, void* temp, GradPlan* p, size_t* s
   p->header = words(64);
   *sort = parts.at;
   if (tokens <= kFewTokens) return parts.at;
-  const int64_t chunks = cdiv(tokens, kChunk);
+  // some rounds of warps, if the tokens allow it
+  p->chunk = kMostChunk;
+  while (p->chunk > kLeastChunk && tokens / p->chunk * cdiv(width, 512) < 5000) p->chunk /= 2;
+  const int64_t chunks = cdiv(tokens, p->chunk);
   p->chunks = static_cast<int>(chunks);
-  p->arrived = words(chunks * cdiv(width, kWarp));
+  p->arrived = words(2 * chunks * cdiv(width, kWarp));
   p->partial = reinterpret_cast<float*>(
-      words(2 * chunks * static_cast<int64_t>(align_up(static_cast<size_t>(width), 256))));
+      words(2 * chunks * static_cast<int64_t>(align_up(static_cast<size_t>(width), 512))));
   p->list = reinterpret_cast<Entry*>(words(tokens * 4));
   p->key = words(tokens);
   *sort = parts.at;
@@ -462,15 +427,22 @@ size_t lay_out(int64_t tokens, int64_t width, void* temp, GradPlan* p, size_t* s
 
 // One of the gradient's last kernels, by types and vector; f(types...).
 template <int IN, int OUT, class F>
-cudaError_t by_vector(int vec, F&& f) {
+cudaError_t by_vector(int vec, const F& f) {
   constexpr int kEs = sizeof(typename Score<IN>::Raw);
+  if constexpr (F::kMost == 32)
+    if (vec == 32 / kEs) return f(ScoreTag<IN>{}, ScoreTag<OUT>{}, ScoreTag<32 / kEs>{});
   if (vec == 16 / kEs) return f(ScoreTag<IN>{}, ScoreTag<OUT>{}, ScoreTag<16 / kEs>{});
   if constexpr (kEs == 2)
     if (vec == 2) return f(ScoreTag<IN>{}, ScoreTag<OUT>{}, ScoreTag<2>{});
   return f(ScoreTag<IN>{}, ScoreTag<OUT>{}, ScoreTag<1>{});
 }
-template <class F>
-cudaError_t by_types(int type, int out_type, int vec, F&& f) {
+template <int MOST, class F>
+struct UpTo : F {
+  static constexpr int kMost = MOST;
+};
+template <int MOST, class F>
+cudaError_t by_types(int type, int out_type, int vec, F&& launch) {
+  const UpTo<MOST, F> f{launch};
   if (type == RS_SCORE_F32) return by_vector<RS_SCORE_F32, RS_SCORE_F32>(vec, f);
   if (type == RS_SCORE_F16)
     return out_type == RS_SCORE_F32 ? by_vector<RS_SCORE_F16, RS_SCORE_F32>(vec, f)
@@ -520,10 +492,6 @@ cudaError_t list_as(const EmbedGradArgs& a, const GradPlan& p, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = n + 1;
   return cudaLaunchKernelEx(&cfg, kern, a, p, passes, (bits + passes - 1) / passes);
-}
-
-int64_t zero_ctas(const EmbedGradArgs& a, int64_t rows) {
-  return a.mode == kEmbedTable ? cdiv(a.vocab, rows) : 0;
 }
 
 }  // namespace
@@ -578,30 +546,37 @@ cudaError_t launch_embed_grad(int type, int out_type, const EmbedGradArgs& a, in
   size_t sort;
   lay_out(a.tokens, a.width, a.temp, &p, &sort);
   const int es = score_bytes(type), out_es = score_bytes(out_type);
-  const int vec = vector_of(a.width, es, a.grad, a.grad_stride, out_es, a.out, a.out_stride);
+  const bool few = a.tokens <= kFewTokens;
+  const int vec = vector_of(few ? 16 : 32, a.width, es, a.grad, a.grad_stride, out_es, a.out,
+                            a.out_stride);
   const int64_t blocks = cdiv(a.width, static_cast<int64_t>(kWarp) * vec);
   const int sms = device_sm_count();
-  if (a.tokens <= kFewTokens) {
-    // every CTA sorts: no more of them than two per SM, for the zeros too
+  if (few) {
+    // every CTA sorts: no more of them than one per SM, or two for the zeros
     const int64_t rows = std::min<int64_t>(kZeroMostRows, cdiv(a.vocab, 2 * sms));
     const int64_t sums =
-        std::max<int64_t>(1, std::min<int64_t>(cdiv(a.tokens * blocks, kFewWarps), 2 * sms));
-    int size = 2, shift = 1;
-    while (size < a.tokens) {
-      size *= 2;
-      ++shift;
-    }
-    const dim3 ctas(static_cast<unsigned>(sums + zero_ctas(a, rows)));
-    return by_types(type, out_type, vec, [&](auto in, auto out, auto v) {
+        std::max<int64_t>(1, std::min<int64_t>(cdiv(a.tokens * blocks, kFewWarps), sms));
+    int shift = 1;
+    while (int64_t(1) << shift < a.tokens) ++shift;
+    const int bits = key_bits(a.vocab), passes = (bits + 8) / 9;
+    const dim3 ctas(
+        static_cast<unsigned>(sums + (a.mode == kEmbedTable ? cdiv(a.vocab, rows) : 0)));
+    return by_types<16>(type, out_type, vec, [&](auto in, auto out, auto v) {
       auto go = [&](auto word) {
         using W = decltype(word);
-        constexpr size_t kSmem =
-            sizeof(FewShared<W>) + sizeof(float) * kFewThreads * decltype(v)::value;
-        static_assert(kSmem <= 48 * 1024);
-        return launch_kernel(embed_grad_few_kernel<decltype(in)::value, decltype(out)::value,
-                                                   decltype(v)::value, W>,
-                             ctas, dim3(kFewThreads), kSmem, s, a, size, shift,
-                             static_cast<int>(blocks), static_cast<int>(sums), rows);
+        constexpr int kSmem = static_cast<int>(
+            sizeof(FewShared<W>) + sizeof(Sum<decltype(v)::value>) * kFewThreads);
+        static_assert(sizeof(FewShared<W>) % 8 == 0);
+        static std::atomic<uint64_t> done{0};
+        auto kern = embed_grad_few_kernel<decltype(in)::value, decltype(out)::value,
+                                          decltype(v)::value, W>;
+        if (kSmem > 48 * 1024) {
+          const cudaError_t e = allow(kern, kSmem, &done);
+          if (e != cudaSuccess) return e;
+        }
+        return launch_kernel(kern, ctas, dim3(kFewThreads), kSmem, s, a, shift, passes,
+                             (bits + passes - 1) / passes, static_cast<int>(blocks),
+                             static_cast<int>(sums), rows);
       };
       return key_bits(a.vocab) + shift <= 32 ? go(uint32_t{}) : go(uint64_t{});
     });
@@ -630,8 +605,10 @@ cudaError_t launch_embed_grad(int type, int out_type, const EmbedGradArgs& a, in
   const int64_t sum_ctas = cdiv(static_cast<int64_t>(p.chunks) * p.blocks, kGradWarps);
   p.rows_per_zero =
       std::min<int64_t>(kZeroMostRows, std::max<int64_t>(1, 131072 / (a.width * out_es)));
-  const dim3 ctas(static_cast<unsigned>(sum_ctas + zero_ctas(a, p.rows_per_zero)));
-  return by_types(type, out_type, vec, [&](auto in, auto out, auto v) {
+  const dim3 ctas(static_cast<unsigned>(
+      sum_ctas +
+      (a.mode == kEmbedTable ? cdiv(a.vocab, p.rows_per_zero) : 0)));
+  return by_types<32>(type, out_type, vec, [&](auto in, auto out, auto v) {
     return launch_kernel(
         embed_grad_kernel<decltype(in)::value, decltype(out)::value, decltype(v)::value>, ctas,
         dim3(kGradThreads), 0, s, a, p, sum_ctas);

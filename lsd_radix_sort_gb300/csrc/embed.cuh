@@ -14,8 +14,8 @@
 
 namespace lsdrs {
 
-// VEC consecutive elements of a row in one access (16 bytes at most per
-// instruction): as floats, and rounded back.
+// VEC consecutive elements of a row in one access of up to 32 bytes (a 16-bit
+// row's 32-bit gradient in two): as floats, and rounded back.
 template <int TYPE, int VEC>
 struct Pack {
   using Raw = typename Score<TYPE>::Raw;
@@ -25,7 +25,14 @@ struct Pack {
 
   __device__ __forceinline__ static Pack load(const Raw* p) {
     Pack r;
-    if constexpr (kBytes >= 16) {
+    if constexpr (kBytes >= 32) {
+#pragma unroll
+      for (int i = 0; i < kWords; i += 8)
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(r.w[i]), "=r"(r.w[i + 1]), "=r"(r.w[i + 2]), "=r"(r.w[i + 3]),
+                       "=r"(r.w[i + 4]), "=r"(r.w[i + 5]), "=r"(r.w[i + 6]), "=r"(r.w[i + 7])
+                     : "l"(__cvta_generic_to_global(reinterpret_cast<const uint32_t*>(p) + i)));
+    } else if constexpr (kBytes == 16) {
 #pragma unroll
       for (int i = 0; i < kWords; i += 4) {
         const uint4 v = reinterpret_cast<const uint4*>(p)[i / 4];
@@ -46,7 +53,15 @@ struct Pack {
     return r;
   }
   __device__ __forceinline__ void store(Raw* p) const {
-    if constexpr (kBytes >= 16) {
+    if constexpr (kBytes >= 32) {
+#pragma unroll
+      for (int i = 0; i < kWords; i += 8)
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                         __cvta_generic_to_global(reinterpret_cast<uint32_t*>(p) + i)),
+                     "r"(w[i]), "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]), "r"(w[i + 4]),
+                     "r"(w[i + 5]), "r"(w[i + 6]), "r"(w[i + 7])
+                     : "memory");
+    } else if constexpr (kBytes == 16) {
 #pragma unroll
       for (int i = 0; i < kWords; i += 4)
         reinterpret_cast<uint4*>(p)[i / 4] = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
@@ -91,7 +106,7 @@ struct Pack {
 // One vector per thread and step, four steps at once, over all of the output
 // in its order: an id, its row's vector, a store.
 constexpr int kEmbedThreads = 256;
-constexpr int kEmbedBatch = 4;
+constexpr int kEmbedBatch = 2;
 
 template <int TYPE, int VEC>
 __global__ void __launch_bounds__(kEmbedThreads)
@@ -142,33 +157,71 @@ struct __align__(16) Entry {
 
 constexpr int kGradThreads = 256;
 constexpr int kGradWarps = kGradThreads / kWarp;
-constexpr int kGradBatch = 8;   // rows of a warp under way
+// Rows of a warp under way: with many tokens 4 and four CTAs per SM (rows of 32,768
+// x 4,096 bf16 77 us; 8 and three 83), with few, where warps are few too, 8.
+constexpr int kGradBatch = 4;
+constexpr int kFewBatch = 8;
 
-template <int IN, int OUT, int VEC>
+// A thread's sum of VEC columns, two to a register pair.
+template <int VEC>
+struct Sum {
+  static constexpr int kPairs = (VEC + 1) / 2;
+  uint64_t v[kPairs];
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) v[i] = 0;
+  }
+  template <int TYPE>
+  __device__ __forceinline__ void add(const Pack<TYPE, VEC>& p) {
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+      if constexpr (VEC == 1)
+        v[i] = add2(v[i], pack2(p.get(0), 0.0f));
+      else if constexpr (TYPE == RS_SCORE_F32)
+        v[i] = add2(v[i], pack2(__uint_as_float(p.w[2 * i]), __uint_as_float(p.w[2 * i + 1])));
+      else
+        v[i] = add2(v[i], ScoreVec<TYPE>::pair(p.w[i]));
+    }
+  }
+  __device__ __forceinline__ void add(const Sum& s) {
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) v[i] = add2(v[i], s.v[i]);
+  }
+};
+
+template <int OUT, int VEC>
 __device__ __forceinline__ void store_sum(const EmbedGradArgs& a, uint32_t row, int64_t col,
-                                          const float (&sum)[VEC]) {
+                                          const Sum<VEC>& sum) {
   using O = Pack<OUT, VEC>;
   typename O::Raw* to = static_cast<typename O::Raw*>(a.out) + row * a.out_stride + col;
-  float v[VEC];
+  float v[2 * Sum<VEC>::kPairs], w[VEC];
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) v[i] = sum[i] * a.scale;
+  for (int i = 0; i < Sum<VEC>::kPairs; ++i)
+    unpack2(mul2(sum.v[i], pack2(a.scale, a.scale)), v[2 * i], v[2 * i + 1]);
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) w[i] = v[i];
   if (a.mode == kEmbedAdd) {
     const O was = O::load(to);
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) v[i] += was.get(i);
+    for (int i = 0; i < VEC; ++i) w[i] += was.get(i);
   }
-  O::of(v).store(to);
+  O::of(w).store(to);
 }
 
 // ---- many tokens: the list in memory
-// Work is dealt out in chunks of kChunk sorted tokens, a warp for each 32
-// vectors of columns.  A warp adds up the runs that begin in its chunk, to
-// their ends.  Runs of more than kPiece tokens are divided into such pieces,
-// whose sums, in 32 bits, meet in scratch: whoever finishes a run's last
-// piece adds them up, in their order.
-constexpr int kChunk = 32;
-constexpr int kPiece = 64;
-static_assert(kPiece >= kChunk, "a chunk holds the beginnings of two pieces at most");
+// Work is dealt out in chunks of 8 to 32 sorted tokens (few where there would
+// be too few warps), a warp for each 32 vectors of columns.  A warp adds up the
+// runs that begin in its chunk, to their ends.  Runs of more than kPiece tokens
+// are divided into such pieces, whose sums, in 32 bits, meet in scratch: of
+// each 16 neighbours whoever finishes last adds them up, in their order, and
+// brings the result to its 16 neighbours.  So a run of any length takes few
+// steps one after another (of 32 tokens each; with pieces of 64 that one warp
+// added up, the most frequent of 8,191 tokens alone took 30 us).
+constexpr int kMostChunk = 32, kLeastChunk = 8;
+constexpr int kPiece = 32;
+static_assert(kPiece >= kMostChunk, "a chunk holds the beginnings of two pieces at most");
+constexpr int kFan = 16;
 
 constexpr int kRunsCount = 0, kRunsLive = 1, kRunsFailed = 2;  // words of the header
 struct GradPlan {
@@ -176,60 +229,84 @@ struct GradPlan {
   Entry* list;
   uint32_t* key;         // the id of each run
   float* partial;        // [2 * chunks][padded width]: later pieces, first pieces
-  uint32_t* arrived;     // [chunks][blocks]: pieces of the run that begins there
-  int chunks, blocks;
+  uint32_t* arrived;     // [2 * chunks][blocks]: neighbours of the piece there
+  int chunk, chunks, blocks;
   int64_t rows_per_zero;
   // where the list is made by the sort of whole keys
   const uint32_t* sort_error;
   uint32_t *keys, *vals, *sorted_keys, *sorted_vals, *slot, *start, *tile_heads;
 };
 
+// Brings the sum of a piece to the others of its run.  True for whoever comes
+// last of all: `sum` is then that of the run.  A group of neighbours has its
+// sum where the first of them had its own, and its counter, at step n, at the
+// n-th of them (there are that many wherever a step n is needed).
 template <int VEC>
-struct Sum {
-  float v[VEC];
-};
-
-// The sum of a piece; the last of its run's to arrive gets the whole sum, in
-// `sum`, and true.
-template <int VEC>
-__device__ __noinline__ bool join_pieces(const GradPlan& p, int block, uint32_t start,
+__device__ __forceinline__ bool join_pieces(const GradPlan& p, int block, uint32_t start,
                                          uint32_t end, uint32_t at, Sum<VEC>* sum) {
+  using S = Sum<VEC>;
   const int lane = static_cast<int>(lane_id());
-  const int64_t padded = static_cast<int64_t>(p.blocks) * kWarp * VEC;
-  const int64_t col = (static_cast<int64_t>(block) * kWarp + lane) * VEC;
-  const uint32_t pieces = (end - start + kPiece - 1) / kPiece, number = (at - start) / kPiece;
-  auto place = [&](uint32_t n) {
-    return p.partial + (2 * static_cast<int64_t>((start + n * kPiece) / kChunk) + (n == 0)) * padded +
-           col;
+  auto place = [&](uint32_t piece) {  // of later pieces, and of first ones
+    return 2 * static_cast<int64_t>((start + piece * kPiece) / p.chunk) + (piece == 0);
   };
+  // 32 * VEC floats: a lane's next pair is 32 pairs on (VEC = 1: one float)
+  auto sums = [&](uint32_t piece) {
+    return p.partial + (place(piece) * p.blocks + block) * (kWarp * VEC) + lane * min(VEC, 2);
+  };
+  auto put = [&](uint32_t piece, const S& v) {
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) __stcg(place(number) + i, sum->v[i]);
-  __threadfence();
-  __syncwarp();
-  uint32_t before = 0;
-  if (lane == 0)
-    before = atomicAdd(&p.arrived[static_cast<int64_t>(start / kChunk) * p.blocks + block], 1u);
-  if (__shfl_sync(kFull, before, 0) != pieces - 1) return false;
-  __threadfence();
-  Sum<VEC> all;
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) all.v[i] = 0.0f;
-  constexpr int kAhead = VEC >= 8 ? 4 : 8;
-  for (uint32_t n0 = 0; n0 < pieces; n0 += kAhead) {
-    float v[kAhead][VEC];
-#pragma unroll
-    for (int n = 0; n < kAhead; ++n) {
-      const float* from = place(min(n0 + n, pieces - 1));
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) v[n][i] = __ldcg(from + i);
+    for (int i = 0; i < S::kPairs; ++i) {
+      float x, y;
+      unpack2(v.v[i], x, y);
+      if constexpr (VEC == 1)
+        __stcg(sums(piece), x);
+      else
+        __stcg(reinterpret_cast<float2*>(sums(piece)) + i * kWarp, make_float2(x, y));
     }
+  };
+  auto get = [&](uint32_t piece) {
+    S v;
 #pragma unroll
-    for (int n = 0; n < kAhead; ++n)
-      if (n0 + n < pieces)
+    for (int i = 0; i < S::kPairs; ++i) {
+      if constexpr (VEC == 1) {
+        v.v[i] = pack2(__ldcg(sums(piece)), 0.0f);
+      } else {
+        const float2 f = __ldcg(reinterpret_cast<const float2*>(sums(piece)) + i * kWarp);
+        v.v[i] = pack2(f.x, f.y);
+      }
+    }
+    return v;
+  };
+  uint32_t units = (end - start + kPiece - 1) / kPiece, unit = (at - start) / kPiece;
+  uint32_t pieces = 1;  // of a unit
+  S mine = *sum;
+  for (uint32_t step = 0; units > 1; ++step) {
+    const uint32_t first = unit / kFan * kFan, n = min(units - first, uint32_t(kFan));
+    if (n > 1) {
+      put(unit * pieces, mine);
+      __threadfence();
+      __syncwarp();
+      uint32_t before = 0;
+      if (lane == 0)
+        before = atomicAdd(&p.arrived[place(first * pieces + step) * p.blocks + block], 1u);
+      if (__shfl_sync(kFull, before, 0) != n - 1) return false;
+      __threadfence();
+      mine.clear();
+      constexpr int kAhead = VEC >= 16 ? 2 : VEC >= 8 ? 4 : 8;
+      for (uint32_t u0 = 0; u0 < n; u0 += kAhead) {
+        S part[kAhead];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) all.v[i] += v[n][i];
+        for (int u = 0; u < kAhead; ++u) part[u] = get((first + min(u0 + u, n - 1)) * pieces);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+          if (u0 + u < n) mine.add(part[u]);
+      }
+    }
+    unit = first / kFan;
+    units = (units + kFan - 1) / kFan;
+    pieces *= kFan;
   }
-  *sum = all;
+  *sum = mine;
   return true;
 }
 
@@ -243,72 +320,110 @@ __device__ __forceinline__ void sum_chunk(const EmbedGradArgs& a, const GradPlan
   const int64_t col = (static_cast<int64_t>(block) * kWarp + lane) * VEC;
   const bool mine = col < a.width;
   const Raw* from = static_cast<const Raw*>(a.grad) + (mine ? col : 0);
-  float sum[VEC];
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) sum[i] = 0.0f;
-  bool open = false;  // a piece is under way
-  for (uint32_t window = chunk * kChunk; window < live; window += kChunk) {
-    const uint32_t at = window + lane;
-    Entry e{0, 0, 0, 0};
-    if (at < live) e = p.list[at];
-    const unsigned begins = __ballot_sync(kFull, at < live && (at - e.start) % kPiece == 0);
-    const unsigned ends = __ballot_sync(
-        kFull, at < live && (at + 1 == e.end || (at + 1 - e.start) % kPiece == 0));
-    int t = 0, last;  // tokens [t, last) of the window are this warp's
-    if (open) {       // what began before, to its end
-      last = ends != 0 ? __ffs(static_cast<int>(ends)) : kWarp;
-    } else {
-      if (begins == 0) return;
-      t = __ffs(static_cast<int>(begins)) - 1;
-      last = static_cast<int>(min(static_cast<uint32_t>(kWarp), live - window));
-    }
+  const uint32_t begin = static_cast<uint32_t>(chunk) * p.chunk;
+  const Entry none{0, 0, 0, 0};
+  Entry e = begin + lane < live ? p.list[begin + lane] : none;
+  // where a short run of the chunk may go on
+  const Entry next = begin + kWarp + lane < live ? p.list[begin + kWarp + lane] : none;
+  const unsigned pieces = __ballot_sync(kFull, lane < p.chunk && begin + lane < live &&
+                                                   e.end - e.start > kPiece &&
+                                                   (begin + lane - e.start) % kPiece == 0);
+  const uint32_t long_start = e.start, long_end = e.end;
+  Sum<VEC> sum;
+  sum.clear();
 #pragma unroll 1
-    for (; t < last; t += kGradBatch) {
+  for (int window = 0; window < 2; ++window) {  // short runs that begin in the chunk
+    const uint32_t at = begin + window * kWarp + lane;
+    if (window == 1) e = next;
+    const bool ours = at < live && e.end - e.start <= kPiece && e.start >= begin &&
+                      e.start < begin + p.chunk;
+    const unsigned ends = __ballot_sync(kFull, at + 1 == e.end);
+    unsigned todo = __ballot_sync(kFull, ours);
+    while (todo != 0) {
       P r[kGradBatch];
+      unsigned left = todo;
 #pragma unroll
       for (int u = 0; u < kGradBatch; ++u) {
-        const uint32_t pos = __shfl_sync(kFull, e.pos, min(t + u, kWarp - 1));
-        r[u] = mine && t + u < last ? P::load(from + pos * a.grad_stride) : P::zero();
+        const uint32_t pos = __shfl_sync(kFull, e.pos, __ffs(static_cast<int>(left)) - 1);
+        r[u] = mine && left != 0 ? P::load(from + pos * a.grad_stride) : P::zero();
+        left &= left - 1;
       }
 #pragma unroll
       for (int u = 0; u < kGradBatch; ++u) {
-        if (t + u < last) {
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) sum[i] += r[u].get(i);
-          if ((ends >> (t + u) & 1) != 0) {  // the end of a run, or of a piece of one
-            const uint32_t b = __shfl_sync(kFull, e.start, t + u);
-            const uint32_t n = __shfl_sync(kFull, e.end, t + u) - b;
-            const uint32_t row = __shfl_sync(kFull, e.row, t + u);
-            bool whole = true;
-            if (n > kPiece) {
-              Sum<VEC> s;
-#pragma unroll
-              for (int i = 0; i < VEC; ++i) s.v[i] = sum[i];
-              whole = join_pieces<VEC>(p, block, b, b + n, window + t + u, &s);
-#pragma unroll
-              for (int i = 0; i < VEC; ++i) sum[i] = s.v[i];
-            }
-            if (whole && mine) store_sum<IN, OUT, VEC>(a, row, col, sum);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) sum[i] = 0.0f;
+        if (todo != 0) {
+          const int t = __ffs(static_cast<int>(todo)) - 1;
+          todo &= todo - 1;
+          sum.add(r[u]);
+          if ((ends >> t & 1) != 0) {
+            const uint32_t row = __shfl_sync(kFull, e.row, t);
+            if (mine) store_sum<OUT, VEC>(a, row, col, sum);
+            sum.clear();
           }
         }
       }
     }
-    open = last == kWarp && (ends >> (kWarp - 1)) == 0;
-    if (!open) return;
+  }
+#pragma unroll 1
+  for (unsigned todo = pieces; todo != 0; todo &= todo - 1) {  // two at most
+    const int t = __ffs(static_cast<int>(todo)) - 1;
+    const uint32_t start = __shfl_sync(kFull, long_start, t);
+    const uint32_t end = __shfl_sync(kFull, long_end, t), first = begin + t;
+    const int n = static_cast<int>(min(end - first, static_cast<uint32_t>(kPiece)));
+    const Entry own = lane < n ? p.list[first + lane] : none;
+    sum.clear();
+    for (int i = 0; i < n; i += kGradBatch) {
+      P r[kGradBatch];
+#pragma unroll
+      for (int u = 0; u < kGradBatch; ++u) {
+        const uint32_t pos = __shfl_sync(kFull, own.pos, (i + u) % kWarp);
+        r[u] = mine && i + u < n ? P::load(from + pos * a.grad_stride) : P::zero();
+      }
+#pragma unroll
+      for (int u = 0; u < kGradBatch; ++u)
+        if (i + u < n) sum.add(r[u]);
+    }
+    const uint32_t row = __shfl_sync(kFull, own.row, 0);
+    if (join_pieces<VEC>(p, block, start, end, first, &sum) && mine)
+      store_sum<OUT, VEC>(a, row, col, sum);
   }
 }
 
-// Zeros (or `fill`) for the rows of the table [first, last) that no run names;
-// key: the ids of the runs, in order, in memory or shared memory.
+// A token's sort key: its id, or the table's length for one without a row.
+__device__ __forceinline__ uint32_t key_of(const EmbedGradArgs& a, int64_t i) {
+  const int64_t id = load_index(a.ids, a.index_bytes, i);
+  return static_cast<uint32_t>(id < 0 || id >= a.vocab || id == a.padding_id ? a.vocab : id);
+}
+
+// Zeros (or `fill`) for the rows of the table [first, last) that are not marked.
+template <int OUT>
+__device__ __forceinline__ void fill_rows(const EmbedGradArgs& a, int64_t first, int64_t last,
+                                          float fill, const uint32_t* named) {
+  using Raw = typename Score<OUT>::Raw;
+  const Raw raw = Score<OUT>::store(fill);
+  const uint32_t word = sizeof(Raw) == 4 ? raw : raw | static_cast<uint32_t>(raw) << 16;
+  const int tid = static_cast<int>(threadIdx.x), lane = static_cast<int>(lane_id());
+  for (int64_t v = first + tid / kWarp; v < last; v += blockDim.x / kWarp) {
+    if (named[(v - first) / 32] >> ((v - first) % 32) & 1) continue;
+    Raw* to = static_cast<Raw*>(a.out) + v * a.out_stride;
+    // 16 bytes at a time where they are aligned
+    const int lead = static_cast<int>((16 - reinterpret_cast<uintptr_t>(to) % 16) % 16 / sizeof(Raw));
+    const int64_t head = min(static_cast<int64_t>(lead), a.width);
+    constexpr int kN = 16 / static_cast<int>(sizeof(Raw));
+    const int64_t vecs = (a.width - head) / kN;
+    if (lane < head) to[lane] = raw;
+    for (int64_t i = lane; i < vecs; i += kWarp)
+      __stcs(reinterpret_cast<uint4*>(to + head) + i, make_uint4(word, word, word, word));
+    const int64_t tail = head + vecs * kN + lane;
+    if (tail < a.width) to[tail] = raw;
+  }
+}
+
+// The same of those that no run names; key: the ids of the runs, in order, in
+// memory or shared memory.
 template <int OUT>
 __device__ __forceinline__ void zero_rows(const EmbedGradArgs& a, const uint32_t* key, int runs,
                                           int64_t first, int64_t last, float fill,
                                           uint32_t* named) {
-  using Raw = typename Score<OUT>::Raw;
-  const Raw raw = Score<OUT>::store(fill);
-  const uint32_t word = sizeof(Raw) == 4 ? raw : raw | static_cast<uint32_t>(raw) << 16;
   const int tid = static_cast<int>(threadIdx.x), lane = static_cast<int>(lane_id());
   const int threads = static_cast<int>(blockDim.x);
   const int words = static_cast<int>((last - first + 31) / 32);
@@ -332,26 +447,13 @@ __device__ __forceinline__ void zero_rows(const EmbedGradArgs& a, const uint32_t
     atomicOr(&named[v / 32], 1u << (v % 32));
   }
   __syncthreads();
-  for (int64_t v = first + tid / kWarp; v < last; v += threads / kWarp) {
-    if (named[(v - first) / 32] >> ((v - first) % 32) & 1) continue;
-    Raw* to = static_cast<Raw*>(a.out) + v * a.out_stride;
-    // 16 bytes at a time where they are aligned
-    const int lead = static_cast<int>((16 - reinterpret_cast<uintptr_t>(to) % 16) % 16 / sizeof(Raw));
-    const int64_t head = min(static_cast<int64_t>(lead), a.width);
-    constexpr int kN = 16 / static_cast<int>(sizeof(Raw));
-    const int64_t vecs = (a.width - head) / kN;
-    if (lane < head) to[lane] = raw;
-    for (int64_t i = lane; i < vecs; i += kWarp)
-      __stcs(reinterpret_cast<uint4*>(to + head) + i, make_uint4(word, word, word, word));
-    const int64_t tail = head + vecs * kN + lane;
-    if (tail < a.width) to[tail] = raw;
-  }
+  fill_rows<OUT>(a, first, last, fill, named);
 }
 
 constexpr int kZeroMostRows = 4096;  // of one CTA
 
 template <int IN, int OUT, int VEC>
-__global__ void __launch_bounds__(kGradThreads, VEC * sizeof(typename Score<IN>::Raw) == 16 ? 3 : 4)
+__global__ void __launch_bounds__(kGradThreads, VEC * sizeof(typename Score<IN>::Raw) == 32 ? 3 : 4)
     embed_grad_kernel(const __grid_constant__ EmbedGradArgs a, const __grid_constant__ GradPlan p,
                       const int64_t sum_ctas) {
   __shared__ uint32_t named[kZeroMostRows / 32];
@@ -377,81 +479,155 @@ __global__ void __launch_bounds__(kGradThreads, VEC * sizeof(typename Score<IN>:
 constexpr int kFewTokens = 2048;
 constexpr int kFewThreads = 512;
 constexpr int kFewWarps = kFewThreads / kWarp;
-constexpr int kLongRun = 64;
+constexpr int kLongRun = 16;
 
-// A token's sort key: its id, or the table's length for one without a row.
-__device__ __forceinline__ uint32_t key_of(const EmbedGradArgs& a, int64_t i) {
-  const int64_t id = load_index(a.ids, a.index_bytes, i);
-  return static_cast<uint32_t>(id < 0 || id >= a.vocab || id == a.padding_id ? a.vocab : id);
+// Ranks of a warp's 32 * ITEMS words by a digit, in their order: a word's place
+// among the warp's of its digit, and how many each digit has.
+constexpr int kMaxRadix = 512;
+template <int ITEMS, class W>
+__device__ __forceinline__ void rank_words(const W (&w)[ITEMS], int shift, int bits,
+                                           uint16_t* counts, uint32_t (&place)[ITEMS]) {
+  const uint32_t radix = 1u << bits;
+  for (uint32_t i = lane_id(); i < radix / 8 + 1 && i < kMaxRadix / 8; i += kWarp)
+    reinterpret_cast<uint4*>(counts)[i] = make_uint4(0, 0, 0, 0);
+  __syncwarp();
+#pragma unroll
+  for (int u = 0; u < ITEMS; ++u) {
+    const uint32_t d = static_cast<uint32_t>(w[u] >> shift) & (radix - 1);
+    unsigned same = kFull;
+    for (int b = 0; b < bits; ++b) {
+      const unsigned set = __ballot_sync(kFull, d >> b & 1);
+      same &= (d >> b & 1) != 0 ? set : ~set;
+    }
+    const unsigned before = same & lanemask_lt();
+    const uint32_t was = counts[d];
+    __syncwarp();
+    place[u] = was + __popc(before);
+    if (before == 0) counts[d] = static_cast<uint16_t>(was + __popc(same));
+    __syncwarp();
+  }
+}
+
+// A digit's counts by warp become those of the warps before; returns their sum.
+template <int WARPS>
+__device__ __forceinline__ uint32_t sum_warps(uint16_t (*counts)[kMaxRadix], uint32_t digit) {
+  uint32_t n[WARPS], total = 0;
+#pragma unroll
+  for (int i = 0; i < WARPS; ++i) n[i] = counts[i][digit];
+#pragma unroll
+  for (int i = 0; i < WARPS; ++i) {
+    counts[i][digit] = static_cast<uint16_t>(total);
+    total += n[i];
+  }
+  return total;
+}
+
+// Sums of v over the threads before this one; all: over all of them.
+template <int WARPS>
+__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* part, uint32_t* all) {
+  const uint32_t lane = lane_id(), warp = threadIdx.x / kWarp;
+  uint32_t upto = v;
+#pragma unroll
+  for (int o = 1; o < kWarp; o *= 2) {
+    const uint32_t n = __shfl_up_sync(kFull, upto, o);
+    if (lane >= static_cast<uint32_t>(o)) upto += n;
+  }
+  __syncthreads();  // (what was there before has been read)
+  if (lane == kWarp - 1) part[warp] = upto;
+  __syncthreads();
+  const uint32_t n = lane < WARPS ? part[lane] : 0;
+  *all = __reduce_add_sync(kFull, n);
+  return __reduce_add_sync(kFull, lane < warp ? n : 0) + upto - v;
 }
 
 // W: words that hold an id and a place (shift bits), 32 or 64 bits.
 template <class W>
 struct FewShared {
+  uint16_t counts[kFewWarps][kMaxRadix];
   W word[kFewTokens];
+  uint32_t base[kMaxRadix];
   uint32_t key[kFewTokens];        // of each run
-  uint16_t start[kFewTokens + 1];
-  uint32_t part[kFewWarps];
+  uint16_t start[kFewTokens + 8];
+  uint16_t long_run[kFewTokens / kLongRun];
+  uint32_t part[kWarp];
   uint32_t named[kZeroMostRows / 32];
 };
 
+// The tokens in order of their ids, ITEMS per thread.
+template <int ITEMS, class W>
+__device__ __forceinline__ void sort_few(const EmbedGradArgs& a, FewShared<W>& sh, int shift,
+                                         int passes, int bits) {
+  const int tid = static_cast<int>(threadIdx.x), warp = tid / kWarp;
+  const int first = warp * kWarp * ITEMS + static_cast<int>(lane_id());
+  W w[ITEMS];
+#pragma unroll
+  for (int u = 0; u < ITEMS; ++u) {
+    const int i = first + u * kWarp;
+    w[u] = i < a.tokens ? static_cast<W>(key_of(a, i)) << shift | static_cast<W>(i)
+                        : ~static_cast<W>(0);
+  }
+  for (int pass = 0; pass < passes; ++pass) {
+    const int at = shift + pass * bits;
+    uint32_t place[ITEMS], all;
+    rank_words<ITEMS>(w, at, bits, sh.counts[warp], place);
+    __syncthreads();
+    const bool digit = tid < 1 << bits;
+    const uint32_t total = digit ? sum_warps<kFewWarps>(sh.counts, tid) : 0;
+    const uint32_t smaller = block_scan<kFewWarps>(total, sh.part, &all);
+    if (digit) sh.base[tid] = smaller;
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < ITEMS; ++u) {
+      const uint32_t d = static_cast<uint32_t>(w[u] >> at) & ((1u << bits) - 1);
+      sh.word[sh.base[d] + sh.counts[warp][d] + place[u]] = w[u];
+    }
+    __syncthreads();
+    if (pass + 1 < passes) {
+#pragma unroll
+      for (int u = 0; u < ITEMS; ++u) w[u] = sh.word[first + u * kWarp];
+    }
+  }
+}
+
 // The sum of rows [from, to) of the list.
 template <int IN, int VEC, class W>
-__device__ __forceinline__ void sum_rows(const EmbedGradArgs& a, const W* word, W places, int from,
-                                         int to, int64_t col, float (&sum)[VEC]) {
+__device__ __forceinline__ Sum<VEC> sum_rows(const EmbedGradArgs& a, const W* word, W places,
+                                             int from, int to, int64_t col) {
   using P = Pack<IN, VEC>;
   const auto* up = static_cast<const typename P::Raw*>(a.grad) + col;
+  Sum<VEC> sum;
+  sum.clear();
+  for (int t = from; t < to; t += kFewBatch) {
+    P r[kFewBatch];
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) sum[i] = 0.0f;
-  for (int t = from; t < to; t += kGradBatch) {
-    P r[kGradBatch];
-#pragma unroll
-    for (int u = 0; u < kGradBatch; ++u)
+    for (int u = 0; u < kFewBatch; ++u)
       r[u] = t + u < to ? P::load(up + static_cast<int64_t>(word[t + u] & places) * a.grad_stride)
                         : P::zero();
 #pragma unroll
-    for (int u = 0; u < kGradBatch; ++u)
-      if (t + u < to)
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) sum[i] += r[u].get(i);
+    for (int u = 0; u < kFewBatch; ++u)
+      if (t + u < to) sum.add(r[u]);
   }
+  return sum;
 }
 
 template <int IN, int OUT, int VEC, class W>
 __global__ void __launch_bounds__(kFewThreads)
-    embed_grad_few_kernel(const __grid_constant__ EmbedGradArgs a, const int size, const int shift,
-                          const int blocks, const int sum_ctas, const int64_t rows_per_zero) {
+    embed_grad_few_kernel(const __grid_constant__ EmbedGradArgs a, const int shift,
+                          const int passes, const int bits, const int blocks, const int sum_ctas,
+                          const int64_t rows_per_zero) {
   extern __shared__ __align__(16) unsigned char smem[];
   FewShared<W>& sh = *reinterpret_cast<FewShared<W>*>(smem);
   const int tid = static_cast<int>(threadIdx.x), warp = tid / kWarp;
   const int lane = static_cast<int>(lane_id());
   grid_dependency_sync();
-  // the list: words in ascending order, `size` of them, a power of two
-  const int tokens = static_cast<int>(a.tokens);
-  for (int i = tid; i < size; i += kFewThreads)
-    sh.word[i] = i < tokens ? static_cast<W>(key_of(a, i)) << shift | static_cast<W>(i)
-                            : ~static_cast<W>(0);
-  __syncthreads();
-  for (int run = 2; run <= size; run *= 2)
-    for (int step = run / 2; step > 0; step /= 2) {
-      for (int q = tid; q < size / 2; q += kFewThreads) {
-        const int i = (q & ~(step - 1)) * 2 + (q & (step - 1)), j = i + step;
-        const W x = sh.word[i], y = sh.word[j];
-        if ((x > y) == ((i & run) == 0)) {
-          sh.word[i] = y;
-          sh.word[j] = x;
-        }
-      }
-      // 64 neighbouring words are one warp's as long as steps stay inside
-      if (step > kWarp || (step == 1 && run >= 2 * kWarp))
-        __syncthreads();
-      else
-        __syncwarp();
-    }
-  __syncthreads();
-  // its runs: the places where a live id differs from the one before
   constexpr int kEach = kFewTokens / kFewThreads;
-  const int each = size > kFewThreads ? kEach : 1, base = tid * each;
+  const int tokens = static_cast<int>(a.tokens);
+  const int each = tokens > kFewThreads ? kEach : 1, base = tid * each;
+  if (each == 1)
+    sort_few<1>(a, sh, shift, passes, bits);
+  else
+    sort_few<kEach>(a, sh, shift, passes, bits);
+  // its runs: the places where a live id differs from the one before
   uint32_t heads = 0, live = 0;
 #pragma unroll
   for (int u = 0; u < kEach; ++u) {
@@ -462,20 +638,11 @@ __global__ void __launch_bounds__(kFewThreads)
     ++live;
     if (i == 0 || sh.word[i - 1] >> shift != key) heads |= 1u << u;
   }
-  const uint32_t mine = static_cast<uint32_t>(__popc(heads)) << 16 | live;  // both at once
-  uint32_t upto = mine;
-#pragma unroll
-  for (int o = 1; o < kWarp; o *= 2) {
-    const uint32_t n = __shfl_up_sync(kFull, upto, o);
-    if (lane >= o) upto += n;
-  }
-  if (lane == kWarp - 1) sh.part[warp] = upto;
-  __syncthreads();
-  uint32_t before = lane < kFewWarps ? sh.part[lane] : 0, all = before;
-  before = __reduce_add_sync(kFull, lane < warp ? before : 0);
-  all = __reduce_add_sync(kFull, all);
+  uint32_t all;  // runs and tokens at once
+  int run = static_cast<int>(
+      block_scan<kFewWarps>(static_cast<uint32_t>(__popc(heads)) << 16 | live, sh.part, &all) >>
+      16);
   const int runs = static_cast<int>(all >> 16);
-  int run = static_cast<int>((before + upto - mine) >> 16);
 #pragma unroll
   for (int u = 0; u < kEach; ++u) {
     if ((heads >> u & 1) == 0) continue;
@@ -500,36 +667,48 @@ __global__ void __launch_bounds__(kFewThreads)
   const W places = (static_cast<W>(1) << shift) - 1;
   const int items = runs * blocks;
   auto row_of = [&](int r) { return a.mode == kEmbedRows ? static_cast<uint32_t>(r) : sh.key[r]; };
-  for (int w = cta * kFewWarps + warp; w < items; w += sum_ctas * kFewWarps) {
-    const int r = w / blocks, from = sh.start[r], to = sh.start[r + 1];
-    const int64_t col = (static_cast<int64_t>(w - r * blocks) * kWarp + lane) * VEC;
-    if (to - from > kLongRun || col >= a.width) continue;
-    float sum[VEC];
-    sum_rows<IN, VEC, W>(a, sh.word, places, from, to, col, sum);
-    store_sum<IN, OUT, VEC>(a, row_of(r), col, sum);
-  }
-  // long runs, in as many parts as warps, joined in their order
-  float* parts = reinterpret_cast<float*>(smem + sizeof(FewShared<W>));
-  for (int w = cta; w < items; w += sum_ctas) {
-    const int r = w / blocks, from = sh.start[r], to = sh.start[r + 1];
-    if (to - from <= kLongRun) continue;
-    const int64_t col = (static_cast<int64_t>(w - r * blocks) * kWarp + lane) * VEC;
-    const int per = (to - from + kFewWarps - 1) / kFewWarps;
-    float sum[VEC];
-    if (col < a.width) {
-      sum_rows<IN, VEC, W>(a, sh.word, places, min(from + warp * per, to),
-                           min(from + (warp + 1) * per, to), col, sum);
+  // long runs, in as many parts as warps, joined in their order; every CTA lists
+  // them in the same order
+  uint32_t longs = 0;
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) parts[(warp * VEC + i) * kWarp + lane] = sum[i];
+  for (int u = 0; u < kEach; ++u)
+    if (u < each && base + u < runs && sh.start[base + u + 1] - sh.start[base + u] > kLongRun)
+      longs |= 1u << u;
+  uint32_t long_runs;
+  uint32_t nth = block_scan<kFewWarps>(static_cast<uint32_t>(__popc(longs)), sh.part, &long_runs);
+#pragma unroll
+  for (int u = 0; u < kEach; ++u)
+    if ((longs >> u & 1) != 0) sh.long_run[nth++] = static_cast<uint16_t>(base + u);
+  __syncthreads();
+  uint64_t* parts = reinterpret_cast<uint64_t*>(smem + sizeof(FewShared<W>));
+  for (int w = cta; w < static_cast<int>(long_runs) * blocks; w += sum_ctas) {
+    const int n = w / blocks, r = sh.long_run[n], from = sh.start[r], to = sh.start[r + 1];
+    const int64_t col = (static_cast<int64_t>(w - n * blocks) * kWarp + lane) * VEC;
+    const int per = (to - from + kFewWarps - 1) / kFewWarps;
+    Sum<VEC> sum;
+    if (col < a.width) {
+      sum = sum_rows<IN, VEC, W>(a, sh.word, places, min(from + warp * per, to),
+                                 min(from + (warp + 1) * per, to), col);
+#pragma unroll
+      for (int i = 0; i < Sum<VEC>::kPairs; ++i)
+        parts[(warp * Sum<VEC>::kPairs + i) * kWarp + lane] = sum.v[i];
     }
     __syncthreads();
     if (warp == 0 && col < a.width) {
       for (int n = 1; n < kFewWarps; ++n)
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) sum[i] += parts[(n * VEC + i) * kWarp + lane];
-      store_sum<IN, OUT, VEC>(a, row_of(r), col, sum);
+        for (int i = 0; i < Sum<VEC>::kPairs; ++i)
+          sum.v[i] = add2(sum.v[i], parts[(n * Sum<VEC>::kPairs + i) * kWarp + lane]);
+      store_sum<OUT, VEC>(a, row_of(r), col, sum);
     }
     __syncthreads();
+  }
+  for (int w = cta * kFewWarps + warp; w < items; w += sum_ctas * kFewWarps) {
+    const int r = w / blocks, from = sh.start[r], to = sh.start[r + 1];
+    const int64_t col = (static_cast<int64_t>(w - r * blocks) * kWarp + lane) * VEC;
+    if (to - from > kLongRun || col >= a.width) continue;
+    store_sum<OUT, VEC>(a, row_of(r), col,
+                        sum_rows<IN, VEC, W>(a, sh.word, places, from, to, col));
   }
 }
 

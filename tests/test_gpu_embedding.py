@@ -135,6 +135,18 @@ def test_gradient_of_one_id(rs, n):
     check_grad(rs, up, mixed, 90)
 
 
+@pytest.mark.parametrize("n", [1000, 2048, 5000, 20000])
+@pytest.mark.parametrize("ids_named", [3, 20, 60, 100])
+def test_gradient_of_many_long_runs(rs, n, ids_named):
+    """Runs of more than a warp's tokens in wide rows: each run's columns are
+    shared by many warps, which have to agree on who adds up what."""
+    g = gen(n + ids_named)
+    ids = torch.randperm(5000, generator=g, device="cuda")[:ids_named][ids_of(g, n, ids_named, "all")]
+    check_grad(rs, randn(g, n, 2056, dtype=torch.bfloat16), ids, 5000, dtype=torch.float32)
+    check_grad(rs, randn(g, n, 515), ids, 5000)
+    check_grad(rs, randn(g, n, 3001, dtype=torch.float16), ids, 5000)  # element by element
+
+
 @pytest.mark.parametrize("n", [700, 6000])
 def test_gradient_of_dropped_and_padded_tokens(rs, n):
     g = gen(3)
@@ -173,6 +185,17 @@ def test_gradient_strides_shapes_and_alignments(rs, dtype, n):
         rs.embedding_grad(up, ids, 200, grad_out=out[:, 2:2 + width])
         assert torch.equal(out[:, 2:2 + width], table)
         assert (out[:, :2] == 9).all() and (out[:, 2 + width:] == 9).all()
+    # outputs that begin 16 bytes into a line, of either type
+    up = randn(g, n, 64, dtype=dtype)
+    for out_type in {dtype, torch.float32}:
+        first = 16 // torch.empty(0, dtype=out_type).element_size()
+        buf = torch.full((200 * 64 + 2 * first,), 9.0, dtype=out_type, device="cuda")
+        out = buf[first:first + 200 * 64].view(200, 64)
+        rs.embedding_grad(up, ids, 200, grad_out=out)
+        assert torch.equal(out, rs.embedding_grad(up, ids, 200, dtype=out_type))
+        assert (buf[:first] == 9).all() and (buf[first + 200 * 64:] == 9).all()
+        table = buf[first:first + 200 * 64].view(200, 64)
+        assert torch.equal(rs.embedding(table, ids, 2.0), lookup(table, ids, 2.0))
     up = randn(g, 4, n // 4, 16, dtype=dtype)
     check_grad(rs, up, ids[:4 * (n // 4)].reshape(4, n // 4), 200)
 
