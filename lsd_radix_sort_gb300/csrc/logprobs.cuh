@@ -954,10 +954,11 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas)
 // as they take, each at its share of the measured bandwidth, batch by batch,
 // and what a segment's end costs.
 template <int TYPE>
-LpPlan logprobs_plan(int64_t rows, int64_t cols, int top) {
+LpPlan make_logprobs_plan(int64_t rows, int64_t cols, int top, bool aligned, int64_t sms) {
   constexpr int kN = ScoreVec<TYPE>::kCount;
-  const int64_t warps = int64_t(device_sm_count()) * kLpCtas * (kLpBlock / kWarp);
-  const int64_t vecs = (cols + 2 * (kN - 1)) / kN;  // however the rows begin
+  const int64_t warps = sms * kLpCtas * (kLpBlock / kWarp);
+  // (rows that begin anywhere may have parts of one more)
+  const int64_t vecs = (cols + (aligned ? 1 : 2) * (kN - 1)) / kN;
   LpPlan p{1, 0, 0, kWarp, false, 0};
   const double ns_per_batch = 16.0 * kLpStep * static_cast<double>(warps) / 6791.0;
   double best = 1e300;
@@ -990,15 +991,39 @@ LpPlan logprobs_plan(int64_t rows, int64_t cols, int top) {
   return p;
 }
 
+// The same as the last of this thread, where the sizes are (the search takes a
+// microsecond or two, as much as a launch).
+template <int TYPE>
+LpPlan logprobs_plan(int64_t rows, int64_t cols, int top, bool aligned) {
+  struct Last {
+    int64_t rows, cols, sms;
+    int top;
+    LpPlan plan;
+  };
+  static thread_local Last last[2] = {{-1, 0, 0, 0, {}}, {-1, 0, 0, 0, {}}};
+  const int64_t sms = device_sm_count();
+  Last& l = last[aligned];
+  if (l.rows != rows || l.cols != cols || l.top != top || l.sms != sms)
+    l = Last{rows, cols, sms, top, make_logprobs_plan<TYPE>(rows, cols, top, aligned, sms)};
+  return l.plan;
+}
+
 template <int TYPE>
 size_t logprobs_temp(int64_t rows, int64_t cols, int top) {
-  const LpPlan p = logprobs_plan<TYPE>(rows, cols, top);
-  return stats_bytes(rows, p) + (top == 0 ? 0 : static_cast<size_t>(rows) * p.groups() * 2);
+  size_t most = 0;  // however the rows begin
+  for (const bool aligned : {false, true}) {
+    const LpPlan p = logprobs_plan<TYPE>(rows, cols, top, aligned);
+    most = std::max(most, stats_bytes(rows, p) +
+                              (top == 0 ? 0 : static_cast<size_t>(rows) * p.groups() * 2));
+  }
+  return most;
 }
 
 template <int TYPE>
 cudaError_t launch_logprobs_as(const LogprobArgs& a, int* launched, cudaStream_t s) {
-  const LpPlan p = logprobs_plan<TYPE>(a.rows, a.cols, a.top);
+  const bool aligned = reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 &&
+                       (a.rows == 1 || a.stride % ScoreVec<TYPE>::kCount == 0);
+  const LpPlan p = logprobs_plan<TYPE>(a.rows, a.cols, a.top, aligned);
   constexpr int kEach = kLpBlock / kWarp;
   const uint32_t items = static_cast<uint32_t>(a.rows * p.split);
   const uint32_t ctas = std::min<uint32_t>((items + kEach - 1) / kEach,
