@@ -1,6 +1,10 @@
-"""Sorts and losses together: a small mixture-of-experts student.
+"""Sorts, losses and a vocabulary's two ends together: a small mixture-of-experts
+student.
 
     python examples/train_step.py [--steps N]
+
+The student looks its words up in a table of its own (embedding; padded places
+are words of id -1), whose gradient is summed over each word's places.
 
 1. The teacher's rows of logits are sorted once, descending; the first k
    values and columns of each row, as they lie there, are what the student is
@@ -11,7 +15,9 @@
    counts are the lengths of its segments.
 3. Then the student samples answers from its own rows, and policy_loss raises
    the probability of those that the teacher would have given, held near the
-   distilled student by the KL term.
+   distilled student by the KL term.  token_logprobs gives the answers' log
+   probabilities under both, and the entropy whose bonus keeps the student from
+   settling too early.
 """
 import argparse
 import os
@@ -22,12 +28,13 @@ import torch
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import lsd_radix_sort_gb300 as rs  # noqa: E402
 
-TOKENS, WIDTH, VOCAB, EXPERTS, TOP_K, LIST = 512, 64, 2000, 8, 2, 32
+TOKENS, WORDS, WIDTH, VOCAB, EXPERTS, TOP_K, LIST = 512, 300, 64, 2000, 8, 2, 32
 
 
 class Student(torch.nn.Module):
-    def __init__(self, gen):
+    def __init__(self, gen, table):
         super().__init__()
+        self.table = torch.nn.Parameter(table.clone())
 
         def weights(*shape):
             drawn = torch.randn(*shape, generator=gen, device="cuda")
@@ -37,8 +44,9 @@ class Student(torch.nn.Module):
         self.experts = weights(EXPERTS, WIDTH, WIDTH)
         self.head = weights(WIDTH, VOCAB)
 
-    def forward(self, x, keep):
-        """(logits, balance loss, counts) of the tokens x."""
+    def forward(self, words, keep):
+        """(logits, balance loss, counts) of the words' places."""
+        x = rs.embedding(self.table, words)
         scores = x @ self.router
         ids = rs.segmented_sort(scores.detach().bfloat16(), descending=True)[1][:, :TOP_K]
         balance, counts, _, _ = rs.balance_loss(scores, ids, token_mask=keep)
@@ -60,18 +68,21 @@ class Student(torch.nn.Module):
 
 def main(steps=30, seed=0):
     gen = torch.Generator(device="cuda").manual_seed(seed)
-    x = torch.randn(TOKENS, WIDTH, generator=gen, device="cuda")
+    table = torch.randn(WORDS, WIDTH, generator=gen, device="cuda")
+    words = torch.randint(0, WORDS, (TOKENS,), generator=gen, device="cuda")
+    x = rs.embedding(table, words)  # what the teacher sees
     keep = torch.ones(TOKENS, dtype=torch.bool, device="cuda")
     keep[-TOKENS // 8:] = False  # padding
+    words = torch.where(keep, words, -1)
     weights = keep.float() / keep.sum()
     teacher = (x @ torch.randn(WIDTH, VOCAB, generator=gen, device="cuda") * 0.5).bfloat16()
     values, columns = rs.segmented_sort(teacher, descending=True)
-    student = Student(gen)
+    student = Student(gen, table)
     optimizer = torch.optim.Adam(student.parameters(), lr=5e-3)
 
     history = {"distill": [], "balance": [], "reward": []}
     for _ in range(steps):
-        logits, balance, counts = student(x, keep)
+        logits, balance, counts = student(words, keep)
         losses, _ = rs.distill_loss(logits, values[:, :LIST], columns[:, :LIST], 2.0, weights)
         assert int(counts.sum()) == int(keep.sum()) * TOP_K
         optimizer.zero_grad()
@@ -81,22 +92,25 @@ def main(steps=30, seed=0):
         history["balance"].append(balance.item())
 
     with torch.no_grad():
-        reference = student(x, keep)[0].log_softmax(1)
+        reference = student(words, keep)[0]
     optimizer = torch.optim.Adam(student.parameters(), lr=1e-3)
     for _ in range(steps):
         with torch.no_grad():
-            old = student(x, keep)[0].log_softmax(1)
-            actions = torch.multinomial(old.exp(), 1, generator=gen)
+            logits = student(words, keep)[0]
+            actions = torch.multinomial(logits.softmax(1), 1, generator=gen)
+            taken = actions[:, 0].contiguous()
+            old = rs.token_logprobs(logits, taken).logprobs
+            ref = rs.token_logprobs(reference, taken).logprobs
             reward = (columns[:, :LIST] == actions).any(1).float()
         history["reward"].append((reward * weights).sum().item())
         advantages = reward - (reward * weights).sum()
         for _ in range(4):  # passes over the same answers: ratios leave 1, clips hold
-            logits, balance, _ = student(x, keep)
-            losses, _, _ = rs.policy_loss(
-                logits, actions[:, 0], old.gather(1, actions)[:, 0].contiguous(), advantages,
-                reference.gather(1, actions)[:, 0].contiguous(), kl_coef=0.02, weights=weights)
+            logits, balance, _ = student(words, keep)
+            losses, _, _ = rs.policy_loss(logits, taken, old, advantages, ref, kl_coef=0.02,
+                                          weights=weights)
+            entropy = (rs.token_logprobs(logits).entropy * weights).sum()
             optimizer.zero_grad()
-            (losses.sum() + 0.01 * balance).backward()
+            (losses.sum() + 0.01 * balance - 1e-3 * entropy).backward()
             optimizer.step()
     return history
 

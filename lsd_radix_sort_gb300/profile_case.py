@@ -14,6 +14,9 @@ CASE is one of
   distill     losses and gradient of (R, C) bf16 logits against 64 targets each
   policy      losses and gradient of (R, C) bf16 logits and one action each
   balance     loss, counts and gradient of (R, C) bf16 router scores, 8 ids each
+  logprobs    log probabilities of (R, C) bf16 logits, a token and 20 alternatives
+  embed       (R, C) bf16 rows of a table of 131,072 (C = its width) by token
+  embed_rows  the gradient of those rows by token, named rows only
 
 Each sort is timed with CUDA events around every kernel the library enqueues
 (on the launching stream) and the script prints one JSON line with the
@@ -32,7 +35,8 @@ import numpy as np
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("case", choices=["pairs_u32", "keys_u32", "pairs_u64", "rows_f16",
-                                     "rows_bf16", "distill", "policy", "balance"])
+                                     "rows_bf16", "distill", "policy", "balance", "logprobs", "embed",
+                                     "embed_rows"])
     ap.add_argument("--log2", type=int, default=25)
     ap.add_argument("--bits", type=int, default=8)
     ap.add_argument("--end-bit", type=int, default=None)
@@ -101,6 +105,31 @@ def main():
                     rs.distill_loss_grad(x, values, indices, grad_out=grad)
                 else:
                     rs.balance_loss_grad(x, indices, grad_out=grad)
+        units = rows * cols
+    elif args.case == "logprobs":
+        rows, cols = args.rows, args.cols
+        torch.manual_seed(0)
+        x = (torch.randn(rows, cols, device=dev) * 2.5).to(torch.bfloat16)
+        tokens = torch.randint(0, cols, (rows, 1), device=dev)
+        temp = torch.zeros(1024, dtype=torch.uint8, device=dev)  # no status of its own
+
+        def sort():
+            rs.token_logprobs(x, tokens, 20)
+        units = rows * cols
+    elif args.case in ("embed", "embed_rows"):
+        rows, cols = args.rows, args.cols
+        torch.manual_seed(0)
+        share = 1.0 / (torch.arange(131072, device=dev, dtype=torch.float64) + 2.7)
+        ids = torch.multinomial(share.float(), rows, replacement=True)
+        ids = torch.randperm(131072, device=dev)[ids]
+        x = torch.randn(131072 if args.case == "embed" else rows, cols, device=dev).bfloat16()
+        temp = torch.zeros(1024, dtype=torch.uint8, device=dev)  # no status of their own
+
+        def sort():
+            if args.case == "embed":
+                rs.embedding(x, ids, scale=2.0)
+            else:
+                rs.embedding_grad_rows(x, ids, 131072)
         units = rows * cols
     else:
         kind = "f16" if args.case == "rows_f16" else "bf16"
