@@ -20,7 +20,7 @@ namespace {
 constexpr int kClusterCtas = 16;
 constexpr int kClusterThreads = 1024;
 constexpr int kClusterWarps = kClusterThreads / kWarp;
-constexpr int kClusterItems = 8;
+constexpr int kClusterItems = 4;
 constexpr int64_t kClusterTokens = int64_t(kClusterCtas) * kClusterThreads * kClusterItems;
 
 struct ClusterShared {
@@ -585,11 +585,10 @@ cudaError_t launch_embed_grad(int type, int out_type, const EmbedGradArgs& a, in
   cudaError_t e = cudaSuccess;
   if (!embed_grad_sorts(a.tokens)) {
     const int64_t each = cdiv(a.tokens, kClusterCtas * kClusterThreads);
-    static_assert(kClusterItems == 8);
+    static_assert(kClusterItems == 4);
     e = each <= 1   ? list_as<1>(a, p, s)
         : each <= 2 ? list_as<2>(a, p, s)
-        : each <= 4 ? list_as<4>(a, p, s)
-                    : list_as<8>(a, p, s);
+                    : list_as<4>(a, p, s);
     *launched = 2;
   } else {
     const dim3 tiles(static_cast<unsigned>(cdiv(a.tokens, kPlanTile)));

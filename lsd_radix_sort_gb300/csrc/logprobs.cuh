@@ -612,6 +612,37 @@ __device__ __noinline__ void select_exactly(const Selection<TYPE, WARPS>& sel, u
   row_sync<WARPS>();
 }
 
+// The same among n candidates in shared memory, until no more than `limit` are
+// left.  Worth it for more than twice as many (the 300 best of 16,384 x 2,000
+// bf16: 672 us, 1,434 with all 2,000 put in order); for fewer the order costs
+// less (128 best of 8,192 x 32,000: 248 us, 311).
+template <int TYPE, int WARPS>
+__device__ __noinline__ void narrow(const Selection<TYPE, WARPS>& sel, int n, int limit) {
+  constexpr int kThreads = WARPS * kWarp;
+  const int tid = static_cast<int>(threadIdx.x);
+  uint64_t prefix = 0;
+  int shift = 64, above = 0;
+  do {
+    shift -= 8;
+    sel.clear_counts();
+    for (int i = tid; i < n; i += kThreads) {
+      const uint64_t e = sel.cand[i];
+      if (shift == 56 || (e ^ prefix) >> (shift + 8) == 0)
+        count_digit(sel.sh->hist, static_cast<uint32_t>(e >> shift) & 0xFFu);
+    }
+    sel.pick(prefix, shift, above);
+    prefix = sel.sh->prefix;
+    above = sel.sh->above;
+  } while (sel.sh->reach > limit && shift > 0);
+  if (tid == 0) sel.sh->count = 0;
+  for (int i0 = 0; i0 < n; i0 += kThreads) {
+    const uint64_t e = i0 + tid < n ? sel.cand[i0 + tid] : 0;
+    row_sync<WARPS>();  // written below are places that have all been read
+    if (e >= prefix && e != 0) sel.add(e);
+  }
+  row_sync<WARPS>();
+}
+
 // Puts n entries in order: place(position, entry), the largest first.  There
 // is room for the next power of two.
 template <int WARPS, class F>
@@ -788,6 +819,13 @@ __global__ void __launch_bounds__(WARPS* kWarp)
     row_sync<WARPS>();
     if (!fits) select_exactly(sel, least);
     found = sh.count;
+    int limit = 4 * kThreads;
+    while (limit < top) limit *= 2;
+    if (WARPS > 1 && found > 2 * limit) {
+      row_sync<WARPS>();
+      narrow(sel, found, limit);
+      found = sh.count;
+    }
     // warps without a result to write
     if (found <= kThreads && tid - lane >= max(found, max(top - found, a.k))) return;
   }
@@ -820,6 +858,15 @@ constexpr int kLpWarps = kLpThreads / kWarp;
 struct Pull {
   float c0, c1;
 };
+// Entries of a row that are compared in pairs; more are sorted by column (2,048 x
+// 65,536 bf16: 128 entries 111 us, 121 in pairs; 2,048 entries 332, 4,400).
+constexpr int kLpPairs = 64;
+__host__ __device__ constexpr inline size_t entries_smem(int n) {
+  size_t size = kLpPairs;
+  while (size < static_cast<size_t>(n)) size *= 2;
+  return n <= kLpPairs ? static_cast<size_t>(n) * 12
+                       : (static_cast<size_t>(n) * 12 + 15) / 16 * 16 + size * 8;
+}
 
 template <int TYPE>
 __global__ void __launch_bounds__(kLpThreads, kLpCtas)
@@ -931,21 +978,57 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas)
   __syncthreads();
   const int64_t first = static_cast<int64_t>(begin) * V::kCount - vecs.lead;
   const int64_t last = static_cast<int64_t>(end) * V::kCount - vecs.lead;
-  for (int i = tid; i < n; i += kLpThreads) {
-    const int c = col[i];
-    if (c < 0 || c < first || c >= last) continue;
-    // a column named more than once: its first entry writes, for all of them
-    bool mine = true;
-    float total = 0.0f;
-    for (int j = 0; j < n && mine; ++j) {
-      if (col[j] != c) continue;
-      mine = j >= i;
-      total += up[j];
-    }
-    if (!mine) continue;
+  auto write = [&](int i, float total) {
     const float y = above_nothing(__fmaf_rn(score[i], e.scale, -e.os2));
-    g[c] = S::store(exp2_approx(y) * __fmaf_rn(pull.c1, y, pull.c0) +
-                    (empty ? 0.0f : total * a.inv_tau));
+    g[col[i]] = S::store(exp2_approx(y) * __fmaf_rn(pull.c1, y, pull.c0) +
+                         (empty ? 0.0f : total * a.inv_tau));
+  };
+  // a column named more than once: its first entry writes, for all of them
+  if (n <= kLpPairs) {
+    for (int i = tid; i < n; i += kLpThreads) {
+      const int c = col[i];
+      if (c < 0 || c < first || c >= last) continue;
+      bool mine = true;
+      float total = 0.0f;
+      for (int j = 0; j < n && mine; ++j) {
+        if (col[j] != c) continue;
+        mine = j >= i;
+        total += up[j];
+      }
+      if (mine) write(i, total);
+    }
+    return;
+  }
+  // many: by column, then by place
+  uint64_t* key = reinterpret_cast<uint64_t*>(smem + (static_cast<size_t>(n) * 12 + 15) / 16 * 16);
+  int size = kLpPairs;
+  while (size < n) size *= 2;
+  for (int i = tid; i < size; i += kLpThreads) {
+    const int c = i < n ? col[i] : -1;
+    key[i] = c < 0 || c < first || c >= last
+                 ? ~uint64_t(0)
+                 : static_cast<uint64_t>(c) << 32 | static_cast<uint32_t>(i);
+  }
+  __syncthreads();
+  for (int run = 2; run <= size; run *= 2)
+    for (int step = run / 2; step > 0; step /= 2) {
+      for (int q = tid; q < size / 2; q += kLpThreads) {
+        const int i = (q & ~(step - 1)) * 2 + (q & (step - 1)), j = i + step;
+        const uint64_t x = key[i], y = key[j];
+        if ((x > y) == ((i & run) == 0)) {
+          key[i] = y;
+          key[j] = x;
+        }
+      }
+      __syncthreads();
+    }
+  for (int i = tid; i < n; i += kLpThreads) {
+    const uint64_t own = key[i];
+    if (own == ~uint64_t(0) || (i > 0 && key[i - 1] >> 32 == own >> 32)) continue;
+    float total = 0.0f;
+    for (int j = i; j < n && key[j] >> 32 == own >> 32; ++j)
+      total += up[static_cast<uint32_t>(key[j])];
+    write(static_cast<int>(static_cast<uint32_t>(own)), total);
   }
 }
 
@@ -977,9 +1060,13 @@ LpPlan make_logprobs_plan(int64_t rows, int64_t cols, int top, bool aligned, int
   p.per = static_cast<int>((vecs + p.split - 1) / p.split);
   const int64_t batches = (p.per + kLpStep - 1) / kLpStep;
   if (top > 0) {
-    // single vectors where there are few: the best of short rows are then
-    // bounded by several times `top` maxima
-    p.single = p.split * batches * kLpStep <= (top <= kLpShort ? kLpFewGroups : kLpManyGroups);
+    // single vectors where there are few, or for a long list too few groups of
+    // more: the best of short rows are then bounded by several times `top` maxima
+    // (16,384 x 2,000 bf16 with 20 alternatives 68 us, 523 with groups of four;
+    // 8,192 x 32,000 with 300 in 1,024 groups of four 440, in single ones 625)
+    p.single = top <= kLpShort ? p.split * batches * kLpStep <= kLpFewGroups
+                               : p.split * batches * kLpStep <= kLpManyGroups &&
+                                     p.split * batches * kWarp < 2 * top;
     const int64_t most = top <= kLpShort ? kLpGroups : kLpManyGroups;
     auto slots = [&] {
       return p.single ? batches * kLpStep : (((batches - 1) >> p.shift) + 1) * kWarp;
@@ -1035,8 +1122,12 @@ cudaError_t launch_logprobs_as(const LogprobArgs& a, int* launched, cudaStream_t
   if (e != cudaSuccess) return e;
   *launched = 2;
   static_assert(select_smem(1024) + sizeof(RowSelected) <= 48 * 1024);
-  const bool one_warp =
-      a.top == 0 || (a.top <= kLpShort && p.groups() <= kLpFewGroups && a.rows >= 1024);
+  // A warp per row where there are rows enough for all SMs and a lane holds 32 of
+  // its groups: no barriers.  With 20 alternatives 2,500 x 8,000 bf16 takes 33
+  // us (39 with four warps), 1,024 x 8,000 27 (23); with 128 8,192 x 32,000 248
+  // (290), 2,500 x 8,000 86 (73).
+  const bool one_warp = a.top == 0 || (a.top <= kLpShort && p.groups() <= kLpFewGroups &&
+                                       a.rows >= (a.top <= 32 ? 2048 : 4096));
   const dim3 rows(static_cast<unsigned>(a.rows));
   return one_warp ? launch_kernel(logprobs_rows_kernel<TYPE, 1>, rows, dim3(kWarp),
                                   select_smem(a.top), s, a, p)
@@ -1058,7 +1149,9 @@ cudaError_t launch_logprobs_backward_as(const LogprobArgs& a, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.rows * split));
   cfg.blockDim = dim3(kLpThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(a.k + a.top) * 12;
+  static_assert(entries_smem(2 * RS_MAX_TOP) <= 48 * 1024 - 512);
+  cfg.dynamicSmemBytes = entries_smem((a.grad_logprobs != nullptr ? a.k : 0) +
+                                      (a.grad_top != nullptr ? a.top : 0));
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   cfg.attrs = attr;

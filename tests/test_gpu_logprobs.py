@@ -96,6 +96,19 @@ def test_long_lists(rs, rows, cols, top, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,cols,top", [(4100, 600, 100), (4500, 2000, 128), (4100, 2000, 40),
+                                           (300, 2000, 300), (300, 2048, 700), (40, 1500, 129),
+                                           (20, 9000, 1024)])
+def test_long_lists_of_short_rows(rs, rows, cols, top, dtype):
+    """Nearly all of a row's scores are candidates, and more than are put in
+    order at once."""
+    x, g = rows_of(rows, cols, dtype, top)
+    check(rs, x, None, top)
+    tied = torch.randint(0, 5, x.shape, generator=g, device="cuda").to(dtype)
+    check(rs, tied, None, top)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("rows,cols", [(4, 300), (3, 20000), (2, 131072), (600, 9000)])
 def test_ties_go_to_the_lower_column(rs, rows, cols, dtype):
     x, g = rows_of(rows, cols, dtype, 7)
@@ -295,6 +308,21 @@ def test_gradient_masks_and_repeats(rs):
 def test_gradient_of_long_lists(rs):
     x, g = rows_of(3, 5000, torch.float32, 15)
     check_grad(rs, x, g, k=1024, top=1024)
+
+
+@pytest.mark.parametrize("rows,cols", [(2, 900), (5, 60000), (500, 3001)])
+def test_gradient_of_long_lists_that_repeat(rs, rows, cols):
+    x, g = rows_of(rows, cols, torch.bfloat16, 18)
+    for k, top in ((64, 0), (65, 0), (200, 130), (1024, 100)):
+        t = torch.randint(0, 40, (rows, k), generator=g, device="cuda")
+        t[0] = 7                # one column alone
+        t[1, ::3] = -1
+        t[1, 1::3] = cols       # outside as well
+        check_grad(rs, x, g, tokens=t, top=top)
+        again = [rs.token_logprobs_backward(x, rs.token_logprobs(x).stats, tokens=t,
+                                            grad_logprobs=torch.ones(rows, k, device="cuda") / 3)
+                 for _ in range(2)]
+        assert torch.equal(*again)
 
 
 def test_gradient_is_that_of_differences(rs):
