@@ -14,9 +14,11 @@ namespace {
 // 16 CTAs hold the tokens' (key, place) in shared memory and sort them there,
 // digit by digit from the least: a warp ranks its 32 * ITEMS neighbouring words
 // by ballots, the CTAs tell each other their digits' counts, and every word is
-// written to its place in the CTA that this lies in.  (The sort of whole keys
-// takes 7 launches, 31 us for 16,384 tokens.)  Two passes of 9 bits for a
-// vocabulary of 131,072.
+// written to its place in the CTA that this lies in: two passes of 9 bits for a
+// vocabulary of 131,072, and 12 us for 8,191 tokens, 15 for 16,384, 19 for
+// 32,768, bound by the latency of barriers and ranks.  The sort of whole keys
+// takes 7 launches and 31 us for 16,384.  The gradient of 65,536 rows of 256
+// takes 62 us this way, 72 that; of 100,000, with 8 words per thread, 82 and 78.
 constexpr int kClusterCtas = 16;
 constexpr int kClusterThreads = 1024;
 constexpr int kClusterWarps = kClusterThreads / kWarp;
@@ -101,11 +103,6 @@ __global__ void __launch_bounds__(kClusterThreads, 1)
     // behind the last token: past every key
     w[u] = i < tokens ? static_cast<uint64_t>(key_of(a, i)) << 32 | i : ~uint64_t(0);
   }
-  {
-    const int64_t words = 2 * static_cast<int64_t>(p.chunks) * p.blocks;
-    for (int64_t i = rank * kClusterThreads + tid; i < words; i += kClusterCtas * kClusterThreads)
-      p.arrived[i] = 0;
-  }
   for (int pass = 0; pass < passes; ++pass) {
     const int shift = 32 + pass * bits;
     uint32_t place[ITEMS];
@@ -185,6 +182,10 @@ __global__ void __launch_bounds__(kClusterThreads, 1)
                  : "memory");
   }
   cluster_barrier();  // from here on no CTA reads another's memory
+  // (written before, these words would be waited for at every barrier)
+  const int64_t words = 2 * static_cast<int64_t>(p.chunks) * p.blocks;
+  for (int64_t i = rank * kClusterThreads + tid; i < words; i += kClusterCtas * kClusterThreads)
+    p.arrived[i] = 0;
   uint32_t run = runs_before, runs = 0, total_live = 0, next = 0xFFFFFFFFu;
   for (uint32_t r = 0; r < kClusterCtas; ++r) {
     const uint4 e = sh.ends[r];

@@ -126,10 +126,18 @@ __device__ __forceinline__ int entry_col(uint64_t e) {
 // of rows of its own, without a pause between two of them, and leaves of each
 // segment its statistics and the largest score of every few vectors of a lane
 // (a group); it needs that maximum for the softmax anyway.  The second joins
-// them, a CTA per row, and finds the top alternatives: from the groups'
+// them, a CTA or a warp per row, and finds the top alternatives: from the groups'
 // maxima a bound that `top` of them reach, so that no score below it can be
 // among the `top` best, and few others do (of 64 groups about 24 scores reach
-// 20th largest maximum); only groups that reach it are read again.
+// the 20th largest maximum); only groups that reach it are read again.
+//
+// 4,096 x 131,072 bf16 scores with 20 alternatives take 213 us, of which the
+// first kernel has 180 (88% of the measured copy bandwidth) and the second 31,
+// bound by its latency of about 10 us per row and 8 rows per SM.  Kernels that
+// chose each row's alternatives where its scores were read took 252 us (a CTA
+// or a cluster per row) and 254 (one warp of a persistent CTA chooses): the
+// loads of other rows then wait for the choice.  Three CTAs per SM: with two
+// the first kernel takes 211 us, with four (64 registers) 233.
 constexpr int kLpBlock = 256;     // threads of the first kernel's CTAs
 constexpr int kLpCtas = 3;        // per SM
 constexpr int kLpStep = kWarp * kStreamBatch;  // vectors of a warp's batch
@@ -151,7 +159,10 @@ __host__ __device__ constexpr inline size_t select_smem(int top) {
 
 // A warp's batch is 2 KB in one piece.  A lane reads every other vector of half
 // a 128-byte line, so that its four vectors lie in one line (they are read
-// again together) and a load of the warp still takes whole sectors.
+// again together) and a load of the warp still takes whole sectors.  (Vectors
+// 512 bytes apart: 8,192 x 32,000 bf16 with 20 alternatives 147 us instead of
+// 141.  Four neighbouring vectors per lane, by shuffles: 1,368 x 131,072 72 us
+// instead of 65.)
 __host__ __device__ constexpr inline int lane_vector(int lane) { return lane / 2 * 8 + lane % 2; }
 constexpr int kLaneStride = 2;
 
@@ -776,11 +787,7 @@ __global__ void __launch_bounds__(WARPS* kWarp)
                                     : make_uint4(0, 0, 0, 0);
   }
   const float4* part = static_cast<const float4*>(a.temp) + row * p.split;
-  float4 parts[kLpSplit / kWarp];
-#pragma unroll
-  for (int i = 0; i < kLpSplit / kWarp; ++i)
-    parts[i] = i * kWarp + lane < p.split ? part[i * kWarp + lane]
-                                          : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+  float4 own = lane < p.split ? part[lane] : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
   const Token<TYPE> token(a, row, tid);
 
   const Selection<TYPE, WARPS> sel{
@@ -829,14 +836,12 @@ __global__ void __launch_bounds__(WARPS* kWarp)
     // warps without a result to write
     if (found <= kThreads && tid - lane >= max(found, max(top - found, a.k))) return;
   }
-  Stats st{-INFINITY, 0.0f, 0.0f};
-#pragma unroll
-  for (int i = 0; i < kLpSplit / kWarp; ++i) {  // of a lane
-    if (i * kWarp >= p.split) break;
-    const float m = fmaxf(st.m, parts[i].x), o = origin(m);
+  Stats st{own.x, own.y, own.z};
+  for (int i = kWarp + lane; i < p.split; i += kWarp) {
+    own = part[i];
+    const float m = fmaxf(st.m, own.x), o = origin(m);
     const Stats x = moved(st, m, (st.m - o) * a.scale2);
-    const Stats y = moved(Stats{parts[i].x, parts[i].y, parts[i].z}, m,
-                          (parts[i].x - o) * a.scale2);
+    const Stats y = moved(Stats{own.x, own.y, own.z}, m, (own.x - o) * a.scale2);
     st = Stats{m, x.sum + y.sum, x.dot + y.dot};
   }
   const RowStats s(warp_join(st, a.scale2));
@@ -852,7 +857,9 @@ __global__ void __launch_bounds__(WARPS* kWarp)
 //
 // that is 2^y_j (c0 + c1 y_j) with y_j the exponent from the row's maximum, in
 // units of log 2: two multiply-adds and one exponential per score.  The
-// entries' columns are written last.
+// entries' columns are written last.  2,048 x 65,536 bf16 in 84 us, 94% of the
+// measured copy bandwidth for reading the scores and writing their gradient:
+// HBM bounds it.
 constexpr int kLpThreads = kStreamThreads;
 constexpr int kLpWarps = kLpThreads / kWarp;
 struct Pull {

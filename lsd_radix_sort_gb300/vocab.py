@@ -13,7 +13,10 @@ some token names, summed over tokens that are sorted by id.
 The formulas, and what happens to padded tokens, -inf and NaN, are stated in
 include/lsdrs.h.  As in the rest of the package the work is enqueued on
 ``stream`` (the current stream by default) and nothing synchronises; results
-are allocated by torch on that stream unless given.
+are allocated by torch on that stream unless given.  All calls capture into a
+CUDA graph; a captured training step is best made of the explicit backward
+calls, since torch's engine ties a leaf to the stream of the first graph that
+used it, and a capture must not wait for a graph that is still alive outside.
 """
 from __future__ import annotations
 
@@ -28,8 +31,9 @@ from . import losses as _l
 from .losses import (_F, _I, _I64, _P, _SZ, MAX_TOP, _device, _grad_stride, _index_bytes, _kind,
                      _matrix, _on, _ptr, _vector, _wants_grad)
 
-__all__ = ["TokenLogprobs", "token_logprobs", "token_logprobs_temp_bytes", "token_logprobs_backward", "embedding",
-           "embedding_grad", "embedding_grad_rows", "embedding_grad_temp_bytes"]
+__all__ = ["TokenLogprobs", "token_logprobs", "token_logprobs_temp_bytes",
+           "token_logprobs_backward", "embedding", "embedding_grad", "embedding_grad_rows",
+           "embedding_grad_temp_bytes"]
 
 EMBED_TABLE, EMBED_ADD, EMBED_ROWS = range(3)
 
