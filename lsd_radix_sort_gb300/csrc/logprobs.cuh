@@ -406,6 +406,7 @@ __device__ __forceinline__ uint32_t largest_of(const uint32_t (&v)[N], int top) 
 struct RowSelected {
   int hits, count;
   uint32_t words[4][4][kWarp];   // maxima by word, warp, lane
+  uint32_t least;
   uint32_t hist[kLpRadix];
   uint64_t prefix;
   int above, reach;
@@ -432,7 +433,8 @@ struct Selection {
   RowSelected* sh;
 
   // A bound (the upper half of an order) that `top` scores reach, or 0: the
-  // `top`-th largest of 64 * WORDS maxima, of this thread's in g.
+  // `top`-th largest of 64 * WORDS maxima, of this thread's in g.  The first warp
+  // finds it for all of them.
   template <int WORDS>
   __device__ __forceinline__ uint32_t bound_of(const uint32_t (&g)[4]) const {
     const int lane = static_cast<int>(lane_id()), warp = static_cast<int>(threadIdx.x) / kWarp;
@@ -442,20 +444,30 @@ struct Selection {
 #pragma unroll
     for (int i = WORDS; i < 4; ++i) w[i % WORDS] = __vmaxu2(w[i % WORDS], g[i]);
     if constexpr (WARPS > 1) {
+      if (warp != 0) {
 #pragma unroll
-      for (int i = 0; i < WORDS; ++i) sh->words[i][warp][lane] = w[i];
+        for (int i = 0; i < WORDS; ++i) sh->words[i][warp][lane] = w[i];
+      }
       __syncthreads();
-#pragma unroll
-      for (int i = 0; i < WORDS; ++i)
-#pragma unroll
-        for (int j = 0; j < WARPS; ++j) w[i] = __vmaxu2(w[i], sh->words[i][j][lane]);
     }
+    if (warp == 0) {
+      if constexpr (WARPS > 1) {
 #pragma unroll
-    for (int i = 0; i < WORDS; ++i) {
-      v[2 * i] = w[i] & 0xFFFFu;
-      v[2 * i + 1] = w[i] >> 16;
+        for (int i = 0; i < WORDS; ++i)
+#pragma unroll
+          for (int j = 1; j < WARPS; ++j) w[i] = __vmaxu2(w[i], sh->words[i][j][lane]);
+      }
+#pragma unroll
+      for (int i = 0; i < WORDS; ++i) {
+        v[2 * i] = w[i] & 0xFFFFu;
+        v[2 * i + 1] = w[i] >> 16;
+      }
+      const uint32_t best = largest_of(v, a.top);
+      if constexpr (WARPS == 1) return best;
+      if (lane == 0) sh->least = best;
     }
-    return largest_of(v, a.top);
+    if constexpr (WARPS > 1) __syncthreads();
+    return sh->least;
   }
 
   // One digit of a selection by counts: sh->prefix, above, reach.
@@ -500,18 +512,28 @@ struct Selection {
     const int at = atomicAdd(&sh->hits, 1);
     if (at < room) work[at] = static_cast<uint32_t>(group);
   }
-  // Lists those of 8 groups that reach the bound.
-  __device__ __forceinline__ void hits_of(int group, const uint4& w, uint32_t least) const {
+  // Lists those of a thread's groups (8 of each vector) that reach the bound.
+  template <int VECS>
+  __device__ __forceinline__ void hits_of(const uint4 (&v)[VECS], uint32_t largest,
+                                          uint32_t least) const {
     const uint32_t below = (least - 1) * 0x10001u;  // (least is not 0)
-    if (__vmaxu2(__vmaxu2(__vmaxu2(w.x, w.y), __vmaxu2(w.z, w.w)), below) == below) return;
-    const uint32_t words[4] = {w.x, w.y, w.z, w.w};
-    uint32_t reach = 0;
+    if (__vmaxu2(largest, below) == below) return;
+    uint32_t reach = 0;  // a bit per group
+    static_assert(VECS <= 4);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t over = __vmaxu2(words[j], below) ^ below;
-      reach |= (over & 0xFFFFu ? 1u << 2 * j : 0u) | (over >> 16 ? 2u << 2 * j : 0u);
+    for (int i = 0; i < VECS; ++i) {
+      const uint32_t words[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t over = __vmaxu2(words[j], below) ^ below;
+        if (over & 0xFFFFu) reach |= 1u << (8 * i + 2 * j);
+        if (over >> 16) reach |= 2u << (8 * i + 2 * j);
+      }
     }
-    for (; reach != 0; reach &= reach - 1) hit(group + __ffs(static_cast<int>(reach)) - 1);
+    for (; reach != 0; reach &= reach - 1) {
+      const int bit = __ffs(static_cast<int>(reach)) - 1;
+      hit((bit / 8 * kThreads + static_cast<int>(threadIdx.x)) * 8 + bit % 8);
+    }
   }
 
   __device__ __forceinline__ void add(uint64_t e) const {
@@ -808,8 +830,7 @@ __global__ void __launch_bounds__(WARPS* kWarp)
                         : sel.template bound_of<4>(g);
     least = max(least, kOrderLeast >> 16);
     if (WARPS == 1) __syncwarp();
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) sel.hits_of((i * kThreads + tid) * 8, v[i], least);
+    sel.hits_of(v, __vmaxu2(__vmaxu2(g[0], g[1]), __vmaxu2(g[2], g[3])), least);
   } else if (top > 0) {
     least = max(sel.bound_of_all(), kOrderLeast >> 16);
     for (int g = tid; g < groups; g += kThreads)
