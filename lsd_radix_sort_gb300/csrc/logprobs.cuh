@@ -131,8 +131,8 @@ __device__ __forceinline__ int entry_col(uint64_t e) {
 // among the `top` best, and few others do (of 64 groups about 24 scores reach
 // the 20th largest maximum); only groups that reach it are read again.
 //
-// 4,096 x 131,072 bf16 scores with 20 alternatives take 213 us, of which the
-// first kernel has 180 (88% of the measured copy bandwidth) and the second 31,
+// 4,096 x 131,072 bf16 scores with 20 alternatives take 208 us, of which the
+// first kernel has 180 (88% of the measured copy bandwidth) and the second 28,
 // bound by its latency of about 10 us per row and 8 rows per SM.  Kernels that
 // chose each row's alternatives where its scores were read took 252 us (a CTA
 // or a cluster per row) and 254 (one warp of a persistent CTA chooses): the
@@ -410,6 +410,7 @@ struct RowSelected {
   uint32_t hist[kLpRadix];
   uint64_t prefix;
   int above, reach;
+  int part[4];
 };
 
 template <int WARPS>
@@ -614,34 +615,107 @@ struct Selection {
       }
     }
   }
+
+  // Candidates: the first `want` columns, from the lowest on, whose score has
+  // this order.
+  __device__ __forceinline__ void first_of(uint32_t least, uint32_t order, int want) const {
+    constexpr int kN = ScoreVec<TYPE>::kCount, kEach = 4;
+    static_assert(kN * kEach <= 32);
+    const Segment<TYPE> whole(a, row, 0, 0);
+    const int tid = static_cast<int>(threadIdx.x), lane = static_cast<int>(lane_id());
+    int taken = 0;
+    for (int64_t v0 = 0; v0 < whole.vecs.count && taken < want; v0 += kEach * kThreads) {
+      const int64_t first = v0 + tid * kEach;  // neighbouring vectors of each thread
+      uint32_t equal = 0;
+#pragma unroll
+      for (int u = 0; u < kEach; ++u) {
+        if (first + u >= whole.vecs.count) continue;
+        const int v = static_cast<int>(first) + u, rank = v / p.per;
+        if (kept[rank * p.slots + p.group_of(v - rank * p.per)] < least) continue;
+        const uint4 r = whole.vecs.load(whole.vec0(), whole.x, v);
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+          using Raw = typename Score<TYPE>::Raw;
+          const uint32_t o = order_of(Score<TYPE>::load(
+              static_cast<Raw>(kN == 4 ? w[i & 3] : w[i >> 1] >> (16 * (i & 1)))));
+          if (o == order) equal |= 1u << (u * kN + i);
+        }
+      }
+      int upto = __popc(equal);
+      const int own = upto;
+#pragma unroll
+      for (int o = 1; o < kWarp; o *= 2) {
+        const int n = __shfl_up_sync(kFull, upto, o);
+        if (lane >= o) upto += n;
+      }
+      int before = taken + upto - own;
+      if (lane == kWarp - 1) sh->part[tid / kWarp] = upto;
+      row_sync<WARPS>();
+#pragma unroll
+      for (int i = 0; i < WARPS; ++i) {
+        if (i < tid / kWarp) before += sh->part[i];
+        taken += sh->part[i];
+      }
+      for (; equal != 0 && before < want; equal &= equal - 1, ++before)
+        add(entry_of(order, static_cast<int>(first) * kN + __ffs(static_cast<int>(equal)) - 1 -
+                                whole.vecs.lead));
+      row_sync<WARPS>();
+    }
+  }
 };
 
 // More candidates than there is room for (many equal scores, or a long list):
-// entries are narrowed down digit by digit, 8 bits from the top, by counting
-// those that share the digits so far, until what is at and above them fits.
-// Entries differ, so they do at last.
+// scores are narrowed down digit by digit, 8 bits of their order from the top,
+// by counting those that share the digits so far, until what is at and above
+// them fits, or is one score: then the lowest columns that have it are looked
+// up from the beginning.  (20 of 1,024 x 65,536 equal bf16 scores: 83 us;
+// 1,240 with all 64 bits of score and column narrowed down.)
 template <int TYPE, int WARPS>
 __device__ __noinline__ void select_exactly(const Selection<TYPE, WARPS>& sel, uint32_t least) {
+  // the order's bits below are 0 of positive scores and 1 of negative ones
+  constexpr int kLast = TYPE == RS_SCORE_BF16 ? 48 : TYPE == RS_SCORE_F16 ? 40 : 32;
+  if (threadIdx.x == 0) sel.sh->count = 0;
+  row_sync<WARPS>();
+  sel.each(least + 1, [&](uint32_t o, int col) { sel.add(entry_of(o, col)); });
+  row_sync<WARPS>();
   uint64_t prefix = 0;  // entries from it on are kept, those of its digits divided further
-  int shift = 64, above = 0;
-  do {
+  int shift = 64, above = sel.sh->count;
+  // `top` scores reach the bound, so that the last of them has its digits where
+  // fewer are beyond it
+  const bool known = above < sel.a.top;
+  if (known) {
+    prefix = static_cast<uint64_t>(least) << 48;
+    shift = 48;
+  } else {
+    above = 0;
+  }
+  bool more = true;
+  while (more && shift > kLast) {
     shift -= 8;
     sel.clear_counts();
-    sel.each(least, [&](uint32_t o, int col) {
-      const uint64_t e = entry_of(o, col);
+    sel.each(least, [&](uint32_t o, int) {
+      const uint64_t e = static_cast<uint64_t>(o) << 32;
       if (shift == 56 || (e ^ prefix) >> (shift + 8) == 0)
         count_digit(sel.sh->hist, static_cast<uint32_t>(e >> shift) & 0xFFu);
     });
     sel.pick(prefix, shift, above);
     prefix = sel.sh->prefix;
     above = sel.sh->above;
-  } while (sel.sh->reach > sel.room && shift > 0);
-  if (threadIdx.x == 0) sel.sh->count = 0;
-  row_sync<WARPS>();
-  sel.each(least, [&](uint32_t o, int col) {
-    const uint64_t e = entry_of(o, col);
-    if (e >= prefix) sel.add(e);
-  });
+    more = sel.sh->reach > sel.room;
+  }
+  const uint32_t order = static_cast<uint32_t>(prefix >> 32) |
+                         (prefix >> 63 ? 0u : static_cast<uint32_t>((uint64_t(1) << (kLast - 32)) - 1));
+  if (!known || shift != 48) {  // (else those above are there)
+    row_sync<WARPS>();
+    if (threadIdx.x == 0) sel.sh->count = 0;
+    row_sync<WARPS>();
+    sel.each(least, [&](uint32_t o, int col) {
+      const uint64_t e = entry_of(o, col);
+      if (more ? o > order : e >= prefix) sel.add(e);
+    });
+  }
+  if (more) sel.first_of(least, order, sel.a.top - above);
   row_sync<WARPS>();
 }
 

@@ -122,6 +122,25 @@ def test_ties_go_to_the_lower_column(rs, rows, cols, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,cols,shift", [(3, 5003, 3), (4200, 3000, 0), (2, 200001, 0)])
+def test_long_ties_below_a_few_better_ones(rs, rows, cols, shift, dtype):
+    """More equal scores than fit beside others that are better, positive and
+    negative, the first of them early, late, or one in a hundred."""
+    x, g = rows_of(rows, cols, dtype, 21, shift % 2, shift)
+    for value in (1.0, -3.0, 0.0):
+        x.fill_(value)
+        x[:, 7::1000] = value + 0.5
+        x[:, cols - 3] = 9.0
+        check(rs, x, None, 60)
+        x[:, :cols // 2] = -20.0     # ties from the middle on
+        check(rs, x, None, 100)
+        check(rs, x, None, 300)
+        x.fill_(-20.0)
+        x[:, ::100] = value
+        check(rs, x, None, min(20, cols // 200))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 def test_orders_that_gather_the_best_in_one_place(rs, dtype):
     for cols in (5000, 70000):
         x, g = rows_of(6, cols, dtype, 8)
@@ -416,6 +435,33 @@ def test_graph_replays_on_new_scores(rs):
         assert all(torch.equal(a, b) for a, b in zip(got, want))
         assert torch.equal(grad, rs.token_logprobs_backward(x, want.stats, want.entropy, t,
                                                             want.top_ids, up))
+
+
+def test_offsets_beyond_32_bits(rs):
+    rows, cols = 33000, 131072  # 4.3e9 scores
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda")
+    for part in x.split(3000):
+        part.normal_()
+    t = torch.randint(0, cols, (rows,), device="cuda")
+    got = rs.token_logprobs(x, t, 5)
+    grad = rs.token_logprobs_backward(x, got.stats, got.entropy, t, grad_logprobs=torch.ones(rows, device="cuda"),
+                                      grad_entropy=torch.ones(rows, device="cuda"))
+    for r in (0, 16384, 32767, 32768, rows - 2):
+        rest = x[r:r + 2]
+        want = vo.Logprobs(rest, 1.0)
+        within(got.entropy[r:r + 2], want.entropy, want.entropy_error, "entropy")
+        assert torch.equal(got.top_ids[r:r + 2], want.top(5))
+        logp, bound = want.logprobs(t[r:r + 2, None])
+        within(got.logprobs[r:r + 2, None], logp, bound, "logprobs")
+        ones = torch.ones(2, 1, device="cuda")
+        g, bound = want.grad([(t[r:r + 2, None], ones)], ones[:, 0], None)
+        within(grad[r:r + 2], g, bound, "gradient")
+
+
+@pytest.mark.parametrize("top", [3, 200])
+def test_one_row_of_many_scores(rs, top):
+    x, g = rows_of(1, 100_000_003, torch.bfloat16, 22)
+    check(rs, x, tokens_of(x, 2, g), top)
 
 
 def test_same_bits_in_every_run(rs):
