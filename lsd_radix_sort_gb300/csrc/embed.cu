@@ -364,6 +364,14 @@ cudaError_t embed_as(const EmbedArgs& a, cudaStream_t s) {
                        dim3(kEmbedThreads), 0, s, a, static_cast<uint32_t>(per_row));
 }
 
+template <int TYPE, int UNIT>
+cudaError_t embed_narrow_as(const EmbedArgs& a, cudaStream_t s) {
+  const int64_t blocks = cdiv(a.width, kWarp * kNarrow);
+  const int64_t ctas = cdiv(a.tokens * blocks, kEmbedThreads / kWarp);
+  return launch_kernel(embed_narrow_kernel<TYPE, UNIT>, dim3(static_cast<unsigned>(ctas)),
+                       dim3(kEmbedThreads), 0, s, a, static_cast<uint32_t>(blocks));
+}
+
 template <int TYPE>
 cudaError_t embed_of(const EmbedArgs& a, cudaStream_t s) {
   constexpr int kEs = sizeof(typename Score<TYPE>::Raw);
@@ -371,8 +379,8 @@ cudaError_t embed_of(const EmbedArgs& a, cudaStream_t s) {
   if (vec == 32 / kEs) return embed_as<TYPE, 32 / kEs>(a, s);
   if (vec == 16 / kEs) return embed_as<TYPE, 16 / kEs>(a, s);
   if constexpr (kEs == 2)
-    if (vec == 2) return embed_as<TYPE, 2>(a, s);
-  return embed_as<TYPE, 1>(a, s);
+    if (vec == 2) return embed_narrow_as<TYPE, 2>(a, s);
+  return embed_narrow_as<TYPE, 1>(a, s);
 }
 
 int score_bytes(int type) { return type == RS_SCORE_F32 ? 4 : 2; }
@@ -429,16 +437,18 @@ size_t lay_out(int64_t tokens, int64_t width, void* temp, GradPlan* p, size_t* s
   return parts.at;
 }
 
-// One of the gradient's last kernels, by types and vector; f(types...).
+// One of the gradient's last kernels; f(types, elements of a lane, of an access).
 template <int IN, int OUT, class F>
 cudaError_t by_vector(int vec, const F& f) {
   constexpr int kEs = sizeof(typename Score<IN>::Raw);
+  constexpr ScoreTag<IN> in{};
+  constexpr ScoreTag<OUT> out{};
   if constexpr (F::kMost == 32)
-    if (vec == 32 / kEs) return f(ScoreTag<IN>{}, ScoreTag<OUT>{}, ScoreTag<32 / kEs>{});
-  if (vec == 16 / kEs) return f(ScoreTag<IN>{}, ScoreTag<OUT>{}, ScoreTag<16 / kEs>{});
+    if (vec == 32 / kEs) return f(in, out, ScoreTag<32 / kEs>{}, ScoreTag<32 / kEs>{});
+  if (vec == 16 / kEs) return f(in, out, ScoreTag<16 / kEs>{}, ScoreTag<16 / kEs>{});
   if constexpr (kEs == 2)
-    if (vec == 2) return f(ScoreTag<IN>{}, ScoreTag<OUT>{}, ScoreTag<2>{});
-  return f(ScoreTag<IN>{}, ScoreTag<OUT>{}, ScoreTag<1>{});
+    if (vec == 2) return f(in, out, ScoreTag<kNarrow>{}, ScoreTag<2>{});
+  return f(in, out, ScoreTag<kNarrow>{}, ScoreTag<1>{});
 }
 template <int MOST, class F>
 struct UpTo : F {
@@ -553,7 +563,7 @@ cudaError_t launch_embed_grad(int type, int out_type, const EmbedGradArgs& a, in
   const bool few = a.tokens <= kFewTokens;
   const int vec = vector_of(few ? 16 : 32, a.width, es, a.grad, a.grad_stride, out_es, a.out,
                             a.out_stride);
-  const int64_t blocks = cdiv(a.width, static_cast<int64_t>(kWarp) * vec);
+  const int64_t blocks = cdiv(a.width, kWarp * (vec * es >= 16 ? vec : kNarrow));
   const int sms = device_sm_count();
   if (few) {
     // every CTA sorts: no more of them than one per SM, or two for the zeros
@@ -565,7 +575,7 @@ cudaError_t launch_embed_grad(int type, int out_type, const EmbedGradArgs& a, in
     const int bits = key_bits(a.vocab), passes = (bits + 8) / 9;
     const dim3 ctas(
         static_cast<unsigned>(sums + (a.mode == kEmbedTable ? cdiv(a.vocab, rows) : 0)));
-    return by_types<16>(type, out_type, vec, [&](auto in, auto out, auto v) {
+    return by_types<16>(type, out_type, vec, [&](auto in, auto out, auto v, auto unit) {
       auto go = [&](auto word) {
         using W = decltype(word);
         constexpr int kSmem = static_cast<int>(
@@ -573,7 +583,7 @@ cudaError_t launch_embed_grad(int type, int out_type, const EmbedGradArgs& a, in
         static_assert(sizeof(FewShared<W>) % 8 == 0);
         static std::atomic<uint64_t> done{0};
         auto kern = embed_grad_few_kernel<decltype(in)::value, decltype(out)::value,
-                                          decltype(v)::value, W>;
+                                          decltype(v)::value, decltype(unit)::value, W>;
         if (kSmem > 48 * 1024) {
           const cudaError_t e = allow(kern, kSmem, &done);
           if (e != cudaSuccess) return e;
@@ -611,10 +621,11 @@ cudaError_t launch_embed_grad(int type, int out_type, const EmbedGradArgs& a, in
   const dim3 ctas(static_cast<unsigned>(
       sum_ctas +
       (a.mode == kEmbedTable ? cdiv(a.vocab, p.rows_per_zero) : 0)));
-  return by_types<32>(type, out_type, vec, [&](auto in, auto out, auto v) {
+  return by_types<32>(type, out_type, vec, [&](auto in, auto out, auto v, auto unit) {
     return launch_kernel(
-        embed_grad_kernel<decltype(in)::value, decltype(out)::value, decltype(v)::value>, ctas,
-        dim3(kGradThreads), 0, s, a, p, sum_ctas);
+        embed_grad_kernel<decltype(in)::value, decltype(out)::value, decltype(v)::value,
+                          decltype(unit)::value>,
+        ctas, dim3(kGradThreads), 0, s, a, p, sum_ctas);
   });
 }
 

@@ -102,6 +102,57 @@ struct Pack {
   }
 };
 
+// A lane's part of a row: VEC consecutive elements, or, of rows that allow only
+// UNIT elements (up to 4 bytes) at a time, VEC / UNIT of those, 32 units apart, so
+// that a warp's access is still in one piece.  `left`: elements from the first
+// one on to the row's end.
+template <int TYPE, int VEC, int UNIT>
+struct Part {
+  using Unit = Pack<TYPE, UNIT>;
+  using Raw = typename Unit::Raw;
+  static constexpr int kUnits = VEC / UNIT, kStep = kWarp * UNIT;
+  Unit u[kUnits];
+
+  __device__ __forceinline__ static Part load(const Raw* p, int left) {
+    Part r;
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i)
+      r.u[i] = i * kStep < left ? Unit::load(p + i * kStep) : Unit::zero();
+    return r;
+  }
+  __device__ __forceinline__ static Part zero() {
+    Part r;
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) r.u[i] = Unit::zero();
+    return r;
+  }
+  __device__ __forceinline__ void store(Raw* p, int left) const {
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i)
+      if (i * kStep < left) u[i].store(p + i * kStep);
+  }
+  __device__ __forceinline__ float get(int i) const { return u[i / UNIT].get(i % UNIT); }
+  // elements 2 * i and 2 * i + 1
+  __device__ __forceinline__ uint64_t pair(int i) const {
+    if constexpr (UNIT > 1 && sizeof(Raw) == 2)
+      return ScoreVec<TYPE>::pair(u[2 * i / UNIT].w[i % (UNIT / 2)]);
+    else
+      return pack2(get(2 * i), get(2 * i + 1));
+  }
+  __device__ __forceinline__ static Part of(const float (&v)[VEC]) {
+    Part r;
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      float w[UNIT];
+#pragma unroll
+      for (int j = 0; j < UNIT; ++j) w[j] = v[i * UNIT + j];
+      r.u[i] = Unit::of(w);
+    }
+    return r;
+  }
+};
+constexpr int kNarrow = 8;  // elements of a lane in narrow accesses
+
 // ---------------------------------------------------------------------- lookup
 // One vector per thread and step, two steps at once, over all of the output in
 // its order: an id, its row's vector, a store.  Bound by HBM: 65,536 tokens of
@@ -151,6 +202,34 @@ __global__ void __launch_bounds__(kEmbedThreads)
   }
 }
 
+// Rows that allow only narrow accesses: a warp per token and 32 * kNarrow columns,
+// whose accesses are then in one piece, with one division for all of them.
+template <int TYPE, int UNIT>
+__global__ void __launch_bounds__(kEmbedThreads)
+    embed_narrow_kernel(const __grid_constant__ EmbedArgs a, const uint32_t blocks) {
+  using P = Part<TYPE, kNarrow, UNIT>;
+  using Raw = typename P::Raw;
+  grid_dependency_sync();
+  const int64_t w = static_cast<int64_t>(blockIdx.x) * (kEmbedThreads / kWarp) + threadIdx.x / kWarp;
+  const int64_t row = w / blocks;
+  if (row >= a.tokens) return;
+  const int64_t col = (w - row * blocks) * (kWarp * kNarrow) + lane_id() * UNIT;
+  const int64_t id = load_index(a.ids, a.index_bytes, row);
+  const int left = static_cast<int>(a.width - col);
+  Raw* out = static_cast<Raw*>(a.out) + row * a.out_stride + col;
+  P p = P::zero();  // an id outside the table gives zeros, whatever the scale
+  if (id >= 0 && id < a.vocab) {
+    p = P::load(static_cast<const Raw*>(a.table) + id * a.table_stride + col, left);
+    if (a.scale != 1.0f) {
+      float v[kNarrow];
+#pragma unroll
+      for (int i = 0; i < kNarrow; ++i) v[i] = p.get(i) * a.scale;
+      p = P::of(v);
+    }
+  }
+  p.store(out, left);
+}
+
 // -------------------------------------------------------------------- gradient
 // A token of the sorted list: its place in the call, the row of the output
 // that its run of equal ids goes to, and that run's part of the list.
@@ -168,24 +247,17 @@ constexpr int kFewBatch = 8;
 // A thread's sum of VEC columns, two to a register pair.
 template <int VEC>
 struct Sum {
-  static constexpr int kPairs = (VEC + 1) / 2;
+  static constexpr int kPairs = VEC / 2;
   uint64_t v[kPairs];
 
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int i = 0; i < kPairs; ++i) v[i] = 0;
   }
-  template <int TYPE>
-  __device__ __forceinline__ void add(const Pack<TYPE, VEC>& p) {
+  template <int TYPE, int UNIT>
+  __device__ __forceinline__ void add(const Part<TYPE, VEC, UNIT>& p) {
 #pragma unroll
-    for (int i = 0; i < kPairs; ++i) {
-      if constexpr (VEC == 1)
-        v[i] = add2(v[i], pack2(p.get(0), 0.0f));
-      else if constexpr (TYPE == RS_SCORE_F32)
-        v[i] = add2(v[i], pack2(__uint_as_float(p.w[2 * i]), __uint_as_float(p.w[2 * i + 1])));
-      else
-        v[i] = add2(v[i], ScoreVec<TYPE>::pair(p.w[i]));
-    }
+    for (int i = 0; i < kPairs; ++i) v[i] = add2(v[i], p.pair(i));
   }
   __device__ __forceinline__ void add(const Sum& s) {
 #pragma unroll
@@ -193,23 +265,22 @@ struct Sum {
   }
 };
 
-template <int OUT, int VEC>
+template <int OUT, int VEC, int UNIT>
 __device__ __forceinline__ void store_sum(const EmbedGradArgs& a, uint32_t row, int64_t col,
                                           const Sum<VEC>& sum) {
-  using O = Pack<OUT, VEC>;
+  using O = Part<OUT, VEC, UNIT>;
   typename O::Raw* to = static_cast<typename O::Raw*>(a.out) + row * a.out_stride + col;
-  float v[2 * Sum<VEC>::kPairs], w[VEC];
+  const int left = static_cast<int>(a.width - col);
+  float v[VEC];
 #pragma unroll
-  for (int i = 0; i < Sum<VEC>::kPairs; ++i)
+  for (int i = 0; i < VEC / 2; ++i)
     unpack2(mul2(sum.v[i], pack2(a.scale, a.scale)), v[2 * i], v[2 * i + 1]);
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) w[i] = v[i];
   if (a.mode == kEmbedAdd) {
-    const O was = O::load(to);
+    const O was = O::load(to, left);
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) w[i] += was.get(i);
+    for (int i = 0; i < VEC; ++i) v[i] += was.get(i);
   }
-  O::of(w).store(to);
+  O::of(v).store(to, left);
 }
 
 // ---- many tokens: the list in memory
@@ -261,31 +332,24 @@ __device__ __forceinline__ bool join_pieces(const GradPlan& p, int block, uint32
   auto place = [&](uint32_t piece) {  // of later pieces, and of first ones
     return 2 * static_cast<int64_t>((start + piece * kPiece) / p.chunk) + (piece == 0);
   };
-  // 32 * VEC floats: a lane's next pair is 32 pairs on (VEC = 1: one float)
+  // 32 * VEC floats: a lane's next pair is 32 pairs on
   auto sums = [&](uint32_t piece) {
-    return p.partial + (place(piece) * p.blocks + block) * (kWarp * VEC) + lane * min(VEC, 2);
+    return p.partial + (place(piece) * p.blocks + block) * (kWarp * VEC) + lane * 2;
   };
   auto put = [&](uint32_t piece, const S& v) {
 #pragma unroll
     for (int i = 0; i < S::kPairs; ++i) {
       float x, y;
       unpack2(v.v[i], x, y);
-      if constexpr (VEC == 1)
-        __stcg(sums(piece), x);
-      else
-        __stcg(reinterpret_cast<float2*>(sums(piece)) + i * kWarp, make_float2(x, y));
+      __stcg(reinterpret_cast<float2*>(sums(piece)) + i * kWarp, make_float2(x, y));
     }
   };
   auto get = [&](uint32_t piece) {
     S v;
 #pragma unroll
     for (int i = 0; i < S::kPairs; ++i) {
-      if constexpr (VEC == 1) {
-        v.v[i] = pack2(__ldcg(sums(piece)), 0.0f);
-      } else {
-        const float2 f = __ldcg(reinterpret_cast<const float2*>(sums(piece)) + i * kWarp);
-        v.v[i] = pack2(f.x, f.y);
-      }
+      const float2 f = __ldcg(reinterpret_cast<const float2*>(sums(piece)) + i * kWarp);
+      v.v[i] = pack2(f.x, f.y);
     }
     return v;
   };
@@ -322,22 +386,23 @@ __device__ __forceinline__ bool join_pieces(const GradPlan& p, int block, uint32
   return true;
 }
 
-template <int IN, int OUT, int VEC>
+template <int IN, int OUT, int VEC, int UNIT>
 __device__ __forceinline__ void sum_chunk(const EmbedGradArgs& a, const GradPlan& p, int chunk,
                                           int block) {
-  using P = Pack<IN, VEC>;
+  using P = Part<IN, VEC, UNIT>;
   using Raw = typename P::Raw;
   const int lane = static_cast<int>(lane_id());
   const uint32_t live = p.header[kRunsLive];
-  const int64_t col = (static_cast<int64_t>(block) * kWarp + lane) * VEC;
+  const int64_t col = static_cast<int64_t>(block) * kWarp * VEC + lane * UNIT;
   const bool mine = col < a.width;
+  const int cols = static_cast<int>(a.width - col);
   const Raw* from = static_cast<const Raw*>(a.grad) + (mine ? col : 0);
   const uint32_t begin = static_cast<uint32_t>(chunk) * p.chunk;
   const Entry none{0, 0, 0, 0};
   Entry e = begin + lane < live ? p.list[begin + lane] : none;
   // A small chunk's rows are all brought to L2 at once: the loads below wait for
   // four at a time.  (32,768 rows of 4,096 bf16 94 us, 98 without.)
-  if constexpr (VEC * sizeof(Raw) >= 16) {
+  if constexpr (UNIT * sizeof(Raw) >= 16) {
     const int64_t from_col = static_cast<int64_t>(block) * kWarp * VEC;
     const uint32_t bytes =
         static_cast<uint32_t>(min(a.width - from_col, static_cast<int64_t>(kWarp * VEC)) * sizeof(Raw));
@@ -369,7 +434,7 @@ __device__ __forceinline__ void sum_chunk(const EmbedGradArgs& a, const GradPlan
 #pragma unroll
       for (int u = 0; u < kGradBatch; ++u) {
         const uint32_t pos = __shfl_sync(kFull, e.pos, __ffs(static_cast<int>(left)) - 1);
-        r[u] = mine && left != 0 ? P::load(from + pos * a.grad_stride) : P::zero();
+        r[u] = mine && left != 0 ? P::load(from + pos * a.grad_stride, cols) : P::zero();
         left &= left - 1;
       }
 #pragma unroll
@@ -380,7 +445,7 @@ __device__ __forceinline__ void sum_chunk(const EmbedGradArgs& a, const GradPlan
           sum.add(r[u]);
           if ((ends >> t & 1) != 0) {
             const uint32_t row = __shfl_sync(kFull, e.row, t);
-            if (mine) store_sum<OUT, VEC>(a, row, col, sum);
+            if (mine) store_sum<OUT, VEC, UNIT>(a, row, col, sum);
             sum.clear();
           }
         }
@@ -400,7 +465,7 @@ __device__ __forceinline__ void sum_chunk(const EmbedGradArgs& a, const GradPlan
 #pragma unroll
       for (int u = 0; u < kGradBatch; ++u) {
         const uint32_t pos = __shfl_sync(kFull, own.pos, (i + u) % kWarp);
-        r[u] = mine && i + u < n ? P::load(from + pos * a.grad_stride) : P::zero();
+        r[u] = mine && i + u < n ? P::load(from + pos * a.grad_stride, cols) : P::zero();
       }
 #pragma unroll
       for (int u = 0; u < kGradBatch; ++u)
@@ -408,7 +473,7 @@ __device__ __forceinline__ void sum_chunk(const EmbedGradArgs& a, const GradPlan
     }
     const uint32_t row = __shfl_sync(kFull, own.row, 0);
     if (join_pieces<VEC>(p, block, start, end, first, &sum) && mine)
-      store_sum<OUT, VEC>(a, row, col, sum);
+      store_sum<OUT, VEC, UNIT>(a, row, col, sum);
   }
 }
 
@@ -476,8 +541,9 @@ __device__ __forceinline__ void zero_rows(const EmbedGradArgs& a, const uint32_t
 
 constexpr int kZeroMostRows = 4096;  // of one CTA
 
-template <int IN, int OUT, int VEC>
-__global__ void __launch_bounds__(kGradThreads, VEC * sizeof(typename Score<IN>::Raw) == 32 ? 3 : 4)
+template <int IN, int OUT, int VEC, int UNIT>
+__global__ void __launch_bounds__(
+    kGradThreads, VEC * sizeof(typename Score<IN>::Raw) == 32 || UNIT < VEC ? 3 : 4)
     embed_grad_kernel(const __grid_constant__ EmbedGradArgs a, const __grid_constant__ GradPlan p,
                       const int64_t sum_ctas) {
   __shared__ uint32_t named[kZeroMostRows / 32];
@@ -492,7 +558,7 @@ __global__ void __launch_bounds__(kGradThreads, VEC * sizeof(typename Score<IN>:
   }
   const int64_t w = cta * kGradWarps + threadIdx.x / kWarp, chunk = w / p.blocks;
   if (chunk < p.chunks)
-    sum_chunk<IN, OUT, VEC>(a, p, static_cast<int>(chunk), static_cast<int>(w % p.blocks));
+    sum_chunk<IN, OUT, VEC, UNIT>(a, p, static_cast<int>(chunk), static_cast<int>(w % p.blocks));
 }
 
 // ---- few tokens: every CTA makes the list by itself
@@ -618,19 +684,21 @@ __device__ __forceinline__ void sort_few(const EmbedGradArgs& a, FewShared<W>& s
 }
 
 // The sum of rows [from, to) of the list.
-template <int IN, int VEC, class W>
+template <int IN, int VEC, int UNIT, class W>
 __device__ __forceinline__ Sum<VEC> sum_rows(const EmbedGradArgs& a, const W* word, W places,
                                              int from, int to, int64_t col) {
-  using P = Pack<IN, VEC>;
+  using P = Part<IN, VEC, UNIT>;
   const auto* up = static_cast<const typename P::Raw*>(a.grad) + col;
+  const int cols = static_cast<int>(a.width - col);
   Sum<VEC> sum;
   sum.clear();
   for (int t = from; t < to; t += kFewBatch) {
     P r[kFewBatch];
 #pragma unroll
     for (int u = 0; u < kFewBatch; ++u)
-      r[u] = t + u < to ? P::load(up + static_cast<int64_t>(word[t + u] & places) * a.grad_stride)
-                        : P::zero();
+      r[u] = t + u < to
+                 ? P::load(up + static_cast<int64_t>(word[t + u] & places) * a.grad_stride, cols)
+                 : P::zero();
 #pragma unroll
     for (int u = 0; u < kFewBatch; ++u)
       if (t + u < to) sum.add(r[u]);
@@ -638,7 +706,7 @@ __device__ __forceinline__ Sum<VEC> sum_rows(const EmbedGradArgs& a, const W* wo
   return sum;
 }
 
-template <int IN, int OUT, int VEC, class W>
+template <int IN, int OUT, int VEC, int UNIT, class W>
 __global__ void __launch_bounds__(kFewThreads)
     embed_grad_few_kernel(const __grid_constant__ EmbedGradArgs a, const int shift,
                           const int passes, const int bits, const int blocks, const int sum_ctas,
@@ -711,11 +779,11 @@ __global__ void __launch_bounds__(kFewThreads)
   uint64_t* parts = reinterpret_cast<uint64_t*>(smem + sizeof(FewShared<W>));
   for (int w = cta; w < static_cast<int>(long_runs) * blocks; w += sum_ctas) {
     const int n = w / blocks, r = sh.long_run[n], from = sh.start[r], to = sh.start[r + 1];
-    const int64_t col = (static_cast<int64_t>(w - n * blocks) * kWarp + lane) * VEC;
+    const int64_t col = static_cast<int64_t>(w - n * blocks) * kWarp * VEC + lane * UNIT;
     const int per = (to - from + kFewWarps - 1) / kFewWarps;
     Sum<VEC> sum;
     if (col < a.width) {
-      sum = sum_rows<IN, VEC, W>(a, sh.word, places, min(from + warp * per, to),
+      sum = sum_rows<IN, VEC, UNIT, W>(a, sh.word, places, min(from + warp * per, to),
                                  min(from + (warp + 1) * per, to), col);
 #pragma unroll
       for (int i = 0; i < Sum<VEC>::kPairs; ++i)
@@ -727,16 +795,16 @@ __global__ void __launch_bounds__(kFewThreads)
 #pragma unroll
         for (int i = 0; i < Sum<VEC>::kPairs; ++i)
           sum.v[i] = add2(sum.v[i], parts[(n * Sum<VEC>::kPairs + i) * kWarp + lane]);
-      store_sum<OUT, VEC>(a, row_of(r), col, sum);
+      store_sum<OUT, VEC, UNIT>(a, row_of(r), col, sum);
     }
     __syncthreads();
   }
   for (int w = cta * kFewWarps + warp; w < items; w += sum_ctas * kFewWarps) {
     const int r = w / blocks, from = sh.start[r], to = sh.start[r + 1];
-    const int64_t col = (static_cast<int64_t>(w - r * blocks) * kWarp + lane) * VEC;
+    const int64_t col = static_cast<int64_t>(w - r * blocks) * kWarp * VEC + lane * UNIT;
     if (to - from > kLongRun || col >= a.width) continue;
-    store_sum<OUT, VEC>(a, row_of(r), col,
-                        sum_rows<IN, VEC, W>(a, sh.word, places, from, to, col));
+    store_sum<OUT, VEC, UNIT>(a, row_of(r), col,
+                        sum_rows<IN, VEC, UNIT, W>(a, sh.word, places, from, to, col));
   }
 }
 
