@@ -339,6 +339,8 @@ __global__ void __launch_bounds__(kPlanThreads)
                     p.start[slot], p.start[slot + 1]};
 }
 
+constexpr int64_t kZeroFewBytes = 128 * 1024;
+
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 bool aligned(const void* p, int64_t stride, int64_t bytes, int es) {
@@ -566,8 +568,13 @@ cudaError_t launch_embed_grad(int type, int out_type, const EmbedGradArgs& a, in
   const int64_t blocks = cdiv(a.width, kWarp * (vec * es >= 16 ? vec : kNarrow));
   const int sms = device_sm_count();
   if (few) {
-    // every CTA sorts: no more of them than one per SM, or two for the zeros
-    const int64_t rows = std::min<int64_t>(kZeroMostRows, cdiv(a.vocab, 2 * sms));
+    // every CTA sorts, so that there is one per SM for the sums; those of the zeros
+    // only look which tokens are in their rows: four per SM, or 128 KB each (64
+    // tokens into 131,072 x 1,024 f32 76 us, 80 with 512 KB; 1,500 into 32,000 x
+    // 1,000 f16 21, 31 where they sorted too)
+    const int64_t rows =
+        std::min({static_cast<int64_t>(kZeroMostRows), cdiv(a.vocab, 4 * sms),
+                  std::max<int64_t>(1, kZeroFewBytes / (a.width * out_es))});
     const int64_t sums =
         std::max<int64_t>(1, std::min<int64_t>(cdiv(a.tokens * blocks, kFewWarps), sms));
     int shift = 1;

@@ -719,7 +719,20 @@ __global__ void __launch_bounds__(kFewThreads)
   const int lane = static_cast<int>(lane_id());
   grid_dependency_sync();
   constexpr int kEach = kFewTokens / kFewThreads;
-  const int tokens = static_cast<int>(a.tokens);
+  const int tokens = static_cast<int>(a.tokens), cta = static_cast<int>(blockIdx.x);
+  if (cta >= sum_ctas) {  // the zeros need no order
+    const int64_t first = (cta - sum_ctas) * rows_per_zero;
+    const int64_t last = min(first + rows_per_zero, a.vocab);
+    for (int i = tid; i < kZeroMostRows / 32; i += kFewThreads) sh.named[i] = 0;
+    __syncthreads();
+    for (int i = tid; i < tokens; i += kFewThreads) {
+      const int64_t v = static_cast<int64_t>(key_of(a, i)) - first;
+      if (v >= 0 && v < last - first) atomicOr(&sh.named[v / 32], 1u << (v % 32));
+    }
+    __syncthreads();
+    fill_rows<OUT>(a, first, last, 0.0f, sh.named);
+    return;
+  }
   const int each = tokens > kFewThreads ? kEach : 1, base = tid * each;
   if (each == 1)
     sort_few<1>(a, sh, shift, passes, bits);
@@ -755,12 +768,6 @@ __global__ void __launch_bounds__(kFewThreads)
     for (int i = tid; i < rows; i += kFewThreads)
       a.row_ids[i] = i < runs ? static_cast<int64_t>(sh.key[i]) : -1;
     if (tid == 0) *a.count = runs;
-  }
-  const int cta = static_cast<int>(blockIdx.x);
-  if (cta >= sum_ctas) {
-    const int64_t first = (cta - sum_ctas) * rows_per_zero;
-    zero_rows<OUT>(a, sh.key, runs, first, min(first + rows_per_zero, a.vocab), 0.0f, sh.named);
-    return;
   }
   const W places = (static_cast<W>(1) << shift) - 1;
   const int items = runs * blocks;
