@@ -111,6 +111,7 @@ __device__ __forceinline__ float score_of(uint32_t o) {
   return __uint_as_float(o ^ ((o >> 31) != 0 ? 0x80000000u : 0xFFFFFFFFu));
 }
 constexpr uint32_t kOrderLeast = 0x00800000u;  // of the lowest finite score
+constexpr uint32_t kOrderMost = 0xFF800000u;   // of +inf; NaN is above
 
 // A score and its column in one word: the larger word is the better score, of
 // equal ones the one of the lower column.
@@ -582,7 +583,9 @@ struct Selection {
     }
   }
 
-  // f(order, column) for every score of the row that reaches the bound
+  // f(order, column) for every score of the row that reaches the bound.  NaN is
+  // left out, as the groups' maxima and collect() do: counts of scores hold only
+  // over one set of them, and say what fits among the candidates.
   template <class F>
   __device__ __forceinline__ void each(uint32_t least, F&& f) const {
     constexpr int kN = ScoreVec<TYPE>::kCount, kAhead = 4;
@@ -609,7 +612,7 @@ struct Selection {
             using Raw = typename Score<TYPE>::Raw;
             const uint32_t o = order_of(Score<TYPE>::load(
                 static_cast<Raw>(kN == 4 ? w[i & 3] : w[i >> 1] >> (16 * (i & 1)))));
-            if (o >> 16 >= least) f(o, col + i);
+            if (o >> 16 >= least && o <= kOrderMost) f(o, col + i);
           }
         }
       }
@@ -920,13 +923,13 @@ __global__ void __launch_bounds__(WARPS* kWarp)
     const bool fits = sh.hits <= room && sh.count <= room;
     row_sync<WARPS>();
     if (!fits) select_exactly(sel, least);
-    found = sh.count;
+    found = min(sh.count, room);
     int limit = 4 * kThreads;
     while (limit < top) limit *= 2;
     if (WARPS > 1 && found > 2 * limit) {
       row_sync<WARPS>();
       narrow(sel, found, limit);
-      found = sh.count;
+      found = min(sh.count, room);
     }
     // warps without a result to write
     if (found <= kThreads && tid - lane >= max(found, max(top - found, a.k))) return;

@@ -222,6 +222,36 @@ def test_nan_and_infinity_stay_in_their_rows(rs, dtype, cols):
     assert grad[bad].isnan().all() and not grad[good].isnan().any()
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,cols", [(4, 65536), (4, 20001), (4200, 3000)])
+def test_nan_beside_long_ties(rs, rows, cols, dtype):
+    """Rows of more equal scores than fit among the candidates, with NaN in a few
+    columns, in thousands, and in nearly all: values NaN, ids -1, whatever the
+    ties' sign; rows without NaN between them are not touched by it."""
+    x, g = rows_of(rows, cols, dtype, 25)
+    t = tokens_of(x, 1, g)
+    draw = torch.rand(rows, cols, generator=g, device="cuda")
+    for value in (1.0, 0.0, -3.0, torch.finfo(dtype).min):
+        for better in (False, True):
+            x.fill_(value)
+            if better:
+                x[:, 7::50] = value + 0.5 if value > -1e4 else 0.0
+            clean = x.clone()
+            for share in (0.001, 0.3, 0.99):
+                gone = draw < share
+                gone[:, 0] = True
+                gone[1::4] = False
+                x.copy_(torch.where(gone, torch.full_like(x, math.nan), clean))
+                for top in (20, 128, 300):
+                    got = rs.token_logprobs(x, t, top)
+                    want = rs.token_logprobs(clean[1::4], t[1::4], top)
+                    bad = gone[:, 0]
+                    for name in ("logprobs", "entropy", "lse", "top_logprobs"):
+                        assert getattr(got, name)[bad].isnan().all(), name
+                    assert (got.top_ids[bad] == -1).all()
+                    assert all(torch.equal(a[1::4], b) for a, b in zip(got, want))
+
+
 def test_tokens_outside_and_repeated_and_many(rs):
     x, g = rows_of(7, 3001, torch.bfloat16, 12)
     t = tokens_of(x, 6, g)
