@@ -37,7 +37,7 @@ __device__ __forceinline__ Stats moved(const Stats& s, float m, float d) {
 
 __device__ __forceinline__ Stats warp_join(const Stats& v, float scale2) {
   const float m = warp_max(v.m);
-  const Stats s = moved(v, m, (v.m - origin(m)) * scale2);
+  const Stats s = moved(v, m, apart2(v.m, origin(m), scale2));
   return {m, warp_sum(s.sum), warp_sum(s.dot)};
 }
 
@@ -64,7 +64,7 @@ struct RunningStats {
     return {o, (a + b) * mend, (c + d + lack() * (a + b)) * mend};
   }
   __device__ __forceinline__ void move(float m, float scale2) {
-    const Stats s = moved(at_origin(), m, (o - m) * scale2);
+    const Stats s = moved(at_origin(), m, apart2(o, m, scale2));
     o = m;
     limit = m + 8.0f / scale2;
     const Exponent e(m, scale2);
@@ -97,7 +97,7 @@ struct RunningStats {
   }
   __device__ __forceinline__ Stats result(float scale2) const {
     const Stats s = at_origin();
-    return top > o ? moved(s, top, (o - top) * scale2) : s;
+    return top > o ? moved(s, top, apart2(o, top, scale2)) : s;
   }
 };
 
@@ -938,8 +938,8 @@ __global__ void __launch_bounds__(WARPS* kWarp)
   for (int i = kWarp + lane; i < p.split; i += kWarp) {
     own = part[i];
     const float m = fmaxf(st.m, own.x), o = origin(m);
-    const Stats x = moved(st, m, (st.m - o) * a.scale2);
-    const Stats y = moved(Stats{own.x, own.y, own.z}, m, (own.x - o) * a.scale2);
+    const Stats x = moved(st, m, apart2(st.m, o, a.scale2));
+    const Stats y = moved(Stats{own.x, own.y, own.z}, m, apart2(own.x, o, a.scale2));
     st = Stats{m, x.sum + y.sum, x.dot + y.dot};
   }
   const RowStats s(warp_join(st, a.scale2));

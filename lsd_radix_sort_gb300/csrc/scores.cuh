@@ -78,6 +78,12 @@ struct Softmax {
 // (so that -inf - m stays -inf).
 __device__ __forceinline__ float origin(float m) { return m == -INFINITY ? 0.0f : m; }
 
+// (a - b) scale, where the difference of two finite scores may be more than a
+// float holds (its half is none; both factors are exact).
+__device__ __forceinline__ float apart2(float a, float b, float scale) {
+  return (0.5f * a - 0.5f * b) * (2.0f * scale);
+}
+
 // Both halves of a row: scale2 = log2(e) / temperature.
 __device__ __forceinline__ Softmax join(Softmax a, Softmax b, float scale2) {
   const float m = fmaxf(a.m, b.m), o = origin(m);

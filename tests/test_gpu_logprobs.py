@@ -196,6 +196,24 @@ def test_large_scores_and_temperatures(rs):
             within(torch.where(held, got.logprobs.double(), logp), logp, bound, f"logprobs at {tau}")
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,cols", [(8, 64), (8, 3000), (300, 12000), (8, 40000), (8, 400003)])
+def test_scores_further_apart_than_a_float(rs, rows, cols, dtype):
+    """Scores of both signs at the type's limits, at temperatures that make
+    their difference a small one; the larger ones early, late, and anywhere."""
+    for tau in (1e36, 1e37, 8e37, 3.3e38):
+        x, g = rows_of(rows, cols, dtype, 26)
+        x[0::4, :cols // 2], x[0::4, cols // 2:] = -3.3e38, 3.3e38
+        x[1::4], x[1::4, cols - 1] = -3.3e38, 3.3e38
+        x[2::4] = ((torch.rand(rows // 4, cols, generator=g, device="cuda") * 2 - 1) * 3.3e38).to(dtype)
+        x[3::4, :cols // 2] = -3.3e38
+        t = tokens_of(x, 2, g)
+        t[:, 0] = cols - 1
+        check(rs, x, t, 20, tau)
+        if tau < 2.0 ** 126:  # (above, 1 / tau has fewer than 24 bits)
+            check_grad(rs, x, g, tokens=t, top=3, tau=tau)
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("cols", [50, 40000])
 def test_nan_and_infinity_stay_in_their_rows(rs, dtype, cols):
