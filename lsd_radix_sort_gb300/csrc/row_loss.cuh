@@ -26,11 +26,12 @@ struct Targets {
   float* x;    // its score
 };
 
-// A distillation loss is added up in units of scores, a quarter of it at a
-// time: a target masked by the type's lowest value is twice that from the
-// largest score there may be, more than a float holds, and so is the lowest
-// value over a temperature below 1; weight and temperature come last.
-constexpr float kPart = 0.25f;
+// A distillation loss is added up in units of scores, a 64th of it at a time: a
+// target masked by the type's lowest value is twice that from the largest score
+// there may be, more than a float holds, and so is the lowest value over a
+// temperature below 1, or 21 temperatures (the logarithm of 2^30 columns) near
+// a float's end; weight and temperature come last.
+constexpr float kPart = 1.0f / 64;
 
 // What the target warp hands to the threads that hold the row.
 struct Head {
@@ -149,15 +150,15 @@ __device__ __forceinline__ void load_targets(const RowLossArgs& a, int64_t row, 
   vm = origin(warp_max(vm));
   xm = origin(warp_max(xm));
   float sum = 0.0f;
-  for (int k = lane; k < a.k; k += kWarp) sum += exp2_approx((t.p[k] - vm) * scale2);
+  for (int k = lane; k < a.k; k += kWarp) sum += exp2_approx(apart2(t.p[k], vm, scale2));
   sum = warp_sum(sum);
   const float log_sum = logf(sum);
   float acc = 0.0f;
   for (int k = lane; k < a.k; k += kWarp) {
-    const float v = t.p[k] - vm;
-    const float p = sum == 0.0f ? 0.0f : exp2_approx(v * scale2) / sum;
+    const float v = 0.5f * t.p[k] - 0.5f * vm;
+    const float p = sum == 0.0f ? 0.0f : exp2_approx(v * (2.0f * scale2)) / sum;
     if (MODE != kLossBwd && p != 0.0f)
-      acc += p * (kPart * v - kPart * a.tau * log_sum - (kPart * t.x[k] - kPart * xm));
+      acc += p * (2.0f * kPart * v - kPart * a.tau * log_sum - (kPart * t.x[k] - kPart * xm));
     t.p[k] = p;
   }
   if (MODE != kLossBwd) acc = warp_sum(acc);
@@ -239,13 +240,13 @@ __device__ __forceinline__ RowResult row_result(const RowLossArgs& a, const Head
     const bool none = empty || !h.live;
     r.logp = 0.0f;
     r.loss = none ? 0.0f
-                  : a.tau * h.w / kPart *
-                        (h.a + (kPart * m - kPart * h.ref + kPart * a.tau * log_sum));
+                  : a.tau * h.w *
+                        (h.a + (kPart * m - kPart * h.ref + kPart * a.tau * log_sum)) / kPart;
     r.c = none ? 0.0f : h.up * a.tau;
   } else {
     const float logp = empty               ? -INFINITY
                        : MODE == kLossBwd ? h.x0 / a.tau - m
-                                          : (h.x0 - m) * a.inv_tau - log_sum;
+                                          : (0.5f * h.x0 - 0.5f * m) * (2.0f * a.inv_tau) - log_sum;
     const float adv = h.adv;
     const float ratio = expf(logp - h.old);
     const bool held = (adv > 0.0f && ratio > a.clip_high) || (adv < 0.0f && ratio < a.clip_low);

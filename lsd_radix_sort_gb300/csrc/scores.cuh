@@ -79,20 +79,21 @@ struct Softmax {
 __device__ __forceinline__ float origin(float m) { return m == -INFINITY ? 0.0f : m; }
 
 // (a - b) scale, where the difference of two finite scores may be more than a
-// float holds (its half is none; both factors are exact).
+// float holds (half of it is not; the factors of 2 are exact).
 __device__ __forceinline__ float apart2(float a, float b, float scale) {
-  return (0.5f * a - 0.5f * b) * (2.0f * scale);
+  return __fmaf_rn(0.5f, a, -0.5f * b) * scale * 2.0f;
 }
 
 // Both halves of a row: scale2 = log2(e) / temperature.
 __device__ __forceinline__ Softmax join(Softmax a, Softmax b, float scale2) {
   const float m = fmaxf(a.m, b.m), o = origin(m);
-  return {m, a.sum * exp2_approx((a.m - o) * scale2) + b.sum * exp2_approx((b.m - o) * scale2)};
+  return {m, a.sum * exp2_approx(apart2(a.m, o, scale2)) +
+                 b.sum * exp2_approx(apart2(b.m, o, scale2))};
 }
 
 __device__ __forceinline__ Softmax warp_join(Softmax v, float scale2) {
   const float m = warp_max(v.m);
-  return {m, warp_sum(v.sum * exp2_approx((v.m - origin(m)) * scale2))};
+  return {m, warp_sum(v.sum * exp2_approx(apart2(v.m, origin(m), scale2)))};
 }
 
 // ---- 16-byte vectors of scores --------------------------------------------
@@ -361,7 +362,7 @@ struct RunningSoftmax {
     return (a + b) * e.mend;
   }
   __device__ __forceinline__ void move(float m) {
-    const float sum = total() * exp2_approx((o - m) * scale);
+    const float sum = total() * exp2_approx(apart2(o, m, scale));
     o = m;
     limit = m + slack;
     e = Exponent(m, scale);
@@ -378,7 +379,7 @@ struct RunningSoftmax {
   }
   __device__ __forceinline__ Softmax result() const {
     const float sum = total();
-    return {top, top > o ? sum * exp2_approx((o - top) * scale) : sum};
+    return {top, top > o ? sum * exp2_approx(apart2(o, top, scale)) : sum};
   }
 };
 

@@ -138,6 +138,46 @@ def test_small_temperatures(rs, n, cols, dtype):
                      weights=torch.full((n,), tau, device="cuda"))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n,cols", [(16, 64), (16, 3000), (304, 12000), (304, 30000), (16, 40000), (160, 40000),
+                                    (8, 400003)])
+def test_scores_further_apart_than_a_float(rs, n, cols, dtype):
+    """Scores of both signs at the type's limits, at temperatures that make
+    their difference a small one; the larger ones early, late, and anywhere."""
+    for tau in (1e30, 1e36, 1e37, 8e37):
+        x, g = scores(n, cols, dtype, 3)
+        x[0::4, :cols // 2], x[0::4, cols // 2:] = -3.3e38, 3.3e38
+        x[1::4], x[1::4, cols - 1] = -3.3e38, 3.3e38
+        x[2::4] = ((torch.rand(n // 4, cols, generator=g, device="cuda") * 2 - 1) * 3.3e38).to(dtype)
+        x[3::4, :cols // 2] = -3.3e38
+        rows = lb.Rows(x, tau)
+        actions = torch.randint(0, cols, (n,), generator=g, device="cuda")
+        actions[1::8] = cols - 1
+        if tau < 1e36:
+            # A log-probability of -6.6e8 is held to 2^5 by a float: the ratio
+            # of two such, the exponential of their difference, has no bound
+            # (e^d - 1 <= 2 d holds for d <= 1), and so have losses and
+            # gradients.  The log-probability itself does.
+            logp = -rows.dist.gather(1, actions[:, None])[:, 0] - rows.log_sum
+            zero = torch.zeros(n, device="cuda")
+            bound = 2.0 ** -24 * 4 * (rows.dist.gather(1, actions[:, None])[:, 0] + lb.LAG + rows.log_sum)
+            got = rs.policy_loss(x, actions, zero, zero, temperature=tau)
+            lb.within(got[1], logp, bound + rows.sum_error, "log-probabilities")
+            continue
+        check_policy(rs, x, tau, actions, g, rows=rows, kl=0.0)
+        # the teacher's list is as far apart as its rows
+        indices = torch.stack([torch.zeros_like(actions), actions], 1)
+        indices[actions == 0, 1] = -1
+        values = torch.tensor([-3.3e38, 3.3e38], device="cuda").expand(n, 2).contiguous()
+        weights = torch.full((n,), 1e-3 / tau / tau * 1e38, device="cuda")
+        losses, loss_bound, grad, bound, _ = lb.distill(rows, x, values, indices, weights)
+        kw = {"temperature": tau, "weights": weights}
+        lb.within(rs.distill_loss(x, values, indices, **kw)[0], losses, loss_bound, "losses")
+        got = rs.distill_loss_grad(x, values, indices, **kw)
+        lb.within(got[0], losses, loss_bound, "losses with gradient")
+        lb.within(got[2], grad, bound, "gradient")
+
+
 def balance64(x, ids, mask=None):
     """(loss, mean probabilities, gradient, scale of its terms) in 64 bits."""
     n, experts = x.shape
