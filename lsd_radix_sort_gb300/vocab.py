@@ -231,6 +231,12 @@ def _scale(scale):
     return scale
 
 
+def _padding_id(padding_id):
+    if padding_id < -1:
+        raise ValueError(f"padding_id must be an id, or -1 for none, got {padding_id}")
+    return padding_id
+
+
 def _embed(table, ids, scale, out, stream):
     torch = _l._torch or _l._load()
     kind = _kind(table, "table")
@@ -259,6 +265,7 @@ def embedding(table, ids, scale: float = 1.0, padding_id: int = -1, out=None, st
     of any shape; an id outside [0, vocab) gives zeros.  Differentiable in
     ``table``; tokens of ``padding_id`` are looked up like any other, but take
     no part in the gradient."""
+    _padding_id(padding_id)
     if _wants_grad(table, stream, out):
         return _autograd().Embedding.apply(table, ids, float(scale), int(padding_id))
     return _embed(table, ids, scale, out, stream)
@@ -284,8 +291,7 @@ def _embed_grad(grad, ids, vocab, scale, padding_id, dtype, out, mode, row_ids, 
     grad_stride = _rows_of(grad, ids, width, "grad")
     if not 1 <= vocab < 1 << 31:
         raise ValueError(f"vocab must be from 1 to 2^31 - 1, got {vocab}")
-    if padding_id < -1:
-        raise ValueError(f"padding_id must be an id, or -1 for none, got {padding_id}")
+    _padding_id(padding_id)
     if dtype is None:
         dtype = grad.dtype if out is None else out.dtype
     if dtype is not grad.dtype and dtype is not torch.float32:

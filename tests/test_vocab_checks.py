@@ -122,6 +122,12 @@ def test_scales_that_are_none(scale):
         vocab._scale(scale)
 
 
+def test_a_padding_id_that_is_none_is_refused_before_the_backward_call():
+    for table in (f(4, 9), f(4, 9).requires_grad_(True)):
+        with pytest.raises(ValueError, match="padding_id must be an id"):
+            rs.embedding(table, i(3), padding_id=-2)
+
+
 # ------------------------------------------------------------------- the C ABI
 BASE = 0x10000000  # addresses that no call here may touch
 NAN, INF = float("nan"), float("inf")
