@@ -477,7 +477,12 @@ def row_wait_timeout_probe(timeout_ns: int, stream=None) -> int:
 def _wants_grad(x, stream, *outs):
     """Whether the call is recorded by autograd, which allocates the outputs and
     runs the backward call on the stream that was current in the forward one."""
-    if not x.requires_grad or not (_torch or _load()).is_grad_enabled():
+    fwd = (_torch or _load()).autograd.forward_ad
+    # (no level entered: nothing has a tangent, and asking costs a microsecond)
+    if getattr(fwd, "_current_level", 0) >= 0 and fwd.unpack_dual(x).tangent is not None:
+        raise ValueError("there are no forward-mode derivatives: give the primal tensor "
+                         "(torch.autograd.forward_ad.unpack_dual)")
+    if not x.requires_grad or not _torch.is_grad_enabled():
         return False
     if stream is not None or any(o is not None for o in outs):
         raise ValueError("outputs or a stream cannot be given for scores that require a "

@@ -122,6 +122,24 @@ def test_scales_that_are_none(scale):
         vocab._scale(scale)
 
 
+def test_forward_mode_is_refused():
+    """A tangent is not dropped without a word, by the losses neither."""
+    fwd = torch.autograd.forward_ad
+    calls = [lambda x: rs.token_logprobs(x, i(4)), lambda x: rs.embedding(x, i(3)),
+             lambda x: rs.distill_loss(x, f(4, 2), i(4, 2)), lambda x: rs.policy_loss(x, i(4), f(4), f(4)),
+             lambda x: rs.balance_loss(x, i(4, 2))]
+    for call in calls:
+        for x in (f(4, 9), f(4, 9).requires_grad_(True)):
+            with fwd.dual_level():
+                dual = fwd.make_dual(x, f(4, 9))
+                with pytest.raises(ValueError, match="no forward-mode derivatives"):
+                    call(dual)
+                with pytest.raises(ValueError, match="CUDA device"):
+                    call(fwd.unpack_dual(dual).primal.detach())
+            with pytest.raises(ValueError, match="no forward-mode derivatives"):
+                torch.func.jvp(call, (x,), (f(4, 9),))
+
+
 def test_a_padding_id_that_is_none_is_refused_before_the_backward_call():
     for table in (f(4, 9), f(4, 9).requires_grad_(True)):
         with pytest.raises(ValueError, match="padding_id must be an id"):
