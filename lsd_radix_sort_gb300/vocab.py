@@ -97,7 +97,6 @@ def _dense(t, shape, what, dtype=None):
                          f"{t.dtype} of {tuple(t.shape)}")
 
 
-@functools.lru_cache(maxsize=256)
 def token_logprobs_temp_bytes(rows: int, cols: int, logits_type: int, top: int = 0) -> int:
     """Scratch size of ``token_logprobs`` on the current device, for logits of
     an rs_score_type (0 float16, 1 bfloat16, 2 float32)."""
@@ -105,6 +104,12 @@ def token_logprobs_temp_bytes(rows: int, cols: int, logits_type: int, top: int =
     _check(_lib_of().rs_token_logprobs_temp_bytes(rows, cols, logits_type, top, ctypes.byref(n)),
            "rs_token_logprobs_temp_bytes")
     return n.value
+
+
+@functools.lru_cache(maxsize=256)
+def _logprobs_scratch(index, rows, cols, kind, top):
+    """The same, kept for each device: the sizes go with its number of SMs."""
+    return token_logprobs_temp_bytes(rows, cols, kind, top)
 
 
 def _logprobs(logits, tokens, top, temperature, temp, stream):
@@ -115,7 +120,7 @@ def _logprobs(logits, tokens, top, temperature, temp, stream):
     if not 0 <= top <= MAX_TOP:
         raise ValueError(f"0 to {MAX_TOP} top alternatives per row, got {top}")
     index = _device(stream, logits, tokens, temp)
-    need = token_logprobs_temp_bytes(rows, cols, kind, top)
+    need = _logprobs_scratch(index, rows, cols, kind, top)
     with _on(stream):
         device, f32 = logits.device, torch.float32
         logprobs = None if tokens is None else torch.empty(tokens.shape, dtype=f32, device=device)

@@ -122,6 +122,31 @@ def test_scales_that_are_none(scale):
         vocab._scale(scale)
 
 
+def test_scratch_sizes_are_kept_for_each_device(monkeypatch):
+    """Devices of unlike numbers of SMs divide the same rows differently."""
+    on, asked = [0], []
+
+    class Lib:
+        @staticmethod
+        def rs_token_logprobs_temp_bytes(rows, cols, kind, top, out):
+            out._obj.value = 256 * (1 + on[0])
+            return 0
+
+        @staticmethod
+        def rs_token_logprobs(args, stream):
+            asked.append(args._obj.temp_bytes)
+            return 0
+
+    monkeypatch.setattr(vocab, "_lib_of", lambda: Lib)
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: on[0])
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: on[0])
+    monkeypatch.setattr(vocab._l, "_raw_stream", lambda index: 0)
+    for on[0] in (0, 1, 0, 1):
+        rs.token_logprobs(f(4, 977))
+        assert rs.token_logprobs_temp_bytes(4, 977, 2) == 256 * (1 + on[0])
+    assert asked == [256, 512, 256, 512]
+
+
 def test_forward_mode_is_refused():
     """A tangent is not dropped without a word, by the losses neither."""
     fwd = torch.autograd.forward_ad
