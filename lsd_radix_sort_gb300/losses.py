@@ -153,6 +153,14 @@ def _grad_stride(x, grad_out):
     return _matrix(grad_out, "grad_out")[2]
 
 
+def _room(temp):
+    """Bytes of a scratch tensor (one that repeats its memory has fewer than it
+    says)."""
+    if not temp.is_contiguous():
+        raise ValueError("temp must be contiguous")
+    return temp.numel() * temp.element_size()
+
+
 _CURRENT = contextlib.nullcontext()
 
 
@@ -399,7 +407,7 @@ def _balance(scores, ids, mask, scale, grad, with_grad, temp, stream):
     args = BalanceArgs(scores.data_ptr(), stride, tokens, ids.data_ptr(), ids_stride, _ptr(mask),
                        loss.data_ptr(), mean.data_ptr(), counts.data_ptr(), n.data_ptr(),
                        _ptr(grad), grad_stride, _ptr(temp),
-                       0 if temp is None else temp.numel() * temp.element_size(),
+                       0 if temp is None else _room(temp),
                        kind, experts, ib, k, scale)
     s = _raw_stream(index) if stream is None else stream.cuda_stream
     _check(_lib_of().rs_balance_loss(ctypes.byref(args), s), "rs_balance_loss")

@@ -29,7 +29,7 @@ import typing
 from . import _check, _lib_of
 from . import losses as _l
 from .losses import (_F, _I, _I64, _P, _SZ, MAX_TOP, _device, _grad_stride, _index_bytes, _kind,
-                     _matrix, _on, _ptr, _vector, _wants_grad)
+                     _matrix, _on, _ptr, _room, _vector, _wants_grad)
 
 __all__ = ["TokenLogprobs", "token_logprobs", "token_logprobs_temp_bytes",
            "token_logprobs_backward", "embedding", "embedding_grad", "embedding_grad_rows",
@@ -136,7 +136,7 @@ def _logprobs(logits, tokens, top, temperature, temp, stream):
     args = LogprobsArgs(logits.data_ptr(), stride, rows, cols, _ptr(tokens), token_stride,
                         _ptr(logprobs), entropy.data_ptr(), lse.data_ptr(), stats.data_ptr(),
                         _ptr(top_logprobs), _ptr(top_ids), None, 0,
-                        temp.data_ptr(), temp.numel() * temp.element_size(), kind, ib, k, top,
+                        temp.data_ptr(), _room(temp), kind, ib, k, top,
                         temperature)
     s = _l._raw_stream(index) if stream is None else stream.cuda_stream
     _check(_lib_of().rs_token_logprobs(ctypes.byref(args), s), "rs_token_logprobs")
@@ -329,7 +329,7 @@ def _embed_grad(grad, ids, vocab, scale, padding_id, dtype, out, mode, row_ids, 
             temp = torch.empty((need,), dtype=torch.uint8, device=device)
     args = EmbeddingGradArgs(grad.data_ptr(), grad_stride, n, width, vocab, ids.data_ptr(),
                              padding_id, out.data_ptr(), out_stride, _ptr(row_ids), _ptr(count),
-                             temp.data_ptr(), temp.numel() * temp.element_size(), _ptr(status),
+                             temp.data_ptr(), _room(temp), _ptr(status),
                              kind, _l._TYPES[dtype], ib, mode, _scale(scale))
     s = _l._raw_stream(index) if stream is None else stream.cuda_stream
     _check(_lib_of().rs_embedding_grad(ctypes.byref(args), s), "rs_embedding_grad")

@@ -137,6 +137,7 @@ def test_scratch_sizes_are_kept_for_each_device(monkeypatch):
             asked.append(args._obj.temp_bytes)
             return 0
 
+    vocab._l._load()
     monkeypatch.setattr(vocab, "_lib_of", lambda: Lib)
     monkeypatch.setattr(torch.Tensor, "get_device", lambda self: on[0])
     monkeypatch.setattr(torch.cuda, "current_device", lambda: on[0])
@@ -145,6 +146,23 @@ def test_scratch_sizes_are_kept_for_each_device(monkeypatch):
         rs.token_logprobs(f(4, 977))
         assert rs.token_logprobs_temp_bytes(4, 977, 2) == 256 * (1 + on[0])
     assert asked == [256, 512, 256, 512]
+
+
+@pytest.mark.parametrize("call", [
+    lambda **kw: rs.token_logprobs(f(4, 9), **kw), lambda **kw: rs.embedding_grad(f(3, 9), i(3), 4, **kw),
+    lambda **kw: rs.embedding_grad_rows(f(3, 9), i(3), 4, **kw), lambda **kw: rs.balance_loss(f(4, 9), i(4, 2), **kw)])
+def test_scratch_that_repeats_its_memory(lib, monkeypatch, call):
+    """A megabyte by its shape, and one byte by its memory."""
+    def reached(*args):
+        raise AssertionError("the call was made")
+
+    vocab._l._load()
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 0)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(vocab._l, "_raw_stream", reached)
+    for temp in (i(1, dtype=torch.uint8).expand(1 << 20), i(1 << 20, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="temp must be contiguous"):
+            call(temp=temp)
 
 
 def test_forward_mode_is_refused():
