@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1)
   }
   cluster_barrier();  // from here on no CTA reads another's memory
   // (written before, these words would be waited for at every barrier)
-  const int64_t words = 2 * static_cast<int64_t>(p.chunks) * p.blocks;
+  const int64_t words = piece_places(a.tokens) * p.blocks;
   for (int64_t i = rank * kClusterThreads + tid; i < words; i += kClusterCtas * kClusterThreads)
     p.arrived[i] = 0;
   uint32_t run = runs_before, runs = 0, total_live = 0, next = 0xFFFFFFFFu;
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     p.keys[i] = key_of(a, i);
     p.vals[i] = static_cast<uint32_t>(i);
   }
-  const int64_t words = 2 * static_cast<int64_t>(p.chunks) * p.blocks;
+  const int64_t words = piece_places(a.tokens) * p.blocks;
   for (int64_t i = first; i < words; i += step) p.arrived[i] = 0;
 }
 
@@ -420,9 +420,11 @@ size_t lay_out(int64_t tokens, int64_t width, void* temp, GradPlan* p, size_t* s
   while (p->chunk > kLeastChunk && tokens / p->chunk * cdiv(width, 512) < 5000) p->chunk /= 2;
   const int64_t chunks = cdiv(tokens, p->chunk);
   p->chunks = static_cast<int>(chunks);
-  p->arrived = words(2 * chunks * cdiv(width, kWarp));
-  p->partial = reinterpret_cast<float*>(
-      words(2 * chunks * static_cast<int64_t>(align_up(static_cast<size_t>(width), 512))));
+  // an eighth of a 16-bit upstream gradient's size, and some
+  const int64_t places = piece_places(tokens);
+  p->arrived = words(places * cdiv(width, kLeastBlock));
+  const size_t padded = align_up(static_cast<size_t>(width), width % 16 == 0 ? 512 : 256);
+  p->partial = reinterpret_cast<float*>(words(places * static_cast<int64_t>(padded)));
   p->list = reinterpret_cast<Entry*>(words(tokens * 4));
   p->key = words(tokens);
   *sort = parts.at;
@@ -538,7 +540,7 @@ cudaError_t launch_embed_keys(const EmbedGradArgs& a, cudaStream_t s) {
   GradPlan p{};
   size_t sort;
   lay_out(a.tokens, a.width, a.temp, &p, &sort);
-  p.blocks = static_cast<int>(cdiv(a.width, kWarp));  // any launch has no more
+  p.blocks = static_cast<int>(cdiv(a.width, kLeastBlock));  // any launch has no more
   const int64_t ctas = std::min<int64_t>(cdiv(a.tokens, kPlanThreads), 4 * device_sm_count());
   return launch_kernel(embed_keys_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kPlanThreads), 0,
                        s, a, p);

@@ -305,14 +305,22 @@ constexpr int kMostChunk = 32, kLeastChunk = 8;
 constexpr int kPiece = 32;
 static_assert(kPiece >= kMostChunk, "a chunk holds the beginnings of two pieces at most");
 constexpr int kFan = 16;
+constexpr int kLeastBlock = 4 * kWarp;  // columns of a warp at least
+
+// Scratch has two places for each kPiece sorted tokens: two later pieces of
+// runs, or two first ones, never begin in the same kPiece (a run with pieces
+// is longer than that), a later and a first one may.
+__host__ __device__ constexpr inline int64_t piece_places(int64_t tokens) {
+  return 2 * ((tokens + kPiece - 1) / kPiece);
+}
 
 constexpr int kRunsCount = 0, kRunsLive = 1, kRunsFailed = 2;  // words of the header
 struct GradPlan {
   uint32_t* header;
   Entry* list;
   uint32_t* key;         // the id of each run
-  float* partial;        // [2 * chunks][padded width]: later pieces, first pieces
-  uint32_t* arrived;     // [2 * chunks][blocks]: neighbours of the piece there
+  float* partial;        // [piece_places][padded width]: later pieces, first pieces
+  uint32_t* arrived;     // [piece_places][blocks]: neighbours of the piece there
   int chunk, chunks, blocks;
   int64_t rows_per_zero;
   // where the list is made by the sort of whole keys
@@ -330,7 +338,7 @@ __device__ __forceinline__ bool join_pieces(const GradPlan& p, int block, uint32
   using S = Sum<VEC>;
   const int lane = static_cast<int>(lane_id());
   auto place = [&](uint32_t piece) {  // of later pieces, and of first ones
-    return 2 * static_cast<int64_t>((start + piece * kPiece) / p.chunk) + (piece == 0);
+    return 2 * static_cast<int64_t>(start / kPiece + piece) + (piece == 0);
   };
   // 32 * VEC floats: a lane's next pair is 32 pairs on
   auto sums = [&](uint32_t piece) {
@@ -548,6 +556,7 @@ __global__ void __launch_bounds__(
     kGradThreads, VEC * sizeof(typename Score<IN>::Raw) == 32 || UNIT < VEC ? 3 : 4)
     embed_grad_kernel(const __grid_constant__ EmbedGradArgs a, const __grid_constant__ GradPlan p,
                       const int64_t sum_ctas) {
+  static_assert(kWarp * VEC >= kLeastBlock && kWarp * VEC <= (VEC == 16 ? 512 : 256));
   __shared__ uint32_t named[kZeroMostRows / 32];
   grid_dependency_sync();
   const int64_t cta = blockIdx.x;

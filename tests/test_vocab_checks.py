@@ -293,3 +293,13 @@ def test_scratch_size(lib):
         assert lib.rs_embedding_grad_temp_bytes(*bad, ctypes.byref(out)) == 1
     assert lib.rs_embedding_grad_temp_bytes(10, 8, 8, None) == 1
     assert rs.embedding_grad_temp_bytes(100000, 1000, 64) > rs.embedding_grad_temp_bytes(1000, 1000, 64) > 0
+
+
+def test_scratch_of_a_gradient_is_a_fraction_of_it(lib):
+    """Two sums of 32-bit columns for 32 tokens, a few counters, and the list of
+    16 bytes a token (beyond 65,536 tokens the sort's as well)."""
+    for tokens, width in ((32768, 4096), (65536, 8), (65536, 2047), (100000, 1024)):
+        columns = -(-width // (512 if width % 16 == 0 else 256)) * (512 if width % 16 == 0 else 256)
+        places = 2 * -(-tokens // 32)
+        rest = 24 * tokens if tokens <= 65536 else 60 * tokens + (1 << 22)
+        assert rs.embedding_grad_temp_bytes(tokens, 131072, width) <= places * (columns + columns // 64) * 4 + rest
