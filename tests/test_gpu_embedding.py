@@ -147,6 +147,20 @@ def test_gradient_of_many_long_runs(rs, n, ids_named):
     check_grad(rs, randn(g, n, 3001, dtype=torch.float16), ids, 5000)  # element by element
 
 
+@pytest.mark.parametrize("n,width,dtype", [(70001, 2056, torch.bfloat16), (70001, 515, torch.float32),
+                                           (80003, 3001, torch.float16), (131073, 1024, torch.bfloat16),
+                                           (66000, 40, torch.float16)])
+@pytest.mark.parametrize("ids_named", [3, 60, 3000])
+def test_gradient_of_many_tokens_in_wide_rows(rs, ids_named, n, width, dtype):
+    """More tokens than one cluster sorts, in rows that many warps share: long
+    runs of each, of a third of all and of some, and short ones."""
+    g = gen(n + ids_named)
+    ids = torch.randperm(5000, generator=g, device="cuda")[:ids_named][ids_of(g, n, ids_named, "all")]
+    ids[: n // 3] = ids[-1]
+    ids[1::1000] = -1
+    check_grad(rs, randn(g, n, width, dtype=dtype), ids, 5000, dtype=torch.float32)
+
+
 @pytest.mark.parametrize("n", [700, 6000])
 def test_gradient_of_dropped_and_padded_tokens(rs, n):
     g = gen(3)
