@@ -329,3 +329,81 @@ def test_temp_is_the_callers(rs):
             assert int(status) == 0
         with pytest.raises(rs.RadixSortError):
             rs.embedding_grad(up, ids, 400, temp=temp[:-256])
+
+
+class FailedSort:
+    """The sort inside a call on `temp` fails: while the call runs, the word that
+    its tiles say so by, the first of the sort's part of the scratch, is written
+    again and again from another stream."""
+
+    def __init__(self, rs, temp, n, vocab):
+        sort = -(-rs.temp_bytes(n, 4, 4, 0, vocab.bit_length(), 8) // 256) * 256
+        self.word = temp[temp.numel() - sort:][:4].view(torch.int32)
+        self.stream = torch.cuda.Stream()
+        self.stream.wait_stream(torch.cuda.current_stream())
+        self.graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(self.graph, stream=self.stream):
+            for _ in range(1000):
+                self.word.fill_(4)
+        self.graph.replay()
+        torch.cuda.synchronize()
+
+    def __call__(self, call):
+        torch.cuda._sleep(20_000_000)  # all is queued before any of it begins
+        begin = torch.cuda.current_stream().record_event()
+        torch.cuda._sleep(100_000)     # the word's writer first
+        self.stream.wait_event(begin)
+        with torch.cuda.stream(self.stream):
+            self.graph.replay()
+        got = call()
+        torch.cuda.synchronize()
+        return got
+
+
+@pytest.mark.parametrize("n,vocab,dtype", [(100_000, 5000, torch.bfloat16), (300_000, 200, torch.float32)])
+def test_a_sort_that_fails(rs, n, vocab, dtype):
+    """A whole table is NaN, one that is added to stays as it was, there are no
+    rows, and the status says so; the next call on the same scratch is right."""
+    g = gen(13)
+    width = 24
+    up, ids = randn(g, n, width, dtype=dtype), ids_of(g, n, vocab)
+    before = randn(g, vocab, width)
+    temp = torch.empty(rs.embedding_grad_temp_bytes(n, vocab, width), dtype=torch.uint8, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    table, sums = (torch.full((vocab, width), 7.0, device="cuda", dtype=t) for t in (dtype, torch.float32))
+    sums.copy_(before)
+    row_ids = torch.full((vocab,), 7, dtype=torch.int64, device="cuda")
+    rows, count = torch.full((vocab, width), 7.0, device="cuda", dtype=dtype), status + 7
+    kw = {"temp": temp, "status_out": status}
+
+    def whole():
+        return rs.embedding_grad(up, ids, vocab, grad_out=table, **kw)
+
+    def added():
+        return rs.embedding_grad(up, ids, vocab, grad_out=sums, accumulate=True, **kw)
+
+    def named():
+        return rs.embedding_grad_rows(up, ids, vocab, row_ids_out=row_ids, rows_out=rows, count_out=count, **kw)
+
+    fails = FailedSort(rs, temp, n, vocab)
+    for call in (whole, added, named):
+        call()  # (kernels are loaded, which waits for all streams)
+        assert int(status) == 0 and int(fails.word) == 0
+    for out in (table, rows, row_ids, count):
+        out.fill_(7)
+    sums.copy_(before)
+    for call in (whole, added, named):
+        status.zero_()
+        fails(call)
+        assert int(status) == rs.RS_ERR_LOOKBACK_TIMEOUT
+    assert table.isnan().all()
+    assert torch.equal(sums, before)
+    assert int(count) == 0 and (row_ids == -1).all() and (rows == 7).all()
+    fails(lambda: rs.embedding_grad(up, ids, vocab, grad_out=table, temp=temp))  # nobody asks
+    assert table.isnan().all()
+    status.zero_()
+    want, size, terms = vo.embedding_grad(up, ids, vocab)
+    within(whole(), want, vo.embedding_bound(want, size, terms, dtype), "the next call")
+    named()
+    c = int(count)
+    assert torch.equal(rows[:c], table[row_ids[:c]]) and int(status) == 0
