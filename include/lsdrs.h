@@ -687,7 +687,9 @@ typedef struct rs_embedding_grad_args {
   float scale;
 } rs_embedding_grad_args;
 
-/* Scratch size of rs_embedding_grad (host only). */
+/* Scratch size of rs_embedding_grad (host only): 256 bytes up to 2,048 tokens;
+ * else about tokens x width / 4 and 20 bytes a token, and beyond 65,536 tokens
+ * that of a sort of as many pairs. */
 rs_status rs_embedding_grad_temp_bytes(int64_t tokens, int64_t vocab, int64_t width,
                                        size_t* bytes);
 rs_status rs_embedding_grad(const rs_embedding_grad_args* args, void* stream);

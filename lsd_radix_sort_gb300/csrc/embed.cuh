@@ -239,8 +239,9 @@ struct __align__(16) Entry {
 
 constexpr int kGradThreads = 256;
 constexpr int kGradWarps = kGradThreads / kWarp;
-// Rows of a warp under way: with many tokens 4 and four CTAs per SM (rows of 32,768
-// x 4,096 bf16 77 us; 8 and three 83), with few, where warps are few too, 8.
+// Rows of a warp under way: with many tokens 4 (rows of 32,768 x 4,096 bf16 96 us
+// with their list and cold caches, 113 with 8; three CTAs per SM where accesses are
+// of 32 bytes or narrow, four of 16 bytes), with few, where warps are few too, 8.
 constexpr int kGradBatch = 4;
 constexpr int kFewBatch = 8;
 

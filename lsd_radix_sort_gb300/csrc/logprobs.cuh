@@ -134,7 +134,7 @@ __device__ __forceinline__ int entry_col(uint64_t e) {
 //
 // 4,096 x 131,072 bf16 scores with 20 alternatives take 205 us, of which the
 // first kernel has 180 (88% of the measured copy bandwidth) and the second 25,
-// bound by its latency of about 10 us per row and 8 rows per SM.  Kernels that
+// bound by latency: three rounds of 9 rows per SM, about 8 us each.  Kernels that
 // chose each row's alternatives where its scores were read took 252 us (a CTA
 // or a cluster per row) and 254 (one warp of a persistent CTA chooses): the
 // loads of other rows then wait for the choice.  Three CTAs per SM: with two
